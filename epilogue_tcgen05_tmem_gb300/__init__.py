@@ -8,13 +8,18 @@ epilogue_tcgen05_tmem_gb300._build``).
 
 Names follow the C ABI: ``eg_plan_create``, ``eg_plan_run``,
 ``eg_plan_run_unfused``, ``eg_plan_destroy``, ... and a small ``Plan`` class
-that takes torch tensors and passes their device pointers.
+that takes torch tensors and passes their device pointers.  The operators
+between the linear layers (``include/eg_decoder.h``) are in ``decoder`` and
+re-exported here.
 """
 from __future__ import annotations
 
 import ctypes
 import os
 import threading
+
+from . import decoder
+from .decoder import kv_append, qk_norm_rope, qk_norm_rope_backward  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libeg.so")
@@ -126,6 +131,7 @@ def lib() -> ctypes.CDLL:
             L.eg_status_string.restype = ctypes.c_char_p
             L.eg_last_error_detail.argtypes = []
             L.eg_last_error_detail.restype = ctypes.c_char_p
+            decoder.declare(L)
             _lib = L
     return _lib
 

@@ -17,6 +17,7 @@
 #include "eg_kernel.cuh"
 #include "eg_registry.h"
 #include "eg_gated.h"
+#include "eg_host.h"
 #include "eg_quant.h"
 #include "eg_tuning.h"
 
@@ -47,10 +48,7 @@ eg_status cuda_fail(cudaError_t e, const char* what) {
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point, so the
 // library needs no link-time dependency on libcuda.
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+using eg::EncodeTiledFn;
 
 EncodeTiledFn encode_fn() {
   static std::once_flag once;
@@ -87,6 +85,36 @@ int out_elt_bytes(uint32_t flags) {
 }
 
 }  // namespace
+
+namespace eg {
+
+eg_status host_fail(eg_status s, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  return fail(s, "%s", buf);
+}
+
+eg_status host_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+eg_status host_check_device(int* dev) {
+  EG_CUDA(cudaGetDevice(dev), "cudaGetDevice");
+  int major = 0, minor = 0;
+  EG_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev), "device query");
+  EG_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev), "device query");
+  if (major != 10 || minor != 3)
+    return fail(EG_ERR_UNSUPPORTED, "the kernels are built for sm_103a; device %d is sm_%d%d", *dev,
+                major, minor);
+  return EG_OK;
+}
+
+EncodeTiledFn host_encode_tiled() { return encode_fn(); }
+
+uint64_t host_wait_limit_ns() { return default_wait_limit_ns(); }
+
+}  // namespace eg
 
 struct GraphEntry {
   eg_args args;

@@ -1,0 +1,230 @@
+"""The operators between a decoder's linear layers: thin Python binding of
+``include/eg_decoder.h``.
+
+``qk_norm_rope`` / ``qk_norm_rope_backward`` norm queries and keys per head and
+rotate them by their positions; ``kv_append`` does the same on the way into a
+paged key/value cache.  All take torch CUDA tensors [tokens, heads, head_dim]
+by their strides (the last dimension contiguous), so parts of one projection's
+output are passed as they are, and run on the current stream unless ``stream``
+gives another.
+"""
+from __future__ import annotations
+
+import ctypes
+import struct
+
+EL_DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
+
+EXPORTED = ("eg_qk_norm_rope", "eg_qk_norm_rope_backward", "eg_qk_norm_rope_workspace_bytes",
+            "eg_kv_append")
+
+_i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
+
+
+class eg_rope_args(ctypes.Structure):
+    _fields_ = [("tokens", _i64), ("q_heads", _i32), ("kv_heads", _i32), ("head_dim", _i32),
+                ("rot_dim", _i32), ("dtype", _i32), ("pairs", _i32), ("eps", _f32),
+                ("page_size", _i32), ("cos_sin", _p), ("max_positions", _i64), ("positions", _p),
+                ("q_weight", _p), ("k_weight", _p), ("q", _p), ("k", _p), ("v", _p),
+                ("q_token", _i64), ("q_head", _i64), ("k_token", _i64), ("k_head", _i64),
+                ("v_token", _i64), ("v_head", _i64), ("q_out", _p), ("k_out", _p),
+                ("qo_token", _i64), ("qo_head", _i64), ("ko_token", _i64), ("ko_head", _i64)]
+
+
+class eg_rope_grads(ctypes.Structure):
+    _fields_ = [("dq", _p), ("dk", _p), ("dq_token", _i64), ("dq_head", _i64), ("dk_token", _i64),
+                ("dk_head", _i64), ("dq_weight", _p), ("dk_weight", _p), ("workspace", _p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
+class eg_kv_cache(ctypes.Structure):
+    _fields_ = [("k", _p), ("v", _p), ("num_pages", _i64), ("page_stride", _i64),
+                ("token_stride", _i64), ("head_stride", _i64)]
+
+
+def _packer(cls):
+    """Fills a C struct in one step: the same layout as the ctypes class."""
+    code = {_i64: "q", _i32: "i", _f32: "f", _p: "Q", ctypes.c_size_t: "Q"}
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_))
+    assert s.size == ctypes.sizeof(cls)
+    return s.pack
+
+
+_pack_rope, _pack_grads, _pack_cache = _packer(eg_rope_args), _packer(eg_rope_grads), _packer(eg_kv_cache)
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument and result types of the entry points."""
+    for name, args in (("eg_qk_norm_rope", [_p, _p]),
+                       ("eg_qk_norm_rope_backward", [_p, _p, _p]),
+                       ("eg_qk_norm_rope_workspace_bytes", [_p, ctypes.POINTER(ctypes.c_size_t)]),
+                       ("eg_kv_append", [_p, _p, _p, _p])):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, ctypes.c_int
+
+
+def _eg():
+    import epilogue_tcgen05_tmem_gb300 as eg
+    return eg
+
+
+_CODES = {}
+
+
+def _code(t) -> int:
+    if not _CODES:
+        import torch
+        _CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
+    try:
+        return _CODES[t.dtype]
+    except KeyError:
+        raise ValueError(f"bf16, fp16 or float32 tensors are taken, not {t.dtype}") from None
+
+
+def _stream_of(t, stream):
+    """The stream to queue on; the tensor's device has to be the current one."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError("CUDA tensors are taken")
+    at = t.device.index
+    if at != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on cuda:{at}, which is not the current device")
+    return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream
+
+
+def _new(shape, dtype, device, stream):
+    """An uninitialised tensor, allocated for the stream that the call is queued on."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _rows(name, t, like=None, heads=None):
+    """(pointer, token stride, head stride) of a [tokens, heads, head_dim] tensor."""
+    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
+    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]
+                             or t.device != like.device or (heads is not None and t.shape[1] != heads)):
+        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype} does not match {tuple(like.shape)} {like.dtype}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _side(name, t, dtype, shape, device):
+    """Pointer of a contiguous side input, 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}: got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _table(cos_sin, q):
+    """(pointer, positions, rot_dim) of the table of cosines and sines."""
+    import torch
+    if cos_sin is None:
+        return 0, 0, 0
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or cos_sin.device != q.device:
+        raise ValueError("cos_sin must be a contiguous float32 tensor [positions, rot_dim] on the tensors' device")
+    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+
+
+def _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, page, v=(0, 0, 0), q_heads=None):
+    import torch
+    t, dim = k.shape[0], k.shape[2]
+    hq = q.shape[1] if q is not None else 0
+    table, count, rot = _table(cos_sin, k)
+    qp, qt, qh = _rows("q", q, k) if q is not None else (0, 0, 0)
+    kp, kt, kh = _rows("k", k)
+    return (t, hq, k.shape[1], dim, rot, _code(k), int(bool(pairs)), eps, page, table, count,
+            _side("positions", positions, torch.int64, (t,), k.device),
+            _side("q_weight", q_weight, k.dtype, (dim,), k.device),
+            _side("k_weight", k_weight, k.dtype, (dim,), k.device),
+            qp, kp, v[0], qt, qh, kt, kh, v[1], v[2])
+
+
+def qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False,
+                 q_out=None, k_out=None, stream=None):
+    """Queries [T, Hq, D] and keys [T, Hk, D], each normed per head where its
+    weight [D] is given, then rotated by cos_sin [positions, rot_dim] float32
+    (cosines, then sines); positions int64 [T] (None: 0, 1, 2, ...).  With
+    ``pairs`` neighbouring values are a pair, else values rot_dim / 2 apart.
+    Returns (q_out, k_out), new tensors unless given (they may be q and k)."""
+    import torch
+    eg = _eg()
+    st = _stream_of(k, stream)
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0)
+    q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+    k_out = _new(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
+    qo, qot, qoh = _rows("q_out", q_out, q, q.shape[1])
+    ko, kot, koh = _rows("k_out", k_out, k, k.shape[1])
+    eg._check(eg.lib().eg_qk_norm_rope(_pack_rope(*fields, qo, ko, qot, qoh, kot, koh), st))
+    return q_out, k_out
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, cos_sin, positions=None, q_weight=None, k_weight=None,
+                          eps=1e-6, pairs=False, dq=None, dk=None, stream=None):
+    """Gradients of ``qk_norm_rope`` for the given gradients of its outputs:
+    (dq, dk, dq_weight, dk_weight), the weights' in float32 (None without a
+    weight).  dq / dk may be dq_out / dk_out."""
+    import torch
+    eg = _eg()
+    st = _stream_of(k, stream)
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0)
+    qo, qot, qoh = _rows("dq_out", dq_out, q, q.shape[1])
+    ko, kot, koh = _rows("dk_out", dk_out, k, k.shape[1])
+    args = _pack_rope(*fields, qo, ko, qot, qoh, kot, koh)
+    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
+    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
+    pq, qt, qh = _rows("dq", dq, q, q.shape[1])
+    pk, kt, kh = _rows("dk", dk, k, k.shape[1])
+    dqw = dkw = work = None
+    need = ctypes.c_size_t(0)
+    if q_weight is not None or k_weight is not None:
+        eg._check(eg.lib().eg_qk_norm_rope_workspace_bytes(args, ctypes.byref(need)))
+        work = _new(need.value, torch.uint8, k.device, stream)
+        dqw = _new(q.shape[2], torch.float32, k.device, stream) if q_weight is not None else None
+        dkw = _new(k.shape[2], torch.float32, k.device, stream) if k_weight is not None else None
+    grads = _pack_grads(pq, pk, qt, qh, kt, kh, dqw.data_ptr() if dqw is not None else 0,
+                        dkw.data_ptr() if dkw is not None else 0, work.data_ptr() if work is not None else 0, need.value)
+    eg._check(eg.lib().eg_qk_norm_rope_backward(args, grads, st))
+    return dq, dk, dqw, dkw
+
+
+def _cache(k_cache, v_cache, like):
+    """Packed eg_kv_cache of [pages, page_size, kv_heads, head_dim] tensors (views
+    of heads-first storage too), after checking them against `like`'s last dimensions."""
+    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if c.dim() != 4 or c.dtype != like.dtype or c.device != like.device or (c.stride(3) != 1 and c.shape[3] > 1):
+            raise ValueError(f"{name} must be {like.dtype} [pages, page_size, kv_heads, head_dim] on {like.device} with a "
+                             "contiguous last dimension")
+    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
+        raise ValueError("k_cache and v_cache must have the same shape and strides")
+    s = k_cache.stride()
+    return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], s[0], s[1], s[2])
+
+
+def kv_append(k, v, k_cache, v_cache, slots, q=None, cos_sin=None, positions=None, q_weight=None,
+              k_weight=None, eps=1e-6, pairs=False, q_out=None, stream=None):
+    """Append keys (normed and rotated as by ``qk_norm_rope``) and values
+    [T, Hk, D] to the paged cache [pages, page_size, Hk, D] at slots int64 [T]
+    (page * page_size + place; a slot outside the cache appends nothing).  With
+    q the queries are normed and rotated in the same launch; returns q_out."""
+    import torch
+    eg = _eg()
+    st = _stream_of(k, stream)
+    cache = _cache(k_cache, v_cache, k)
+    if k_cache.shape[2] != k.shape[1] or k_cache.shape[3] != k.shape[2]:
+        raise ValueError(f"the cache {tuple(k_cache.shape)} does not hold heads of k {tuple(k.shape)}")
+    if slots is None:
+        raise ValueError("slots is missing")
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, k_cache.shape[1],
+                          _rows("v", v, k, k.shape[1]))
+    qo, qot, qoh = 0, 0, 0
+    if q is not None:
+        q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
+        qo, qot, qoh = _rows("q_out", q_out, q, q.shape[1])
+    eg._check(eg.lib().eg_kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache,
+                                    _side("slots", slots, torch.int64, (k.shape[0],), k.device), st))
+    return q_out if q is not None else None

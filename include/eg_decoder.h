@@ -1,0 +1,107 @@
+/*
+ * eg_decoder.h -- C ABI of the operators that stand between the fused linear
+ * layers of a decoder (sm_103a): per-head norm of queries and keys with the
+ * position rotation, appending to a paged key/value cache, attention of
+ * drafted token trees over that cache, and the log probabilities of given
+ * tokens.  Same conventions as eg.h: every call returns an eg_status,
+ * argument errors are found before any device work is queued,
+ * eg_last_error_detail() describes the last failure of this thread, the
+ * caller owns every tensor and keeps it alive until the stream has passed it,
+ * calls are queued on `stream` (a cudaStream_t, NULL: the legacy default
+ * stream) of the current device and do not synchronise.
+ *
+ * Strides are in ELEMENTS; the innermost dimension (head_dim, vocabulary) is
+ * contiguous.  Sums, softmax statistics and gradients of weights are float32;
+ * each output is rounded once, to its own type, nearest even.
+ */
+#ifndef EG_DECODER_H
+#define EG_DECODER_H
+
+#include "eg.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+typedef enum { EG_EL_BF16 = 0, EG_EL_F16 = 1, EG_EL_F32 = 2 } eg_el_dtype;
+
+/* ------------------------------------ head norm and position rotation ----
+ *
+ * For each token t and head h, with x the head's head_dim values:
+ *
+ *   z = x * w / sqrt(mean(x^2) + eps)     (z = x where the weight is NULL)
+ *   for each pair i < rot_dim / 2, at position p = positions[t]:
+ *     y_a = z_a c - z_b s,  y_b = z_b c + z_a s,
+ *     c = cos_sin[p][i],    s = cos_sin[p][rot_dim / 2 + i]
+ *   values past rot_dim are z.
+ *
+ * `pairs` 0: pair i is (i, i + rot_dim / 2); 1: (2 i, 2 i + 1).  A token whose
+ * position is outside [0, max_positions) gets NaN in its rotated values (the
+ * table is not read there).  Outputs may be their own inputs (same strides);
+ * they must not overlap them in another way.
+ */
+typedef struct {
+  int64_t tokens;
+  int32_t q_heads, kv_heads;    /* either may be 0 */
+  int32_t head_dim;             /* 2..256, even */
+  int32_t rot_dim;              /* even, 0..head_dim; 0: no rotation */
+  int32_t dtype;                /* eg_el_dtype of q, k, v, weights, outputs, cache */
+  int32_t pairs;
+  float eps;
+  int32_t page_size;            /* eg_kv_append: tokens of a page */
+  const float* cos_sin;         /* [max_positions][rot_dim], contiguous */
+  int64_t max_positions;
+  const int64_t* positions;     /* [tokens]; NULL: 0, 1, 2, ... */
+  const void* q_weight;         /* [head_dim]; NULL: queries are not normed */
+  const void* k_weight;
+  const void *q, *k, *v;        /* [tokens][heads][head_dim] by the strides; v: eg_kv_append */
+  int64_t q_token, q_head, k_token, k_head, v_token, v_head;
+  void *q_out, *k_out;          /* k_out: eg_qk_norm_rope and its backward pass */
+  int64_t qo_token, qo_head, ko_token, ko_head;
+} eg_rope_args;
+
+/* q_out, k_out of the formula above. */
+EG_API eg_status eg_qk_norm_rope(const eg_rope_args* args, void* stream);
+
+/* Gradients of eg_qk_norm_rope.  `fwd` holds the forward call's q, k, weights,
+ * positions and table; its q_out / k_out (with their strides) are the GIVEN
+ * gradients of the outputs and are only read.  Writes dq, dk and, where the
+ * weight is not NULL, dq_weight / dk_weight (float32 [head_dim], NULL: not
+ * wanted), summed over tokens and heads in a fixed order.  dq / dk may be the
+ * given gradients themselves (same strides).  The rotation's table gets no
+ * gradient.  `workspace`: at least eg_qk_norm_rope_workspace_bytes() of
+ * device memory, 16-byte aligned, not shared by calls that overlap. */
+typedef struct {
+  void *dq, *dk;
+  int64_t dq_token, dq_head, dk_token, dk_head;
+  float *dq_weight, *dk_weight;
+  void* workspace;
+  size_t workspace_bytes;
+} eg_rope_grads;
+
+EG_API eg_status eg_qk_norm_rope_backward(const eg_rope_args* fwd, const eg_rope_grads* grads,
+                                          void* stream);
+EG_API eg_status eg_qk_norm_rope_workspace_bytes(const eg_rope_args* fwd, size_t* out);
+
+/* ------------------------------------------------- paged key/value cache --
+ *
+ * k and v: [num_pages][page_size][kv_heads][head_dim] by the strides (shared
+ * by both), so pages may be stored tokens-first or heads-first. */
+typedef struct {
+  void *k, *v;
+  int64_t num_pages;
+  int64_t page_stride, token_stride, head_stride;
+} eg_kv_cache;
+
+/* Append: for each token t with 0 <= slots[t] < num_pages * page_size, the
+ * normed and rotated key and the value go to page slots[t] / page_size, place
+ * slots[t] % page_size; other slots append nothing (a padded token).  Slots
+ * of one call differ from each other.  With q and q_out the queries are
+ * normed and rotated in the same launch, for every token. */
+EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache,
+                              const int64_t* slots, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif /* EG_DECODER_H */

@@ -1,0 +1,85 @@
+"""The C ABI of the decoder operators without a GPU: exports, struct layouts,
+and refusals that come before any device work."""
+import ctypes
+import os
+import re
+
+import pytest
+
+import epilogue_tcgen05_tmem_gb300 as eg
+from epilogue_tcgen05_tmem_gb300 import _build, decoder
+
+HEADER = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "eg_decoder.h")
+
+
+@pytest.fixture(scope="module")
+def L():
+    _build.build()
+    return eg.lib()
+
+
+def _source():
+    return re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+
+
+def test_exports_every_declared_function(L):
+    names = set(re.findall(r"EG_API\s+[\w\s\*]+?\b(eg_\w+)\s*\(", _source()))
+    assert names == set(decoder.EXPORTED)
+    for n in names:
+        assert hasattr(L, n), n
+
+
+def _struct_names():
+    return re.findall(r"typedef struct \{[^}]*\}\s*(eg_\w+);", _source())
+
+
+@pytest.mark.parametrize("name", _struct_names())
+def test_binding_structs_match_header(name):
+    body = re.search(r"typedef struct \{([^}]*)\}\s*" + name + ";", _source()).group(1)
+    fields = []
+    for decl in body.split(";"):
+        decl = decl.strip()
+        if decl:
+            decl = re.sub(r"^const\s+", "", decl)
+            fields += [f.strip().lstrip("*") for f in decl.split(None, 1)[1].split(",")]
+    assert [f for f, _ in getattr(decoder, name)._fields_] == fields
+
+
+def _rope(**kw):
+    a = decoder.eg_rope_args(tokens=4, q_heads=2, kv_heads=1, head_dim=64, rot_dim=64, dtype=0, pairs=0, eps=1e-6, page_size=16,
+                             cos_sin=16, max_positions=8, q=16, k=16, v=16, q_out=16, k_out=16)
+    for n, v in kw.items():
+        setattr(a, n, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(tokens=-1), eg.EG_ERR_INVALID_ARG), (dict(q_heads=-2), eg.EG_ERR_INVALID_ARG), (dict(dtype=3), eg.EG_ERR_INVALID_ARG),
+    (dict(head_dim=63), eg.EG_ERR_UNSUPPORTED), (dict(head_dim=258), eg.EG_ERR_UNSUPPORTED), (dict(rot_dim=66), eg.EG_ERR_INVALID_ARG),
+    (dict(rot_dim=3), eg.EG_ERR_INVALID_ARG), (dict(pairs=2), eg.EG_ERR_INVALID_ARG), (dict(cos_sin=None), eg.EG_ERR_INVALID_ARG),
+    (dict(max_positions=0), eg.EG_ERR_INVALID_ARG), (dict(q=None), eg.EG_ERR_INVALID_ARG), (dict(k=17), eg.EG_ERR_INVALID_ARG),
+    (dict(q_token=-1), eg.EG_ERR_INVALID_ARG), (dict(positions=4), eg.EG_ERR_INVALID_ARG),
+    (dict(q_weight=16, eps=float("nan")), eg.EG_ERR_INVALID_ARG), (dict(tokens=1 << 25), eg.EG_ERR_UNSUPPORTED)])
+def test_rope_refusals_before_device(L, kw, status):
+    a = _rope(**kw)
+    assert L.eg_qk_norm_rope(ctypes.addressof(a), None) == status
+    assert eg.last_error_detail()
+    g = decoder.eg_rope_grads(dq=16, dk=16)
+    if "q" not in kw and "k" not in kw and "q_token" not in kw:  # inputs that an unweighted gradient does not read
+        assert L.eg_qk_norm_rope_backward(ctypes.addressof(a), ctypes.addressof(g), None) == status
+
+
+def test_append_refusals_before_device(L):
+    c = decoder.eg_kv_cache(k=16, v=16, num_pages=1, page_stride=1024, token_stride=64, head_stride=64)
+    a = _rope()
+    for args, cache, slots in ((None, c, 16), (a, None, 16), (a, c, None), (a, c, 12), (_rope(page_size=0), c, 16), (_rope(v=None), c, 16),
+                               (a, decoder.eg_kv_cache(num_pages=1), 16), (a, decoder.eg_kv_cache(k=16, v=16, num_pages=-1), 16)):
+        s = L.eg_kv_append(ctypes.addressof(args) if args else None, ctypes.addressof(cache) if cache else None, slots, None)
+        assert s == eg.EG_ERR_INVALID_ARG and eg.last_error_detail()
+
+
+def test_null_arguments(L):
+    assert L.eg_qk_norm_rope(None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_qk_norm_rope_backward(None, None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_qk_norm_rope_workspace_bytes(None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_qk_norm_rope_workspace_bytes(ctypes.addressof(_rope()), None) == eg.EG_ERR_INVALID_ARG
