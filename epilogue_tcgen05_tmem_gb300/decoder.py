@@ -5,18 +5,20 @@
 rotate them by their positions; ``kv_append`` does the same on the way into a
 paged key/value cache.  All take torch CUDA tensors [tokens, heads, head_dim]
 by their strides (the last dimension contiguous), so parts of one projection's
-output are passed as they are, and run on the current stream unless ``stream``
-gives another.
+output are passed as they are.  ``token_logprobs`` and its gradient take logits
+[rows, vocab].  Every call runs on the current stream unless ``stream`` gives
+another.
 """
 from __future__ import annotations
 
 import ctypes
 import struct
+from typing import NamedTuple
 
 EL_DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 
 EXPORTED = ("eg_qk_norm_rope", "eg_qk_norm_rope_backward", "eg_qk_norm_rope_workspace_bytes",
-            "eg_kv_append")
+            "eg_kv_append", "eg_token_logprobs", "eg_token_logprobs_backward")
 
 _i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -42,6 +44,17 @@ class eg_kv_cache(ctypes.Structure):
                 ("token_stride", _i64), ("head_stride", _i64)]
 
 
+class eg_score_args(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("vocab", _i64), ("dtype", _i32), ("top", _i32), ("logits", _p),
+                ("row_stride", _i64), ("tokens", _p), ("logprob", _p), ("lse", _p),
+                ("entropy", _p), ("top_ids", _p), ("top_logprobs", _p)]
+
+
+class eg_score_grads(ctypes.Structure):
+    _fields_ = [("lse", _p), ("entropy", _p), ("d_logprob", _p), ("d_entropy", _p),
+                ("d_logits", _p), ("d_row_stride", _i64)]
+
+
 def _packer(cls):
     """Fills a C struct in one step: the same layout as the ctypes class."""
     code = {_i64: "q", _i32: "i", _f32: "f", _p: "Q", ctypes.c_size_t: "Q"}
@@ -51,6 +64,7 @@ def _packer(cls):
 
 
 _pack_rope, _pack_grads, _pack_cache = _packer(eg_rope_args), _packer(eg_rope_grads), _packer(eg_kv_cache)
+_pack_score, _pack_score_grads = _packer(eg_score_args), _packer(eg_score_grads)
 
 
 def declare(L: ctypes.CDLL) -> None:
@@ -58,7 +72,9 @@ def declare(L: ctypes.CDLL) -> None:
     for name, args in (("eg_qk_norm_rope", [_p, _p]),
                        ("eg_qk_norm_rope_backward", [_p, _p, _p]),
                        ("eg_qk_norm_rope_workspace_bytes", [_p, ctypes.POINTER(ctypes.c_size_t)]),
-                       ("eg_kv_append", [_p, _p, _p, _p])):
+                       ("eg_kv_append", [_p, _p, _p, _p]),
+                       ("eg_token_logprobs", [_p, _p]),
+                       ("eg_token_logprobs_backward", [_p, _p, _p])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, ctypes.c_int
 
@@ -228,3 +244,63 @@ def kv_append(k, v, k_cache, v_cache, slots, q=None, cos_sin=None, positions=Non
     eg._check(eg.lib().eg_kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache,
                                     _side("slots", slots, torch.int64, (k.shape[0],), k.device), st))
     return q_out if q is not None else None
+
+
+# ---------------------------------------------------- log probabilities ---
+
+class TokenLogProbs(NamedTuple):
+    """Per row: the given token's log probability, log sum exp of the logits,
+    the entropy; and the top alternatives (ids, log probabilities)."""
+    logprob: "torch.Tensor"       # noqa: F821  [rows] float32
+    lse: "torch.Tensor"           # noqa: F821  [rows] float32
+    entropy: "torch.Tensor"       # noqa: F821  [rows] float32
+    top_ids: "torch.Tensor | None"       # noqa: F821  [rows, top] int64
+    top_logprobs: "torch.Tensor | None"  # noqa: F821  [rows, top] float32
+
+
+def _logits(name, x):
+    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
+        raise ValueError(f"{name} must be [rows, vocab] with a contiguous last dimension")
+    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1]))
+
+
+def token_logprobs(logits, tokens=None, top=0, stream=None) -> TokenLogProbs:
+    """Log probabilities of tokens int64 [rows] (an id outside the vocabulary:
+    none is given, 0) under logits [rows, vocab], with lse, entropy and the
+    ``top`` (0..32) best alternatives, of equal logits the lowest id first."""
+    import torch
+    eg = _eg()
+    st = _stream_of(logits, stream)
+    x, stride = _logits("logits", logits)
+    rows, vocab = logits.shape
+    given = _side("tokens", tokens, torch.int64, (rows,), logits.device)
+    logprob, lse, entropy = _new((3, rows), torch.float32, logits.device, stream).unbind(0)
+    ids = best = None
+    if top:
+        ids = _new((rows, top), torch.int64, logits.device, stream)
+        best = _new((rows, top), torch.float32, logits.device, stream)
+    eg._check(eg.lib().eg_token_logprobs(
+        _pack_score(rows, vocab, _code(logits), top, x, stride, given, logprob.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
+                    ids.data_ptr() if top else 0, best.data_ptr() if top else 0), st))
+    return TokenLogProbs(logprob, lse, entropy, ids, best)
+
+
+def token_logprobs_backward(logits, tokens, lse, entropy, d_logprob=None, d_entropy=None, out=None, stream=None):
+    """The gradient to the logits, from what ``token_logprobs`` gave for them
+    and the gradients of its log probabilities and entropies (float32 [rows],
+    None: zero).  ``out`` may be the logits themselves."""
+    import torch
+    eg = _eg()
+    st = _stream_of(logits, stream)
+    x, stride = _logits("logits", logits)
+    rows, vocab = logits.shape
+    out = _new((rows, vocab), logits.dtype, logits.device, stream) if out is None else out
+    d, d_stride = _logits("out", out)
+    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError(f"out {tuple(out.shape)} {out.dtype} does not match {tuple(logits.shape)} {logits.dtype}")
+    side = [_side(n, t, torch.float32, (rows,), logits.device)
+            for n, t in (("lse", lse), ("entropy", entropy), ("d_logprob", d_logprob), ("d_entropy", d_entropy))]
+    given = _side("tokens", tokens, torch.int64, (rows,), logits.device)
+    eg._check(eg.lib().eg_token_logprobs_backward(
+        _pack_score(rows, vocab, _code(logits), 0, x, stride, given, 0, 0, 0, 0, 0), _pack_score_grads(*side, d, d_stride), st))
+    return out

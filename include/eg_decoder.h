@@ -101,6 +101,54 @@ typedef struct {
 EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache,
                               const int64_t* slots, void* stream);
 
+/* ------------------------------------------- log probabilities of tokens --
+ *
+ * For each row of logits x[0..vocab):
+ *
+ *   lse     = log sum_v exp(x_v)
+ *   logprob = x[token] - lse                    (0 where the token is outside
+ *                                                [0, vocab): none is given)
+ *   entropy = -sum_v p_v log p_v, p = exp(x - lse)
+ *   top_ids, top_logprobs: the `top` largest logits, of equal ones the lowest
+ *             id first, and their x - lse.
+ *
+ * Logits of -infinity have probability 0.  A row of nothing else has lse and
+ * log probabilities of -infinity and entropy 0.  A row with +infinity has lse
+ * +infinity and NaN elsewhere; one with a NaN has NaN everywhere and ids -1.
+ * Each output may be NULL (not wanted). */
+typedef struct {
+  int64_t rows, vocab;
+  int32_t dtype;                /* eg_el_dtype of the logits (and of d_logits) */
+  int32_t top;                  /* 0..32, at most vocab */
+  const void* logits;
+  int64_t row_stride;           /* at least vocab */
+  const int64_t* tokens;        /* [rows]; NULL: none is given */
+  float *logprob, *lse, *entropy; /* [rows] */
+  int64_t* top_ids;             /* [rows][top] */
+  float* top_logprobs;          /* [rows][top] */
+} eg_score_args;
+
+EG_API eg_status eg_token_logprobs(const eg_score_args* args, void* stream);
+
+/* The gradient to the logits, from the rows' lse and entropy (as
+ * eg_token_logprobs gave them) and the given gradients of logprob and entropy
+ * (NULL: zero):
+ *
+ *   d_x[v] = d_logprob (1[v = token] - p_v) - d_entropy p_v (log p_v + entropy)
+ *
+ * (no d_logprob where no token is given; 0 for a row whose lse is -infinity).
+ * `args` gives rows, vocab, dtype, logits and tokens; its outputs are not
+ * used.  d_logits may be the logits (same stride). */
+typedef struct {
+  const float *lse, *entropy;   /* [rows]; entropy only with d_entropy */
+  const float *d_logprob, *d_entropy;
+  void* d_logits;
+  int64_t d_row_stride;         /* at least vocab */
+} eg_score_grads;
+
+EG_API eg_status eg_token_logprobs_backward(const eg_score_args* args, const eg_score_grads* grads,
+                                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

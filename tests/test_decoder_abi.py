@@ -83,3 +83,36 @@ def test_null_arguments(L):
     assert L.eg_qk_norm_rope_backward(None, None, None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_qk_norm_rope_workspace_bytes(None, None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_qk_norm_rope_workspace_bytes(ctypes.addressof(_rope()), None) == eg.EG_ERR_INVALID_ARG
+
+
+def _score(**kw):
+    a = decoder.eg_score_args(rows=2, vocab=64, dtype=0, top=2, logits=16, row_stride=64, tokens=16, logprob=16, lse=16, entropy=16,
+                              top_ids=16, top_logprobs=16)
+    for n, v in kw.items():
+        setattr(a, n, v)
+    return a
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), eg.EG_ERR_INVALID_ARG), (dict(vocab=-1), eg.EG_ERR_INVALID_ARG), (dict(vocab=0), eg.EG_ERR_INVALID_ARG),
+    (dict(dtype=7), eg.EG_ERR_INVALID_ARG), (dict(logits=None), eg.EG_ERR_INVALID_ARG), (dict(logits=15), eg.EG_ERR_INVALID_ARG),
+    (dict(row_stride=63), eg.EG_ERR_INVALID_ARG), (dict(tokens=4), eg.EG_ERR_INVALID_ARG), (dict(rows=1 << 25), eg.EG_ERR_UNSUPPORTED)])
+def test_score_refusals_before_device(L, kw, status):
+    a = _score(**kw)
+    g = decoder.eg_score_grads(lse=16, d_logits=16, d_row_stride=64)
+    assert L.eg_token_logprobs(ctypes.addressof(a), None) == status
+    assert L.eg_token_logprobs_backward(ctypes.addressof(a), ctypes.addressof(g), None) == status
+    assert eg.last_error_detail()
+
+
+def test_score_refusals_of_one_direction(L):
+    for kw, status in ((dict(top=-1), eg.EG_ERR_UNSUPPORTED), (dict(top=33), eg.EG_ERR_UNSUPPORTED), (dict(top=30, vocab=8), eg.EG_ERR_INVALID_ARG),
+                       (dict(lse=2), eg.EG_ERR_INVALID_ARG), (dict(top_ids=4), eg.EG_ERR_INVALID_ARG)):
+        assert L.eg_token_logprobs(ctypes.addressof(_score(**kw)), None) == status
+    for kw in (dict(lse=None), dict(d_entropy=16), dict(d_logits=None), dict(d_row_stride=63), dict(d_logprob=2)):
+        g = decoder.eg_score_grads(lse=16, d_logits=16, d_row_stride=64)
+        for n, v in kw.items():
+            setattr(g, n, v)
+        assert L.eg_token_logprobs_backward(ctypes.addressof(_score()), ctypes.addressof(g), None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_token_logprobs(None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_token_logprobs_backward(ctypes.addressof(_score()), None, None) == eg.EG_ERR_INVALID_ARG
