@@ -19,8 +19,8 @@ import os
 import threading
 
 from . import decoder
-from .decoder import (TokenLogProbs, kv_append, qk_norm_rope, qk_norm_rope_backward,  # noqa: F401
-                      token_logprobs, token_logprobs_backward)
+from .decoder import (TokenLogProbs, TreeAttention, kv_append, qk_norm_rope,  # noqa: F401
+                      qk_norm_rope_backward, token_logprobs, token_logprobs_backward)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libeg.so")

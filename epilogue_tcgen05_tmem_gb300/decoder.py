@@ -5,7 +5,8 @@
 rotate them by their positions; ``kv_append`` does the same on the way into a
 paged key/value cache.  All take torch CUDA tensors [tokens, heads, head_dim]
 by their strides (the last dimension contiguous), so parts of one projection's
-output are passed as they are.  ``token_logprobs`` and its gradient take logits
+output are passed as they are.  ``TreeAttention`` is a plan for attention of
+drafted token trees (or single tokens) over that cache.  ``token_logprobs`` and its gradient take logits
 [rows, vocab].  Every call runs on the current stream unless ``stream`` gives
 another.
 """
@@ -18,7 +19,9 @@ from typing import NamedTuple
 EL_DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 
 EXPORTED = ("eg_qk_norm_rope", "eg_qk_norm_rope_backward", "eg_qk_norm_rope_workspace_bytes",
-            "eg_kv_append", "eg_token_logprobs", "eg_token_logprobs_backward")
+            "eg_kv_append", "eg_tree_plan_create", "eg_tree_plan_workspace_bytes",
+            "eg_tree_plan_run", "eg_tree_plan_device_status", "eg_tree_plan_destroy",
+            "eg_token_logprobs", "eg_token_logprobs_backward")
 
 _i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -44,6 +47,18 @@ class eg_kv_cache(ctypes.Structure):
                 ("token_stride", _i64), ("head_stride", _i64)]
 
 
+class eg_tree_problem(ctypes.Structure):
+    _fields_ = [("q_heads", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32),
+                ("page_size", _i32), ("max_batch", _i32), ("max_tree", _i32)]
+
+
+class eg_tree_args(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("tokens", _i32), ("q", _p), ("o", _p), ("q_token", _i64),
+                ("q_head", _i64), ("o_token", _i64), ("o_head", _i64), ("block_table", _p),
+                ("table_stride", _i64), ("context_lens", _p), ("q_start", _p), ("mask", _p),
+                ("mask_stride", _i64), ("scale", _f32), ("lse", _p)]
+
+
 class eg_score_args(ctypes.Structure):
     _fields_ = [("rows", _i64), ("vocab", _i64), ("dtype", _i32), ("top", _i32), ("logits", _p),
                 ("row_stride", _i64), ("tokens", _p), ("logprob", _p), ("lse", _p),
@@ -58,12 +73,13 @@ class eg_score_grads(ctypes.Structure):
 def _packer(cls):
     """Fills a C struct in one step: the same layout as the ctypes class."""
     code = {_i64: "q", _i32: "i", _f32: "f", _p: "Q", ctypes.c_size_t: "Q"}
-    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_))
+    s = struct.Struct("@" + "".join(code[t] for _, t in cls._fields_) + "0q")
     assert s.size == ctypes.sizeof(cls)
     return s.pack
 
 
 _pack_rope, _pack_grads, _pack_cache = _packer(eg_rope_args), _packer(eg_rope_grads), _packer(eg_kv_cache)
+_pack_tree = _packer(eg_tree_args)
 _pack_score, _pack_score_grads = _packer(eg_score_args), _packer(eg_score_grads)
 
 
@@ -73,6 +89,11 @@ def declare(L: ctypes.CDLL) -> None:
                        ("eg_qk_norm_rope_backward", [_p, _p, _p]),
                        ("eg_qk_norm_rope_workspace_bytes", [_p, ctypes.POINTER(ctypes.c_size_t)]),
                        ("eg_kv_append", [_p, _p, _p, _p]),
+                       ("eg_tree_plan_create", [_p, ctypes.POINTER(_p)]),
+                       ("eg_tree_plan_workspace_bytes", [_p, ctypes.POINTER(ctypes.c_size_t)]),
+                       ("eg_tree_plan_run", [_p, _p, _p, _p]),
+                       ("eg_tree_plan_device_status", [_p]),
+                       ("eg_tree_plan_destroy", [_p]),
                        ("eg_token_logprobs", [_p, _p]),
                        ("eg_token_logprobs_backward", [_p, _p, _p])):
         f = getattr(L, name)
@@ -244,6 +265,86 @@ def kv_append(k, v, k_cache, v_cache, slots, q=None, cos_sin=None, positions=Non
     eg._check(eg.lib().eg_kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache,
                                     _side("slots", slots, torch.int64, (k.shape[0],), k.device), st))
     return q_out if q is not None else None
+
+
+# ------------------------------------------------------- tree attention ---
+
+class TreeAttention:
+    """A plan for attention of drafted token trees over a paged cache:
+    ``max_batch`` sequences of up to ``max_tree`` drafted tokens each (1: ordinary
+    decoding).  It owns the workspace for sequences split over the GPU; its runs
+    must not overlap on the GPU."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, dtype="bf16", page_size=16, max_batch=1, max_tree=1):
+        eg = _eg()
+        self.handle = None
+        self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
+        self.max_batch, self.max_tree = max_batch, max_tree
+        h = _p()
+        problem = eg_tree_problem(q_heads, kv_heads, head_dim, EL_DTYPES[dtype], page_size, max_batch, max_tree)
+        eg._check(eg.lib().eg_tree_plan_create(ctypes.addressof(problem), ctypes.byref(h)))
+        self.handle, self._dtype = h.value, EL_DTYPES[dtype]
+
+    @property
+    def workspace_bytes(self) -> int:
+        eg, n = _eg(), ctypes.c_size_t()
+        eg._check(eg.lib().eg_tree_plan_workspace_bytes(self.handle, ctypes.byref(n)))
+        return n.value
+
+    def run(self, q, k_cache, v_cache, block_table, context_lens, q_start, mask=None, scale=None, out=None, lse=None, stream=None):
+        """Packed queries q [tokens, q_heads, head_dim] of the sequences' trees
+        (rows q_start[b] .. q_start[b + 1]) over the cache [pages, page_size,
+        kv_heads, head_dim]; block_table int32 [batch, pages of a sequence],
+        context_lens int32 [batch], q_start int32 [batch + 1]; mask int32 words
+        [tokens, words] (None: each token sees the drafted ones up to itself).
+        The drafted tokens' own keys and values are in the cache already, after
+        the context.  ``scale``: of the scores, 1 / sqrt(head_dim) when None.
+        Returns o like q; lse float32 [tokens, q_heads] is written where given."""
+        import torch
+        eg = _eg()
+        st = _stream_of(q, stream)
+        qp, qt, qh = _rows("q", q)
+        tokens, heads, dim = q.shape
+        if heads != self.q_heads or dim != self.head_dim or _code(q) != self._dtype:
+            raise ValueError(f"q {tuple(q.shape)} {q.dtype} does not fit the plan")
+        cache = _cache(k_cache, v_cache, q)
+        if k_cache.shape[1:] != (self.page_size, self.kv_heads, dim):
+            raise ValueError(f"the cache {tuple(k_cache.shape)} does not fit the plan")
+        batch = context_lens.shape[0]
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != batch or block_table.device != q.device \
+                or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
+            raise ValueError("block_table must be int32 [batch, pages] with contiguous rows on the tensors' device")
+        stride = block_table.shape[1]
+        if batch > 1 and block_table.stride(0) != stride:
+            raise ValueError("block_table must be contiguous")
+        words = 0
+        if mask is not None:
+            if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] != tokens or not mask.is_contiguous() or mask.device != q.device:
+                raise ValueError("mask must be contiguous int32 words [tokens, words] on the tensors' device")
+            words = mask.shape[1]
+        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
+        op, ot, oh = _rows("out", out, q, heads)
+        args = _pack_tree(batch, tokens, qp, op, qt, qh, ot, oh, block_table.data_ptr(), stride,
+                          _side("context_lens", context_lens, torch.int32, (batch,), q.device),
+                          _side("q_start", q_start, torch.int32, (batch + 1,), q.device),
+                          mask.data_ptr() if mask is not None else 0, words, dim ** -0.5 if scale is None else scale,
+                          _side("lse", lse, torch.float32, (tokens, heads), q.device))
+        eg._check(eg.lib().eg_tree_plan_run(self.handle, args, cache, st))
+        return out
+
+    def device_status(self) -> int:
+        return _eg().lib().eg_tree_plan_device_status(self.handle)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _eg().lib().eg_tree_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
 
 
 # ---------------------------------------------------- log probabilities ---

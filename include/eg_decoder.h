@@ -101,6 +101,65 @@ typedef struct {
 EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache,
                               const int64_t* slots, void* stream);
 
+/* ------------------------------ attention of drafted trees over the cache --
+ *
+ * Sequence b has context_lens[b] cached tokens and n_b = q_start[b + 1] -
+ * q_start[b] drafted ones (0 or more; 1 for ordinary decoding), whose keys and
+ * values follow the context in the same cache: place j of the sequence is in
+ * page block_table[b][j / page_size], place j % page_size.  Token t of the
+ * tree (packed row q_start[b] + t of q) attends to the whole context and to
+ * the drafted tokens u whose bit u is set in its mask words (bit u % 32 of
+ * mask[row][u / 32]); without a mask to u <= t.  For query head h, with the
+ * cached head h / (q_heads / kv_heads):
+ *
+ *   o = sum_j softmax_j(scale q . k_j) v_j      over the places j it attends to
+ *   lse = log sum_j exp(scale q . k_j)
+ *
+ * A token that attends to nothing has o = 0 and lse = -infinity.  Places that
+ * a token does not attend to, slots of the cache past a sequence's end and
+ * table entries past its pages have no part, whatever they hold.  Sequence
+ * lengths are read on the device, so a captured graph replays with new ones;
+ * lengths beyond the plan's limits, the table or the packed rows are cut to
+ * them, and table entries outside [0, num_pages) read as zero keys and values.
+ *
+ * A plan owns the partial results of sequences that it splits over the GPU;
+ * runs of one plan must not overlap on the GPU. */
+typedef struct {
+  int32_t q_heads, kv_heads;    /* q_heads a multiple of kv_heads */
+  int32_t head_dim;             /* a multiple of 8, 8..128 */
+  int32_t dtype;                /* EG_EL_BF16 or EG_EL_F16 (q, cache and o) */
+  int32_t page_size;            /* a multiple of 8 */
+  int32_t max_batch;            /* sequences of a run, 1..65536 */
+  int32_t max_tree;             /* drafted tokens of a sequence, 1..256 */
+} eg_tree_problem;
+
+typedef struct {
+  int32_t batch;
+  int32_t tokens;               /* rows of q and o */
+  const void* q;                /* [tokens][q_heads][head_dim] by the strides, 16-byte aligned rows */
+  void* o;
+  int64_t q_token, q_head, o_token, o_head;
+  const int32_t* block_table;   /* [batch][table_stride], table_stride entries of each may be read */
+  int64_t table_stride;
+  const int32_t* context_lens;  /* [batch] */
+  const int32_t* q_start;       /* [batch + 1], rising */
+  const uint32_t* mask;         /* [tokens][mask_stride] words, or NULL */
+  int64_t mask_stride;          /* at least max_tree / 32, rounded up */
+  float scale;
+  float* lse;                   /* [tokens][q_heads], or NULL */
+} eg_tree_args;
+
+typedef struct eg_tree_plan eg_tree_plan;
+
+EG_API eg_status eg_tree_plan_create(const eg_tree_problem* problem, eg_tree_plan** out);
+EG_API eg_status eg_tree_plan_workspace_bytes(const eg_tree_plan* plan, size_t* out);
+EG_API eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args,
+                                  const eg_kv_cache* cache, void* stream);
+/* Synchronise the plan's device and report a wait in its kernels that ran past
+ * its limit (EG_ERR_DEVICE_TIMEOUT, then cleared). */
+EG_API eg_status eg_tree_plan_device_status(eg_tree_plan* plan);
+EG_API eg_status eg_tree_plan_destroy(eg_tree_plan* plan);
+
 /* ------------------------------------------- log probabilities of tokens --
  *
  * For each row of logits x[0..vocab):

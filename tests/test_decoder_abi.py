@@ -116,3 +116,26 @@ def test_score_refusals_of_one_direction(L):
         assert L.eg_token_logprobs_backward(ctypes.addressof(_score()), ctypes.addressof(g), None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_token_logprobs(None, None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_token_logprobs_backward(ctypes.addressof(_score()), None, None) == eg.EG_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q_heads=0), eg.EG_ERR_INVALID_ARG), (dict(q_heads=5), eg.EG_ERR_INVALID_ARG), (dict(head_dim=0), eg.EG_ERR_UNSUPPORTED),
+    (dict(head_dim=132), eg.EG_ERR_UNSUPPORTED), (dict(dtype=2), eg.EG_ERR_UNSUPPORTED), (dict(dtype=-1), eg.EG_ERR_INVALID_ARG),
+    (dict(page_size=20), eg.EG_ERR_UNSUPPORTED), (dict(max_batch=0), eg.EG_ERR_UNSUPPORTED), (dict(max_tree=300), eg.EG_ERR_UNSUPPORTED)])
+def test_tree_refusals_before_device(L, kw, status):
+    p = decoder.eg_tree_problem(q_heads=4, kv_heads=2, head_dim=64, dtype=0, page_size=16, max_batch=1, max_tree=1)
+    for n, v in kw.items():
+        setattr(p, n, v)
+    h = ctypes.c_void_p()
+    assert L.eg_tree_plan_create(ctypes.addressof(p), ctypes.byref(h)) == status and not h.value
+    assert eg.last_error_detail()
+
+
+def test_tree_null_arguments(L):
+    h = ctypes.c_void_p()
+    assert L.eg_tree_plan_create(None, ctypes.byref(h)) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_create(None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_run(None, None, None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_workspace_bytes(None, None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_device_status(None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_destroy(None) == eg.EG_OK
