@@ -317,17 +317,17 @@ class TreeAttention:
         stride = block_table.shape[1]
         if batch > 1 and block_table.stride(0) != stride:
             raise ValueError("block_table must be contiguous")
-        words = 0
+        words = at_mask = 0
         if mask is not None:
             if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] != tokens or not mask.is_contiguous() or mask.device != q.device:
                 raise ValueError("mask must be contiguous int32 words [tokens, words] on the tensors' device")
-            words = mask.shape[1]
+            words, at_mask = mask.shape[1], mask.data_ptr() or 4  # no words: refused for their number, not taken for no mask
         out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
         op, ot, oh = _rows("out", out, q, heads)
         args = _pack_tree(batch, tokens, qp, op, qt, qh, ot, oh, block_table.data_ptr(), stride,
                           _side("context_lens", context_lens, torch.int32, (batch,), q.device),
                           _side("q_start", q_start, torch.int32, (batch + 1,), q.device),
-                          mask.data_ptr() if mask is not None else 0, words, dim ** -0.5 if scale is None else scale,
+                          at_mask, words, dim ** -0.5 if scale is None else scale,
                           _side("lse", lse, torch.float32, (tokens, heads), q.device))
         eg._check(eg.lib().eg_tree_plan_run(self.handle, args, cache, st))
         return out
