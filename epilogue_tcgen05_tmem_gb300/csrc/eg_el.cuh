@@ -14,6 +14,7 @@ struct El;
 
 template <>
 struct El<__nv_bfloat16> {
+  static constexpr bool kBf16 = true;
   static __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
   // the two elements of one 32-bit word (low half first)
@@ -28,6 +29,7 @@ struct El<__nv_bfloat16> {
 
 template <>
 struct El<__half> {
+  static constexpr bool kBf16 = false;
   static __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
   static __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
   static __device__ __forceinline__ float2 unpack2(uint32_t w) {

@@ -1,96 +1,18 @@
-// eg_tree.cu -- attention of drafted token trees over a paged cache
-// (include/eg_decoder.h has the formulas), the plain form: one CTA for each
-// token and query head, its warps take every fourth key and join at the end.
+// eg_tree.cu -- host side of tree attention over a paged cache
+// (include/eg_decoder.h has the formulas, eg_tree_kernel.cuh the kernels):
+// plans, argument checks, tensor maps and launches.
 #include <cuda_runtime.h>
-#include <math_constants.h>
 
+#include <algorithm>
 #include <new>
 
 #include "../../include/eg_decoder.h"
-#include "eg_el.cuh"
 #include "eg_host.h"
-#include "eg_ptx.cuh"
-#include "eg_tree.h"
+#include "eg_tree_kernel.cuh"
 
 namespace eg {
 
 namespace {
-
-constexpr int kWarps = 4;
-
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) tree_simple_kernel(const TreeParams p) {
-  const int row = blockIdx.x, head = blockIdx.y;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // the last sequence that starts at or before the row
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.q_start[mid] <= row) lo = mid;
-    else hi = mid;
-  }
-  const int start = p.q_start[lo];
-  const int t = row - start;
-  const int n = min(min(p.q_start[lo + 1], p.tokens) - start, p.max_tree);
-  if (t < 0 || t >= n) return;
-  const int64_t room = p.table_stride * p.page_size;
-  const int64_t ctx = min(static_cast<int64_t>(max(p.context_lens[lo], 0)), room);
-  const int64_t keys = min(ctx + n, room);
-  const int32_t* table = p.block_table + lo * p.table_stride;
-  const int64_t at_head = static_cast<int64_t>(head / p.group) * p.head_stride;
-  float q[4], o[4] = {0, 0, 0, 0}, m = -CUDART_INF_F, l = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int e = lane * 4 + i;
-    q[i] = e < p.head_dim ? El<T>::to_float(static_cast<const T*>(p.q)[row * p.q_token + head * p.q_head + e]) : 0.0f;
-  }
-  for (int64_t j = warp; j < keys; j += kWarps) {
-    if (j >= ctx) {
-      const int u = static_cast<int>(j - ctx);
-      const bool sees = p.mask ? (p.mask[row * p.mask_stride + (u >> 5)] >> (u & 31)) & 1u : u <= t;
-      if (!sees) continue;
-    }
-    const int page = table[j / p.page_size];
-    const bool ok = page >= 0 && page < p.num_pages;
-    const int64_t at = (ok ? page : 0) * p.page_stride + (j % p.page_size) * p.token_stride + at_head;
-    float k[4], v[4], s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int e = lane * 4 + i;
-      const bool in = ok && e < p.head_dim;
-      k[i] = in ? El<T>::to_float(static_cast<const T*>(p.k)[at + e]) : 0.0f;
-      v[i] = in ? El<T>::to_float(static_cast<const T*>(p.v)[at + e]) : 0.0f;
-      s += q[i] * k[i];
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale;
-    const float next = fmaxf(m, s);
-    const float ref = next == -CUDART_INF_F ? 0.0f : next;
-    const float f = expf(m - ref), e = expf(s - ref);
-    l = l * f + e;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = o[i] * f + e * v[i];
-    m = next;
-  }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][128];
-  if (lane == 0) sm[warp] = m, sl[warp] = l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) so[warp][lane * 4 + i] = o[i];
-  __syncthreads();
-  float top = -CUDART_INF_F;
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-  const float ref = top == -CUDART_INF_F ? 0.0f : top;
-  float total = 0.0f, y = 0.0f;
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = expf(sm[w] - ref);
-    total += sl[w] * f;
-    y += so[w][threadIdx.x] * f;
-  }
-  if (threadIdx.x < p.head_dim)
-    static_cast<T*>(p.o)[row * p.o_token + head * p.o_head + threadIdx.x] = El<T>::from_float(total == 0.0f ? 0.0f : y / total);
-  if (p.lse && threadIdx.x == 0) p.lse[static_cast<int64_t>(row) * p.q_heads + head] = total == 0.0f ? -CUDART_INF_F : top + logf(total);
-}
 
 bool multiple16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -102,7 +24,13 @@ using namespace eg;
 struct eg_tree_plan {
   eg_tree_problem prob{};
   int device = -1;
+  int hd = 0, q_tiles = 0, stages = 0, grid = 0;
+  uint32_t smem = 0;
   size_t ws_bytes = 0;
+  uint8_t* ws = nullptr;  // partial sums, their statistics, the CTAs' ranges, the status word
+  size_t ml_at = 0, meta_at = 0, status_at = 0;
+  uint64_t wait_limit_ns = 0;
+  int stall = 0;
 };
 
 namespace {
@@ -144,12 +72,79 @@ eg_status check_run(const eg_tree_plan* plan, const eg_tree_args* a, const eg_kv
     return host_fail(EG_ERR_UNSUPPORTED, "a sequence's table must cover between 1 page and 2^31 tokens (table_stride=%lld)", (long long)a->table_stride);
   if (a->mask && a->mask_stride < (p.max_tree + 31) / 32)
     return host_fail(EG_ERR_INVALID_ARG, "mask_stride=%lld is less than the words of max_tree=%d", (long long)a->mask_stride, p.max_tree);
-  if (!(a->scale == a->scale)) return host_fail(EG_ERR_INVALID_ARG, "scale is not a number");
+  if (!(a->scale > 0.0f && a->scale < 1e30f)) return host_fail(EG_ERR_INVALID_ARG, "scale must be positive and finite");
   if (!c->k || !c->v || !multiple16(c->k) || !multiple16(c->v))
     return host_fail(EG_ERR_INVALID_ARG, "the cache is NULL or not 16-byte aligned");
   if (c->num_pages < 1 || c->num_pages > INT32_MAX) return host_fail(EG_ERR_INVALID_ARG, "num_pages=%lld", (long long)c->num_pages);
-  for (int64_t s : {c->page_stride, c->token_stride, c->head_stride})
-    if (s < 0 || s % 8) return host_fail(EG_ERR_INVALID_ARG, "the cache's strides must be multiples of 8 elements");
+  // the stride of a dimension of one is not used
+  const int64_t strides[3] = {c->num_pages > 1 ? c->page_stride : 8, c->token_stride, p.kv_heads > 1 ? c->head_stride : 8};
+  for (int64_t s : strides)
+    if (s < 8 || s % 8) return host_fail(EG_ERR_INVALID_ARG, "the cache's strides must be positive multiples of 8 elements");
+  return EG_OK;
+}
+
+// The tensor map of keys or values: columns, then token and head in the order
+// of their strides, then pages; boxes of 64 columns by `box_rows` tokens.
+eg_status encode_cache(const eg_tree_problem& p, const eg_kv_cache& c, const void* base, int box_rows, bool heads_inner, CUtensorMap* map) {
+  EncodeTiledFn fn = host_encode_tiled();
+  if (!fn) return host_fail(EG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t heads = static_cast<cuuint64_t>(p.kv_heads), places = static_cast<cuuint64_t>(p.page_size);
+  const cuuint64_t head_bytes = p.kv_heads > 1 ? static_cast<cuuint64_t>(c.head_stride) * 2 : 16;
+  const cuuint64_t place_bytes = static_cast<cuuint64_t>(c.token_stride) * 2;
+  const cuuint64_t page_bytes = c.num_pages > 1 ? static_cast<cuuint64_t>(c.page_stride) * 2 : 16;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim), heads_inner ? heads : places, heads_inner ? places : heads,
+                              static_cast<cuuint64_t>(c.num_pages)};
+  const cuuint64_t strides[3] = {heads_inner ? head_bytes : place_bytes, heads_inner ? place_bytes : head_bytes, page_bytes};
+  const cuuint32_t rows = static_cast<cuuint32_t>(box_rows);
+  const cuuint32_t box[4] = {64, heads_inner ? 1u : rows, heads_inner ? rows : 1u, 1};
+  const cuuint32_t steps[4] = {1, 1, 1, 1};
+  const CUresult r = fn(map, p.dtype == EG_EL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+                        const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return host_fail(EG_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for the cache", static_cast<int>(r));
+  return EG_OK;
+}
+
+using TreeKernel = void (*)(TreeParams, CUtensorMap, CUtensorMap);
+using JoinKernel = void (*)(TreeParams);
+
+TreeKernel main_kernel(const eg_tree_plan& pl) {
+  if (pl.prob.dtype == EG_EL_BF16) return pl.hd == 64 ? tree_kernel<__nv_bfloat16, 64> : tree_kernel<__nv_bfloat16, 128>;
+  return pl.hd == 64 ? tree_kernel<__half, 64> : tree_kernel<__half, 128>;
+}
+JoinKernel join_kernel(const eg_tree_plan& pl) {
+  if (pl.prob.dtype == EG_EL_BF16) return pl.hd == 64 ? tree_join_kernel<__nv_bfloat16, 64> : tree_join_kernel<__nv_bfloat16, 128>;
+  return pl.hd == 64 ? tree_join_kernel<__half, 64> : tree_join_kernel<__half, 128>;
+}
+
+int rows_of(const eg_tree_plan& pl) {
+  return std::min(128 * pl.q_tiles, pl.prob.max_tree * (pl.prob.q_heads / pl.prob.kv_heads));
+}
+
+eg_status set_up(eg_tree_plan* pl) {
+  int sms = 0;
+  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, pl->device);
+  if (e != cudaSuccess) return host_cuda_fail(e, "device query");
+  const eg_tree_problem& p = pl->prob;
+  pl->hd = p.head_dim <= 64 ? 64 : 128;
+  // 256 rows of an item share each key tile where a tree can have more than 128
+  pl->q_tiles = p.max_tree * (p.q_heads / p.kv_heads) > 128 ? 2 : 1;
+  const uint32_t tile = pl->hd == 64 ? TreeSmem<64>::kTileBytes : TreeSmem<128>::kTileBytes;
+  const uint32_t extra = TreeSmem<64>::kExtra;
+  pl->stages = std::min<int>(12, static_cast<int>((232448u - extra) / tile) - pl->q_tiles);
+  pl->smem = (pl->q_tiles + pl->stages) * tile + extra;
+  pl->grid = sms;
+  const size_t rows = static_cast<size_t>(pl->grid) * 2 * 128 * pl->q_tiles;
+  pl->ml_at = rows * pl->hd * 4;
+  pl->meta_at = pl->ml_at + rows * 8;
+  pl->status_at = pl->meta_at + pl->grid * sizeof(TreeMeta);
+  pl->ws_bytes = pl->status_at + 16;
+  if ((e = cudaMalloc(&pl->ws, pl->ws_bytes)) != cudaSuccess) return host_cuda_fail(e, "allocating the plan's workspace");
+  if ((e = cudaMemset(pl->ws + pl->meta_at, 0, pl->ws_bytes - pl->meta_at)) != cudaSuccess) return host_cuda_fail(e, "clearing the plan's workspace");
+  if ((e = cudaFuncSetAttribute(reinterpret_cast<const void*>(main_kernel(*pl)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                static_cast<int>(pl->smem))) != cudaSuccess)
+    return host_cuda_fail(e, "cudaFuncSetAttribute");
+  pl->wait_limit_ns = host_wait_limit_ns();
   return EG_OK;
 }
 
@@ -168,6 +163,11 @@ eg_status eg_tree_plan_create(const eg_tree_problem* problem, eg_tree_plan** out
   if (!pl) return host_fail(EG_ERR_NO_MEMORY, "no host memory for a plan");
   pl->prob = *problem;
   pl->device = dev;
+  if ((s = set_up(pl)) != EG_OK) {
+    if (pl->ws) cudaFree(pl->ws);
+    delete pl;
+    return s;
+  }
   *out = pl;
   return EG_OK;
 }
@@ -187,29 +187,68 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   if (a.batch == 0 || a.tokens == 0) return EG_OK;
   TreeParams p{};
   p.q_heads = b.q_heads, p.kv_heads = b.kv_heads, p.group = b.q_heads / b.kv_heads, p.head_dim = b.head_dim;
-  p.page_size = b.page_size, p.max_batch = b.max_batch, p.max_tree = b.max_tree;
+  p.page_size = b.page_size, p.max_tree = b.max_tree;
+  p.box_rows = std::min(128, b.page_size & -b.page_size);
+  p.heads_inner = b.kv_heads > 1 && cache->head_stride < cache->token_stride ? 1 : 0;
+  p.q_tiles = plan->q_tiles, p.stages = plan->stages;
   p.batch = a.batch, p.tokens = a.tokens;
   p.q = a.q, p.o = a.o, p.q_token = a.q_token, p.q_head = a.q_head, p.o_token = a.o_token, p.o_head = a.o_head;
   p.block_table = a.block_table, p.table_stride = a.table_stride, p.context_lens = a.context_lens, p.q_start = a.q_start;
-  p.mask = a.mask, p.mask_stride = a.mask_stride, p.scale = a.scale, p.lse = a.lse;
-  p.k = cache->k, p.v = cache->v, p.num_pages = cache->num_pages;
+  p.mask = a.mask, p.mask_stride = a.mask_stride, p.scale_log2 = a.scale * 1.4426950408889634f, p.lse = a.lse;
+  p.v = cache->v, p.num_pages = cache->num_pages;
   p.page_stride = cache->page_stride, p.token_stride = cache->token_stride, p.head_stride = cache->head_stride;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const dim3 grid(static_cast<unsigned>(a.tokens), static_cast<unsigned>(b.q_heads));
-  if (b.dtype == EG_EL_BF16) tree_simple_kernel<__nv_bfloat16><<<grid, kWarps * 32, 0, st>>>(p);
-  else tree_simple_kernel<__half><<<grid, kWarps * 32, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
-  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching tree attention");
+  p.partial = reinterpret_cast<float*>(plan->ws);
+  p.partial_ml = reinterpret_cast<float*>(plan->ws + plan->ml_at);
+  p.meta = reinterpret_cast<TreeMeta*>(plan->ws + plan->meta_at);
+  p.status = reinterpret_cast<int32_t*>(plan->ws + plan->status_at);
+  p.wait_limit_ns = plan->wait_limit_ns, p.stall = plan->stall;
+  CUtensorMap map_k, map_v;
+  if ((s = encode_cache(b, *cache, cache->k, p.box_rows, p.heads_inner != 0, &map_k)) != EG_OK) return s;
+  if ((s = encode_cache(b, *cache, cache->v, p.box_rows, p.heads_inner != 0, &map_v)) != EG_OK) return s;
+
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan->grid));
+  cfg.blockDim = dim3(kTreeThreads);
+  cfg.dynamicSmemBytes = plan->smem;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan), p, map_k, map_v);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launching tree attention");
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(plan->grid - 1), static_cast<unsigned>((rows_of(*plan) + 7) / 8));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, join_kernel(*plan), p);
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching the join of tree attention");
 }
 
 eg_status eg_tree_plan_device_status(eg_tree_plan* plan) {
   if (!plan) return host_fail(EG_ERR_INVALID_ARG, "plan is NULL");
-  const cudaError_t e = cudaDeviceSynchronize();
-  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "synchronising the plan's device");
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return host_cuda_fail(e, "synchronising the plan's device");
+  int32_t status = 0;
+  if ((e = cudaMemcpy(&status, plan->ws + plan->status_at, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
+    return host_cuda_fail(e, "reading the plan's status");
+  if (status == 0) return EG_OK;
+  if ((e = cudaMemset(plan->ws + plan->status_at, 0, 4)) != cudaSuccess) return host_cuda_fail(e, "clearing the plan's status");
+  return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the tree attention kernel ran past its limit");
+}
+
+eg_status eg_tree_plan_set_test_stall(eg_tree_plan* plan, uint64_t wait_limit_ns, int32_t stall_producer) {
+  if (!plan) return host_fail(EG_ERR_INVALID_ARG, "plan is NULL");
+  if (stall_producer != 0 && stall_producer != 1) return host_fail(EG_ERR_INVALID_ARG, "stall_producer must be 0 or 1");
+  plan->wait_limit_ns = wait_limit_ns ? wait_limit_ns : host_wait_limit_ns();
+  plan->stall = stall_producer;
+  return EG_OK;
 }
 
 eg_status eg_tree_plan_destroy(eg_tree_plan* plan) {
   if (!plan) return EG_OK;
+  cudaDeviceSynchronize();
+  cudaFree(plan->ws);
   delete plan;
   return EG_OK;
 }

@@ -1,14 +1,32 @@
-// eg_tree.h -- launch description of the tree attention kernels.
+// eg_tree.h -- launch description of the tree attention kernels, shared by
+// the host side (eg_tree.cu) and the kernels (eg_tree_kernel.cuh).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
 
 namespace eg {
 
+// What a CTA of the main kernel tells the joining kernel: where its range of
+// work units starts and which item (sequence, cached head, row group) that
+// unit belongs to.
+struct TreeMeta {
+  int64_t from;         // the CTA's first unit
+  int64_t begin, end;   // the units of the item that holds it
+  int64_t total;        // units of the run
+  int32_t ctas;         // CTAs that have units
+  int32_t start, rows, row0, head;  // the item's first packed row, rows, first row in the sequence, cached head
+  int32_t pad;
+};
+
 struct TreeParams {
   // the problem
-  int32_t q_heads, kv_heads, group, head_dim, page_size, max_batch, max_tree;
+  int32_t q_heads, kv_heads, group, head_dim, page_size, max_tree;
+  int32_t box_rows;     // keys of one TMA box: the power of two that divides page_size, at most 128
+  int32_t heads_inner;  // the tensor maps' second dimension is the head, not the token
+  int32_t q_tiles;      // 128-row tiles of one item: 1 or 2
+  int32_t stages;
   // the run
   int32_t batch, tokens;
   const void* q;
@@ -20,11 +38,26 @@ struct TreeParams {
   const int32_t* q_start;
   const uint32_t* mask;
   int64_t mask_stride;
-  float scale;
+  float scale_log2;     // scale * log2(e)
   float* lse;
-  // the cache
-  const void *k, *v;
+  // the values again, for the rows that attend to a value that is not finite
+  const void* v;
   int64_t num_pages, page_stride, token_stride, head_stride;
+  // the plan's
+  float* partial;       // [CTAs][2][128 q_tiles][HD] sums, then
+  float* partial_ml;    // [CTAs][2][128 q_tiles][2] their maximum (log2) and weight
+  TreeMeta* meta;       // [CTAs]
+  int32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t stall;        // test hook: the producer issues nothing
+};
+
+// Shared memory of the main kernel for a head of HD columns.
+template <int HD>
+struct TreeSmem {
+  static constexpr uint32_t kTileBytes = 128u * HD * 2u;  // 128 rows of queries, keys or values
+  static constexpr uint32_t kExtra = 2560u;               // barriers, schedule, exchange of row statistics
+  static uint32_t bytes(int q_tiles, int stages) { return (q_tiles + stages) * kTileBytes + kExtra; }
 };
 
 }  // namespace eg

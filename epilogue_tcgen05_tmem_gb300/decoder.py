@@ -20,7 +20,8 @@ EL_DTYPES = {"bf16": 0, "f16": 1, "f32": 2}
 
 EXPORTED = ("eg_qk_norm_rope", "eg_qk_norm_rope_backward", "eg_qk_norm_rope_workspace_bytes",
             "eg_kv_append", "eg_tree_plan_create", "eg_tree_plan_workspace_bytes",
-            "eg_tree_plan_run", "eg_tree_plan_device_status", "eg_tree_plan_destroy",
+            "eg_tree_plan_run", "eg_tree_plan_device_status", "eg_tree_plan_set_test_stall",
+            "eg_tree_plan_destroy",
             "eg_token_logprobs", "eg_token_logprobs_backward")
 
 _i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
@@ -93,6 +94,7 @@ def declare(L: ctypes.CDLL) -> None:
                        ("eg_tree_plan_workspace_bytes", [_p, ctypes.POINTER(ctypes.c_size_t)]),
                        ("eg_tree_plan_run", [_p, _p, _p, _p]),
                        ("eg_tree_plan_device_status", [_p]),
+                       ("eg_tree_plan_set_test_stall", [_p, ctypes.c_uint64, _i32]),
                        ("eg_tree_plan_destroy", [_p]),
                        ("eg_token_logprobs", [_p, _p]),
                        ("eg_token_logprobs_backward", [_p, _p, _p])):
@@ -334,6 +336,10 @@ class TreeAttention:
 
     def device_status(self) -> int:
         return _eg().lib().eg_tree_plan_device_status(self.handle)
+
+    def set_test_stall(self, wait_limit_ns: int, stall_producer: int):
+        eg = _eg()
+        eg._check(eg.lib().eg_tree_plan_set_test_stall(self.handle, wait_limit_ns, int(stall_producer)))
 
     def close(self):
         if getattr(self, "handle", None):

@@ -145,7 +145,7 @@ typedef struct {
   const int32_t* q_start;       /* [batch + 1], rising */
   const uint32_t* mask;         /* [tokens][mask_stride] words, or NULL */
   int64_t mask_stride;          /* at least max_tree / 32, rounded up */
-  float scale;
+  float scale;                  /* positive */
   float* lse;                   /* [tokens][q_heads], or NULL */
 } eg_tree_args;
 
@@ -158,6 +158,12 @@ EG_API eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args,
 /* Synchronise the plan's device and report a wait in its kernels that ran past
  * its limit (EG_ERR_DEVICE_TIMEOUT, then cleared). */
 EG_API eg_status eg_tree_plan_device_status(eg_tree_plan* plan);
+/* Testing hook for failure detection, as eg_plan_set_test_stall: limit the
+ * kernels' waits to `wait_limit_ns` (0: the default) and, with
+ * `stall_producer` 1, have no keys loaded, so that the first wait runs out. */
+EG_API eg_status eg_tree_plan_set_test_stall(eg_tree_plan* plan, uint64_t wait_limit_ns,
+                                             int32_t stall_producer);
+/* Free everything the plan owns, after synchronising its device. */
 EG_API eg_status eg_tree_plan_destroy(eg_tree_plan* plan);
 
 /* ------------------------------------------- log probabilities of tokens --

@@ -138,4 +138,5 @@ def test_tree_null_arguments(L):
     assert L.eg_tree_plan_run(None, None, None, None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_tree_plan_workspace_bytes(None, None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_tree_plan_device_status(None) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_tree_plan_set_test_stall(None, 0, 0) == eg.EG_ERR_INVALID_ARG
     assert L.eg_tree_plan_destroy(None) == eg.EG_OK

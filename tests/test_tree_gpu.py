@@ -280,6 +280,20 @@ def test_lengths_beyond_the_limits_are_cut():
     plan.close()
 
 
+def test_a_wait_that_runs_out_is_reported():
+    c = Case("bf16", 8, 2, 128, 16, [900, 0], [5, 2], False, seed=13)
+    d, plan = c.device(), c.plan()
+    plan.set_test_stall(5_000_000, 1)
+    plan.run(**d)
+    torch.cuda.synchronize()
+    assert plan.device_status() == eg.EG_ERR_DEVICE_TIMEOUT
+    assert plan.device_status() == eg.EG_OK  # reported once
+    plan.set_test_stall(0, 0)
+    _check(c, plan.run(**d))
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
 def test_nothing_to_do():
     c = Case("bf16", 4, 2, 64, 16, [30], [2], True)
     d, plan = c.device(), c.plan()
@@ -297,7 +311,7 @@ def test_refusals():
     for kw in bad:
         with pytest.raises(ValueError):
             plan.run(**dict(d, **kw))
-    for kw in (dict(mask=d["mask"][:, :0].contiguous()), dict(scale=math.nan)):
+    for kw in (dict(mask=d["mask"][:, :0].contiguous()), dict(scale=math.nan), dict(scale=-1.0), dict(scale=0.0)):
         with pytest.raises(eg.EgError) as e:
             plan.run(**dict(d, **kw))
         assert e.value.status == eg.EG_ERR_INVALID_ARG
