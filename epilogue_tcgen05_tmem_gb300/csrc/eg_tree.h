@@ -56,7 +56,7 @@ struct TreeParams {
 template <int HD>
 struct TreeSmem {
   static constexpr uint32_t kTileBytes = 128u * HD * 2u;  // 128 rows of queries, keys or values
-  static constexpr uint32_t kExtra = 2560u;               // barriers, schedule, exchange of row statistics
+  static constexpr uint32_t kExtra = 3072u;               // barriers, schedule, exchange of row statistics
   static uint32_t bytes(int q_tiles, int stages) { return (q_tiles + stages) * kTileBytes + kExtra; }
 };
 

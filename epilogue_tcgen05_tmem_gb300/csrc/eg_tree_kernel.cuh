@@ -68,6 +68,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// Two float32 lanes in one instruction.
+__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpack64(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 __device__ __forceinline__ float tree_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -83,20 +103,30 @@ struct TreeSeq {
   int32_t groups;      // row groups
 };
 
-__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int32_t start, int32_t n, int32_t ctx) {
   TreeSeq s;
   const int32_t room = static_cast<int32_t>(p.table_stride * p.page_size);
-  s.start = min(max(p.q_start[b], 0), p.tokens);
-  s.n = min(min(max(p.q_start[b + 1], s.start), p.tokens) - s.start, p.max_tree);
-  s.ctx = min(max(p.context_lens[b], 0), room);
-  s.keys = min(s.ctx + s.n, room);
-  s.tiles = (s.keys + static_cast<int32_t>(kTreeKeys) - 1) / static_cast<int32_t>(kTreeKeys);
-  s.groups = (s.n * p.group + 128 * p.q_tiles - 1) / (128 * p.q_tiles);
+  s.start = start, s.n = n, s.ctx = ctx;
+  s.keys = min(ctx + n, room);
+  s.tiles = (s.keys + static_cast<int32_t>(kTreeKeys) - 1) >> 7;
+  s.groups = (n * p.group + 128 * p.q_tiles - 1) >> (6 + p.q_tiles);
   return s;
 }
-__device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& s) {
-  return static_cast<int64_t>(s.tiles) * s.groups * p.kv_heads;
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  const int32_t room = static_cast<int32_t>(p.table_stride * p.page_size);
+  const int32_t from = __ldg(p.q_start + b), to = __ldg(p.q_start + b + 1), ctx = __ldg(p.context_lens + b);
+  const int32_t start = min(max(from, 0), p.tokens);
+  return tree_seq(p, start, min(min(max(to, start), p.tokens) - start, p.max_tree), min(max(ctx, 0), room));
 }
+// Units of one item: its key tiles, and kTreeFixed for what an item costs
+// beside them (queries, the first and the last tile's latency, the result).
+constexpr int32_t kTreeFixed = 2;
+__device__ __forceinline__ int32_t tree_item_units(const TreeSeq& s) { return s.tiles + kTreeFixed; }
+__device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& s) {
+  return static_cast<int64_t>(tree_item_units(s)) * (s.groups * p.kv_heads);
+}
+
+constexpr int kTreeNear = 16;  // sequences whose lengths a CTA keeps in shared memory
 
 // A walk over a CTA's range: one segment (consecutive key tiles of one item)
 // at a time.
@@ -108,23 +138,38 @@ struct TreeWalk {
   // the segment
   int32_t head, row0, rows, first, count;
 
+  const int32_t (*near_)[4];  // start, n, ctx of the sequences from near_b on
+  int32_t near_b;
+
+  __device__ __forceinline__ void load(const TreeParams& p) {
+    const int i = b - near_b;
+    seq = i < kTreeNear ? tree_seq(p, near_[i][0], near_[i][1], near_[i][2]) : tree_seq(p, b);
+  }
   __device__ __forceinline__ bool next(const TreeParams& p) {
-    if (at >= to) return false;
     for (;;) {
-      const int64_t units = tree_units(p, seq);
-      if (at - before < units) break;
-      before += units;
-      seq = tree_seq(p, ++b);
+      if (at >= to) return false;
+      int64_t units = tree_units(p, seq);
+      while (at - before >= units) {
+        before += units;
+        ++b;
+        load(p);
+        units = tree_units(p, seq);
+      }
+      const int64_t idx = at - before;
+      const int32_t each = tree_item_units(seq);
+      const int32_t item = units >> 32 ? static_cast<int32_t>(idx / each) : static_cast<int32_t>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(each));
+      const int32_t in = static_cast<int32_t>(idx - static_cast<int64_t>(item) * each);
+      const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(each - in), to - at));
+      at += take;
+      // units 0..kTreeFixed-1 of an item stand for no tile
+      first = max(in - kTreeFixed, 0);
+      count = in + take - kTreeFixed - first;
+      if (count <= 0) continue;
+      head = item / seq.groups;
+      row0 = (item - head * seq.groups) << (6 + p.q_tiles);
+      rows = min(seq.n * p.group - row0, 64 << p.q_tiles);
+      return true;
     }
-    const int64_t idx = at - before;
-    const int32_t item = static_cast<int32_t>(idx / seq.tiles);
-    first = static_cast<int32_t>(idx - static_cast<int64_t>(item) * seq.tiles);
-    head = item / seq.groups;
-    row0 = (item - head * seq.groups) * 128 * p.q_tiles;
-    rows = min(seq.n * p.group - row0, 128 * p.q_tiles);
-    count = static_cast<int32_t>(min(static_cast<int64_t>(seq.tiles - first), to - at));
-    at += count;
-    return true;
   }
   __device__ __forceinline__ bool whole() const { return first == 0 && count == seq.tiles; }
 };
@@ -138,12 +183,12 @@ struct TreeShared {
   int32_t abort;
   int32_t poisoned[2];            // the last segment (counted from 1) that found a value that is not finite
   int32_t b;
-  int32_t pad;
-  int64_t before, from, to, total;
-  int64_t warps[12];
+  int64_t before;
+  int64_t warps[2][12];
+  int32_t near_[kTreeNear][4];
   float2 stats[2][128];           // a warpgroup's row references and weights
 };
-static_assert(sizeof(TreeShared) <= 2560, "fits the room after the tiles");
+static_assert(sizeof(TreeShared) <= TreeSmem<64>::kExtra, "fits the room after the tiles");
 
 // Position of a tile's load in the ring's order: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ uint32_t tree_pos_k(uint32_t i) { return i == 0 ? 0 : 2 * i - 1; }
@@ -169,12 +214,18 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
   griddep_launch_dependents();
 
-  // ---- this CTA's range of units
+  // ---- this CTA's range of units.  One pass over the sequences where every
+  // thread has one; else a pass for the total and one to find the place.
+  const bool once = p.batch <= kTreeThreads;
   int64_t mine = 0;
   for (int b = tid; b < p.batch; b += kTreeThreads) mine += tree_units(p, tree_seq(p, b));
+  int64_t upto = mine;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) sh.warps[warp] = mine;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.warps[0][warp] = upto;
   if (tid == 0) {
     for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_done[i], 1);
@@ -187,31 +238,38 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     sh.poisoned[0] = sh.poisoned[1] = 0;
   }
   __syncthreads();
-  int64_t total = 0;
-  for (int w = 0; w < kTreeThreads / 32; ++w) total += sh.warps[w];
+  int64_t total = 0, base = 0;
+#pragma unroll
+  for (int w = 0; w < kTreeThreads / 32; ++w) {
+    if (w < warp) base += sh.warps[0][w];
+    total += sh.warps[0][w];
+  }
   const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), total));
   if (static_cast<int32_t>(blockIdx.x) >= ctas) {
     if (blockIdx.x == 0 && tid == 0) p.meta[0].ctas = 0;
     return;
   }
   const int64_t from = total * blockIdx.x / ctas, to = total * (blockIdx.x + 1) / ctas;
-  {
+  if (once) {
+    if (base + upto - mine <= from && from < base + upto) sh.b = tid, sh.before = base + upto - mine;
+  } else {
     int64_t before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kTreeThreads) {
       const int64_t units = b0 + tid < p.batch ? tree_units(p, tree_seq(p, b0 + tid)) : 0;
-      int64_t upto = units;
+      upto = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += x;
       }
       __syncthreads();
-      if (lane == 31) sh.warps[warp] = upto;
+      if (lane == 31) sh.warps[1][warp] = upto;
       __syncthreads();
-      int64_t chunk = 0, base = before;
+      int64_t chunk = 0;
+      base = before;
       for (int w = 0; w < kTreeThreads / 32; ++w) {
-        if (w < warp) base += sh.warps[w];
-        chunk += sh.warps[w];
+        if (w < warp) base += sh.warps[1][w];
+        chunk += sh.warps[1][w];
       }
       if (base + upto - units <= from && from < base + upto) sh.b = b0 + tid, sh.before = base + upto - units;
       before += chunk;
@@ -227,18 +285,16 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  if (tid < kTreeNear && sh.b + tid < p.batch) {
+    const TreeSeq q = tree_seq(p, sh.b + tid);
+    sh.near_[tid][0] = q.start, sh.near_[tid][1] = q.n, sh.near_[tid][2] = q.ctx;
+  }
+  __syncthreads();
 
   TreeWalk walk;
   walk.b = sh.b, walk.before = sh.before, walk.at = from, walk.to = to;
-  walk.seq = tree_seq(p, walk.b);
-  if (tid == 0) {
-    TreeWalk w = walk;
-    w.next(p);
-    TreeMeta m;
-    m.from = from, m.begin = from - w.first, m.end = m.begin + w.seq.tiles, m.total = total;
-    m.ctas = ctas, m.start = w.seq.start, m.rows = w.rows, m.row0 = w.row0, m.head = w.head, m.pad = 0;
-    p.meta[blockIdx.x] = m;
-  }
+  walk.near_ = sh.near_, walk.near_b = sh.b;
+  walk.load(p);
 
   // Bounded wait: false once any wait of the CTA has run past its limit.
   volatile int32_t* abort = &sh.abort;
@@ -260,6 +316,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   };
 
+  // Registers from the four warps that need few to the two warpgroups that
+  // hold a row of 128 scores a thread: 4 x 32 x 88 + 8 x 32 x 208 is what the
+  // block was launched with (384 x 168).
+  if (warp >= 8) {
+  setmaxnreg_dec<88>();
   if (warp == 8) {
     // ------------------------------------------------------- producer ----
     uint32_t pos = 0;  // loads so far
@@ -316,60 +377,50 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (lane == 0) {
       constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
       constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
-      uint32_t base = 0, segment = 0;
-      uint32_t uses[2] = {0, 0};  // tiles given to each warpgroup
+      uint32_t base = 0, segment = 0, used = 0;  // loads, segments and tiles given to warpgroup 0 and 1 (16 bits each) so far
+      const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
+      const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
       bool ok = true;
       while (ok && walk.next(p)) {
         const uint32_t count = walk.count;
         const bool pair = walk.rows > 128;
-        // S of key tile i for warpgroup s
-        auto product_s = [&](uint32_t i, int s, bool first_use, bool last_use) {
-          const uint32_t at = base + tree_pos_k(i), slot = at % stages;
-          if (first_use && !wait(&sh.full[slot], at / stages)) return false;
-          tc_fence_after();
-          const uint32_t a = smem_u32(q_smem) + (pair ? s : 0) * kTile, b = smem_u32(ring + slot * kTile);
+        const uint32_t shift = pair ? 1 : 0, jobs = count << shift;
+        if (!(ok = wait(&sh.q_full, segment))) break;
+        // job j is warpgroup j & 1's next tile; the scores of two jobs run
+        // ahead of the weighted sums
+        for (uint32_t j = 0; ok && j < jobs + 2; ++j) {
+          if (j >= 2) {
+            // O += P V of job j - 2
+            const uint32_t s = j & 1, i = (j - 2) >> shift;
+            const uint32_t at = base + tree_pos_v(i, count), slot = at % stages;
+            const uint32_t tiles = s ? used >> 16 : used & 0xFFFFu;
+            ok = ((pair && s) || wait(&sh.full[slot], at / stages)) && wait(&sh.p_ready[s], tiles);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t v = v_desc + (slot * kTile >> 4);
+            const uint32_t first = i == 0 || (!pair && i == 1) ? 0 : 1;
 #pragma unroll
-          for (int k = 0; k < HD / 16; ++k) {
-            const uint32_t step = (k / 4) * kPart + (k % 4) * 32;
-            umma_f16(tmem + s * 128, sdesc_k_sw128(a + step), sdesc_k_sw128(b + step), kIdescS, k > 0);
+            for (int k = 0; k < 8; ++k)
+              umma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, v + k * (2048 >> 4), kIdescO, k > 0 ? 1 : first);
+            umma_commit(&sh.o_done[s]);
+            if (!pair || s) umma_commit(&sh.empty[slot]);
+            used = s ? used + 0x10000u : (used & 0xFFFF0000u) | ((used + 1) & 0xFFFFu);
           }
-          umma_commit(&sh.s_full[s]);
-          if (last_use) umma_commit(&sh.empty[slot]);
-          return true;
-        };
-        // O += P V of key tile i for warpgroup s
-        auto product_o = [&](uint32_t i, int s, bool first, bool first_use, bool last_use) {
-          const uint32_t at = base + tree_pos_v(i, count), slot = at % stages;
-          if (first_use && !wait(&sh.full[slot], at / stages)) return false;
-          if (!wait(&sh.p_ready[s], uses[s])) return false;
-          tc_fence_after();
-          const uint32_t b = smem_u32(ring + slot * kTile);
+          if (j < jobs) {
+            // S of job j
+            const uint32_t s = j & 1, i = j >> shift;
+            const uint32_t at = base + tree_pos_k(i), slot = at % stages;
+            if (!(pair && s) && !(ok = wait(&sh.full[slot], at / stages))) break;
+            tc_fence_after();
+            const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0), key = k_desc + (slot * kTile >> 4);
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            umma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, sdesc_mn_sw128(b + k * 2048, kPart), kIdescO, k > 0 || !first);
-          umma_commit(&sh.o_done[s]);
-          if (last_use) umma_commit(&sh.empty[slot]);
-          ++uses[s];
-          return true;
-        };
-        ok = wait(&sh.q_full, segment);
-        if (!ok) break;
-        if (pair) {
-          ok = product_s(0, 0, true, false) && product_s(0, 1, false, true);
-          if (count == 1) umma_commit(&sh.q_empty);
-          for (uint32_t i = 0; ok && i < count; ++i) {
-            const bool more = i + 1 < count;
-            ok = product_o(i, 0, i == 0, true, false) && (!more || product_s(i + 1, 0, true, false)) &&
-                 product_o(i, 1, i == 0, false, true) && (!more || product_s(i + 1, 1, false, true));
-            if (i + 2 == count) umma_commit(&sh.q_empty);
-          }
-        } else {
-          ok = product_s(0, 0, true, true);
-          if (count == 1) umma_commit(&sh.q_empty);
-          for (uint32_t i = 0; ok && i < count; ++i) {
-            if (i + 1 < count) ok = product_s(i + 1, (i + 1) & 1, true, true);
-            if (i + 2 == count) umma_commit(&sh.q_empty);
-            ok = ok && product_o(i, i & 1, i < 2, true, true);
+            for (int k = 0; k < HD / 16; ++k) {
+              const uint32_t step = ((k / 4) * kPart + (k % 4) * 32) >> 4;
+              umma_f16(tmem + s * 128, q + step, key + step, kIdescS, k > 0);
+            }
+            umma_commit(&sh.s_full[s]);
+            if (!pair || s) umma_commit(&sh.empty[slot]);
+            if (j + 1 == jobs) umma_commit(&sh.q_empty);
           }
         }
         base += 2 * count;
@@ -379,27 +430,47 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       umma_commit(&sh.drained);
       if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
     }
-  } else if (warp >= 10) {
+  } else {
     // -------------------------------------------------------- queries ----
     const int at = tid - 320;  // 0..63
-    const int vecs = p.head_dim / 8;
+    const int vecs = p.head_dim >> 3;
+    // thread at takes 16-byte column c of rows r, r + step, ...
+    const int step = 64 / vecs, c = at % vecs;
     uint32_t segment = 0;
+    if (at == 63) {
+      // what the joining kernel has to know of this CTA's first item
+      TreeMeta m;
+      m.from = from;
+      const int64_t idx = from - sh.before;
+      const int32_t each = tree_item_units(walk.seq);
+      m.begin = from - idx % each, m.end = m.begin + each, m.total = total;
+      m.ctas = ctas;
+      const int32_t item = static_cast<int32_t>(idx / each), head = item / walk.seq.groups;
+      m.start = walk.seq.start, m.row0 = (item - head * walk.seq.groups) << (6 + p.q_tiles), m.head = head;
+      m.rows = min(walk.seq.n * p.group - m.row0, 64 << p.q_tiles), m.pad = 0;
+      p.meta[blockIdx.x] = m;
+    }
     while (walk.next(p)) {
       if (!wait(&sh.q_empty, segment + 1)) break;
-      for (int i = at; i < walk.rows * vecs; i += 64) {
-        const int r = i / vecs, c = i - r * vecs;
-        const int t = (walk.row0 + r) / p.group, g = (walk.row0 + r) - t * p.group;
-        const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(walk.seq.start + t) * p.q_token +
-                       static_cast<int64_t>(walk.head * p.group + g) * p.q_head + c * 8;
-        const uint32_t to_ = (r >> 7) * kTile + (c >> 3) * kPart + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4);
-        *reinterpret_cast<uint4*>(q_smem + to_) = __ldg(reinterpret_cast<const uint4*>(src));
+      if (at < step * vecs) {
+        const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(walk.head) * p.group * p.q_head + c * 8;
+        const uint32_t to_ = (c >> 3) * kPart;
+        for (int r = at / vecs; r < walk.rows; r += step) {
+          const uint32_t row = static_cast<uint32_t>(walk.row0 + r), t = row / static_cast<uint32_t>(p.group), g = row - t * p.group;
+          cp_async_16(q_smem + to_ + (r >> 7) * kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                      src + static_cast<int64_t>(walk.seq.start + t) * p.q_token + static_cast<int64_t>(g) * p.q_head, 16);
+        }
       }
+      cp_async_commit();
+      cp_async_wait<0>();
       fence_proxy_async_smem();
       mbar_arrive(&sh.q_full);
       ++segment;
     }
+  }
   } else {
     // -------------------------------------------------------- softmax ----
+    setmaxnreg_inc<208>();
     const int s = warp >> 2;            // the warpgroup
     const int row_in = tid & 127;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
@@ -443,24 +514,33 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool edge = key0 + static_cast<int>(kTreeKeys) > walk.seq.ctx;
         if (!(ok = wait_all(&sh.s_full[s], uses))) break;
         tc_fence_after();
+        if (busy && edge) {
+          // a tile with drafted places or past the end: -infinity where the
+          // row does not attend to.  In tensor memory and in a loop: the code
+          // of rare tiles stays small and out of the others' registers.
+#pragma unroll 1
+          for (int w = 0; w < 4; ++w) {
+            const int d = walk.seq.ctx - (key0 + 32 * w);  // context places of this word
+            const uint32_t bits = d >= 32  ? 0xFFFFFFFFu
+                                  : d <= 0 ? drafted_bits(-d)
+                                           : ((1u << d) - 1u) | (drafted_bits(0) << d);
+            uint32_t x[32];
+            tmem_ld32p(t_s + w * 32, x);
+            tmem_ld_wait();
+            reg_fence<32>(x);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(bits >> j & 1u)) x[j] = 0xFF800000u;
+            tmem_st32(t_s + w * 32, x);
+          }
+          tmem_st_wait();
+        }
         if (busy) {
           uint32_t x[128];
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32p(t_s + j * 32, x + j * 32);
           tmem_ld_wait();
           reg_fence<128>(x);
-          if (edge) {
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const int d = walk.seq.ctx - (key0 + 32 * w);  // context places of this word
-              const uint32_t bits = d >= 32  ? 0xFFFFFFFFu
-                                    : d <= 0 ? drafted_bits(-d)
-                                             : ((1u << d) - 1u) | (drafted_bits(0) << d);
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) x[w * 32 + j] = 0xFF800000u;
-            }
-          }
           float top[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(x[j]);
@@ -477,7 +557,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             const float f = next == m ? 1.0f : tree_ex2(m - next);
             if (!(ok = wait_all(&sh.o_done[s], uses - 1))) break;
             tc_fence_after();
-#pragma unroll
+#pragma unroll 1
             for (int j = 0; j < HD; j += 16) {
               uint32_t y[16];
               tmem_ld16(t_o + s * 128 + j, y);
@@ -491,15 +571,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             m = next;
           }
           const float ref = m == -CUDART_INF_F ? 0.0f : kShift - m;
-          float sum[2] = {0.0f, 0.0f};
+          const uint64_t c2 = pack64(__float_as_uint(c), __float_as_uint(c)), ref2 = pack64(__float_as_uint(ref), __float_as_uint(ref));
+          uint64_t sum2[2] = {0, 0};
 #pragma unroll
           for (int j = 0; j < 64; ++j) {
-            const float a = tree_ex2(fmaf(__uint_as_float(x[2 * j]), c, ref));
-            const float b = tree_ex2(fmaf(__uint_as_float(x[2 * j + 1]), c, ref));
-            sum[0] += a, sum[1] += b;
+            float a, b;
+            unpack64(fma2(pack64(x[2 * j], x[2 * j + 1]), c2, ref2), &a, &b);
+            a = tree_ex2(a), b = tree_ex2(b);
+            sum2[j & 1] = add2(sum2[j & 1], pack64(__float_as_uint(a), __float_as_uint(b)));
             x[j] = El<T>::pack2(a, b);
           }
-          l += sum[0] + sum[1];
+          float sum_a, sum_b;
+          unpack64(add2(sum2[0], sum2[1]), &sum_a, &sum_b);
+          l += sum_a + sum_b;
           tmem_st32(t_s, x);
           tmem_st32(t_s + 32, x + 32);
           tmem_st_wait();
@@ -515,11 +599,12 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int key = key0 + row_in;
           uint8_t* v_row = ring + slot * kTile + row_in * 128;
           if (key >= walk.seq.keys) {
-#pragma unroll
+#pragma unroll 4
             for (int j = 0; j < kChunks * 8; ++j) *reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
           } else if (key >= walk.seq.ctx) {
             constexpr uint32_t kInf = El<T>::kBf16 ? 0x7F80u : 0x7C00u;
             bool found = false;
+#pragma unroll 1
             for (int j = 0; j < kChunks * 8; ++j) {
               uint4* at_v = reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16);
               uint4 v = *at_v;
@@ -576,6 +661,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const int64_t at = slot * 128 * p.q_tiles + r;
         T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head;
         float* part = p.partial + at * HD;
+#pragma unroll 1
         for (int j = from_col; j < to_col; j += 32) {
           uint32_t a[32];
           tmem_ld32p(t_o + (pair ? s * 128 : 0) + j, a);
@@ -660,18 +746,21 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
   griddep_wait();
   const int cut = blockIdx.x + 1;
   const int ctas = p.meta[0].ctas;
-  if (cut >= ctas) return;
   const TreeMeta m = p.meta[cut];
-  if (m.from <= m.begin || p.meta[cut - 1].from > m.begin) return;
+  const int64_t from_before = p.meta[cut - 1].from;
+  if (cut >= ctas || m.from <= m.begin || from_before > m.begin) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
   if (r >= m.rows) return;
-  // the last CTA with a unit of the item
+  // the CTAs with the item's first tile and with its last: those between them
+  // have some too
+  const int lead = static_cast<int>(((m.begin + kTreeFixed + 1) * ctas + m.total - 1) / m.total) - 1;
   const int last = static_cast<int>((m.end * ctas + m.total - 1) / m.total) - 1;
+  if (lead == last) return;
   const int64_t stride = static_cast<int64_t>(128) * p.q_tiles;
-  auto row_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == cut - 1 ? 1 : 0)) * stride + r; };
+  auto row_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * stride + r; };
   float top = -CUDART_INF_F;
-  for (int c = cut - 1 + lane; c <= last; c += 32) top = fmaxf(top, p.partial_ml[row_of(c) * 2]);
+  for (int c = lead + lane; c <= last; c += 32) top = fmaxf(top, p.partial_ml[row_of(c) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -CUDART_INF_F ? 0.0f : top;
@@ -679,7 +768,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
 #pragma unroll
   for (int i = 0; i < V; ++i) y[i] = 0.0f;
 #pragma unroll 4
-  for (int c = cut - 1; c <= last; ++c) {
+  for (int c = lead; c <= last; ++c) {
     const int64_t row = row_of(c);
     const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + row * 2);
     const float f = tree_ex2(ml.x - ref);
