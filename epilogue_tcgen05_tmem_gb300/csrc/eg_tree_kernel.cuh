@@ -68,6 +68,29 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// The products with an accumulator that is added to (the predicate is a
+// constant here: no instruction for it).
+__device__ __forceinline__ void umma_f16_add(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+__device__ __forceinline__ void umma_f16_ts_add(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc)
+      : "memory");
+}
+
 // Two float32 lanes in one instruction.
 __device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
   uint64_t v;
@@ -316,6 +339,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   };
 
+  // The whole warp goes on or gives up.
+  auto wait_all = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
+
   // Registers from the four warps that need few to the two warpgroups that
   // hold a row of 128 scores a thread: 4 x 32 x 88 + 8 x 32 x 208 is what the
   // block was launched with (384 x 168).
@@ -340,7 +366,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       };
       auto issue = [&](const CUtensorMap* map, bool has, int page, int off) {
         const uint32_t slot = pos % stages;
-        if (!__all_sync(0xffffffffu, wait(&sh.empty[slot], pos / stages + 1))) return false;
+        if (!wait_all(&sh.empty[slot], pos / stages + 1)) return false;
         ++pos;
         const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, has)) * p.box_rows * 128u * kChunks;
         if (p.stall) return true;
@@ -374,62 +400,84 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     }
   } else if (warp == 9) {
     // --------------------------------------------------------- issuer ----
-    if (lane == 0) {
-      constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
-      constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
-      uint32_t base = 0, segment = 0, used = 0;  // loads, segments and tiles given to warpgroup 0 and 1 (16 bits each) so far
-      const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
-      const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
-      bool ok = true;
-      while (ok && walk.next(p)) {
-        const uint32_t count = walk.count;
-        const bool pair = walk.rows > 128;
-        const uint32_t shift = pair ? 1 : 0, jobs = count << shift;
-        if (!(ok = wait(&sh.q_full, segment))) break;
-        // job j is warpgroup j & 1's next tile; the scores of two jobs run
-        // ahead of the weighted sums
-        for (uint32_t j = 0; ok && j < jobs + 2; ++j) {
-          if (j >= 2) {
-            // O += P V of job j - 2
-            const uint32_t s = j & 1, i = (j - 2) >> shift;
-            const uint32_t at = base + tree_pos_v(i, count), slot = at % stages;
-            const uint32_t tiles = s ? used >> 16 : used & 0xFFFFu;
-            ok = ((pair && s) || wait(&sh.full[slot], at / stages)) && wait(&sh.p_ready[s], tiles);
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t v = v_desc + (slot * kTile >> 4);
-            const uint32_t first = i == 0 || (!pair && i == 1) ? 0 : 1;
+    // The whole warp walks, so that addresses stay in uniform registers; one
+    // elected lane issues.  What the tensor cores wait for most is this
+    // warp: positions in the ring are stepped, not divided out.
+    constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
+    constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
+    const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
+    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
+    uint32_t segment = 0, used0 = 0, used1 = 0;  // segments, and tiles given to each warpgroup
+    uint32_t slot0 = 0, turn0 = 0;               // the segment's first place in the ring, and how often the ring was full
+    auto step = [&](uint32_t& slot, uint32_t& turn, uint32_t by) {
+      slot += by;
+      if (slot >= stages) slot -= stages, ++turn;
+    };
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const uint32_t count = walk.count;
+      const bool pair = walk.rows > 128;
+      const uint32_t jobs = pair ? 2 * count : count;
+      uint32_t slot_k = slot0, turn_k = turn0, slot_v = slot0, turn_v = turn0;
+      step(slot_v, turn_v, count == 1 ? 1 : 2);
+      if (!(ok = wait_all(&sh.q_full, segment))) break;
+      // job j is warpgroup j & 1's next tile; the scores of two jobs run
+      // ahead of the weighted sums
+      for (uint32_t j = 0; j < jobs + 2; ++j) {
+        const uint32_t s = j & 1;
+        const bool first_use = !pair || s == 0, last_use = !pair || s == 1;
+        if (j >= 2) {
+          // O += P V of job j - 2
+          if (first_use && !(ok = wait_all(&sh.full[slot_v], turn_v))) break;
+          if (!(ok = wait_all(&sh.p_ready[s], s ? used1 : used0))) break;
+          tc_fence_after();
+          const uint64_t v = v_desc + (slot_v * kTile >> 4);
+          const uint32_t o = tmem + 256 + s * 128, w = tmem + s * 128;
+          if (elect_one()) {
+            umma_f16_ts(o, w, v, kIdescO, j >= 4 ? 1 : 0);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              umma_f16_ts(tmem + 256 + s * 128, tmem + s * 128 + k * 8, v + k * (2048 >> 4), kIdescO, k > 0 ? 1 : first);
+            for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2048 >> 4), kIdescO);
             umma_commit(&sh.o_done[s]);
-            if (!pair || s) umma_commit(&sh.empty[slot]);
-            used = s ? used + 0x10000u : (used & 0xFFFF0000u) | ((used + 1) & 0xFFFFu);
+            if (last_use) umma_commit(&sh.empty[slot_v]);
           }
-          if (j < jobs) {
-            // S of job j
-            const uint32_t s = j & 1, i = j >> shift;
-            const uint32_t at = base + tree_pos_k(i), slot = at % stages;
-            if (!(pair && s) && !(ok = wait(&sh.full[slot], at / stages))) break;
-            tc_fence_after();
-            const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0), key = k_desc + (slot * kTile >> 4);
-#pragma unroll
-            for (int k = 0; k < HD / 16; ++k) {
-              const uint32_t step = ((k / 4) * kPart + (k % 4) * 32) >> 4;
-              umma_f16(tmem + s * 128, q + step, key + step, kIdescS, k > 0);
-            }
-            umma_commit(&sh.s_full[s]);
-            if (!pair || s) umma_commit(&sh.empty[slot]);
-            if (j + 1 == jobs) umma_commit(&sh.q_empty);
+          if (s) ++used1;
+          else ++used0;
+          // V of tile i is 2 i + 2 places on, the last one directly after the one before
+          if (last_use) {
+            const uint32_t i = pair ? (j - 2) >> 1 : j - 2;
+            step(slot_v, turn_v, i + 2 == count ? 1 : 2);
           }
         }
-        base += 2 * count;
-        ++segment;
+        if (j < jobs) {
+          // S of job j
+          if (first_use && !(ok = wait_all(&sh.full[slot_k], turn_k))) break;
+          tc_fence_after();
+          const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0), key = k_desc + (slot_k * kTile >> 4);
+          const uint32_t d = tmem + s * 128;
+          if (elect_one()) {
+            umma_f16(d, q, key, kIdescS, 0);
+#pragma unroll
+            for (int k = 1; k < HD / 16; ++k) {
+              const uint32_t at = ((k / 4) * kPart + (k % 4) * 32) >> 4;
+              umma_f16_add(d, q + at, key + at, kIdescS);
+            }
+            umma_commit(&sh.s_full[s]);
+            if (last_use) umma_commit(&sh.empty[slot_k]);
+            if (j + 1 == jobs) umma_commit(&sh.q_empty);
+          }
+          if (last_use) step(slot_k, turn_k, j < (pair ? 2 : 1) ? 1 : 2);
+        }
       }
-      // products in flight have to end before tensor memory is freed
-      umma_commit(&sh.drained);
-      if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
+      // the segment took 2 count places
+      uint32_t places = 2 * count;
+      turn0 += places / stages;
+      step(slot0, turn0, places % stages);
+      ++segment;
     }
+    // products in flight have to end before tensor memory is freed
+    if (elect_one()) umma_commit(&sh.drained);
+    __syncwarp();
+    if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
   } else {
     // -------------------------------------------------------- queries ----
     const int at = tid - 320;  // 0..63
@@ -479,8 +527,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint32_t base = 0, uses = 0, exchanges = 0;
     int32_t segment = 0;
     bool ok = true;
-    // the whole warp goes on or gives up
-    auto wait_all = [&](uint64_t* bar, uint32_t phase) { return __all_sync(0xffffffffu, wait(bar, phase)) != 0; };
     while (ok && walk.next(p)) {
       ++segment;
       const bool pair = walk.rows > 128;
