@@ -217,7 +217,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(plan->grid - 1), static_cast<unsigned>((rows_of(*plan) + 7) / 8));
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(static_cast<unsigned>(plan->hd * 2));
   cfg.dynamicSmemBytes = 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;

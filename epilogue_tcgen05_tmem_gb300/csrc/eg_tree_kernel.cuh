@@ -241,7 +241,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // thread has one; else a pass for the total and one to find the place.
   const bool once = p.batch <= kTreeThreads;
   int64_t mine = 0;
-  for (int b = tid; b < p.batch; b += kTreeThreads) mine += tree_units(p, tree_seq(p, b));
+  TreeSeq seq{};
+  for (int b = tid; b < p.batch; b += kTreeThreads) {
+    seq = tree_seq(p, b);
+    mine += tree_units(p, seq);
+  }
   int64_t upto = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -299,6 +303,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (before > from) break;  // the same for every thread
     }
   }
+  __syncthreads();
+  const int near_b = sh.b;
+  if (once ? tid >= near_b && tid < min(near_b + kTreeNear, p.batch) : tid < kTreeNear && near_b + tid < p.batch) {
+    if (!once) seq = tree_seq(p, near_b + tid);
+    int32_t* at = sh.near_[once ? tid - near_b : tid];
+    at[0] = seq.start, at[1] = seq.n, at[2] = seq.ctx;
+  }
   if (warp == 8) tmem_alloc(&sh.tmem, 512);
   if (p.head_dim < HD) {  // columns past head_dim: keys are zero there, so are queries
     for (uint32_t i = tid; i < p.q_tiles * kTile / 16; i += kTreeThreads) reinterpret_cast<uint4*>(q_smem)[i] = make_uint4(0, 0, 0, 0);
@@ -308,15 +319,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  if (tid < kTreeNear && sh.b + tid < p.batch) {
-    const TreeSeq q = tree_seq(p, sh.b + tid);
-    sh.near_[tid][0] = q.start, sh.near_[tid][1] = q.n, sh.near_[tid][2] = q.ctx;
-  }
-  __syncthreads();
 
   TreeWalk walk;
-  walk.b = sh.b, walk.before = sh.before, walk.at = from, walk.to = to;
-  walk.near_ = sh.near_, walk.near_b = sh.b;
+  walk.b = near_b, walk.before = sh.before, walk.at = from, walk.to = to;
+  walk.near_ = sh.near_, walk.near_b = near_b;
   walk.load(p);
 
   // Bounded wait: false once any wait of the CTA has run past its limit.
@@ -503,10 +509,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (at < step * vecs) {
         const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(walk.head) * p.group * p.q_head + c * 8;
         const uint32_t to_ = (c >> 3) * kPart;
-        for (int r = at / vecs; r < walk.rows; r += step) {
-          const uint32_t row = static_cast<uint32_t>(walk.row0 + r), t = row / static_cast<uint32_t>(p.group), g = row - t * p.group;
+        const int r0 = at / vecs;
+        int t = (walk.row0 + r0) / p.group, g = walk.row0 + r0 - t * p.group;
+        src += static_cast<int64_t>(walk.seq.start + t) * p.q_token;
+        for (int r = r0; r < walk.rows; r += step) {
           cp_async_16(q_smem + to_ + (r >> 7) * kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                      src + static_cast<int64_t>(walk.seq.start + t) * p.q_token + static_cast<int64_t>(g) * p.q_head, 16);
+                      src + static_cast<int64_t>(g) * p.q_head, 16);
+          for (g += step; g >= p.group; g -= p.group) src += p.q_token;
         }
       }
       cp_async_commit();
@@ -705,8 +714,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const float scale = whole ? (weight == 0.0f ? 0.0f : 1.0f / weight) : 1.0f;
         const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (walk.first == 0 ? 1 : 0);
         const int64_t at = slot * 128 * p.q_tiles + r;
+        const int part_rows = 128 * p.q_tiles;
         T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head;
-        float* part = p.partial + at * HD;
+        // [slot][4 columns][row][column]: a warp's rows are stored side by side
+        float* part = p.partial + slot * part_rows * HD + r * 4;
 #pragma unroll 1
         for (int j = from_col; j < to_col; j += 32) {
           uint32_t a[32];
@@ -735,8 +746,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               out.set(y);
               out.store(o + j + k);
             } else {
-              *reinterpret_cast<float4*>(part + j + k) = make_float4(y[0], y[1], y[2], y[3]);
-              *reinterpret_cast<float4*>(part + j + k + 4) = make_float4(y[4], y[5], y[6], y[7]);
+              *reinterpret_cast<float4*>(part + static_cast<int64_t>(j + k) * part_rows) = make_float4(y[0], y[1], y[2], y[3]);
+              *reinterpret_cast<float4*>(part + static_cast<int64_t>(j + k + 4) * part_rows) = make_float4(y[4], y[5], y[6], y[7]);
             }
           }
         }
@@ -758,7 +769,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
               const float x = El<T>::to_float(v[e]);
               if (fabsf(x) < CUDART_INF_F) continue;
               if (whole) o[e] = El<T>::from_float(El<T>::to_float(o[e]) + x);
-              else part[e] += x;
+              else part[static_cast<int64_t>(e & ~3) * part_rows + (e & 3)] += x;
             }
           }
         }
@@ -784,66 +795,53 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
 
 // Joins the partial results of the items that a cut between CTAs divides: the
 // blocks of cut x (between CTAs x - 1 and x) serve the item whose first cut it
-// is; a warp takes one row.
+// is, eight rows each.  A thread has four columns of a row; a warp has eight
+// rows of 16 columns, which is how they lie side by side.
 template <typename T, int HD>
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
   constexpr float kShift = El<T>::kBf16 ? 0.0f : 7.0f;
-  constexpr int V = HD / 32;  // columns of a lane
   griddep_wait();
   const int cut = blockIdx.x + 1;
   const int ctas = p.meta[0].ctas;
   const TreeMeta m = p.meta[cut];
   const int64_t from_before = p.meta[cut - 1].from;
   if (cut >= ctas || m.from <= m.begin || from_before > m.begin) return;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  if (r >= m.rows) return;
   // the CTAs with the item's first tile and with its last: those between them
   // have some too
   const int lead = static_cast<int>(((m.begin + kTreeFixed + 1) * ctas + m.total - 1) / m.total) - 1;
   const int last = static_cast<int>((m.end * ctas + m.total - 1) / m.total) - 1;
   if (lead == last) return;
-  const int64_t stride = static_cast<int64_t>(128) * p.q_tiles;
-  auto row_of = [&](int c) { return (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * stride + r; };
-  float top = -CUDART_INF_F;
-  for (int c = lead + lane; c <= last; c += 32) top = fmaxf(top, p.partial_ml[row_of(c) * 2]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  const float ref = top == -CUDART_INF_F ? 0.0f : top;
-  float y[V], weight = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) y[i] = 0.0f;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 8 + (lane & 7), col = ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4;
+  if (r >= m.rows) return;
+  const int64_t rows = static_cast<int64_t>(128) * p.q_tiles;
+  const float2* ml = reinterpret_cast<const float2*>(p.partial_ml) + r;
+  const float* part = p.partial + static_cast<int64_t>(col) * rows + r * 4;
+  // both to the reference of the largest maximum so far
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float top = -CUDART_INF_F, weight = 0.0f;
 #pragma unroll 4
   for (int c = lead; c <= last; ++c) {
-    const int64_t row = row_of(c);
-    const float2 ml = *reinterpret_cast<const float2*>(p.partial_ml + row * 2);
-    const float f = tree_ex2(ml.x - ref);
-    float x[V];
-    if constexpr (V == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p.partial + row * HD + lane * 4);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(p.partial + row * HD + lane * 2);
-      x[0] = v.x, x[1] = v.y;
-    }
-    weight = fmaf(ml.y, f, weight);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (ml.y != 0.0f) y[i] = fmaf(x[i], f, y[i]);
+    const int64_t slot = (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * rows;
+    const float2 w = ml[slot];
+    const float4 x = *reinterpret_cast<const float4*>(part + slot * HD);
+    const float next = fmaxf(top, w.x);
+    const float ref = next == -CUDART_INF_F ? 0.0f : next;
+    const float f_old = tree_ex2(top - ref), f = tree_ex2(w.x - ref);
+    top = next;
+    weight = weight * f_old + w.y * f;
+    y.x *= f_old, y.y *= f_old, y.z *= f_old, y.w *= f_old;
+    if (w.y != 0.0f) y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
   }
   const int t = (m.row0 + r) / p.group;
   const int64_t packed = m.start + t;
   const int head = m.head * p.group + (m.row0 + r) - t * p.group;
   const float scale = weight == 0.0f ? 0.0f : 1.0f / weight;
-  T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head;
-  if (lane * V < p.head_dim) {
-    if constexpr (V == 4) {
-      *reinterpret_cast<uint2*>(o + lane * 4) = make_uint2(El<T>::pack2(y[0] * scale, y[1] * scale), El<T>::pack2(y[2] * scale, y[3] * scale));
-    } else {
-      *reinterpret_cast<uint32_t*>(o + lane * 2) = El<T>::pack2(y[0] * scale, y[1] * scale);
-    }
+  if (col < p.head_dim) {
+    T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head + col;
+    *reinterpret_cast<uint2*>(o) = make_uint2(El<T>::pack2(y.x * scale, y.y * scale), El<T>::pack2(y.z * scale, y.w * scale));
   }
-  if (p.lse && lane == 0)
+  if (p.lse && col == 0)
     p.lse[packed * p.q_heads + head] = weight == 0.0f ? -CUDART_INF_F : (top - kShift + __log2f(weight)) * 0.6931471805599453f;
 }
 
