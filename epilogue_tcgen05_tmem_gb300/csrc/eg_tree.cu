@@ -14,6 +14,14 @@ namespace eg {
 
 namespace {
 
+// Rows of one box of queries: the fewest tokens whose heads (`group` each) make
+// a multiple of 8 rows, the unit of the shared-memory swizzle.
+int row_box(int group) {
+  int box = group;
+  while (box % 8) box += group;
+  return box;
+}
+
 bool multiple16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 }  // namespace
@@ -24,7 +32,7 @@ using namespace eg;
 struct eg_tree_plan {
   eg_tree_problem prob{};
   int device = -1;
-  int hd = 0, q_tiles = 0, stages = 0, grid = 0;
+  int hd = 0, tile_rows = 0, q_tiles = 0, stages = 0, grid = 0;
   uint32_t smem = 0;
   size_t ws_bytes = 0;
   uint8_t* ws = nullptr;  // partial sums, their statistics, the CTAs' ranges, the status word
@@ -42,6 +50,8 @@ eg_status check_problem(const eg_tree_problem* p) {
   if (p->q_heads < 1 || p->kv_heads < 1 || p->q_heads % p->kv_heads)
     return host_fail(EG_ERR_INVALID_ARG, "q_heads=%d must be a positive multiple of kv_heads=%d", p->q_heads, p->kv_heads);
   if (p->q_heads > 1024) return host_fail(EG_ERR_UNSUPPORTED, "at most 1024 query heads (got %d)", p->q_heads);
+  if (row_box(p->q_heads / p->kv_heads) > 128)
+    return host_fail(EG_ERR_UNSUPPORTED, "%d query heads for each cached head do not fit a tile of 128 rows in groups of 8 rows", p->q_heads / p->kv_heads);
   if (p->head_dim < 8 || p->head_dim > 128 || p->head_dim % 8)
     return host_fail(EG_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 in 8..128 (got %d)", p->head_dim);
   if (p->page_size < 8 || p->page_size % 8 || p->page_size > 65536)
@@ -62,8 +72,9 @@ eg_status check_run(const eg_tree_plan* plan, const eg_tree_args* a, const eg_kv
   if (a->batch == 0 || a->tokens == 0) return EG_OK;
   if (!a->q || !a->o || !multiple16(a->q) || !multiple16(a->o))
     return host_fail(EG_ERR_INVALID_ARG, "q or o is NULL or not 16-byte aligned");
-  for (int64_t s : {a->q_token, a->q_head, a->o_token, a->o_head})
-    if (s < 0 || s % 8) return host_fail(EG_ERR_INVALID_ARG, "the strides of q and o must be multiples of 8 elements");
+  // the stride of a dimension of one is not used
+  for (int64_t s : {a->tokens > 1 ? a->q_token : 8, p.q_heads > 1 ? a->q_head : 8, a->tokens > 1 ? a->o_token : 8, p.q_heads > 1 ? a->o_head : 8})
+    if (s < 8 || s % 8) return host_fail(EG_ERR_INVALID_ARG, "the strides of q and o must be positive multiples of 8 elements");
   if (!a->block_table || !a->context_lens || !a->q_start) return host_fail(EG_ERR_INVALID_ARG, "block_table, context_lens or q_start is NULL");
   for (const void* x : {static_cast<const void*>(a->block_table), static_cast<const void*>(a->context_lens),
                         static_cast<const void*>(a->q_start), static_cast<const void*>(a->mask), static_cast<const void*>(a->lse)})
@@ -105,7 +116,23 @@ eg_status encode_cache(const eg_tree_problem& p, const eg_kv_cache& c, const voi
   return EG_OK;
 }
 
-using TreeKernel = void (*)(TreeParams, CUtensorMap, CUtensorMap);
+// The tensor map of queries: columns, heads, packed tokens; boxes of 64
+// columns by the heads of one cached head by `box_tokens` tokens.
+eg_status encode_queries(const eg_tree_problem& p, const eg_tree_args& a, int box_tokens, CUtensorMap* map) {
+  EncodeTiledFn fn = host_encode_tiled();
+  if (!fn) return host_fail(EG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(p.head_dim), static_cast<cuuint64_t>(p.q_heads), static_cast<cuuint64_t>(a.tokens)};
+  const cuuint64_t strides[2] = {p.q_heads > 1 ? static_cast<cuuint64_t>(a.q_head) * 2 : 16, a.tokens > 1 ? static_cast<cuuint64_t>(a.q_token) * 2 : 16};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.q_heads / p.kv_heads), static_cast<cuuint32_t>(box_tokens)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = fn(map, p.dtype == EG_EL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+                        const_cast<void*>(a.q), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return host_fail(EG_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for the queries", static_cast<int>(r));
+  return EG_OK;
+}
+
+using TreeKernel = void (*)(TreeParams, CUtensorMap, CUtensorMap, CUtensorMap);
 using JoinKernel = void (*)(TreeParams);
 
 TreeKernel main_kernel(const eg_tree_plan& pl) {
@@ -118,7 +145,7 @@ JoinKernel join_kernel(const eg_tree_plan& pl) {
 }
 
 int rows_of(const eg_tree_plan& pl) {
-  return std::min(128 * pl.q_tiles, pl.prob.max_tree * (pl.prob.q_heads / pl.prob.kv_heads));
+  return std::min(pl.tile_rows * pl.q_tiles, pl.prob.max_tree * (pl.prob.q_heads / pl.prob.kv_heads));
 }
 
 eg_status set_up(eg_tree_plan* pl) {
@@ -127,8 +154,10 @@ eg_status set_up(eg_tree_plan* pl) {
   if (e != cudaSuccess) return host_cuda_fail(e, "device query");
   const eg_tree_problem& p = pl->prob;
   pl->hd = p.head_dim <= 64 ? 64 : 128;
-  // 256 rows of an item share each key tile where a tree can have more than 128
-  pl->q_tiles = p.max_tree * (p.q_heads / p.kv_heads) > 128 ? 2 : 1;
+  const int group = p.q_heads / p.kv_heads;
+  pl->tile_rows = 128 / row_box(group) * row_box(group);
+  // two tiles of rows share each key tile where a tree can have more than one
+  pl->q_tiles = p.max_tree * group > pl->tile_rows ? 2 : 1;
   const uint32_t tile = pl->hd == 64 ? TreeSmem<64>::kTileBytes : TreeSmem<128>::kTileBytes;
   const uint32_t extra = TreeSmem<64>::kExtra;
   pl->stages = std::min<int>(12, static_cast<int>((232448u - extra) / tile) - pl->q_tiles);
@@ -191,6 +220,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   p.box_rows = std::min(128, b.page_size & -b.page_size);
   p.heads_inner = b.kv_heads > 1 && cache->head_stride < cache->token_stride ? 1 : 0;
   p.q_tiles = plan->q_tiles, p.stages = plan->stages;
+  p.box_tokens = row_box(p.group) / p.group, p.tile_rows = plan->tile_rows, p.item_rows = plan->tile_rows * plan->q_tiles;
   p.batch = a.batch, p.tokens = a.tokens;
   p.q = a.q, p.o = a.o, p.q_token = a.q_token, p.q_head = a.q_head, p.o_token = a.o_token, p.o_head = a.o_head;
   p.block_table = a.block_table, p.table_stride = a.table_stride, p.context_lens = a.context_lens, p.q_start = a.q_start;
@@ -202,7 +232,8 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   p.meta = reinterpret_cast<TreeMeta*>(plan->ws + plan->meta_at);
   p.status = reinterpret_cast<int32_t*>(plan->ws + plan->status_at);
   p.wait_limit_ns = plan->wait_limit_ns, p.stall = plan->stall;
-  CUtensorMap map_k, map_v;
+  CUtensorMap map_q, map_k, map_v;
+  if ((s = encode_queries(b, a, p.box_tokens, &map_q)) != EG_OK) return s;
   if ((s = encode_cache(b, *cache, cache->k, p.box_rows, p.heads_inner != 0, &map_k)) != EG_OK) return s;
   if ((s = encode_cache(b, *cache, cache->v, p.box_rows, p.heads_inner != 0, &map_v)) != EG_OK) return s;
 
@@ -211,7 +242,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   cfg.blockDim = dim3(kTreeThreads);
   cfg.dynamicSmemBytes = plan->smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan), p, map_k, map_v);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan), p, map_q, map_k, map_v);
   if (e != cudaSuccess) return host_cuda_fail(e, "launching tree attention");
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

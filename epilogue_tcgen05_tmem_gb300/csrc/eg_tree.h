@@ -25,7 +25,10 @@ struct TreeParams {
   int32_t q_heads, kv_heads, group, head_dim, page_size, max_tree;
   int32_t box_rows;     // keys of one TMA box: the power of two that divides page_size, at most 128
   int32_t heads_inner;  // the tensor maps' second dimension is the head, not the token
-  int32_t q_tiles;      // 128-row tiles of one item: 1 or 2
+  int32_t q_tiles;      // tiles of 128 rows that one item has room for: 1 or 2
+  int32_t box_tokens;   // tokens of one TMA box of queries: with their heads a multiple of 8 rows
+  int32_t tile_rows;    // rows of a tile that are used: whole boxes, at most 128
+  int32_t item_rows;    // tile_rows * q_tiles
   int32_t stages;
   // the run
   int32_t batch, tokens;

@@ -45,6 +45,15 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+// 3-D tiled bulk-tensor load global -> shared.
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
 // Matrix descriptor of an operand whose M or N index is the contiguous one,
 // in 128-byte swizzled rows: 64 columns of 8 keys are 1024 bytes, the next 8
 // keys follow (stride byte offset), the next 64 columns are `next` bytes on
@@ -132,7 +141,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int32_t start, 
   s.start = start, s.n = n, s.ctx = ctx;
   s.keys = min(ctx + n, room);
   s.tiles = (s.keys + static_cast<int32_t>(kTreeKeys) - 1) >> 7;
-  s.groups = (n * p.group + 128 * p.q_tiles - 1) >> (6 + p.q_tiles);
+  s.groups = (n * p.group + p.item_rows - 1) / p.item_rows;
   return s;
 }
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
@@ -143,7 +152,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 }
 // Units of one item: its key tiles, and kTreeFixed for what an item costs
 // beside them (queries, the first and the last tile's latency, the result).
-constexpr int32_t kTreeFixed = 2;
+constexpr int32_t kTreeFixed = 4;
 __device__ __forceinline__ int32_t tree_item_units(const TreeSeq& s) { return s.tiles + kTreeFixed; }
 __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& s) {
   return static_cast<int64_t>(tree_item_units(s)) * (s.groups * p.kv_heads);
@@ -189,8 +198,8 @@ struct TreeWalk {
       count = in + take - kTreeFixed - first;
       if (count <= 0) continue;
       head = item / seq.groups;
-      row0 = (item - head * seq.groups) << (6 + p.q_tiles);
-      rows = min(seq.n * p.group - row0, 64 << p.q_tiles);
+      row0 = (item - head * seq.groups) * p.item_rows;
+      rows = min(seq.n * p.group - row0, p.item_rows);
       return true;
     }
   }
@@ -219,7 +228,8 @@ __device__ __forceinline__ uint32_t tree_pos_v(uint32_t i, uint32_t count) { ret
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1)
-    tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+    tree_kernel(const TreeParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v) {
   constexpr uint32_t kTile = TreeSmem<HD>::kTileBytes;
   constexpr int kChunks = HD / 64;           // 64-column parts of a tile, 16 KB each
   constexpr uint32_t kPart = 128u * 128u;    // bytes of one part
@@ -256,7 +266,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_done[i], 1);
-    mbar_init(&sh.q_full, 64);
+    mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.exchange, 256);
     mbar_init(&sh.drained, 1);
@@ -311,10 +321,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     at[0] = seq.start, at[1] = seq.n, at[2] = seq.ctx;
   }
   if (warp == 8) tmem_alloc(&sh.tmem, 512);
-  if (p.head_dim < HD) {  // columns past head_dim: keys are zero there, so are queries
-    for (uint32_t i = tid; i < p.q_tiles * kTile / 16; i += kTreeThreads) reinterpret_cast<uint4*>(q_smem)[i] = make_uint4(0, 0, 0, 0);
-    fence_proxy_async_smem();
-  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     bool ok = true;
     while (ok && walk.next(p)) {
       const uint32_t count = walk.count;
-      const bool pair = walk.rows > 128;
+      const bool pair = walk.rows > p.tile_rows;
       const uint32_t jobs = pair ? 2 * count : count;
       uint32_t slot_k = slot0, turn_k = turn0, slot_v = slot0, turn_v = turn0;
       step(slot_v, turn_v, count == 1 ? 1 : 2);
@@ -486,12 +492,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
   } else {
     // -------------------------------------------------------- queries ----
-    const int at = tid - 320;  // 0..63
-    const int vecs = p.head_dim >> 3;
-    // thread at takes 16-byte column c of rows r, r + step, ...
-    const int step = 64 / vecs, c = at % vecs;
-    uint32_t segment = 0;
-    if (at == 63) {
+    if (tid == kTreeThreads - 1) {
       // what the joining kernel has to know of this CTA's first item
       TreeMeta m;
       m.from = from;
@@ -500,29 +501,30 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       m.begin = from - idx % each, m.end = m.begin + each, m.total = total;
       m.ctas = ctas;
       const int32_t item = static_cast<int32_t>(idx / each), head = item / walk.seq.groups;
-      m.start = walk.seq.start, m.row0 = (item - head * walk.seq.groups) << (6 + p.q_tiles), m.head = head;
-      m.rows = min(walk.seq.n * p.group - m.row0, 64 << p.q_tiles), m.pad = 0;
+      m.start = walk.seq.start, m.row0 = (item - head * walk.seq.groups) * p.item_rows, m.head = head;
+      m.rows = min(walk.seq.n * p.group - m.row0, p.item_rows), m.pad = 0;
       p.meta[blockIdx.x] = m;
     }
-    while (walk.next(p)) {
-      if (!wait(&sh.q_empty, segment + 1)) break;
-      if (at < step * vecs) {
-        const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(walk.head) * p.group * p.q_head + c * 8;
-        const uint32_t to_ = (c >> 3) * kPart;
-        const int r0 = at / vecs;
-        int t = (walk.row0 + r0) / p.group, g = walk.row0 + r0 - t * p.group;
-        src += static_cast<int64_t>(walk.seq.start + t) * p.q_token;
-        for (int r = r0; r < walk.rows; r += step) {
-          cp_async_16(q_smem + to_ + (r >> 7) * kTile + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                      src + static_cast<int64_t>(g) * p.q_head, 16);
-          for (g += step; g >= p.group; g -= p.group) src += p.q_token;
+    if (warp == 10) {
+      // a box is `box_tokens` tokens by the heads that share a cached one;
+      // lane i has box i of each tile
+      uint32_t segment = 0;
+      const int box = p.box_tokens * p.group, boxes = p.tile_rows / box;
+      while (walk.next(p)) {
+        if (!wait_all(&sh.q_empty, segment + 1)) break;
+        const int all = (walk.rows + box - 1) / box;  // boxes that hold a row
+        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, all * box * 128u * kChunks);
+        __syncwarp();
+        for (int i = lane; i < all; i += 32) {
+          const int tile = i >= boxes ? 1 : 0, in = i - tile * boxes;
+#pragma unroll
+          for (int c = 0; c < kChunks; ++c)
+            tma_load_3d(smem_u32(q_smem) + tile * kTile + c * kPart + in * box * 128u, &map_q, &sh.q_full, c * 64, walk.head * p.group,
+                        walk.seq.start + walk.row0 / p.group + i * p.box_tokens);
         }
+        ++segment;
       }
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.q_full);
-      ++segment;
+      if (segment > 0) mbar_wait(&sh.q_full, (segment - 1) & 1, p.wait_limit_ns);  // leaves no copy in flight behind
     }
   }
   } else {
@@ -538,11 +540,11 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     bool ok = true;
     while (ok && walk.next(p)) {
       ++segment;
-      const bool pair = walk.rows > 128;
+      const bool pair = walk.rows > p.tile_rows;
       const int count = walk.count;
-      const int r = (pair ? s * 128 : 0) + row_in;
-      const bool valid = r < walk.rows;
-      const bool busy = (pair ? s * 128 : 0) + (warp & 3) * 32 < walk.rows;  // the warp has a row
+      const int r = (pair ? s * p.tile_rows : 0) + row_in;
+      const bool valid = row_in < p.tile_rows && r < walk.rows;
+      const bool busy = __any_sync(0xffffffffu, valid);  // the warp has a row
       const int t = (walk.row0 + r) / p.group;
       const int64_t packed = walk.seq.start + t;
       const int head = walk.head * p.group + (walk.row0 + r) - t * p.group;
