@@ -24,12 +24,11 @@ namespace eg {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;        // 16-byte loads of a thread in flight
 constexpr int kMostTop = 32;
-constexpr int kKept = 1024;       // room for candidates between two selections
-constexpr int kSelectAt = 256;    // select once this many candidates wait
+constexpr int kWaiting = 2048;    // room for candidates between two selections
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -57,7 +56,10 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // row is far above it, and then the row is done again (see `plain_row`).
 // Its size keeps the rounding of m log2 e, which every y of a thread shares,
 // far below one.
+template <typename T>
 constexpr float kLowest = -65504.0f;
+template <>
+constexpr float kLowest<__nv_bfloat16> = -65536.0f;
 
 // The reference that a maximum stands for: rounded once, the same everywhere.
 __device__ __forceinline__ float reference(float m) { return __fmul_rn(m, kLog2e); }
@@ -99,11 +101,12 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 }
 
 struct TopShared {
-  uint64_t kept[kMostTop];   // the best so far, in order
-  uint64_t waiting[kKept];   // candidates not yet selected from
+  alignas(16) uint64_t waiting[kWaiting];  // candidates not yet selected from
+  alignas(16) uint64_t kept[2][kMostTop];  // the best so far, in order; 0: none
   uint64_t least;            // a value has to reach this to be a candidate
   int count;                 // candidates that asked for a place
-  float groups[kMostTop];
+  int lost;                  // some found none
+  uint64_t groups[kMostTop];
 };
 
 struct RowShared {
@@ -112,35 +115,30 @@ struct RowShared {
   TopShared top;
 };
 
-// The best `top` of kept and waiting into kept, in order; the next candidate
-// has to be better than the last of them.  All threads.
-__device__ __forceinline__ void select_top(TopShared& sh, int top) {
+// The best `top` of kept[cur] and waiting into kept[cur ^ 1], in order; the
+// next candidate has to be better than the last of them.  All threads; the
+// place of each is the number of better ones.
+__device__ __forceinline__ void select_top(TopShared& sh, int top, int& cur) {
   __syncthreads();
-  const int waiting = min(sh.count, kKept);
+  const int waiting = min(sh.count, kWaiting);
   const int total = waiting + top;
-  uint64_t mine[(kKept + kMostTop + kThreads - 1) / kThreads];
-  int rank[(kKept + kMostTop + kThreads - 1) / kThreads];
-#pragma unroll
-  for (int i = 0; i < (kKept + kMostTop + kThreads - 1) / kThreads; ++i) {
-    const int at = threadIdx.x + i * kThreads;
-    rank[i] = kMostTop;
-    if (at >= total) continue;
-    mine[i] = at < top ? sh.kept[at] : sh.waiting[at - top];
-    if (mine[i] == 0) continue;
+  for (int at = threadIdx.x; at < total; at += kThreads) {
+    const uint64_t mine = at < top ? sh.kept[cur][at] : sh.waiting[at - top];
+    if (mine == 0) continue;
     int better = 0;
-    for (int j = 0; j < top; ++j) better += sh.kept[j] > mine[i];
-    for (int j = 0; j < waiting; ++j) better += sh.waiting[j] > mine[i];
-    rank[i] = better;
+    for (int j = 0; j < top; ++j) better += sh.kept[cur][j] > mine;
+    int j = 0;
+    for (; j + 1 < waiting; j += 2) {
+      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh.waiting[j]);
+      better += (two.x > mine) + (two.y > mine);
+    }
+    if (j < waiting) better += sh.waiting[j] > mine;
+    if (better < top) sh.kept[cur ^ 1][better] = mine;
   }
-  __syncthreads();
-  if (threadIdx.x < top) sh.kept[threadIdx.x] = 0;
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < (kKept + kMostTop + kThreads - 1) / kThreads; ++i)
-    if (rank[i] < top) sh.kept[rank[i]] = mine[i];
+  cur ^= 1;
   __syncthreads();
   if (threadIdx.x == 0) {
-    const uint64_t last = sh.kept[top - 1];
+    const uint64_t last = sh.kept[cur][top - 1];
     if (last) sh.least = last + 1;
     sh.count = 0;
   }
@@ -149,7 +147,7 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top) {
 
 // The outputs of one row by one thread group of the CTA that holds the sums.
 __device__ __forceinline__ void write_row(const ScoreParams& p, int64_t row, float lse, float entropy, float token_logit,
-                                          bool given, bool nan_row, const TopShared* top) {
+                                          bool given, bool nan_row, const uint64_t* top) {
   const float nan = __int_as_float(0x7FC00000);
   const bool nothing = lse == -CUDART_INF_F;
   if (threadIdx.x == 0) {
@@ -158,7 +156,7 @@ __device__ __forceinline__ void write_row(const ScoreParams& p, int64_t row, flo
     if (p.logprob) p.logprob[row] = !given ? 0.0f : nothing ? -CUDART_INF_F : lse == CUDART_INF_F ? nan : token_logit - lse;
   }
   if (top && threadIdx.x < p.top) {
-    const uint64_t c = top->kept[threadIdx.x];
+    const uint64_t c = top[threadIdx.x];
     const int64_t at = row * p.top + threadIdx.x;
     if (p.top_ids) p.top_ids[at] = nan_row ? -1 : static_cast<int64_t>(candidate_id(c));
     if (p.top_logprobs)
@@ -232,13 +230,90 @@ __device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* lse, fl
   else *lse = m + logf(s), *entropy = logf(s) - t / s;
 }
 
-// One vector of 16 bytes as floats.
+// Elements of one vector of 16 bytes.
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p) {
+// Larger of two words' elements, or not a number where either is none.
+template <typename T>
+__device__ __forceinline__ uint32_t word_max(uint32_t a, uint32_t b) {
+  if constexpr (sizeof(T) == 4) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
+  } else if constexpr (El<T>::kBf16) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  } else {
+    const __half2 m = __hmax2_nan(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+}
+template <typename T>
+__device__ __forceinline__ float word_top(uint32_t w) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(w);
+  else {
+    const float2 f = El<T>::unpack2(w);
+    return max_nan(f.x, f.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t lowest_word() {
+  if constexpr (sizeof(T) == 4) return __float_as_uint(kLowest<T>);
+  else return El<T>::pack2(kLowest<T>, kLowest<T>);
+}
+
+// The part of a row that one CTA of its cluster has.
+template <typename T>
+struct Part {
+  const T* body;     // the row's first 16-byte boundary
+  int64_t head;      // values before it
+  int64_t from, to;  // vectors
+  float odd;         // a value outside whole vectors that this thread has
+  int64_t odd_id;    // -1: none
+};
+
+// The best of a part, when more candidates came between two selections than
+// there is room for (values that rise along the row, many equal ones): batch
+// by batch, with a selection whenever one fills the room.
+template <typename T>
+__device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int top, int* where) {
   constexpr int V = kVec<T>;
+  int cur = 0;
+  __syncthreads();
+  if (threadIdx.x < kMostTop) sh.kept[0][threadIdx.x] = sh.kept[1][threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.least = 1, sh.count = 0;
+  __syncthreads();
+  for (int64_t at = part.from; at < part.to || at == part.from; at += kThreads) {
+    const int64_t v = at + threadIdx.x;
+    bool again = false;
+    for (;;) {
+      const uint64_t least = sh.least;
+      bool lost = false;
+      auto offer = [&](float f, int64_t id) {
+        const uint64_t c = candidate(f, static_cast<uint32_t>(id));
+        if (c < least) return;
+        if (again)
+          for (int j = 0; j < top; ++j)
+            if (sh.kept[cur][j] == c) return;
+        const int place = atomicAdd(&sh.count, 1);
+        if (place < kWaiting) sh.waiting[place] = c;
+        else lost = true;
+      };
+      if (at == part.from && part.odd_id >= 0) offer(part.odd, part.odd_id);
+      if (v < part.to)
+        for (int i = 0; i < V; ++i) offer(El<T>::to_float(part.body[v * V + i]), part.head + v * V + i);
+      const bool more = __syncthreads_or(lost);
+      select_top(sh, top, cur);
+      if (!more) break;
+      again = true;
+    }
+  }
+  *where = cur;
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p) {
+  constexpr int V = kVec<T>;
+  constexpr int W = 4;  // words of a vector
   __shared__ RowShared sh;
   uint32_t ranks, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
@@ -246,26 +321,28 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p)
   const int64_t row = blockIdx.x / ranks;
   const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
   // values before the first 16-byte boundary, whole vectors, and the rest
-  const int64_t head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), p.vocab);
-  const int64_t vectors = (p.vocab - head) / V;
-  const int tail = static_cast<int>(p.vocab - head - vectors * V);
-  const int64_t from = vectors * rank / ranks, to = vectors * (rank + 1) / ranks;
-  const T* body = x + head;
-  constexpr float low = kLowest;
+  Part<T> part;
+  part.head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), p.vocab);
+  const int64_t vectors = (p.vocab - part.head) / V;
+  const int tail = static_cast<int>(p.vocab - part.head - vectors * V);
+  part.from = vectors * rank / ranks, part.to = vectors * (rank + 1) / ranks;
+  part.body = x + part.head;
+  constexpr float low = kLowest<T>;
   Sums acc{low, 0.0f, 0.0f};
+  int cur = 0;
   if (TOP) {
-    if (threadIdx.x < kMostTop) sh.top.kept[threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.top.least = 1, sh.top.count = 0;
+    if (threadIdx.x < kMostTop) sh.top.kept[0][threadIdx.x] = sh.top.kept[1][threadIdx.x] = 0;
+    if (threadIdx.x == 0) sh.top.least = 1, sh.top.count = 0, sh.top.lost = 0;
   }
 
   // the values outside whole vectors: the first and the last CTA of a row
-  float odd = -CUDART_INF_F;
-  int64_t odd_id = -1;
-  if (rank == 0 && threadIdx.x < head) odd_id = threadIdx.x;
-  if (rank == ranks - 1 && threadIdx.x >= 32 && threadIdx.x < 32 + tail) odd_id = head + vectors * V + threadIdx.x - 32;
-  if (odd_id >= 0) {
-    odd = El<T>::to_float(x[odd_id]);
-    const float c = max_nan(odd, low);
+  part.odd = -CUDART_INF_F;
+  part.odd_id = -1;
+  if (rank == 0 && threadIdx.x < part.head) part.odd_id = threadIdx.x;
+  if (rank == ranks - 1 && threadIdx.x >= 32 && threadIdx.x < 32 + tail) part.odd_id = part.head + vectors * V + threadIdx.x - 32;
+  if (part.odd_id >= 0) {
+    part.odd = El<T>::to_float(x[part.odd_id]);
+    const float c = max_nan(part.odd, low);
     const float y = fmaf(c, kLog2e, -reference(c));
     acc.m = c, acc.s = ex2(y), acc.t = acc.s * y;
   }
@@ -277,28 +354,104 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p)
       const int64_t v = at + u * kThreads + threadIdx.x;
       // past the end: -infinity, which adds nothing
       constexpr uint32_t n = kNothing<T>;
-      next[u] = v < to ? __ldcs(reinterpret_cast<const uint4*>(body) + v) : make_uint4(n, n, n, n);
+      next[u] = v < part.to ? __ldcs(reinterpret_cast<const uint4*>(part.body) + v) : make_uint4(n, n, n, n);
     }
   };
-  load(from);
-  bool first = true;
-  for (int64_t at = from; at < to || first; at += kUnroll * kThreads) {
-    Chunk<T, V> now[kUnroll];
+  load(part.from);
+  float bar = -CUDART_INF_F;  // a value below this is no candidate
+  uint32_t batch = 0;
+  for (int64_t at = part.from; at < part.to || batch == 0; at += kUnroll * kThreads, ++batch) {
+    uint32_t now[kUnroll][W];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u].w[0] = next[u].x, now[u].w[1] = next[u].y, now[u].w[2] = next[u].z, now[u].w[3] = next[u].w;
-    if (at + kUnroll * kThreads < to) load(at + kUnroll * kThreads);
-    float best[kUnroll], most = low;
+    for (int u = 0; u < kUnroll; ++u) now[u][0] = next[u].x, now[u][1] = next[u].y, now[u][2] = next[u].z, now[u][3] = next[u].w;
+    if (at + kUnroll * kThreads < part.to) load(at + kUnroll * kThreads);
+    uint32_t high[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float f[V];
-      now[u].get(f);
-      best[u] = f[0];
+    for (int u = 0; u < kUnroll; ++u) high[u] = word_max<T>(word_max<T>(now[u][0], now[u][1]), word_max<T>(now[u][2], now[u][3]));
+    const float most = word_top<T>(word_max<T>(word_max<T>(high[0], high[1]), word_max<T>(high[2], high[3])));
+    if (TOP) {
+      if (batch == 0) {
+        // a first bar: each of 32 groups of threads has a best candidate, and
+        // `top` of those reach the `top`-th of them
+        uint64_t best = 0;
 #pragma unroll
-      for (int i = 1; i < V; ++i) best[u] = max_nan(best[u], f[i]);
-      most = max_nan(most, best[u]);
+        for (int u = kUnroll - 1; u >= 0; --u) {
+          const int64_t v = at + u * kThreads + threadIdx.x;
+          if (v >= part.to) continue;
+          const float own = word_top<T>(high[u]);
+          int in = -1;
+#pragma unroll
+          for (int w = W - 1; w >= 0; --w) {
+            if constexpr (sizeof(T) == 4) {
+              if (__uint_as_float(now[u][w]) == own) in = w;
+            } else {
+              const float2 f = El<T>::unpack2(now[u][w]);
+              if (f.y == own) in = 2 * w + 1;
+              if (f.x == own) in = 2 * w;
+            }
+          }
+          const uint64_t c = in >= 0 ? candidate(own, static_cast<uint32_t>(part.head + v * V + in)) : 0;
+          best = c > best ? c : best;
+        }
+        if (part.odd_id >= 0) {
+          const uint64_t c = candidate(part.odd, static_cast<uint32_t>(part.odd_id));
+          best = c > best ? c : best;
+        }
+#pragma unroll
+        for (int o = kThreads / 64; o > 0; o >>= 1) {
+          const uint64_t c = __shfl_xor_sync(0xffffffffu, best, o);
+          best = c > best ? c : best;
+        }
+        if ((threadIdx.x & (kThreads / 32 - 1)) == 0) sh.top.groups[threadIdx.x / (kThreads / 32)] = best;
+        __syncthreads();
+        if (threadIdx.x < 32) {
+          best = sh.top.groups[threadIdx.x];
+          int better = 0;
+#pragma unroll 8
+          for (int j = 0; j < 32; ++j) better += __shfl_sync(0xffffffffu, best, j) > best;
+          if (better == p.top - 1 && best) sh.top.least = best;
+        }
+        __syncthreads();
+        bar = candidate_value(sh.top.least);
+      }
+      // above the bar, or no bar yet, or not a number; later values that equal
+      // it come after the ones that set it
+      if (batch == 0 ? !(most < bar) || part.odd_id >= 0 : !(most <= bar)) {
+        const uint64_t least = sh.top.least;
+        auto offer = [&](float f, int64_t id) {
+          const uint64_t c = candidate(f, static_cast<uint32_t>(id));
+          if (c < least) return;
+          const int place = atomicAdd(&sh.top.count, 1);
+          if (place < kWaiting) sh.top.waiting[place] = c;
+          else sh.top.lost = 1;
+        };
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int64_t v = at + u * kThreads + threadIdx.x;
+          if (v >= part.to || word_top<T>(high[u]) < bar) continue;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            if (word_top<T>(now[u][w]) < bar) continue;
+            if constexpr (sizeof(T) == 4) {
+              offer(__uint_as_float(now[u][w]), part.head + v * V + w);
+            } else {
+              const float2 f = El<T>::unpack2(now[u][w]);
+              offer(f.x, part.head + v * V + 2 * w);
+              offer(f.y, part.head + v * V + 2 * w + 1);
+            }
+          }
+        }
+        if (batch == 0 && part.odd_id >= 0) offer(part.odd, part.odd_id);
+      }
+      // raise the bar after 1, 4, 16, ... batches: between two selections
+      // about three times `top` values reach it
+      if (((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to) {
+        select_top(sh.top, p.top, cur);
+        bar = candidate_value(sh.top.least);
+      }
     }
-    if (!(most <= acc.m)) {  // a new maximum (or not a number)
-      const float m = max_nan(acc.m, most);
+    const float m = max_nan(acc.m, most);
+    if (!(m <= acc.m)) {  // a new maximum (or not a number)
       const float d = reference(acc.m) - reference(m), f = ex2(d);
       acc.t = (acc.t + acc.s * d) * f;
       acc.s *= f;
@@ -307,82 +460,39 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p)
     const float ref = -reference(acc.m);
     float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      float f[V];
-      now[u].get(f);
+    for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float y = fmaf(max_nan(f[i], low), kLog2e, ref);
-        const float e = ex2(y);
-        s[i & 1] += e;
-        t[i & 1] = fmaf(e, y, t[i & 1]);
+      for (int w = 0; w < W; ++w) {
+        const uint32_t c = word_max<T>(now[u][w], lowest_word<T>());
+        float f[2];
+        if constexpr (sizeof(T) == 4) {
+          f[0] = __uint_as_float(c);
+        } else {
+          const float2 two = El<T>::unpack2(c);
+          f[0] = two.x, f[1] = two.y;
+        }
+#pragma unroll
+        for (int i = 0; i < V / W; ++i) {
+          const float y = fmaf(f[i], kLog2e, ref);
+          const float e = ex2(y);
+          s[(w + i) & 1] += e;
+          t[(w + i) & 1] = fmaf(e, y, t[(w + i) & 1]);
+        }
       }
-    }
     acc.s += s[0] + s[1];
     acc.t += t[0] + t[1];
-    if (TOP) {
-      if (first) {
-        // a first bound: of 32 groups of threads, the lowest group maximum;
-        // at least 32 values reach it
-        float g = max_nan(most, odd);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
-        if ((threadIdx.x & 15) == 0) sh.top.groups[threadIdx.x >> 4] = g;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-          g = sh.top.groups[threadIdx.x];
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) g = fminf(g, __shfl_xor_sync(0xffffffffu, g, o));
-          // groups that hold only values below `low` give no bound
-          if (threadIdx.x == 0 && g > low) sh.top.least = candidate(g, 0xFFFFFFFFu);
-        }
-        __syncthreads();
-      }
-      bool again = false;
-      for (;;) {
-        const uint64_t least = sh.top.least;
-        const float bar = candidate_value(least);
-        bool many = false, lost = false;
-        auto offer = [&](float f, int64_t id) {
-          const uint64_t c = candidate(f, static_cast<uint32_t>(id));
-          if (c < least) return;
-          if (again)
-            for (int j = 0; j < p.top; ++j)
-              if (sh.top.kept[j] == c) return;
-          const int place = atomicAdd(&sh.top.count, 1);
-          if (place < kKept) sh.top.waiting[place] = c;
-          many |= place >= kSelectAt;
-          lost |= place >= kKept;
-        };
-        if (first && odd_id >= 0) offer(odd, odd_id);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const int64_t v = at + u * kThreads + threadIdx.x;
-          // not below the bar, or no bar yet (or not a number)
-          if (v >= to || best[u] < bar) continue;
-          float f[V];
-          now[u].get(f);
-#pragma unroll 1
-          for (int i = 0; i < V; ++i) {
-            float y = f[0];
-#pragma unroll
-            for (int j = 1; j < V; ++j) y = i == j ? f[j] : y;
-            if (!(y < bar)) offer(y, head + v * V + i);
-          }
-        }
-        if (!__syncthreads_or(many || first)) break;
-        const bool more = __syncthreads_or(lost);
-        select_top(sh.top, p.top);
-        if (!more) break;
-        again = true;
-      }
-    }
-    first = false;
   }
 
   Sums all = block_join(acc, sh);
-  if (TOP) select_top(sh.top, p.top);
+  if (TOP) {
+    if (sh.top.lost) careful_top(part, sh.top, p.top, &cur);
+    else select_top(sh.top, p.top, cur);
+  }
   if (ranks > 1) {
+    if (TOP && cur != 0) {  // where the first CTA of the row looks
+      if (threadIdx.x < kMostTop) sh.top.kept[0][threadIdx.x] = sh.top.kept[1][threadIdx.x];
+      cur = 0;
+    }
     cluster_sync_all();
     if (rank == 0) {
       for (uint32_t r = 1; r < ranks; ++r) {
@@ -397,13 +507,13 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p)
         // at most 7 x 32 candidates of the other CTAs
         const int others = static_cast<int>(ranks - 1) * p.top;
         if (threadIdx.x < others) {
-          const uint32_t a = cluster_map(smem_u32(&sh.top.kept[threadIdx.x % p.top]), 1 + threadIdx.x / p.top);
+          const uint32_t a = cluster_map(smem_u32(&sh.top.kept[0][threadIdx.x % p.top]), 1 + threadIdx.x / p.top);
           uint64_t c;
           asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(c) : "r"(a));
           sh.top.waiting[threadIdx.x] = c;
         }
         if (threadIdx.x == 0) sh.top.count = others;
-        select_top(sh.top, p.top);
+        select_top(sh.top, p.top, cur);
       }
     }
     cluster_sync_all();  // the others' shared memory stays until it was read
@@ -421,7 +531,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const ScoreParams p)
   const int64_t token = p.tokens ? p.tokens[row] : -1;
   const bool given = token >= 0 && token < p.vocab;
   const float logit = given && threadIdx.x == 0 ? El<T>::to_float(x[token]) : 0.0f;
-  write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? &sh.top : nullptr);
+  write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept[cur] : nullptr);
 }
 
 // --------------------------------------------------------------- gradient --
