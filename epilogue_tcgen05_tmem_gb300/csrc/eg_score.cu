@@ -28,7 +28,8 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;        // 16-byte loads of a thread in flight
 constexpr int kMostTop = 32;
-constexpr int kWaiting = 2048;    // room for candidates between two selections
+constexpr int kWaiting = 2048;    // room for candidates of one selection
+constexpr int kQueue = 1024;      // room for vectors that may hold one
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -104,8 +105,9 @@ struct TopShared {
   alignas(16) uint64_t waiting[kWaiting];  // candidates not yet selected from
   alignas(16) uint64_t kept[2][kMostTop];  // the best so far, in order; 0: none
   uint64_t least;            // a value has to reach this to be a candidate
-  int count;                 // candidates that asked for a place
+  int count, queued;         // candidates and vectors that asked for a place
   int lost;                  // some found none
+  uint32_t queue[kQueue];    // vectors with a value above the bar
   uint64_t groups[kMostTop];
 };
 
@@ -140,7 +142,7 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top, int& cur) {
   if (threadIdx.x == 0) {
     const uint64_t last = sh.kept[cur][top - 1];
     if (last) sh.least = last + 1;
-    sh.count = 0;
+    sh.count = sh.queued = 0;
   }
   __syncthreads();
 }
@@ -230,6 +232,25 @@ __device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* lse, fl
   else *lse = m + logf(s), *entropy = logf(s) - t / s;
 }
 
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Elements of one vector of 16 bytes.
 template <typename T>
 constexpr int kVec = 16 / static_cast<int>(sizeof(T));
@@ -270,6 +291,34 @@ struct Part {
   float odd;         // a value outside whole vectors that this thread has
   int64_t odd_id;    // -1: none
 };
+
+// Take a value for a candidate.
+__device__ __forceinline__ void offer_top(TopShared& sh, float f, int64_t id) {
+  const uint64_t c = candidate(f, static_cast<uint32_t>(id));
+  if (c < sh.least) return;
+  const int place = atomicAdd(&sh.count, 1);
+  if (place < kWaiting) sh.waiting[place] = c;
+  else sh.lost = 1;
+}
+
+// Candidates of the noted vectors.  All threads; the result (and whether a
+// place was lost) is there for all after it.
+template <typename T>
+__device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh) {
+  constexpr int V = kVec<T>;
+  __syncthreads();
+  const int queued = min(sh.queued, kQueue);
+  for (int i = threadIdx.x; i < queued; i += kThreads) {
+    const int64_t v = sh.queue[i];
+    Chunk<T, V> c;
+    c.load(part.body + v * V);
+    float f[V];
+    c.get(f);
+#pragma unroll
+    for (int j = 0; j < V; ++j) offer_top(sh, f[j], part.head + v * V + j);
+  }
+  __syncthreads();
+}
 
 // The best of a part, when more candidates came between two selections than
 // there is room for (values that rise along the row, many equal ones): batch
@@ -332,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
   int cur = 0;
   if (TOP) {
     if (threadIdx.x < kMostTop) sh.top.kept[0][threadIdx.x] = sh.top.kept[1][threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.top.least = 1, sh.top.count = 0, sh.top.lost = 0;
+    if (threadIdx.x == 0) sh.top.least = 1, sh.top.count = sh.top.queued = sh.top.lost = 0;
   }
 
   // the values outside whole vectors: the first and the last CTA of a row
@@ -415,37 +464,25 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
         bar = candidate_value(sh.top.least);
       }
       // above the bar, or no bar yet, or not a number; later values that equal
-      // it come after the ones that set it
-      if (batch == 0 ? !(most < bar) || part.odd_id >= 0 : !(most <= bar)) {
-        const uint64_t least = sh.top.least;
-        auto offer = [&](float f, int64_t id) {
-          const uint64_t c = candidate(f, static_cast<uint32_t>(id));
-          if (c < least) return;
-          const int place = atomicAdd(&sh.top.count, 1);
-          if (place < kWaiting) sh.top.waiting[place] = c;
-          else sh.top.lost = 1;
-        };
+      // it come after the ones that set it.  The vector is only noted here: a
+      // warp pays for what any of its threads does, so the values are looked
+      // at when all threads have one.
+      if (batch == 0 ? !(most < bar) : !(most <= bar)) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
+          const float own = word_top<T>(high[u]);
           const int64_t v = at + u * kThreads + threadIdx.x;
-          if (v >= part.to || word_top<T>(high[u]) < bar) continue;
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            if (word_top<T>(now[u][w]) < bar) continue;
-            if constexpr (sizeof(T) == 4) {
-              offer(__uint_as_float(now[u][w]), part.head + v * V + w);
-            } else {
-              const float2 f = El<T>::unpack2(now[u][w]);
-              offer(f.x, part.head + v * V + 2 * w);
-              offer(f.y, part.head + v * V + 2 * w + 1);
-            }
+          if (v < part.to && (batch == 0 ? !(own < bar) : !(own <= bar))) {
+            const int place = atomicAdd(&sh.top.queued, 1);
+            if (place < kQueue) sh.top.queue[place] = static_cast<uint32_t>(v);
+            else sh.top.lost = 1;
           }
         }
-        if (batch == 0 && part.odd_id >= 0) offer(part.odd, part.odd_id);
       }
-      // raise the bar after 1, 4, 16, ... batches: between two selections
-      // about three times `top` values reach it
-      if (((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to) {
+      if (batch == 0 && part.odd_id >= 0) offer_top(sh.top, part.odd, part.odd_id);
+      // raise the bar after 4, 16, 64, ... batches
+      if (batch && ((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to) {
+        open_queue(part, sh.top);
         select_top(sh.top, p.top, cur);
         bar = candidate_value(sh.top.least);
       }
@@ -457,34 +494,40 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
       acc.s *= f;
       acc.m = m;
     }
+    // two values in one instruction where there is one
     const float ref = -reference(acc.m);
-    float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
+    const uint64_t ref2 = pair_of(ref, ref), log2e2 = pair_of(kLog2e, kLog2e);
+    uint64_t s2 = 0, t2 = 0;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-      for (int w = 0; w < W; ++w) {
+      for (int w = 0; w < W; w += (sizeof(T) == 4 ? 2 : 1)) {
+        float f0, f1;
         const uint32_t c = word_max<T>(now[u][w], lowest_word<T>());
-        float f[2];
         if constexpr (sizeof(T) == 4) {
-          f[0] = __uint_as_float(c);
+          f0 = __uint_as_float(c);
+          f1 = __uint_as_float(word_max<T>(now[u][w + 1], lowest_word<T>()));
         } else {
           const float2 two = El<T>::unpack2(c);
-          f[0] = two.x, f[1] = two.y;
+          f0 = two.x, f1 = two.y;
         }
-#pragma unroll
-        for (int i = 0; i < V / W; ++i) {
-          const float y = fmaf(f[i], kLog2e, ref);
-          const float e = ex2(y);
-          s[(w + i) & 1] += e;
-          t[(w + i) & 1] = fmaf(e, y, t[(w + i) & 1]);
-        }
+        const uint64_t y = fma_pair(pair_of(f0, f1), log2e2, ref2);
+        float y0, y1;
+        unpair(y, &y0, &y1);
+        const uint64_t e = pair_of(ex2(y0), ex2(y1));
+        s2 = add_pair(s2, e);
+        t2 = fma_pair(e, y, t2);
       }
-    acc.s += s[0] + s[1];
-    acc.t += t[0] + t[1];
+    float a, b;
+    unpair(s2, &a, &b);
+    acc.s += a + b;
+    unpair(t2, &a, &b);
+    acc.t += a + b;
   }
 
   Sums all = block_join(acc, sh);
   if (TOP) {
+    open_queue(part, sh.top);
     if (sh.top.lost) careful_top(part, sh.top, p.top, &cur);
     else select_top(sh.top, p.top, cur);
   }
