@@ -24,12 +24,14 @@ namespace eg {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256;     // that look at values; one more warp loads
 constexpr int kWarps = kThreads / 32;
-constexpr int kUnroll = 4;        // 16-byte loads of a thread in flight
+constexpr int kUnroll = 4;        // 16-byte vectors of a thread and batch
+constexpr int kBatchBytes = kThreads * kUnroll * 16;
+constexpr int kStages = 3;        // batches in flight of a CTA
 constexpr int kMostTop = 32;
-constexpr int kWaiting = 2048;    // room for candidates of one selection
-constexpr int kQueue = 1024;      // room for vectors that may hold one
+constexpr int kWaiting = 1024;    // room for candidates of one selection
+constexpr int kQueue = 128;       // room of a warp for notes of threads' batches that may hold one
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -41,6 +43,17 @@ struct ScoreParams {
   int64_t* top_ids;
   int32_t top;
 };
+
+// Barrier of the threads that look at values.
+__device__ __forceinline__ void sync_lookers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
+__device__ __forceinline__ bool sync_lookers_or(bool v) {
+  uint32_t any;
+  asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.or.pred b, 1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+               : "=r"(any)
+               : "r"(static_cast<uint32_t>(v)), "n"(kThreads)
+               : "memory");
+  return any != 0;
+}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -102,49 +115,66 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
 }
 
 struct TopShared {
-  alignas(16) uint64_t waiting[kWaiting];  // candidates not yet selected from
-  alignas(16) uint64_t kept[2][kMostTop];  // the best so far, in order; 0: none
+  alignas(16) uint64_t waiting[kWaiting];  // candidates
+  alignas(16) uint64_t bests[kThreads];    // the best one of each thread
+  alignas(16) uint64_t kept[kMostTop];     // the best, in order; 0: none
+  alignas(16) float groups[2][32];         // maxima of 32 groups of threads
   uint64_t least;            // a value has to reach this to be a candidate
-  int count, queued;         // candidates and vectors that asked for a place
-  int lost;                  // some found none
-  uint32_t queue[kQueue];    // vectors with a value above the bar
-  uint64_t groups[kMostTop];
+  int count;                 // candidates that asked for a place
+  int lost;                  // some candidates or vectors found none
+  int2 queue[kWarps][kQueue];  // a thread's batches above the bar: the first vector, and the largest value
 };
 
 struct RowShared {
+  alignas(16) uint8_t ring[kStages][kBatchBytes];
+  uint64_t full[kStages], empty[kStages];
+  int abort;
   Sums warps[kWarps];
   Sums cta;
   TopShared top;
 };
 
-// The best `top` of kept[cur] and waiting into kept[cur ^ 1], in order; the
-// next candidate has to be better than the last of them.  All threads; the
-// place of each is the number of better ones.
-__device__ __forceinline__ void select_top(TopShared& sh, int top, int& cur) {
-  __syncthreads();
-  const int waiting = min(sh.count, kWaiting);
-  const int total = waiting + top;
-  for (int at = threadIdx.x; at < total; at += kThreads) {
-    const uint64_t mine = at < top ? sh.kept[cur][at] : sh.waiting[at - top];
-    if (mine == 0) continue;
-    int better = 0;
-    for (int j = 0; j < top; ++j) better += sh.kept[cur][j] > mine;
-    int j = 0;
-    for (; j + 1 < waiting; j += 2) {
-      const ulonglong2 two = *reinterpret_cast<const ulonglong2*>(&sh.waiting[j]);
-      better += (two.x > mine) + (two.y > mine);
-    }
-    if (j < waiting) better += sh.waiting[j] > mine;
-    if (better < top) sh.kept[cur ^ 1][better] = mine;
+// How many of list[0, n) are better than `mine`; the list is zero up to the
+// next multiple of 16.
+__device__ __forceinline__ int better_than(const uint64_t* list, int n, uint64_t mine) {
+  int better = 0;
+  for (int j = 0; j < n; j += 16) {
+    ulonglong2 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const ulonglong2*>(list + j)[i];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) better += (v[i].x > mine) + (v[i].y > mine);
   }
-  cur ^= 1;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const uint64_t last = sh.kept[cur][top - 1];
-    if (last) sh.least = last + 1;
-    sh.count = sh.queued = 0;
+  return better;
+}
+
+// The best `top` of the candidates into kept, in order; kept has room for the
+// next ones to be better than its last.  All threads; the place of each is the
+// number of better ones.
+__device__ __forceinline__ void select_top(TopShared& sh, int top) {
+  sync_lookers();
+  const int n = min(sh.count, kWaiting), padded = min((n + 15) & ~15, kWaiting);
+  if (n + static_cast<int>(threadIdx.x) < padded) sh.waiting[n + threadIdx.x] = 0;
+  if (threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
+  if (threadIdx.x == 0) sh.least = 0;
+  if (n > kThreads) {
+    // more than one for a thread: only what reaches the `top`-th of the
+    // threads' best is placed
+    uint64_t best = 0;
+    for (int at = threadIdx.x; at < n; at += kThreads) best = max(best, sh.waiting[at]);
+    sh.bests[threadIdx.x] = best;
+    sync_lookers();
+    if (better_than(sh.bests, kThreads, best) == top - 1) sh.least = best;
   }
-  __syncthreads();
+  sync_lookers();
+  const uint64_t least = sh.least;
+  for (int at = threadIdx.x; at < n; at += kThreads) {
+    const uint64_t mine = sh.waiting[at];
+    if (mine < least) continue;
+    const int place = better_than(sh.waiting, n, mine);
+    if (place < top) sh.kept[place] = mine;
+  }
+  sync_lookers();
 }
 
 // The outputs of one row by one thread group of the CTA that holds the sums.
@@ -166,51 +196,47 @@ __device__ __forceinline__ void write_row(const ScoreParams& p, int64_t row, flo
   }
 }
 
-__device__ __forceinline__ Sums block_join(Sums v, RowShared& sh) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+// Sums of a warp to the reference of its maximum: the maximum first, then one
+// scaling a lane.
+__device__ __forceinline__ Sums warp_join(Sums v, int lanes) {
+  float m = v.m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    Sums b;
-    b.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-    b.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-    b.t = __shfl_xor_sync(0xffffffffu, v.t, o);
-    v = join(v, b);
-  }
-  __syncthreads();
-  if (lane == 0) sh.warps[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    v = sh.warps[lane < kWarps ? lane : 0];
-    if (lane >= kWarps) v.s = 0.0f, v.t = 0.0f;
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float d = reference(v.m) - reference(m), f = ex2(d);
+  float s = v.s * f, t = (v.t + v.s * d) * f;
 #pragma unroll
-    for (int o = kWarps / 2; o > 0; o >>= 1) {
-      Sums b;
-      b.m = __shfl_xor_sync(0xffffffffu, v.m, o);
-      b.s = __shfl_xor_sync(0xffffffffu, v.s, o);
-      b.t = __shfl_xor_sync(0xffffffffu, v.t, o);
-      v = join(v, b);
+  for (int o = 16; o > 0; o >>= 1)
+    if (o < lanes) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      t += __shfl_xor_sync(0xffffffffu, t, o);
     }
-    if (lane == 0) sh.cta = v;
-  }
-  __syncthreads();
-  return sh.cta;
+  return {m, s, t};
+}
+
+// The CTA's sums, for every thread.
+__device__ __forceinline__ Sums block_join(Sums v, Sums* warps) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  v = warp_join(v, 32);
+  if (lane == 0) warps[warp] = v;
+  sync_lookers();
+  return warp_join(warps[lane % kWarps], kWarps);
 }
 
 // A row whose maximum is so low, so high or so infinite that the pass above
 // does not hold: its statistics from the definition, by one CTA.
 template <typename T>
-__device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* lse, float* entropy) {
-  __shared__ float red[kThreads];
+__device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* red, float* lse, float* entropy) {
   float m = -CUDART_INF_F;
   for (int64_t i = threadIdx.x; i < vocab; i += kThreads) m = max_nan(m, El<T>::to_float(x[i]));
   red[threadIdx.x] = m;
-  __syncthreads();
+  sync_lookers();
   for (int o = kThreads / 2; o > 0; o >>= 1) {
     if (threadIdx.x < o) red[threadIdx.x] = max_nan(red[threadIdx.x], red[threadIdx.x + o]);
-    __syncthreads();
+    sync_lookers();
   }
   m = red[0];
-  __syncthreads();
+  sync_lookers();
   float s = 0.0f, t = 0.0f;
   if (fabsf(m) < CUDART_INF_F)
     for (int64_t i = threadIdx.x; i < vocab; i += kThreads) {
@@ -219,13 +245,13 @@ __device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* lse, fl
     }
   for (int k = 0; k < 2; ++k) {
     red[threadIdx.x] = k ? t : s;
-    __syncthreads();
+    sync_lookers();
     for (int o = kThreads / 2; o > 0; o >>= 1) {
       if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-      __syncthreads();
+      sync_lookers();
     }
     (k ? t : s) = red[0];
-    __syncthreads();
+    sync_lookers();
   }
   if (m == -CUDART_INF_F) *lse = m, *entropy = 0.0f;
   else if (!(fabsf(m) < CUDART_INF_F)) *lse = m, *entropy = __int_as_float(0x7FC00000);
@@ -286,109 +312,225 @@ __device__ __forceinline__ uint32_t lowest_word() {
 template <typename T>
 struct Part {
   const T* body;     // the row's first 16-byte boundary
-  int64_t head;      // values before it
-  int64_t from, to;  // vectors
+  int32_t head;      // values before it
+  int32_t from, to;  // vectors
   float odd;         // a value outside whole vectors that this thread has
-  int64_t odd_id;    // -1: none
+  int32_t odd_id;    // -1: none
 };
 
 // Take a value for a candidate.
-__device__ __forceinline__ void offer_top(TopShared& sh, float f, int64_t id) {
+__device__ __forceinline__ void offer_top(TopShared& sh, uint64_t least, float f, int32_t id) {
   const uint64_t c = candidate(f, static_cast<uint32_t>(id));
-  if (c < sh.least) return;
+  if (c < least) return;
   const int place = atomicAdd(&sh.count, 1);
   if (place < kWaiting) sh.waiting[place] = c;
   else sh.lost = 1;
 }
 
-// Candidates of the noted vectors.  All threads; the result (and whether a
-// place was lost) is there for all after it.
-template <typename T>
-__device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh) {
-  constexpr int V = kVec<T>;
-  __syncthreads();
-  const int queued = min(sh.queued, kQueue);
-  for (int i = threadIdx.x; i < queued; i += kThreads) {
-    const int64_t v = sh.queue[i];
-    Chunk<T, V> c;
-    c.load(part.body + v * V);
-    float f[V];
-    c.get(f);
+// A value that `top` of 32 groups of threads have reached, from each thread's
+// largest so far: at least `top` values reach it, and few more do.  One
+// barrier, after which every warp finds it by itself; `turn` counts the calls.
+__device__ __forceinline__ float group_bar(TopShared& sh, float most, int top, int turn) {
 #pragma unroll
-    for (int j = 0; j < V; ++j) offer_top(sh, f[j], part.head + v * V + j);
+  for (int o = kThreads / 64; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  float* groups = sh.groups[turn & 1];
+  if ((threadIdx.x & (kThreads / 32 - 1)) == 0) groups[threadIdx.x / (kThreads / 32)] = most;
+  sync_lookers();
+  const float g = groups[threadIdx.x & 31];
+  int better = 0, equal = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float4 f = reinterpret_cast<const float4*>(groups)[j];
+    better += (f.x > g) + (f.y > g) + (f.z > g) + (f.w > g);
+    equal += (f.x == g) + (f.y == g) + (f.z == g) + (f.w == g);
   }
-  __syncthreads();
+  const uint32_t is = __ballot_sync(0xffffffffu, better < top && better + equal >= top);
+  return __shfl_sync(0xffffffffu, g, __ffs(is) - 1);
 }
 
-// The best of a part, when more candidates came between two selections than
-// there is room for (values that rise along the row, many equal ones): batch
-// by batch, with a selection whenever one fills the room.
+// The candidates among the values of the vectors that this warp noted: those
+// that reach the last bar.  Where there is no bar, or many were noted (many
+// equal values, a short row), a better bound first: each thread has a best
+// candidate, and `top` of those reach the `top`-th of them.
 template <typename T>
-__device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int top, int* where) {
+__device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, int queued, float bar, int top) {
   constexpr int V = kVec<T>;
-  int cur = 0;
-  __syncthreads();
-  if (threadIdx.x < kMostTop) sh.kept[0][threadIdx.x] = sh.kept[1][threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.least = 1, sh.count = 0;
-  __syncthreads();
-  for (int64_t at = part.from; at < part.to || at == part.from; at += kThreads) {
-    const int64_t v = at + threadIdx.x;
-    bool again = false;
-    for (;;) {
-      const uint64_t least = sh.least;
-      bool lost = false;
-      auto offer = [&](float f, int64_t id) {
-        const uint64_t c = candidate(f, static_cast<uint32_t>(id));
-        if (c < least) return;
-        if (again)
-          for (int j = 0; j < top; ++j)
-            if (sh.kept[cur][j] == c) return;
-        const int place = atomicAdd(&sh.count, 1);
-        if (place < kWaiting) sh.waiting[place] = c;
-        else lost = true;
-      };
-      if (at == part.from && part.odd_id >= 0) offer(part.odd, part.odd_id);
-      if (v < part.to)
-        for (int i = 0; i < V; ++i) offer(El<T>::to_float(part.body[v * V + i]), part.head + v * V + i);
-      const bool more = __syncthreads_or(lost);
-      select_top(sh, top, cur);
-      if (!more) break;
-      again = true;
+  const int2* queue = sh.queue[threadIdx.x >> 5];
+  const int lane = threadIdx.x & 31;
+  queued = min(queued, kQueue);
+  uint64_t least = candidate(bar, 0xFFFFFFFFu);
+  // the vectors of a note that may matter
+  auto open = [&](const int2& note, Chunk<T, V> (&c)[kUnroll]) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int32_t v = note.x + u * kThreads;
+      if (v < part.to) c[u].load(part.body + static_cast<int64_t>(v) * V);
+      else c[u].w[0] = c[u].w[1] = c[u].w[2] = c[u].w[3] = kNothing<T>;
+    }
+  };
+  if (sync_lookers_or(queued > 64 || bar == -CUDART_INF_F)) {
+    uint64_t best = 0;
+    for (int i = lane; i < queued; i += 32) {
+      Chunk<T, V> c[kUnroll];
+      open(queue[i], c);
+#pragma unroll 1
+      for (int u = 0; u < kUnroll; ++u) {
+        float f[V];
+        c[0].get(f);
+        const int32_t v = queue[i].x + u * kThreads;
+        if (v < part.to)
+#pragma unroll
+          for (int j = 0; j < V; ++j) best = max(best, candidate(f[j], static_cast<uint32_t>(part.head + v * V + j)));
+        c[0] = c[1], c[1] = c[2], c[2] = c[3];
+      }
+    }
+    sh.bests[threadIdx.x] = best;
+    sync_lookers();
+    if (best && better_than(sh.bests, kThreads, best) == top - 1) sh.least = best;
+    sync_lookers();
+    least = max(least, sh.least);
+  }
+  for (int i = lane; i < queued; i += 32) {
+    const int2 note = queue[i];
+    if (__int_as_float(note.y) < bar) continue;
+    Chunk<T, V> c[kUnroll];
+    open(note, c);
+#pragma unroll 1
+    for (int u = 0; u < kUnroll; ++u) {
+      const uint32_t high = word_max<T>(word_max<T>(c[0].w[0], c[0].w[1]), word_max<T>(c[0].w[2], c[0].w[3]));
+      const int32_t v = note.x + u * kThreads;
+      if (v < part.to && !(word_top<T>(high) < bar)) {
+        float f[V];
+        c[0].get(f);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (!(f[j] < bar)) offer_top(sh, least, f[j], part.head + v * V + j);
+      }
+      c[0] = c[1], c[1] = c[2], c[2] = c[3];
     }
   }
-  *where = cur;
 }
 
+// The best of a part, when more vectors or candidates came than there is room
+// for (values that rise along the row): some vectors at a time, with a
+// selection after each lot.
+template <typename T>
+__device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int top) {
+  constexpr int V = kVec<T>;
+  constexpr int kLot = (kWaiting - kMostTop - 16) / V < kThreads ? (kWaiting - kMostTop - 16) / V : kThreads;
+  sync_lookers();
+  if (threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
+  for (int32_t at = part.from; at < part.to || at == part.from; at += kLot) {
+    sync_lookers();
+    const uint64_t last = sh.kept[top - 1];
+    if (threadIdx.x < top) sh.waiting[threadIdx.x] = sh.kept[threadIdx.x];
+    if (threadIdx.x == 0) sh.count = top;
+    sync_lookers();
+    // a zero among the kept ones is no candidate: nothing is worse
+    const uint64_t least = last + 1;
+    const int32_t v = at + static_cast<int32_t>(threadIdx.x);
+    if (at == part.from && part.odd_id >= 0) offer_top(sh, least, part.odd, part.odd_id);
+    if (static_cast<int>(threadIdx.x) < kLot && v < part.to)
+      for (int i = 0; i < V; ++i) offer_top(sh, least, El<T>::to_float(part.body[static_cast<int64_t>(v) * V + i]), part.head + v * V + i);
+    select_top(sh, top);
+  }
+}
+
+// Where the row's vectors start, and which of them this CTA of `ranks` has.
+template <typename T>
+__device__ __forceinline__ Part<T> part_of(const T* x, int64_t vocab, uint32_t rank, uint32_t ranks) {
+  Part<T> part;
+  part.head = static_cast<int32_t>(min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), vocab));
+  const uint32_t vectors = static_cast<uint32_t>(vocab - part.head) / kVec<T>;
+  part.from = static_cast<int32_t>(vectors * rank / ranks), part.to = static_cast<int32_t>(vectors * (rank + 1) / ranks);  // 2^29 x 8 fits
+  part.body = x + part.head;
+  return part;
+}
+
+constexpr uint64_t kWaitNs = 2000000000ull;
+
+// Bounded wait; gives up at once after any wait of the CTA has run out.
+__device__ __forceinline__ bool wait_batch(uint64_t* bar, uint32_t phase, int* abort) {
+  if (mbar_try_wait(bar, phase & 1)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, phase & 1)) return true;
+    if ((it & 63u) == 0) {
+      if (*reinterpret_cast<volatile int*>(abort)) return false;
+      if (global_timer_ns() - t0 > kWaitNs) {
+        *reinterpret_cast<volatile int*>(abort) = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// A CTA takes rows (or its part of a cluster's row) one after the other.  The
+// loading warp streams them into a ring of batches and runs ahead into the
+// next row, so the memory stays busy while a row is being finished.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScoreParams p) {
   constexpr int V = kVec<T>;
   constexpr int W = 4;  // words of a vector
-  __shared__ RowShared sh;
+  extern __shared__ __align__(128) uint8_t raw[];
+  RowShared& sh = *reinterpret_cast<RowShared*>(raw);
   uint32_t ranks, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
   rank = cluster_ctarank();
-  const int64_t row = blockIdx.x / ranks;
+  const int64_t first_row = blockIdx.x / ranks, row_step = gridDim.x / ranks;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], kWarps);
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  __syncthreads();
+  if (threadIdx.x >= kThreads) {
+    if (threadIdx.x == kThreads) {
+      uint32_t n = 0;  // batches so far
+      bool ok = true;
+      for (int64_t row = first_row; ok && row < p.rows; row += row_step) {
+        const Part<T> part = part_of(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab, rank, ranks);
+        for (int32_t at = part.from; at < part.to; at += kUnroll * kThreads) {
+          const int slot = n % kStages;
+          if (!(ok = wait_batch(&sh.empty[slot], n / kStages + 1, &sh.abort))) break;
+          const uint32_t bytes = static_cast<uint32_t>(min(part.to - at, kUnroll * kThreads)) * 16u;
+          mbar_arrive_expect_tx(&sh.full[slot], bytes);
+          asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           smem_u32(sh.ring[slot])),
+                       "l"(reinterpret_cast<uint64_t>(part.body + static_cast<int64_t>(at) * V)), "r"(bytes), "r"(smem_u32(&sh.full[slot]))
+                       : "memory");
+          ++n;
+        }
+      }
+      // leave no copy in flight behind
+      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, kWaitNs);
+    }
+    __syncwarp();
+    if (ranks > 1) {  // as often as the other warps below: a cluster has one row
+      cluster_sync_all();
+      cluster_sync_all();
+    }
+    return;
+  }
+  uint32_t batches = 0;
+  for (int64_t row = first_row; row < p.rows; row += row_step) {
   const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
   // values before the first 16-byte boundary, whole vectors, and the rest
-  Part<T> part;
-  part.head = min(static_cast<int64_t>((16 - reinterpret_cast<uintptr_t>(x) % 16) % 16 / sizeof(T)), p.vocab);
-  const int64_t vectors = (p.vocab - part.head) / V;
-  const int tail = static_cast<int>(p.vocab - part.head - vectors * V);
-  part.from = vectors * rank / ranks, part.to = vectors * (rank + 1) / ranks;
-  part.body = x + part.head;
+  Part<T> part = part_of(x, p.vocab, rank, ranks);
+  const int32_t vocab = static_cast<int32_t>(p.vocab), whole = part.head + (vocab - part.head) / V * V;
   constexpr float low = kLowest<T>;
   Sums acc{low, 0.0f, 0.0f};
-  int cur = 0;
-  if (TOP) {
-    if (threadIdx.x < kMostTop) sh.top.kept[0][threadIdx.x] = sh.top.kept[1][threadIdx.x] = 0;
-    if (threadIdx.x == 0) sh.top.least = 1, sh.top.count = sh.top.queued = sh.top.lost = 0;
-  }
+  if (TOP && threadIdx.x == 0) sh.top.least = 0, sh.top.count = sh.top.lost = 0;
+  // the given token's logit, long before it is needed
+  const int64_t token = p.tokens ? p.tokens[row] : -1;
+  const bool given = token >= 0 && token < p.vocab;
+  const float logit = given && threadIdx.x == 0 ? El<T>::to_float(x[token]) : 0.0f;
 
   // the values outside whole vectors: the first and the last CTA of a row
   part.odd = -CUDART_INF_F;
   part.odd_id = -1;
-  if (rank == 0 && threadIdx.x < part.head) part.odd_id = threadIdx.x;
-  if (rank == ranks - 1 && threadIdx.x >= 32 && threadIdx.x < 32 + tail) part.odd_id = part.head + vectors * V + threadIdx.x - 32;
+  if (rank == 0 && static_cast<int>(threadIdx.x) < part.head) part.odd_id = threadIdx.x;
+  if (rank == ranks - 1 && threadIdx.x >= 32 && static_cast<int>(threadIdx.x) - 32 < vocab - whole) part.odd_id = whole + threadIdx.x - 32;
   if (part.odd_id >= 0) {
     part.odd = El<T>::to_float(x[part.odd_id]);
     const float c = max_nan(part.odd, low);
@@ -396,96 +538,58 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
     acc.m = c, acc.s = ex2(y), acc.t = acc.s * y;
   }
 
-  uint4 next[kUnroll];
-  auto load = [&](int64_t at) {
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int64_t v = at + u * kThreads + threadIdx.x;
-      // past the end: -infinity, which adds nothing
-      constexpr uint32_t n = kNothing<T>;
-      next[u] = v < part.to ? __ldcs(reinterpret_cast<const uint4*>(part.body) + v) : make_uint4(n, n, n, n);
-    }
-  };
-  load(part.from);
+  if (TOP) sync_lookers();
   float bar = -CUDART_INF_F;  // a value below this is no candidate
+  float seen = -CUDART_INF_F; // this thread's largest value
+  int turn = 0, queued = 0;   // bars so far; vectors this warp has noted
   uint32_t batch = 0;
-  for (int64_t at = part.from; at < part.to || batch == 0; at += kUnroll * kThreads, ++batch) {
+  bool gave_up = false;  // a load never came
+  for (int32_t at = part.from; at < part.to || batch == 0; at += kUnroll * kThreads, ++batch) {
     uint32_t now[kUnroll][W];
+    if (part.from < part.to) {
+      const int slot = batches % kStages;
+      if (!wait_batch(&sh.full[slot], batches / kStages, &sh.abort)) gave_up = true;
+      const uint4* vec = reinterpret_cast<const uint4*>(sh.ring[slot]);
+const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) now[u][0] = next[u].x, now[u][1] = next[u].y, now[u][2] = next[u].z, now[u][3] = next[u].w;
-    if (at + kUnroll * kThreads < part.to) load(at + kUnroll * kThreads);
+      for (int u = 0; u < kUnroll; ++u) {
+        const uint4 q = vec[u * kThreads + threadIdx.x];
+        now[u][0] = q.x, now[u][1] = q.y, now[u][2] = q.z, now[u][3] = q.w;
+      }
+      if (part.to - at < kUnroll * kThreads) {
+        // past the end: -infinity, which adds nothing
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+          if (u * kThreads >= left) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
+      }
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.empty[slot]);
+      ++batches;
+    } else {
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
+    }
     uint32_t high[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) high[u] = word_max<T>(word_max<T>(now[u][0], now[u][1]), word_max<T>(now[u][2], now[u][3]));
     const float most = word_top<T>(word_max<T>(word_max<T>(high[0], high[1]), word_max<T>(high[2], high[3])));
     if (TOP) {
-      if (batch == 0) {
-        // a first bar: each of 32 groups of threads has a best candidate, and
-        // `top` of those reach the `top`-th of them
-        uint64_t best = 0;
-#pragma unroll
-        for (int u = kUnroll - 1; u >= 0; --u) {
-          const int64_t v = at + u * kThreads + threadIdx.x;
-          if (v >= part.to) continue;
-          const float own = word_top<T>(high[u]);
-          int in = -1;
-#pragma unroll
-          for (int w = W - 1; w >= 0; --w) {
-            if constexpr (sizeof(T) == 4) {
-              if (__uint_as_float(now[u][w]) == own) in = w;
-            } else {
-              const float2 f = El<T>::unpack2(now[u][w]);
-              if (f.y == own) in = 2 * w + 1;
-              if (f.x == own) in = 2 * w;
-            }
-          }
-          const uint64_t c = in >= 0 ? candidate(own, static_cast<uint32_t>(part.head + v * V + in)) : 0;
-          best = c > best ? c : best;
-        }
-        if (part.odd_id >= 0) {
-          const uint64_t c = candidate(part.odd, static_cast<uint32_t>(part.odd_id));
-          best = c > best ? c : best;
-        }
-#pragma unroll
-        for (int o = kThreads / 64; o > 0; o >>= 1) {
-          const uint64_t c = __shfl_xor_sync(0xffffffffu, best, o);
-          best = c > best ? c : best;
-        }
-        if ((threadIdx.x & (kThreads / 32 - 1)) == 0) sh.top.groups[threadIdx.x / (kThreads / 32)] = best;
-        __syncthreads();
-        if (threadIdx.x < 32) {
-          best = sh.top.groups[threadIdx.x];
-          int better = 0;
-#pragma unroll 8
-          for (int j = 0; j < 32; ++j) better += __shfl_sync(0xffffffffu, best, j) > best;
-          if (better == p.top - 1 && best) sh.top.least = best;
-        }
-        __syncthreads();
-        bar = candidate_value(sh.top.least);
+      seen = fmaxf(seen, most);
+      if (batch == 0) bar = group_bar(sh.top, seen, p.top, turn++);
+      // Later values that only equal the bar come after `top` that reach it.
+      // The thread's vectors of this batch are only noted: a warp pays for
+      // what any of its threads does, so the values are looked at when all
+      // threads have some.
+      const bool note = (batch == 0 ? !(most < bar) : !(most <= bar)) && at + static_cast<int32_t>(threadIdx.x) < part.to;
+      const uint32_t all = __ballot_sync(0xffffffffu, note);
+      if (all) {
+        const int place = queued + __popc(all & ((1u << (threadIdx.x & 31)) - 1u));
+        if (note && place < kQueue) sh.top.queue[threadIdx.x >> 5][place] = make_int2(at + threadIdx.x, __float_as_int(most));
+        queued += __popc(all);
       }
-      // above the bar, or no bar yet, or not a number; later values that equal
-      // it come after the ones that set it.  The vector is only noted here: a
-      // warp pays for what any of its threads does, so the values are looked
-      // at when all threads have one.
-      if (batch == 0 ? !(most < bar) : !(most <= bar)) {
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-          const float own = word_top<T>(high[u]);
-          const int64_t v = at + u * kThreads + threadIdx.x;
-          if (v < part.to && (batch == 0 ? !(own < bar) : !(own <= bar))) {
-            const int place = atomicAdd(&sh.top.queued, 1);
-            if (place < kQueue) sh.top.queue[place] = static_cast<uint32_t>(v);
-            else sh.top.lost = 1;
-          }
-        }
-      }
-      if (batch == 0 && part.odd_id >= 0) offer_top(sh.top, part.odd, part.odd_id);
       // raise the bar after 4, 16, 64, ... batches
-      if (batch && ((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to) {
-        open_queue(part, sh.top);
-        select_top(sh.top, p.top, cur);
-        bar = candidate_value(sh.top.least);
-      }
+      if (batch && ((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to)
+        bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
     }
     const float m = max_nan(acc.m, most);
     if (!(m <= acc.m)) {  // a new maximum (or not a number)
@@ -525,17 +629,18 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
     acc.t += a + b;
   }
 
-  Sums all = block_join(acc, sh);
+  if (gave_up) acc.m = __int_as_float(0x7FC00000);
+  Sums all = block_join(acc, sh.warps);
   if (TOP) {
-    open_queue(part, sh.top);
-    if (sh.top.lost) careful_top(part, sh.top, p.top, &cur);
-    else select_top(sh.top, p.top, cur);
+    if (part.odd_id >= 0 && !(part.odd < bar)) offer_top(sh.top, candidate(bar, 0xFFFFFFFFu), part.odd, part.odd_id);
+    if (queued > kQueue) sh.top.lost = 1;
+    if (batch > 1) bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
+    open_queue(part, sh.top, queued, bar, p.top);
+    if (sync_lookers_or(sh.top.lost)) careful_top(part, sh.top, p.top);
+    else select_top(sh.top, p.top);
   }
   if (ranks > 1) {
-    if (TOP && cur != 0) {  // where the first CTA of the row looks
-      if (threadIdx.x < kMostTop) sh.top.kept[0][threadIdx.x] = sh.top.kept[1][threadIdx.x];
-      cur = 0;
-    }
+    if (threadIdx.x == 0) sh.cta = all;
     cluster_sync_all();
     if (rank == 0) {
       for (uint32_t r = 1; r < ranks; ++r) {
@@ -547,16 +652,15 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
         all = join(all, b);
       }
       if (TOP) {
-        // at most 7 x 32 candidates of the other CTAs
-        const int others = static_cast<int>(ranks - 1) * p.top;
-        if (threadIdx.x < others) {
-          const uint32_t a = cluster_map(smem_u32(&sh.top.kept[0][threadIdx.x % p.top]), 1 + threadIdx.x / p.top);
+        // at most 8 x 32 candidates of the row's CTAs
+        if (threadIdx.x < ranks * p.top) {
+          const uint32_t a = cluster_map(smem_u32(&sh.top.kept[threadIdx.x % p.top]), threadIdx.x / p.top);
           uint64_t c;
           asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(c) : "r"(a));
           sh.top.waiting[threadIdx.x] = c;
         }
-        if (threadIdx.x == 0) sh.top.count = others;
-        select_top(sh.top, p.top, cur);
+        if (threadIdx.x == 0) sh.top.count = static_cast<int>(ranks) * p.top;
+        select_top(sh.top, p.top);
       }
     }
     cluster_sync_all();  // the others' shared memory stays until it was read
@@ -564,17 +668,18 @@ __global__ void __launch_bounds__(kThreads, 4) score_kernel(const ScoreParams p)
   }
   const bool nan_row = all.m != all.m;
   float lse, entropy;
-  if (all.m > low + 1024.0f && all.m < -low) {
+  if (nan_row) {
+    lse = entropy = __int_as_float(0x7FC00000);
+  } else if (all.m > low + 1024.0f && all.m < -low) {
     const float l = log2f(all.s);
     lse = (reference(all.m) + l) * kLn2;
     entropy = (l - all.t / all.s) * kLn2;
   } else {
-    plain_row(x, p.vocab, &lse, &entropy);
+    plain_row(x, p.vocab, reinterpret_cast<float*>(sh.top.bests), &lse, &entropy);
   }
-  const int64_t token = p.tokens ? p.tokens[row] : -1;
-  const bool given = token >= 0 && token < p.vocab;
-  const float logit = given && threadIdx.x == 0 ? El<T>::to_float(x[token]) : 0.0f;
-  write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept[cur] : nullptr);
+  write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept : nullptr);
+  if (TOP) sync_lookers();  // the next row clears what was written from
+  }
 }
 
 // --------------------------------------------------------------- gradient --
@@ -682,10 +787,17 @@ int sm_count() {
 }
 
 template <typename T>
-cudaError_t launch_score(const ScoreParams& p, int ranks, cudaStream_t st) {
+cudaError_t launch_score(const ScoreParams& p, int ranks, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(p.rows * ranks));
-  cfg.blockDim = dim3(kThreads);
+  auto kernel = p.top ? score_kernel<T, true> : score_kernel<T, false>;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(sizeof(RowShared)));
+  if (e != cudaSuccess) return e;
+  // three CTAs an SM take rows in turn; a cluster takes one
+  const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, 3 * sms);
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
+  cfg.blockDim = dim3(kThreads + 32);
+  cfg.dynamicSmemBytes = sizeof(RowShared);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -693,7 +805,7 @@ cudaError_t launch_score(const ScoreParams& p, int ranks, cudaStream_t st) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return p.top ? cudaLaunchKernelEx(&cfg, score_kernel<T, true>, p) : cudaLaunchKernelEx(&cfg, score_kernel<T, false>, p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 }  // namespace
@@ -724,12 +836,13 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   p.top_ids = a.top_ids, p.top_logprobs = a.top_logprobs;
   // a cluster for a row while that still leaves every CTA an SM of its own
   // and 16 KB of logits
+  const int sms = sm_count();
   int ranks = 1;
-  while (ranks < 8 && a.rows * ranks * 2 <= sm_count() && a.vocab * el_bytes(a.dtype) / (ranks * 2) >= 16384) ranks *= 2;
+  while (ranks < 8 && a.rows * ranks * 2 <= sms && a.vocab * el_bytes(a.dtype) / (ranks * 2) >= 16384) ranks *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = a.dtype == EG_EL_F32    ? launch_score<float>(p, ranks, st)
-                  : a.dtype == EG_EL_BF16 ? launch_score<__nv_bfloat16>(p, ranks, st)
-                                          : launch_score<__half>(p, ranks, st);
+  cudaError_t e = a.dtype == EG_EL_F32    ? launch_score<float>(p, ranks, sms, st)
+                  : a.dtype == EG_EL_BF16 ? launch_score<__nv_bfloat16>(p, ranks, sms, st)
+                                          : launch_score<__half>(p, ranks, sms, st);
   return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching token_logprobs");
 }
 
