@@ -121,7 +121,8 @@ struct TopShared {
   alignas(16) float groups[2][32];         // maxima of 32 groups of threads
   uint64_t least;            // a value has to reach this to be a candidate
   int count;                 // candidates that asked for a place
-  int lost;                  // some candidates or vectors found none
+  int lost;                  // some candidates or notes found none
+  int flood;                 // a warp has more notes than two for a thread
   int2 queue[kWarps][kQueue];  // a thread's batches above the bar: the first vector, and the largest value
 };
 
@@ -148,26 +149,25 @@ __device__ __forceinline__ int better_than(const uint64_t* list, int n, uint64_t
   return better;
 }
 
-// The best `top` of the candidates into kept, in order; kept has room for the
-// next ones to be better than its last.  All threads; the place of each is the
-// number of better ones.
+// The best `top` of the candidates into kept, in order.  All threads, after a
+// barrier that follows the last candidate (`waiting` is zero behind it); the
+// place of each is the number of better ones.  Ends with a barrier.
 __device__ __forceinline__ void select_top(TopShared& sh, int top) {
-  sync_lookers();
-  const int n = min(sh.count, kWaiting), padded = min((n + 15) & ~15, kWaiting);
-  if (n + static_cast<int>(threadIdx.x) < padded) sh.waiting[n + threadIdx.x] = 0;
-  if (threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
-  if (threadIdx.x == 0) sh.least = 0;
+  const int n = min(sh.count, kWaiting);
+  if (static_cast<int>(threadIdx.x) >= n && threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
+  uint64_t least = 0;
   if (n > kThreads) {
     // more than one for a thread: only what reaches the `top`-th of the
     // threads' best is placed
     uint64_t best = 0;
     for (int at = threadIdx.x; at < n; at += kThreads) best = max(best, sh.waiting[at]);
     sh.bests[threadIdx.x] = best;
+    if (threadIdx.x == 0) sh.least = 0;
     sync_lookers();
     if (better_than(sh.bests, kThreads, best) == top - 1) sh.least = best;
+    sync_lookers();
+    least = sh.least;
   }
-  sync_lookers();
-  const uint64_t least = sh.least;
   for (int at = threadIdx.x; at < n; at += kThreads) {
     const uint64_t mine = sh.waiting[at];
     if (mine < least) continue;
@@ -175,6 +175,12 @@ __device__ __forceinline__ void select_top(TopShared& sh, int top) {
     if (place < top) sh.kept[place] = mine;
   }
   sync_lookers();
+}
+
+// Ready for the next row's candidates; a barrier has to come before the first.
+__device__ __forceinline__ void clear_top(TopShared& sh) {
+  for (int i = threadIdx.x; i < kWaiting; i += kThreads) sh.waiting[i] = 0;
+  if (threadIdx.x == 0) sh.count = sh.lost = sh.flood = 0;
 }
 
 // The outputs of one row by one thread group of the CTA that holds the sums.
@@ -212,15 +218,6 @@ __device__ __forceinline__ Sums warp_join(Sums v, int lanes) {
       t += __shfl_xor_sync(0xffffffffu, t, o);
     }
   return {m, s, t};
-}
-
-// The CTA's sums, for every thread.
-__device__ __forceinline__ Sums block_join(Sums v, Sums* warps) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  v = warp_join(v, 32);
-  if (lane == 0) warps[warp] = v;
-  sync_lookers();
-  return warp_join(warps[lane % kWarps], kWarps);
 }
 
 // A row whose maximum is so low, so high or so infinite that the pass above
@@ -368,7 +365,8 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
       else c[u].w[0] = c[u].w[1] = c[u].w[2] = c[u].w[3] = kNothing<T>;
     }
   };
-  if (sync_lookers_or(queued > 64 || bar == -CUDART_INF_F)) {
+  if (sh.flood || bar == -CUDART_INF_F) {
+    if (threadIdx.x == 0) sh.least = 0;
     uint64_t best = 0;
     for (int i = lane; i < queued; i += 32) {
       Chunk<T, V> c[kUnroll];
@@ -422,6 +420,8 @@ __device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int
   if (threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
   for (int32_t at = part.from; at < part.to || at == part.from; at += kLot) {
     sync_lookers();
+    clear_top(sh);
+    sync_lookers();
     const uint64_t last = sh.kept[top - 1];
     if (threadIdx.x < top) sh.waiting[threadIdx.x] = sh.kept[threadIdx.x];
     if (threadIdx.x == 0) sh.count = top;
@@ -432,6 +432,7 @@ __device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int
     if (at == part.from && part.odd_id >= 0) offer_top(sh, least, part.odd, part.odd_id);
     if (static_cast<int>(threadIdx.x) < kLot && v < part.to)
       for (int i = 0; i < V; ++i) offer_top(sh, least, El<T>::to_float(part.body[static_cast<int64_t>(v) * V + i]), part.head + v * V + i);
+    sync_lookers();
     select_top(sh, top);
   }
 }
@@ -483,6 +484,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScorePara
     fence_mbar_init();
     sh.abort = 0;
   }
+  if (TOP && threadIdx.x < kThreads) clear_top(sh.top);
   __syncthreads();
   if (threadIdx.x >= kThreads) {
     if (threadIdx.x == kThreads) {
@@ -520,7 +522,6 @@ __global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScorePara
   const int32_t vocab = static_cast<int32_t>(p.vocab), whole = part.head + (vocab - part.head) / V * V;
   constexpr float low = kLowest<T>;
   Sums acc{low, 0.0f, 0.0f};
-  if (TOP && threadIdx.x == 0) sh.top.least = 0, sh.top.count = sh.top.lost = 0;
   // the given token's logit, long before it is needed
   const int64_t token = p.tokens ? p.tokens[row] : -1;
   const bool given = token >= 0 && token < p.vocab;
@@ -538,7 +539,6 @@ __global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScorePara
     acc.m = c, acc.s = ex2(y), acc.t = acc.s * y;
   }
 
-  if (TOP) sync_lookers();
   float bar = -CUDART_INF_F;  // a value below this is no candidate
   float seen = -CUDART_INF_F; // this thread's largest value
   int turn = 0, queued = 0;   // bars so far; vectors this warp has noted
@@ -630,13 +630,22 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
   }
 
   if (gave_up) acc.m = __int_as_float(0x7FC00000);
-  Sums all = block_join(acc, sh.warps);
+  // the warps' sums, and the last bar, over one barrier
+  acc = warp_join(acc, 32);
+  if ((threadIdx.x & 31) == 0) sh.warps[threadIdx.x >> 5] = acc;
+  if (TOP) {
+    if (queued > kQueue) sh.top.lost = 1;
+    if (queued > 64) sh.top.flood = 1;
+    bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
+  } else {
+    sync_lookers();
+  }
+  Sums all = warp_join(sh.warps[threadIdx.x % kWarps], kWarps);
   if (TOP) {
     if (part.odd_id >= 0 && !(part.odd < bar)) offer_top(sh.top, candidate(bar, 0xFFFFFFFFu), part.odd, part.odd_id);
-    if (queued > kQueue) sh.top.lost = 1;
-    if (batch > 1) bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
     open_queue(part, sh.top, queued, bar, p.top);
-    if (sync_lookers_or(sh.top.lost)) careful_top(part, sh.top, p.top);
+    sync_lookers();
+    if (sh.top.lost) careful_top(part, sh.top, p.top);
     else select_top(sh.top, p.top);
   }
   if (ranks > 1) {
@@ -653,6 +662,8 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
       }
       if (TOP) {
         // at most 8 x 32 candidates of the row's CTAs
+        clear_top(sh.top);
+        sync_lookers();
         if (threadIdx.x < ranks * p.top) {
           const uint32_t a = cluster_map(smem_u32(&sh.top.kept[threadIdx.x % p.top]), threadIdx.x / p.top);
           uint64_t c;
@@ -660,6 +671,7 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
           sh.top.waiting[threadIdx.x] = c;
         }
         if (threadIdx.x == 0) sh.top.count = static_cast<int>(ranks) * p.top;
+        sync_lookers();
         select_top(sh.top, p.top);
       }
     }
@@ -678,7 +690,8 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
     plain_row(x, p.vocab, reinterpret_cast<float*>(sh.top.bests), &lse, &entropy);
   }
   write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept : nullptr);
-  if (TOP) sync_lookers();  // the next row clears what was written from
+  if (TOP) clear_top(sh.top);
+  else if (ranks == 1) sync_lookers();  // before the next row's sums
   }
 }
 
