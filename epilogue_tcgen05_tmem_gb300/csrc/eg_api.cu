@@ -99,14 +99,30 @@ eg_status host_fail(eg_status s, const char* fmt, ...) {
 
 eg_status host_cuda_fail(cudaError_t e, const char* what) { return cuda_fail(e, what); }
 
-eg_status host_check_device(int* dev) {
+eg_status host_check_device(int* dev, int* sms) {
+  // 0: not asked yet; else the multiprocessors of a device that fits
+  static std::atomic<int> known[64];
   EG_CUDA(cudaGetDevice(dev), "cudaGetDevice");
-  int major = 0, minor = 0;
-  EG_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev), "device query");
-  EG_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev), "device query");
-  if (major != 10 || minor != 3)
-    return fail(EG_ERR_UNSUPPORTED, "the kernels are built for sm_103a; device %d is sm_%d%d", *dev,
-                major, minor);
+  int count = *dev >= 0 && *dev < 64 ? known[*dev].load(std::memory_order_relaxed) : 0;
+  if (count == 0) {
+    int major = 0, minor = 0;
+    EG_CUDA(cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev), "device query");
+    EG_CUDA(cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev), "device query");
+    if (major != 10 || minor != 3)
+      return fail(EG_ERR_UNSUPPORTED, "the kernels are built for sm_103a; device %d is sm_%d%d", *dev,
+                  major, minor);
+    EG_CUDA(cudaDeviceGetAttribute(&count, cudaDevAttrMultiProcessorCount, *dev), "device query");
+    if (*dev >= 0 && *dev < 64) known[*dev].store(count, std::memory_order_relaxed);
+  }
+  if (sms) *sms = count;
+  return EG_OK;
+}
+
+eg_status host_allow_smem(const void* fn, int bytes, int dev, std::atomic<uint64_t>* done) {
+  const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+  if (bit && (done->load(std::memory_order_relaxed) & bit)) return EG_OK;
+  EG_CUDA(cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes), "cudaFuncSetAttribute");
+  done->fetch_or(bit, std::memory_order_relaxed);
   return EG_OK;
 }
 

@@ -4,6 +4,9 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 #include "../../include/eg.h"
 
 namespace eg {
@@ -12,8 +15,12 @@ namespace eg {
 eg_status host_fail(eg_status s, const char* fmt, ...) __attribute__((format(printf, 2, 3)));
 eg_status host_cuda_fail(cudaError_t e, const char* what);
 
-// EG_OK when the current device is one the kernels are built for.
-eg_status host_check_device(int* dev);
+// EG_OK when the current device is one the kernels are built for; its index and
+// its multiprocessors (what does not change is asked of the driver once).
+eg_status host_check_device(int* dev, int* sms = nullptr);
+// Allow `fn` its dynamic shared memory on device `dev`; asked once for each
+// function and device that `done` (one bit a device) has not seen.
+eg_status host_allow_smem(const void* fn, int bytes, int dev, std::atomic<uint64_t>* done);
 
 // cuTensorMapEncodeTiled through the runtime's driver entry point, or NULL.
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,

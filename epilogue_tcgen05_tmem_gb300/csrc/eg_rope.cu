@@ -567,12 +567,6 @@ bool chunks_fit(const eg_rope_args& a, int ch, std::initializer_list<const void*
   return true;
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
 // Lanes of a row's group and the split of a token's rows over warps.  A warp
 // takes all rows of a token (its angles are then read once); where that leaves
 // fewer than four warps a scheduler, the rows are split into batches.
@@ -605,8 +599,7 @@ void launch_backward(const RopeParams& p, bool pairs, int grid, cudaStream_t st)
   else rope_backward_kernel<T, CH, false><<<grid, kThreads, 0, st>>>(p);
 }
 
-eg_status forward(const eg_rope_args& a, RopeParams p, int ch, bool append, cudaStream_t st) {
-  const int sms = sm_count();
+eg_status forward(const eg_rope_args& a, RopeParams p, int ch, bool append, int sms, cudaStream_t st) {
   if (ch) {
     plan_rows(&p, ch, append, sms);
     const int64_t ctas = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
@@ -649,8 +642,8 @@ eg_status eg_qk_norm_rope(const eg_rope_args* args, void* stream) {
   EG_TRY(check_rows("k", a.k, a.k_token, a.k_head, a.kv_heads, a.tokens, a));
   EG_TRY(check_rows("k_out", a.k_out, a.ko_token, a.ko_head, a.kv_heads, a.tokens, a));
   if (a.tokens == 0 || a.q_heads + a.kv_heads == 0) return EG_OK;
-  int dev = 0;
-  EG_TRY(host_check_device(&dev));
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
   int ch = 0;
   for (int c : {8, 4}) {
     if (ch || (c == 8 && a.dtype == EG_EL_F32)) continue;
@@ -660,7 +653,7 @@ eg_status eg_qk_norm_rope(const eg_rope_args* args, void* stream) {
                     kon * a.ko_token, kon * a.ko_head}))
       ch = c;
   }
-  return forward(a, base_params(a), ch, false, static_cast<cudaStream_t>(stream));
+  return forward(a, base_params(a), ch, false, sms, static_cast<cudaStream_t>(stream));
 }
 
 eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache, const int64_t* slots, void* stream) {
@@ -683,8 +676,8 @@ eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache, const
   if (!slots) return host_fail(EG_ERR_INVALID_ARG, "slots is NULL");
   if (reinterpret_cast<uintptr_t>(slots) % 8)
     return host_fail(EG_ERR_INVALID_ARG, "slots are not aligned to their elements");
-  int dev = 0;
-  EG_TRY(host_check_device(&dev));
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
   RopeParams p = base_params(a);
   p.q_heads = a.q_heads;
   p.slots = slots;
@@ -702,13 +695,15 @@ eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache, const
                     kon * a.v_token, kon * a.v_head, cache->page_stride, cache->token_stride, cache->head_stride}))
       ch = c;
   }
-  return forward(a, p, ch, true, static_cast<cudaStream_t>(stream));
+  return forward(a, p, ch, true, sms, static_cast<cudaStream_t>(stream));
 }
 
 eg_status eg_qk_norm_rope_workspace_bytes(const eg_rope_args* fwd, size_t* out) {
   EG_TRY(check_args(fwd));
   if (!out) return host_fail(EG_ERR_INVALID_ARG, "out is NULL");
-  *out = (fwd->q_weight || fwd->k_weight) ? static_cast<size_t>(backward_ctas(*fwd, sm_count())) * 2 * fwd->head_dim * 4 : 0;
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
+  *out = (fwd->q_weight || fwd->k_weight) ? static_cast<size_t>(backward_ctas(*fwd, sms)) * 2 * fwd->head_dim * 4 : 0;
   return EG_OK;
 }
 
@@ -727,9 +722,8 @@ eg_status eg_qk_norm_rope_backward(const eg_rope_args* fwd, const eg_rope_grads*
     if (reinterpret_cast<uintptr_t>(w) % 4) return host_fail(EG_ERR_INVALID_ARG, "a weight's gradient is not aligned to its elements");
   float* dqw = a.q_weight ? d.dq_weight : nullptr;
   float* dkw = a.k_weight ? d.dk_weight : nullptr;
-  int dev = 0;
-  EG_TRY(host_check_device(&dev));
-  const int sms = sm_count();
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
   const int ctas = backward_ctas(a, sms);
   if (dqw || dkw) {
     if (!d.workspace || reinterpret_cast<uintptr_t>(d.workspace) % 16)

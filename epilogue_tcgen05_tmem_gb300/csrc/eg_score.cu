@@ -28,7 +28,7 @@ constexpr int kThreads = 256;     // that look at values; one more warp loads
 constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;        // 16-byte vectors of a thread and batch
 constexpr int kBatchBytes = kThreads * kUnroll * 16;
-constexpr int kStages = 3;        // batches in flight of a CTA
+constexpr int kStages = 2;        // batches in flight of a CTA
 constexpr int kMostTop = 32;
 constexpr int kWaiting = 1024;    // room for candidates of one selection
 constexpr int kQueue = 128;       // room of a warp for notes of threads' batches that may hold one
@@ -379,12 +379,15 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
         if (v < part.to)
 #pragma unroll
           for (int j = 0; j < V; ++j) best = max(best, candidate(f[j], static_cast<uint32_t>(part.head + v * V + j)));
-        c[0] = c[1], c[1] = c[2], c[2] = c[3];
+#pragma unroll
+        for (int i = 0; i + 1 < kUnroll; ++i) c[i] = c[i + 1];
       }
     }
     sh.bests[threadIdx.x] = best;
     sync_lookers();
-    if (best && better_than(sh.bests, kThreads, best) == top - 1) sh.least = best;
+    // only the first threads have any in a short row
+    const int teams = min(kThreads, (part.to - part.from + 31) & ~31);
+    if (best && better_than(sh.bests, teams, best) == top - 1) sh.least = best;
     sync_lookers();
     least = max(least, sh.least);
   }
@@ -404,7 +407,8 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
         for (int j = 0; j < V; ++j)
           if (!(f[j] < bar)) offer_top(sh, least, f[j], part.head + v * V + j);
       }
-      c[0] = c[1], c[1] = c[2], c[2] = c[3];
+#pragma unroll
+      for (int i = 0; i + 1 < kUnroll; ++i) c[i] = c[i + 1];
     }
   }
 }
@@ -470,7 +474,7 @@ __device__ __forceinline__ bool wait_batch(uint64_t* bar, uint32_t phase, int* a
 // loading warp streams them into a ring of batches and runs ahead into the
 // next row, so the memory stays busy while a row is being finished.
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScoreParams p) {
+__global__ void __launch_bounds__(kThreads + 32, 4) score_kernel(const ScoreParams p) {
   constexpr int V = kVec<T>;
   constexpr int W = 4;  // words of a vector
   extern __shared__ __align__(128) uint8_t raw[];
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScorePara
     }
     return;
   }
-  uint32_t batches = 0;
+  uint32_t slot = 0, turns = 0;  // place in the ring, and how often it was passed
   for (int64_t row = first_row; row < p.rows; row += row_step) {
   const T* x = static_cast<const T*>(p.logits) + row * p.row_stride;
   // values before the first 16-byte boundary, whole vectors, and the rest
@@ -547,8 +551,7 @@ __global__ void __launch_bounds__(kThreads + 32, 3) score_kernel(const ScorePara
   for (int32_t at = part.from; at < part.to || batch == 0; at += kUnroll * kThreads, ++batch) {
     uint32_t now[kUnroll][W];
     if (part.from < part.to) {
-      const int slot = batches % kStages;
-      if (!wait_batch(&sh.full[slot], batches / kStages, &sh.abort)) gave_up = true;
+      if (!wait_batch(&sh.full[slot], turns, &sh.abort)) gave_up = true;
       const uint4* vec = reinterpret_cast<const uint4*>(sh.ring[slot]);
 const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
 #pragma unroll
@@ -564,7 +567,7 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
       }
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.empty[slot]);
-      ++batches;
+      if (++slot == kStages) slot = 0, ++turns;
     } else {
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
@@ -572,7 +575,11 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
     uint32_t high[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) high[u] = word_max<T>(word_max<T>(now[u][0], now[u][1]), word_max<T>(now[u][2], now[u][3]));
-    const float most = word_top<T>(word_max<T>(word_max<T>(high[0], high[1]), word_max<T>(high[2], high[3])));
+#pragma unroll
+    for (int step = 1; step < kUnroll; step *= 2)
+#pragma unroll
+      for (int u = 0; u + step < kUnroll; u += 2 * step) high[u] = word_max<T>(high[u], high[u + step]);
+    const float most = word_top<T>(high[0]);
     if (TOP) {
       seen = fmaxf(seen, most);
       if (batch == 0) bar = group_bar(sh.top, seen, p.top, turn++);
@@ -793,21 +800,17 @@ eg_status check_score(const eg_score_args* a) {
   return EG_OK;
 }
 
-int sm_count() {
-  int dev = 0, sms = 152;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
-}
-
-template <typename T>
-cudaError_t launch_score(const ScoreParams& p, int ranks, int sms, cudaStream_t st) {
+template <typename T, bool TOP>
+eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaStream_t st) {
+  static std::atomic<uint64_t> done{0};
   cudaLaunchConfig_t cfg{};
-  auto kernel = p.top ? score_kernel<T, true> : score_kernel<T, false>;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(sizeof(RowShared)));
-  if (e != cudaSuccess) return e;
-  // three CTAs an SM take rows in turn; a cluster takes one
-  const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, 3 * sms);
+  auto kernel = score_kernel<T, TOP>;
+  const eg_status s = host_allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(sizeof(RowShared)), dev, &done);
+  if (s != EG_OK) return s;
+  // four CTAs an SM take rows in turn (4096 x 131072 bf16, 20 alternatives:
+  // three with a ring of three batches 250 us, four with two 231 us, two with
+  // four 267 us); a cluster takes one
+  const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, 4 * sms);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
   cfg.blockDim = dim3(kThreads + 32);
   cfg.dynamicSmemBytes = sizeof(RowShared);
@@ -818,7 +821,13 @@ cudaError_t launch_score(const ScoreParams& p, int ranks, int sms, cudaStream_t 
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p);
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching token_logprobs");
+}
+
+template <typename T>
+eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaStream_t st) {
+  return p.top ? launch_score<T, true>(p, ranks, dev, sms, st) : launch_score<T, false>(p, ranks, dev, sms, st);
 }
 
 }  // namespace
@@ -839,8 +848,8 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   if (reinterpret_cast<uintptr_t>(a.top_ids) % 8) return host_fail(EG_ERR_INVALID_ARG, "top_ids is not aligned to its elements");
   if (a.rows == 0) return EG_OK;
   if (a.top > a.vocab) return host_fail(EG_ERR_INVALID_ARG, "top=%d of %lld logits", a.top, (long long)a.vocab);
-  int dev = 0;
-  if ((s = host_check_device(&dev)) != EG_OK) return s;
+  int dev = 0, sms = 0;
+  if ((s = host_check_device(&dev, &sms)) != EG_OK) return s;
   ScoreParams p{};
   p.rows = a.rows, p.vocab = a.vocab, p.row_stride = a.row_stride;
   p.logits = a.logits, p.tokens = a.tokens;
@@ -849,14 +858,12 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   p.top_ids = a.top_ids, p.top_logprobs = a.top_logprobs;
   // a cluster for a row while that still leaves every CTA an SM of its own
   // and 16 KB of logits
-  const int sms = sm_count();
   int ranks = 1;
   while (ranks < 8 && a.rows * ranks * 2 <= sms && a.vocab * el_bytes(a.dtype) / (ranks * 2) >= 16384) ranks *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = a.dtype == EG_EL_F32    ? launch_score<float>(p, ranks, sms, st)
-                  : a.dtype == EG_EL_BF16 ? launch_score<__nv_bfloat16>(p, ranks, sms, st)
-                                          : launch_score<__half>(p, ranks, sms, st);
-  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching token_logprobs");
+  return a.dtype == EG_EL_F32    ? launch_score<float>(p, ranks, dev, sms, st)
+         : a.dtype == EG_EL_BF16 ? launch_score<__nv_bfloat16>(p, ranks, dev, sms, st)
+                                 : launch_score<__half>(p, ranks, dev, sms, st);
 }
 
 eg_status eg_token_logprobs_backward(const eg_score_args* args, const eg_score_grads* grads, void* stream) {

@@ -150,8 +150,9 @@ int rows_of(const eg_tree_plan& pl) {
 
 eg_status set_up(eg_tree_plan* pl) {
   int sms = 0;
-  cudaError_t e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, pl->device);
-  if (e != cudaSuccess) return host_cuda_fail(e, "device query");
+  const eg_status s = host_check_device(&pl->device, &sms);
+  if (s != EG_OK) return s;
+  cudaError_t e = cudaSuccess;
   const eg_tree_problem& p = pl->prob;
   pl->hd = p.head_dim <= 64 ? 64 : 128;
   const int group = p.q_heads / p.kv_heads;

@@ -102,85 +102,106 @@ def declare(L: ctypes.CDLL) -> None:
         f.argtypes, f.restype = args, ctypes.c_int
 
 
-def _eg():
-    import epilogue_tcgen05_tmem_gb300 as eg
-    return eg
+class _Bound:
+    """torch and the library, bound at the first call: these calls are as short
+    as the kernels they launch, so nothing is looked up twice."""
+    ready = False
+
+    @classmethod
+    def load(cls):
+        import torch
+
+        import epilogue_tcgen05_tmem_gb300 as eg
+        lib = eg.lib()
+        cls.eg, cls.torch, cls.empty = eg, torch, torch.empty
+        cls.raw_stream, cls.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        cls.f32, cls.i32, cls.i64 = torch.float32, torch.int32, torch.int64
+        cls.code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+        for name in EXPORTED:
+            setattr(cls, name[3:], staticmethod(getattr(lib, name)))
+        cls.ready = True
 
 
-_CODES = {}
+_b = _Bound
+
+
+def _fail(status):
+    raise _b.eg.EgError(status, _b.eg.last_error_detail())
 
 
 def _code(t) -> int:
-    if not _CODES:
-        import torch
-        _CODES.update({torch.bfloat16: 0, torch.float16: 1, torch.float32: 2})
     try:
-        return _CODES[t.dtype]
+        return _b.code[t.dtype]
     except KeyError:
         raise ValueError(f"bf16, fp16 or float32 tensors are taken, not {t.dtype}") from None
 
 
 def _stream_of(t, stream):
     """The stream to queue on; the tensor's device has to be the current one."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError("CUDA tensors are taken")
-    at = t.device.index
-    if at != torch._C._cuda_getDevice():
+    at = t.get_device()
+    if at != _b.current():
+        if at < 0:
+            raise ValueError("CUDA tensors are taken")
         raise ValueError(f"the tensors are on cuda:{at}, which is not the current device")
-    return torch._C._cuda_getCurrentRawStream(at) if stream is None else stream
+    return _b.raw_stream(at) if stream is None else stream
 
 
 def _new(shape, dtype, device, stream):
     """An uninitialised tensor, allocated for the stream that the call is queued on."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=device)):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _b.empty(shape, dtype=dtype, device=device)
+    cuda = _b.torch.cuda
+    with cuda.stream(cuda.ExternalStream(stream, device=device)):
+        return _b.empty(shape, dtype=dtype, device=device)
 
 
-def _rows(name, t, like=None, heads=None):
+def _rows(name, t, shape, dtype, device):
     """(pointer, token stride, head stride) of a [tokens, heads, head_dim] tensor."""
-    if t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with a contiguous last dimension")
-    if like is not None and (t.dtype != like.dtype or t.shape[0] != like.shape[0] or t.shape[2] != like.shape[2]
-                             or t.device != like.device or (heads is not None and t.shape[1] != heads)):
-        raise ValueError(f"{name} {tuple(t.shape)} {t.dtype} does not match {tuple(like.shape)} {like.dtype}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    s = t.stride()
+    if t.shape != shape or t.dtype is not dtype or t.device != device or (s[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} with a contiguous last dimension: got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), s[0], s[1]
 
 
 def _side(name, t, dtype, shape, device):
     """Pointer of a contiguous side input, 0 for None."""
     if t is None:
         return 0
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape} on {device}: got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _table(cos_sin, q):
-    """(pointer, positions, rot_dim) of the table of cosines and sines."""
-    import torch
-    if cos_sin is None:
-        return 0, 0, 0
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or not cos_sin.is_contiguous() or cos_sin.device != q.device:
-        raise ValueError("cos_sin must be a contiguous float32 tensor [positions, rot_dim] on the tensors' device")
-    return cos_sin.data_ptr(), cos_sin.shape[0], cos_sin.shape[1]
+def _heads(name, t):
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    return t.shape
 
 
-def _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, page, v=(0, 0, 0), q_heads=None):
-    import torch
-    t, dim = k.shape[0], k.shape[2]
-    hq = q.shape[1] if q is not None else 0
-    table, count, rot = _table(cos_sin, k)
-    qp, qt, qh = _rows("q", q, k) if q is not None else (0, 0, 0)
-    kp, kt, kh = _rows("k", k)
-    return (t, hq, k.shape[1], dim, rot, _code(k), int(bool(pairs)), eps, page, table, count,
-            _side("positions", positions, torch.int64, (t,), k.device),
-            _side("q_weight", q_weight, k.dtype, (dim,), k.device),
-            _side("k_weight", k_weight, k.dtype, (dim,), k.device),
-            qp, kp, v[0], qt, qh, kt, kh, v[1], v[2])
+def _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, page, v):
+    """The fields of eg_rope_args up to the outputs."""
+    tokens, heads, dim = shape = _heads("k", k)
+    dtype, device = k.dtype, k.device
+    kp, kt, kh = _rows("k", k, shape, dtype, device)
+    qp = qt = qh = hq = 0
+    if q is not None:
+        hq = _heads("q", q)[1]
+        qp, qt, qh = _rows("q", q, (tokens, hq, dim), dtype, device)
+    vp = vt = vh = 0
+    if v is not None:
+        vp, vt, vh = _rows("v", v, shape, dtype, device)
+    table = count = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dim() != 2 or cos_sin.dtype is not _b.f32 or not cos_sin.is_contiguous() or cos_sin.device != device:
+            raise ValueError("cos_sin must be a contiguous float32 tensor [positions, rot_dim] on the tensors' device")
+        table = cos_sin.data_ptr()
+        count, rot = cos_sin.shape
+    return (tokens, hq, heads, dim, rot, _code(k), 1 if pairs else 0, eps, page, table, count,
+            0 if positions is None else _side("positions", positions, _b.i64, (tokens,), device),
+            0 if q_weight is None else _side("q_weight", q_weight, dtype, (dim,), device),
+            0 if k_weight is None else _side("k_weight", k_weight, dtype, (dim,), device),
+            qp, kp, vp, qt, qh, kt, kh, vt, vh)
 
 
 def qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False,
@@ -190,15 +211,20 @@ def qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, ep
     (cosines, then sines); positions int64 [T] (None: 0, 1, 2, ...).  With
     ``pairs`` neighbouring values are a pair, else values rot_dim / 2 apart.
     Returns (q_out, k_out), new tensors unless given (they may be q and k)."""
-    import torch
-    eg = _eg()
+    if not _b.ready:
+        _b.load()
     st = _stream_of(k, stream)
-    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0)
-    q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
-    k_out = _new(k.shape, k.dtype, k.device, stream) if k_out is None else k_out
-    qo, qot, qoh = _rows("q_out", q_out, q, q.shape[1])
-    ko, kot, koh = _rows("k_out", k_out, k, k.shape[1])
-    eg._check(eg.lib().eg_qk_norm_rope(_pack_rope(*fields, qo, ko, qot, qoh, kot, koh), st))
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0, None)
+    dtype, device = k.dtype, k.device
+    if q_out is None:
+        q_out = _new(q.shape, dtype, device, stream)
+    if k_out is None:
+        k_out = _new(k.shape, dtype, device, stream)
+    qo, qot, qoh = _rows("q_out", q_out, q.shape, dtype, device)
+    ko, kot, koh = _rows("k_out", k_out, k.shape, dtype, device)
+    status = _b.qk_norm_rope(_pack_rope(*fields, qo, ko, qot, qoh, kot, koh), st)
+    if status:
+        _fail(status)
     return q_out, k_out
 
 
@@ -207,40 +233,46 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos_sin, positions=None, q_weigh
     """Gradients of ``qk_norm_rope`` for the given gradients of its outputs:
     (dq, dk, dq_weight, dk_weight), the weights' in float32 (None without a
     weight).  dq / dk may be dq_out / dk_out."""
-    import torch
-    eg = _eg()
+    if not _b.ready:
+        _b.load()
     st = _stream_of(k, stream)
-    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0)
-    qo, qot, qoh = _rows("dq_out", dq_out, q, q.shape[1])
-    ko, kot, koh = _rows("dk_out", dk_out, k, k.shape[1])
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0, None)
+    dtype, device, dim = k.dtype, k.device, k.shape[2]
+    qo, qot, qoh = _rows("dq_out", dq_out, q.shape, dtype, device)
+    ko, kot, koh = _rows("dk_out", dk_out, k.shape, dtype, device)
     args = _pack_rope(*fields, qo, ko, qot, qoh, kot, koh)
-    dq = _new(q.shape, q.dtype, q.device, stream) if dq is None else dq
-    dk = _new(k.shape, k.dtype, k.device, stream) if dk is None else dk
-    pq, qt, qh = _rows("dq", dq, q, q.shape[1])
-    pk, kt, kh = _rows("dk", dk, k, k.shape[1])
+    if dq is None:
+        dq = _new(q.shape, dtype, device, stream)
+    if dk is None:
+        dk = _new(k.shape, dtype, device, stream)
+    pq, qt, qh = _rows("dq", dq, q.shape, dtype, device)
+    pk, kt, kh = _rows("dk", dk, k.shape, dtype, device)
     dqw = dkw = work = None
     need = ctypes.c_size_t(0)
     if q_weight is not None or k_weight is not None:
-        eg._check(eg.lib().eg_qk_norm_rope_workspace_bytes(args, ctypes.byref(need)))
-        work = _new(need.value, torch.uint8, k.device, stream)
-        dqw = _new(q.shape[2], torch.float32, k.device, stream) if q_weight is not None else None
-        dkw = _new(k.shape[2], torch.float32, k.device, stream) if k_weight is not None else None
-    grads = _pack_grads(pq, pk, qt, qh, kt, kh, dqw.data_ptr() if dqw is not None else 0,
-                        dkw.data_ptr() if dkw is not None else 0, work.data_ptr() if work is not None else 0, need.value)
-    eg._check(eg.lib().eg_qk_norm_rope_backward(args, grads, st))
+        status = _b.qk_norm_rope_workspace_bytes(args, ctypes.byref(need))
+        if status:
+            _fail(status)
+        work = _new(need.value // 4, _b.f32, device, stream)
+        dqw = _new(dim, _b.f32, device, stream) if q_weight is not None else None
+        dkw = _new(dim, _b.f32, device, stream) if k_weight is not None else None
+    grads = _pack_grads(pq, pk, qt, qh, kt, kh, 0 if dqw is None else dqw.data_ptr(), 0 if dkw is None else dkw.data_ptr(),
+                        0 if work is None else work.data_ptr(), need.value)
+    status = _b.qk_norm_rope_backward(args, grads, st)
+    if status:
+        _fail(status)
     return dq, dk, dqw, dkw
 
 
-def _cache(k_cache, v_cache, like):
-    """Packed eg_kv_cache of [pages, page_size, kv_heads, head_dim] tensors (views
-    of heads-first storage too), after checking them against `like`'s last dimensions."""
-    for name, c in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if c.dim() != 4 or c.dtype != like.dtype or c.device != like.device or (c.stride(3) != 1 and c.shape[3] > 1):
-            raise ValueError(f"{name} must be {like.dtype} [pages, page_size, kv_heads, head_dim] on {like.device} with a "
-                             "contiguous last dimension")
-    if k_cache.shape != v_cache.shape or k_cache.stride() != v_cache.stride():
-        raise ValueError("k_cache and v_cache must have the same shape and strides")
+def _cache(k_cache, v_cache, shape, dtype, device):
+    """Packed eg_kv_cache of [pages, *shape] tensors (views of heads-first
+    storage too)."""
     s = k_cache.stride()
+    if k_cache.shape[1:] != shape or k_cache.dtype is not dtype or k_cache.device != device or (s[3] != 1 and shape[2] > 1):
+        raise ValueError(f"k_cache must be {dtype} [pages, {', '.join(map(str, shape))}] on {device} with a contiguous last "
+                         f"dimension: got {k_cache.dtype} {tuple(k_cache.shape)} on {k_cache.device}")
+    if v_cache.shape != k_cache.shape or v_cache.stride() != s or v_cache.dtype is not dtype or v_cache.device != device:
+        raise ValueError("k_cache and v_cache must have the same type, shape and strides")
     return _pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], s[0], s[1], s[2])
 
 
@@ -250,23 +282,26 @@ def kv_append(k, v, k_cache, v_cache, slots, q=None, cos_sin=None, positions=Non
     [T, Hk, D] to the paged cache [pages, page_size, Hk, D] at slots int64 [T]
     (page * page_size + place; a slot outside the cache appends nothing).  With
     q the queries are normed and rotated in the same launch; returns q_out."""
-    import torch
-    eg = _eg()
+    if not _b.ready:
+        _b.load()
     st = _stream_of(k, stream)
-    cache = _cache(k_cache, v_cache, k)
-    if k_cache.shape[2] != k.shape[1] or k_cache.shape[3] != k.shape[2]:
-        raise ValueError(f"the cache {tuple(k_cache.shape)} does not hold heads of k {tuple(k.shape)}")
-    if slots is None:
-        raise ValueError("slots is missing")
-    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, k_cache.shape[1],
-                          _rows("v", v, k, k.shape[1]))
-    qo, qot, qoh = 0, 0, 0
+    if slots is None or k_cache.dim() != 4:
+        raise ValueError("slots is missing" if slots is None else "the cache must be [pages, page_size, kv_heads, head_dim]")
+    page = k_cache.shape[1]
+    fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, page, v)
+    dtype, device = k.dtype, k.device
+    cache = _cache(k_cache, v_cache, (page, fields[2], fields[3]), dtype, device)
+    qo = qot = qoh = 0
     if q is not None:
-        q_out = _new(q.shape, q.dtype, q.device, stream) if q_out is None else q_out
-        qo, qot, qoh = _rows("q_out", q_out, q, q.shape[1])
-    eg._check(eg.lib().eg_kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache,
-                                    _side("slots", slots, torch.int64, (k.shape[0],), k.device), st))
-    return q_out if q is not None else None
+        if q_out is None:
+            q_out = _new(q.shape, dtype, device, stream)
+        qo, qot, qoh = _rows("q_out", q_out, q.shape, dtype, device)
+    else:
+        q_out = None
+    status = _b.kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache, _side("slots", slots, _b.i64, (fields[0],), device), st)
+    if status:
+        _fail(status)
+    return q_out
 
 
 # ------------------------------------------------------- tree attention ---
@@ -278,19 +313,26 @@ class TreeAttention:
     must not overlap on the GPU."""
 
     def __init__(self, q_heads, kv_heads, head_dim, dtype="bf16", page_size=16, max_batch=1, max_tree=1):
-        eg = _eg()
+        if not _b.ready:
+            _b.load()
         self.handle = None
         self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
         self.max_batch, self.max_tree = max_batch, max_tree
         h = _p()
         problem = eg_tree_problem(q_heads, kv_heads, head_dim, EL_DTYPES[dtype], page_size, max_batch, max_tree)
-        eg._check(eg.lib().eg_tree_plan_create(ctypes.addressof(problem), ctypes.byref(h)))
-        self.handle, self._dtype = h.value, EL_DTYPES[dtype]
+        status = _b.tree_plan_create(ctypes.addressof(problem), ctypes.byref(h))
+        if status:
+            _fail(status)
+        self.handle = h.value
+        self._dtype = {"bf16": _b.torch.bfloat16, "f16": _b.torch.float16}[dtype]
+        self._place = (page_size, kv_heads, head_dim)
 
     @property
     def workspace_bytes(self) -> int:
-        eg, n = _eg(), ctypes.c_size_t()
-        eg._check(eg.lib().eg_tree_plan_workspace_bytes(self.handle, ctypes.byref(n)))
+        n = ctypes.c_size_t()
+        status = _b.tree_plan_workspace_bytes(self.handle, ctypes.byref(n))
+        if status:
+            _fail(status)
         return n.value
 
     def run(self, q, k_cache, v_cache, block_table, context_lens, q_start, mask=None, scale=None, out=None, lse=None, stream=None):
@@ -302,48 +344,44 @@ class TreeAttention:
         The drafted tokens' own keys and values are in the cache already, after
         the context.  ``scale``: of the scores, 1 / sqrt(head_dim) when None.
         Returns o like q; lse float32 [tokens, q_heads] is written where given."""
-        import torch
-        eg = _eg()
         st = _stream_of(q, stream)
-        qp, qt, qh = _rows("q", q)
-        tokens, heads, dim = q.shape
-        if heads != self.q_heads or dim != self.head_dim or _code(q) != self._dtype:
-            raise ValueError(f"q {tuple(q.shape)} {q.dtype} does not fit the plan")
-        cache = _cache(k_cache, v_cache, q)
-        if k_cache.shape[1:] != (self.page_size, self.kv_heads, dim):
-            raise ValueError(f"the cache {tuple(k_cache.shape)} does not fit the plan")
-        batch = context_lens.shape[0]
-        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != batch or block_table.device != q.device \
-                or (block_table.stride(1) != 1 and block_table.shape[1] > 1):
-            raise ValueError("block_table must be int32 [batch, pages] with contiguous rows on the tensors' device")
-        stride = block_table.shape[1]
-        if batch > 1 and block_table.stride(0) != stride:
-            raise ValueError("block_table must be contiguous")
+        tokens = _heads("q", q)[0]
+        shape, dtype, device = (tokens, self.q_heads, self.head_dim), self._dtype, q.device
+        qp, qt, qh = _rows("q", q, shape, dtype, device)
+        if k_cache.dim() != 4:
+            raise ValueError("the cache must be [pages, page_size, kv_heads, head_dim]")
+        cache = _cache(k_cache, v_cache, self._place, dtype, device)
+        batch, width = block_table.shape
+        table = _side("block_table", block_table, _b.i32, (batch, width), device)
         words = at_mask = 0
         if mask is not None:
-            if mask.dim() != 2 or mask.dtype != torch.int32 or mask.shape[0] != tokens or not mask.is_contiguous() or mask.device != q.device:
-                raise ValueError("mask must be contiguous int32 words [tokens, words] on the tensors' device")
-            words, at_mask = mask.shape[1], mask.data_ptr() or 4  # no words: refused for their number, not taken for no mask
-        out = _new(q.shape, q.dtype, q.device, stream) if out is None else out
-        op, ot, oh = _rows("out", out, q, heads)
-        args = _pack_tree(batch, tokens, qp, op, qt, qh, ot, oh, block_table.data_ptr(), stride,
-                          _side("context_lens", context_lens, torch.int32, (batch,), q.device),
-                          _side("q_start", q_start, torch.int32, (batch + 1,), q.device),
-                          at_mask, words, dim ** -0.5 if scale is None else scale,
-                          _side("lse", lse, torch.float32, (tokens, heads), q.device))
-        eg._check(eg.lib().eg_tree_plan_run(self.handle, args, cache, st))
+            words = mask.shape[1]
+            # a mask without words is refused for their number, not taken for none
+            at_mask = _side("mask", mask, _b.i32, (tokens, words), device) or 4
+        if out is None:
+            out = _new(shape, dtype, device, stream)
+        op, ot, oh = _rows("out", out, shape, dtype, device)
+        args = _pack_tree(batch, tokens, qp, op, qt, qh, ot, oh, table, width,
+                          _side("context_lens", context_lens, _b.i32, (batch,), device),
+                          _side("q_start", q_start, _b.i32, (batch + 1,), device), at_mask, words,
+                          self.head_dim ** -0.5 if scale is None else scale,
+                          0 if lse is None else _side("lse", lse, _b.f32, (tokens, self.q_heads), device))
+        status = _b.tree_plan_run(self.handle, args, cache, st)
+        if status:
+            _fail(status)
         return out
 
     def device_status(self) -> int:
-        return _eg().lib().eg_tree_plan_device_status(self.handle)
+        return _b.tree_plan_device_status(self.handle)
 
     def set_test_stall(self, wait_limit_ns: int, stall_producer: int):
-        eg = _eg()
-        eg._check(eg.lib().eg_tree_plan_set_test_stall(self.handle, wait_limit_ns, int(stall_producer)))
+        status = _b.tree_plan_set_test_stall(self.handle, wait_limit_ns, int(stall_producer))
+        if status:
+            _fail(status)
 
     def close(self):
         if getattr(self, "handle", None):
-            _eg().lib().eg_tree_plan_destroy(self.handle)
+            _b.tree_plan_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -366,29 +404,37 @@ class TokenLogProbs(NamedTuple):
 
 
 def _logits(name, x):
-    if x.dim() != 2 or (x.stride(1) != 1 and x.shape[1] > 1):
-        raise ValueError(f"{name} must be [rows, vocab] with a contiguous last dimension")
-    return x.data_ptr(), (x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1]))
+    """(pointer, row stride) of [rows, vocab] logits."""
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [rows, vocab]")
+    stride, one = x.stride()
+    rows, vocab = x.shape
+    if one != 1 and vocab > 1:
+        raise ValueError(f"{name} must have a contiguous last dimension")
+    return x.data_ptr(), stride if rows > 1 else max(stride, vocab)
 
 
 def token_logprobs(logits, tokens=None, top=0, stream=None) -> TokenLogProbs:
     """Log probabilities of tokens int64 [rows] (an id outside the vocabulary:
     none is given, 0) under logits [rows, vocab], with lse, entropy and the
     ``top`` (0..32) best alternatives, of equal logits the lowest id first."""
-    import torch
-    eg = _eg()
+    if not _b.ready:
+        _b.load()
     st = _stream_of(logits, stream)
     x, stride = _logits("logits", logits)
     rows, vocab = logits.shape
-    given = _side("tokens", tokens, torch.int64, (rows,), logits.device)
-    logprob, lse, entropy = _new((3, rows), torch.float32, logits.device, stream).unbind(0)
+    device, f32 = logits.device, _b.f32
+    given = 0 if tokens is None else _side("tokens", tokens, _b.i64, (rows,), device)
+    logprob, lse, entropy = _new(rows, f32, device, stream), _new(rows, f32, device, stream), _new(rows, f32, device, stream)
     ids = best = None
+    at_ids = at_best = 0
     if top:
-        ids = _new((rows, top), torch.int64, logits.device, stream)
-        best = _new((rows, top), torch.float32, logits.device, stream)
-    eg._check(eg.lib().eg_token_logprobs(
-        _pack_score(rows, vocab, _code(logits), top, x, stride, given, logprob.data_ptr(), lse.data_ptr(), entropy.data_ptr(),
-                    ids.data_ptr() if top else 0, best.data_ptr() if top else 0), st))
+        ids, best = _new((rows, top), _b.i64, device, stream), _new((rows, top), f32, device, stream)
+        at_ids, at_best = ids.data_ptr(), best.data_ptr()
+    status = _b.token_logprobs(_pack_score(rows, vocab, _code(logits), top, x, stride, given, logprob.data_ptr(), lse.data_ptr(),
+                                           entropy.data_ptr(), at_ids, at_best), st)
+    if status:
+        _fail(status)
     return TokenLogProbs(logprob, lse, entropy, ids, best)
 
 
@@ -396,18 +442,22 @@ def token_logprobs_backward(logits, tokens, lse, entropy, d_logprob=None, d_entr
     """The gradient to the logits, from what ``token_logprobs`` gave for them
     and the gradients of its log probabilities and entropies (float32 [rows],
     None: zero).  ``out`` may be the logits themselves."""
-    import torch
-    eg = _eg()
+    if not _b.ready:
+        _b.load()
     st = _stream_of(logits, stream)
     x, stride = _logits("logits", logits)
     rows, vocab = logits.shape
-    out = _new((rows, vocab), logits.dtype, logits.device, stream) if out is None else out
+    device, f32 = logits.device, _b.f32
+    if out is None:
+        out = _new((rows, vocab), logits.dtype, device, stream)
     d, d_stride = _logits("out", out)
-    if out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+    if out.shape != logits.shape or out.dtype is not logits.dtype or out.device != device:
         raise ValueError(f"out {tuple(out.shape)} {out.dtype} does not match {tuple(logits.shape)} {logits.dtype}")
-    side = [_side(n, t, torch.float32, (rows,), logits.device)
+    side = [_side(n, t, f32, (rows,), device)
             for n, t in (("lse", lse), ("entropy", entropy), ("d_logprob", d_logprob), ("d_entropy", d_entropy))]
-    given = _side("tokens", tokens, torch.int64, (rows,), logits.device)
-    eg._check(eg.lib().eg_token_logprobs_backward(
-        _pack_score(rows, vocab, _code(logits), 0, x, stride, given, 0, 0, 0, 0, 0), _pack_score_grads(*side, d, d_stride), st))
+    given = _side("tokens", tokens, _b.i64, (rows,), device)
+    status = _b.token_logprobs_backward(_pack_score(rows, vocab, _code(logits), 0, x, stride, given, 0, 0, 0, 0, 0),
+                                        _pack_score_grads(*side, d, d_stride), st)
+    if status:
+        _fail(status)
     return out
