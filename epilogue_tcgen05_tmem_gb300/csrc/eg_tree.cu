@@ -36,7 +36,8 @@ struct eg_tree_plan {
   uint32_t smem = 0;
   size_t ws_bytes = 0;
   uint8_t* ws = nullptr;  // partial sums, their statistics, the CTAs' ranges, the status word
-  size_t ml_at = 0, meta_at = 0, status_at = 0;
+  size_t ml_at = 0, meta_at = 0, arrivals_at = 0, status_at = 0;
+  bool joins_itself = false;  // the CTA that leaves an item's last part joins it; else a second kernel
   uint64_t wait_limit_ns = 0;
   int stall = 0;
 };
@@ -167,7 +168,8 @@ eg_status set_up(eg_tree_plan* pl) {
   const size_t rows = static_cast<size_t>(pl->grid) * 2 * 128 * pl->q_tiles;
   pl->ml_at = rows * pl->hd * 4;
   pl->meta_at = pl->ml_at + rows * 8;
-  pl->status_at = pl->meta_at + pl->grid * sizeof(TreeMeta);
+  pl->arrivals_at = pl->meta_at + pl->grid * sizeof(TreeMeta);
+  pl->status_at = pl->arrivals_at + (pl->grid * 4 + 15) / 16 * 16;
   pl->ws_bytes = pl->status_at + 16;
   if ((e = cudaMalloc(&pl->ws, pl->ws_bytes)) != cudaSuccess) return host_cuda_fail(e, "allocating the plan's workspace");
   if ((e = cudaMemset(pl->ws + pl->meta_at, 0, pl->ws_bytes - pl->meta_at)) != cudaSuccess) return host_cuda_fail(e, "clearing the plan's workspace");
@@ -175,6 +177,11 @@ eg_status set_up(eg_tree_plan* pl) {
                                 static_cast<int>(pl->smem))) != cudaSuccess)
     return host_cuda_fail(e, "cudaFuncSetAttribute");
   pl->wait_limit_ns = host_wait_limit_ns();
+  // One CTA reads at most the parts of the most CTAs that share an item (those
+  // of a single sequence: the grid over the cached heads): up to 256 KB is
+  // quicker than a second kernel.
+  const int64_t parts = pl->grid / p.kv_heads + 2;
+  pl->joins_itself = parts * rows_of(*pl) * pl->hd * 4 <= 256 * 1024;
   return EG_OK;
 }
 
@@ -231,6 +238,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   p.partial = reinterpret_cast<float*>(plan->ws);
   p.partial_ml = reinterpret_cast<float*>(plan->ws + plan->ml_at);
   p.meta = reinterpret_cast<TreeMeta*>(plan->ws + plan->meta_at);
+  p.arrivals = plan->joins_itself ? reinterpret_cast<int32_t*>(plan->ws + plan->arrivals_at) : nullptr;
   p.status = reinterpret_cast<int32_t*>(plan->ws + plan->status_at);
   p.wait_limit_ns = plan->wait_limit_ns, p.stall = plan->stall;
   CUtensorMap map_q, map_k, map_v;
@@ -245,6 +253,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   cfg.stream = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan), p, map_q, map_k, map_v);
   if (e != cudaSuccess) return host_cuda_fail(e, "launching tree attention");
+  if (plan->joins_itself) return EG_OK;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -265,7 +274,9 @@ eg_status eg_tree_plan_device_status(eg_tree_plan* plan) {
   if ((e = cudaMemcpy(&status, plan->ws + plan->status_at, 4, cudaMemcpyDeviceToHost)) != cudaSuccess)
     return host_cuda_fail(e, "reading the plan's status");
   if (status == 0) return EG_OK;
-  if ((e = cudaMemset(plan->ws + plan->status_at, 0, 4)) != cudaSuccess) return host_cuda_fail(e, "clearing the plan's status");
+  // a CTA that gave up leaves items half counted
+  if ((e = cudaMemset(plan->ws + plan->arrivals_at, 0, plan->ws_bytes - plan->arrivals_at)) != cudaSuccess)
+    return host_cuda_fail(e, "clearing the plan's status");
   return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the tree attention kernel ran past its limit");
 }
 

@@ -50,6 +50,7 @@ struct TreeParams {
   float* partial;       // [CTAs][2][128 q_tiles][HD] sums, then
   float* partial_ml;    // [CTAs][2][128 q_tiles][2] their maximum (log2) and weight
   TreeMeta* meta;       // [CTAs]
+  int32_t* arrivals;    // [CTAs] parts left of the item whose first part that CTA has; NULL: a second kernel joins
   int32_t* status;
   uint64_t wait_limit_ns;
   int32_t stall;        // test hook: the producer issues nothing

@@ -158,6 +158,18 @@ __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq
   return static_cast<int64_t>(tree_item_units(s)) * (s.groups * p.kv_heads);
 }
 
+// The first unit of CTA c, and the CTA that has unit u, when `total` units are
+// cut into `ctas` equal ranges.
+__device__ __forceinline__ int64_t tree_from(int64_t total, int32_t ctas, int32_t c) {
+  if (total < (1 << 20)) return static_cast<uint32_t>(total) * static_cast<uint32_t>(c) / static_cast<uint32_t>(ctas);
+  return total * c / ctas;
+}
+__device__ __forceinline__ int32_t tree_owner(int64_t total, int32_t ctas, int64_t u) {
+  if (total < (1 << 20))
+    return static_cast<int32_t>((static_cast<uint32_t>(u + 1) * static_cast<uint32_t>(ctas) + static_cast<uint32_t>(total) - 1) / static_cast<uint32_t>(total)) - 1;
+  return static_cast<int32_t>(((u + 1) * ctas + total - 1) / total) - 1;
+}
+
 constexpr int kTreeNear = 16;  // sequences whose lengths a CTA keeps in shared memory
 
 // A walk over a CTA's range: one segment (consecutive key tiles of one item)
@@ -169,6 +181,7 @@ struct TreeWalk {
   int64_t at, to;
   // the segment
   int32_t head, row0, rows, first, count;
+  int64_t begin;       // the first unit of its item
 
   const int32_t (*near_)[4];  // start, n, ctx of the sequences from near_b on
   int32_t near_b;
@@ -192,6 +205,7 @@ struct TreeWalk {
       const int32_t item = units >> 32 ? static_cast<int32_t>(idx / each) : static_cast<int32_t>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(each));
       const int32_t in = static_cast<int32_t>(idx - static_cast<int64_t>(item) * each);
       const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(each - in), to - at));
+      begin = at - in;
       at += take;
       // units 0..kTreeFixed-1 of an item stand for no tile
       first = max(in - kTreeFixed, 0);
@@ -215,6 +229,7 @@ struct TreeShared {
   int32_t abort;
   int32_t poisoned[2];            // the last segment (counted from 1) that found a value that is not finite
   int32_t b;
+  int32_t joins;                  // this CTA has the last part of an item
   int64_t before;
   int64_t warps[2][12];
   int32_t near_[kTreeNear][4];
@@ -225,6 +240,39 @@ static_assert(sizeof(TreeShared) <= TreeSmem<64>::kExtra, "fits the room after t
 // Position of a tile's load in the ring's order: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ uint32_t tree_pos_k(uint32_t i) { return i == 0 ? 0 : 2 * i - 1; }
 __device__ __forceinline__ uint32_t tree_pos_v(uint32_t i, uint32_t count) { return i + 1 < count ? 2 * i + 2 : 2 * count - 1; }
+
+// Four columns of one row of an item that CTAs lead..last have parts of, joined
+// in the order of the CTAs.
+template <typename T, int HD>
+__device__ __forceinline__ void tree_join_piece(const TreeParams& p, int lead, int last, int r, int col, int64_t packed, int head) {
+  constexpr float kShift = El<T>::kBf16 ? 0.0f : 7.0f;
+  const int64_t rows = static_cast<int64_t>(128) * p.q_tiles;
+  const float2* ml = reinterpret_cast<const float2*>(p.partial_ml) + r;
+  const float* part = p.partial + static_cast<int64_t>(col) * rows + r * 4;
+  // both to the reference of the largest maximum so far
+  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float top = -CUDART_INF_F, weight = 0.0f;
+#pragma unroll 4
+  for (int c = lead; c <= last; ++c) {
+    const int64_t slot = (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * rows;
+    const float2 w = __ldcg(ml + slot);
+    const float4 x = __ldcg(reinterpret_cast<const float4*>(part + slot * HD));
+    const float next = fmaxf(top, w.x);
+    const float ref = next == -CUDART_INF_F ? 0.0f : next;
+    const float f_old = tree_ex2(top - ref), f = tree_ex2(w.x - ref);
+    top = next;
+    weight = weight * f_old + w.y * f;
+    y.x *= f_old, y.y *= f_old, y.z *= f_old, y.w *= f_old;
+    if (w.y != 0.0f) y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
+  }
+  const float scale = weight == 0.0f ? 0.0f : 1.0f / weight;
+  if (col < p.head_dim) {
+    T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head + col;
+    *reinterpret_cast<uint2*>(o) = make_uint2(El<T>::pack2(y.x * scale, y.y * scale), El<T>::pack2(y.z * scale, y.w * scale));
+  }
+  if (p.lse && col == 0)
+    p.lse[packed * p.q_heads + head] = weight == 0.0f ? -CUDART_INF_F : (top - kShift + __log2f(weight)) * 0.6931471805599453f;
+}
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -286,7 +334,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (blockIdx.x == 0 && tid == 0) p.meta[0].ctas = 0;
     return;
   }
-  const int64_t from = total * blockIdx.x / ctas, to = total * (blockIdx.x + 1) / ctas;
+  const int64_t from = tree_from(total, ctas, blockIdx.x), to = tree_from(total, ctas, blockIdx.x + 1);
   if (once) {
     if (base + upto - mine <= from && from < base + upto) sh.b = tid, sh.before = base + upto - mine;
   } else {
@@ -571,33 +619,27 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         const bool edge = key0 + static_cast<int>(kTreeKeys) > walk.seq.ctx;
         if (!(ok = wait_all(&sh.s_full[s], uses))) break;
         tc_fence_after();
-        if (busy && edge) {
-          // a tile with drafted places or past the end: -infinity where the
-          // row does not attend to.  In tensor memory and in a loop: the code
-          // of rare tiles stays small and out of the others' registers.
-#pragma unroll 1
-          for (int w = 0; w < 4; ++w) {
-            const int d = walk.seq.ctx - (key0 + 32 * w);  // context places of this word
-            const uint32_t bits = d >= 32  ? 0xFFFFFFFFu
-                                  : d <= 0 ? drafted_bits(-d)
-                                           : ((1u << d) - 1u) | (drafted_bits(0) << d);
-            uint32_t x[32];
-            tmem_ld32p(t_s + w * 32, x);
-            tmem_ld_wait();
-            reg_fence<32>(x);
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(bits >> j & 1u)) x[j] = 0xFF800000u;
-            tmem_st32(t_s + w * 32, x);
-          }
-          tmem_st_wait();
-        }
         if (busy) {
           uint32_t x[128];
 #pragma unroll
           for (int j = 0; j < 4; ++j) tmem_ld32p(t_s + j * 32, x + j * 32);
           tmem_ld_wait();
           reg_fence<128>(x);
+          if (edge) {
+            // a tile with drafted places or past the end: -infinity where the
+            // row does not attend to
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int d = walk.seq.ctx - (key0 + 32 * w);  // context places of this word
+              const uint32_t bits = d >= 32  ? 0xFFFFFFFFu
+                                    : d <= 0 ? drafted_bits(-d)
+                                             : ((1u << d) - 1u) | (drafted_bits(0) << d);
+              if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) continue;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(bits >> j & 1u)) x[w * 32 + j] = 0xFF800000u;
+            }
+          }
           float top[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(x[j]);
@@ -646,7 +688,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tmem_st_wait();
         }
         fresh = false;
-        if (edge && (walk.seq.keys < key0 + static_cast<int>(kTreeKeys) || p.mask || drafted > 1)) {
+        const bool cut = walk.seq.keys < key0 + static_cast<int>(kTreeKeys), scan = p.mask || drafted > 1;
+        if (edge && (cut || scan)) {
           // values of places past the end become zero, and so do drafted
           // values that are not finite: a weight of zero times one would
           // reach rows that do not attend to it (`repair` adds it to those
@@ -658,7 +701,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (key >= walk.seq.keys) {
 #pragma unroll 4
             for (int j = 0; j < kChunks * 8; ++j) *reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
-          } else if (key >= walk.seq.ctx) {
+          } else if (scan && key >= walk.seq.ctx) {
             constexpr uint32_t kInf = El<T>::kBf16 ? 0x7F80u : 0x7C00u;
             bool found = false;
 #pragma unroll 1
@@ -777,11 +820,34 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
       // the other warpgroup's accumulator is read: it may be written again
+      if (!whole && p.arrivals) __threadfence();
       tc_fence_before();
       mbar_arrive(&sh.exchange);
       if (!(ok = wait_all(&sh.exchange, exchanges))) break;
       ++exchanges;
       tc_fence_after();
+      if (!whole && p.arrivals) {
+        // the CTA that leaves the last part of the item joins all of them
+        const int32_t lead = tree_owner(total, ctas, walk.begin + kTreeFixed);
+        const int32_t last = tree_owner(total, ctas, walk.begin + tree_item_units(walk.seq) - 1);
+        if (tid == 0) {
+          const int before = atomicAdd(p.arrivals + lead, 1);
+          sh.joins = before == last - lead;
+          if (before == last - lead) p.arrivals[lead] = 0;
+          __threadfence();
+        }
+        mbar_arrive(&sh.exchange);
+        if (!(ok = wait_all(&sh.exchange, exchanges))) break;
+        ++exchanges;
+        if (sh.joins) {
+          const int pieces = walk.rows * (HD / 4);
+          for (int i = tid; i < pieces; i += 256) {
+            const int r_ = i % walk.rows, t_ = (walk.row0 + r_) / p.group;
+            tree_join_piece<T, HD>(p, lead, last, r_, i / walk.rows * 4, walk.seq.start + t_,
+                                   walk.head * p.group + (walk.row0 + r_) - t_ * p.group);
+          }
+        }
+      }
       base += 2 * count;
     }
   }
@@ -795,13 +861,13 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   }
 }
 
-// Joins the partial results of the items that a cut between CTAs divides: the
-// blocks of cut x (between CTAs x - 1 and x) serve the item whose first cut it
-// is, eight rows each.  A thread has four columns of a row; a warp has eight
-// rows of 16 columns, which is how they lie side by side.
+// Joins the partial results of the items that a cut between CTAs divides, where
+// the main kernel leaves that to it: the blocks of cut x (between CTAs x - 1
+// and x) serve the item whose first cut it is, eight rows each.  A thread has
+// four columns of a row; a warp has eight rows of 16 columns, which is how they
+// lie side by side.
 template <typename T, int HD>
 __global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
-  constexpr float kShift = El<T>::kBf16 ? 0.0f : 7.0f;
   griddep_wait();
   const int cut = blockIdx.x + 1;
   const int ctas = p.meta[0].ctas;
@@ -810,41 +876,13 @@ __global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
   if (cut >= ctas || m.from <= m.begin || from_before > m.begin) return;
   // the CTAs with the item's first tile and with its last: those between them
   // have some too
-  const int lead = static_cast<int>(((m.begin + kTreeFixed + 1) * ctas + m.total - 1) / m.total) - 1;
-  const int last = static_cast<int>((m.end * ctas + m.total - 1) / m.total) - 1;
+  const int lead = tree_owner(m.total, ctas, m.begin + kTreeFixed), last = tree_owner(m.total, ctas, m.end - 1);
   if (lead == last) return;
   const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (lane & 7), col = ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4;
+  const int r = blockIdx.y * 8 + (lane & 7);
   if (r >= m.rows) return;
-  const int64_t rows = static_cast<int64_t>(128) * p.q_tiles;
-  const float2* ml = reinterpret_cast<const float2*>(p.partial_ml) + r;
-  const float* part = p.partial + static_cast<int64_t>(col) * rows + r * 4;
-  // both to the reference of the largest maximum so far
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float top = -CUDART_INF_F, weight = 0.0f;
-#pragma unroll 4
-  for (int c = lead; c <= last; ++c) {
-    const int64_t slot = (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * rows;
-    const float2 w = ml[slot];
-    const float4 x = *reinterpret_cast<const float4*>(part + slot * HD);
-    const float next = fmaxf(top, w.x);
-    const float ref = next == -CUDART_INF_F ? 0.0f : next;
-    const float f_old = tree_ex2(top - ref), f = tree_ex2(w.x - ref);
-    top = next;
-    weight = weight * f_old + w.y * f;
-    y.x *= f_old, y.y *= f_old, y.z *= f_old, y.w *= f_old;
-    if (w.y != 0.0f) y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
-  }
   const int t = (m.row0 + r) / p.group;
-  const int64_t packed = m.start + t;
-  const int head = m.head * p.group + (m.row0 + r) - t * p.group;
-  const float scale = weight == 0.0f ? 0.0f : 1.0f / weight;
-  if (col < p.head_dim) {
-    T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head + col;
-    *reinterpret_cast<uint2*>(o) = make_uint2(El<T>::pack2(y.x * scale, y.y * scale), El<T>::pack2(y.z * scale, y.w * scale));
-  }
-  if (p.lse && col == 0)
-    p.lse[packed * p.q_heads + head] = weight == 0.0f ? -CUDART_INF_F : (top - kShift + __log2f(weight)) * 0.6931471805599453f;
+  tree_join_piece<T, HD>(p, lead, last, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
 }
 
 }  // namespace eg
