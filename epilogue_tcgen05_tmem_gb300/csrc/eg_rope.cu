@@ -32,6 +32,7 @@ struct RopeParams {
   int32_t lanes;        // lanes of a row's group (power of two, 1..32)
   int32_t groups_q, groups_k, groups_v;  // row groups (32 / lanes rows) of each kind
   int32_t per_warp, parts;  // row groups of one work unit; units of one token
+  int32_t wide_table;   // the table can be read in 16-byte vectors
   float eps, inv_dim;
   const float* cos_sin;
   int64_t max_positions;
@@ -49,7 +50,8 @@ struct RopeParams {
   // backward
   void *dq, *dk;
   int64_t dq_token, dq_head, dk_token, dk_head;
-  float* partial;       // [CTAs][2][head_dim] sums of the weights' gradients
+  float* partial;       // [CTAs][head_dim] sums of a weight's gradient: of keys for the first key_ctas, then of queries
+  int32_t key_ctas, per_warp_k;
 };
 
 // Cosine and sine of the pairs one lane holds.  Pairs past rot_dim are not
@@ -61,14 +63,26 @@ struct Angles {
 };
 
 template <int CH>
-__device__ __forceinline__ void load_angles(const RopeParams& p, int token, int slot, Angles<CH>& a) {
+__device__ __forceinline__ void load_angles(const RopeParams& p, int64_t pos, int slot, Angles<CH>& a) {
   const int half = p.rot_dim >> 1;
   a.turns = 0u;
   if (slot * CH >= half) return;
-  const int64_t pos = p.positions ? p.positions[token] : token;
   const bool ok = pos >= 0 && pos < p.max_positions;
   const float* row = p.cos_sin + (ok ? pos : 0) * p.rot_dim;
   const float bad = __int_as_float(0x7FC00000);
+  if (p.wide_table && slot * CH + CH <= half) {  // rows and halves on 16-byte boundaries
+    a.turns = (1u << CH) - 1u;
+#pragma unroll
+    for (int i = 0; i < CH; i += 4) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row + slot * CH + i)), s = __ldg(reinterpret_cast<const float4*>(row + half + slot * CH + i));
+      a.c[i] = c.x, a.c[i + 1] = c.y, a.c[i + 2] = c.z, a.c[i + 3] = c.w;
+      a.s[i] = s.x, a.s[i + 1] = s.y, a.s[i + 2] = s.z, a.s[i + 3] = s.w;
+    }
+    if (!ok)
+#pragma unroll
+      for (int i = 0; i < CH; ++i) a.c[i] = a.s[i] = bad;
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < CH; ++i) {
     const int at = slot * CH + i;
@@ -78,6 +92,9 @@ __device__ __forceinline__ void load_angles(const RopeParams& p, int token, int 
       a.s[i] = ok ? __ldg(row + half + at) : bad;
     }
   }
+}
+__device__ __forceinline__ int64_t position_of(const RopeParams& p, int token) {
+  return p.rot_dim == 0 || !p.positions ? token : __ldg(p.positions + token);
 }
 
 // The chunk places of a lane's two chunks.
@@ -110,12 +127,13 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
   return v;
 }
 
-// Rows one lane group has in flight: four rows of 256 bytes a group keep
-// enough loads outstanding to reach the copy bandwidth.
+// Row groups of one work unit, all in flight at once: four rows of 256 bytes a
+// lane group.  The rows' loads go out before the position's and the table's,
+// which depend on each other, so a unit waits twice and not three times.
 constexpr int kBatch = 4;
 
 template <typename T, int CH, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 3) rope_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31;
   const int rows = 32 / p.lanes;                   // rows of a warp at a time
   const int slot = lane & (p.lanes - 1), sub = lane / p.lanes;
@@ -129,71 +147,73 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     const int token = unit / p.parts;
     const int first = static_cast<int>(unit % p.parts) * p.per_warp;
     const int last = min(first + p.per_warp, groups);
+    Chunk<T, CH> x0[kBatch], x1[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int g = first + b;
+      x0[b].zero(), x1[b].zero();
+      if (g >= last) continue;
+      const int kind = g < p.groups_q ? 0 : g < p.groups_q + p.groups_k ? 1 : 2;
+      const int head = (g - (kind == 0 ? 0 : kind == 1 ? p.groups_q : p.groups_q + p.groups_k)) * rows + sub;
+      if (head >= (kind == 0 ? p.q_heads : p.kv_heads)) continue;
+      const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
+                     token * (kind == 0 ? p.q_token : kind == 1 ? p.k_token : p.v_token) +
+                     head * (kind == 0 ? p.q_head : kind == 1 ? p.k_head : p.v_head);
+      if (on0) x0[b].load(src + e0);
+      if (on1) x1[b].load(src + e1);
+    }
     Angles<CH> ang;
-    load_angles<CH>(p, token, slot, ang);
+    ang.turns = 0u;
+    if (first < p.groups_q + p.groups_k) load_angles<CH>(p, position_of(p, token), slot, ang);
     int64_t cache_at = -1;
     if (p.slots && last > p.groups_q) {
-      const int64_t s = p.slots[token];
-      if (s >= 0 && s < p.num_slots)
-        cache_at = s / p.page_size * p.page_stride + s % p.page_size * p.slot_stride;
+      const int64_t s = __ldg(p.slots + token);
+      if (s >= 0 && s < p.num_slots) {
+        const bool small = p.num_slots <= 0x7FFFFFFF;  // a 64-bit division costs a hundred instructions
+        const int64_t page = small ? static_cast<int64_t>(static_cast<uint32_t>(s) / static_cast<uint32_t>(p.page_size)) : s / p.page_size;
+        cache_at = page * p.page_stride + (s - page * p.page_size) * p.slot_stride;
+      }
     }
-    for (int g0 = first; g0 < last; g0 += kBatch) {
-      Chunk<T, CH> x0[kBatch], x1[kBatch];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int g = g0 + b;
-        x0[b].zero(), x1[b].zero();
-        if (g >= last) continue;
-        const int kind = g < p.groups_q ? 0 : g < p.groups_q + p.groups_k ? 1 : 2;
-        const int head = (g - (kind == 0 ? 0 : kind == 1 ? p.groups_q : p.groups_q + p.groups_k)) * rows + sub;
-        if (head >= (kind == 0 ? p.q_heads : p.kv_heads)) continue;
-        const T* src = static_cast<const T*>(kind == 0 ? p.q : kind == 1 ? p.k : p.v) +
-                       token * (kind == 0 ? p.q_token : kind == 1 ? p.k_token : p.v_token) +
-                       head * (kind == 0 ? p.q_head : kind == 1 ? p.k_head : p.v_head);
-        if (on0) x0[b].load(src + e0);
-        if (on1) x1[b].load(src + e1);
-      }
+    for (int b = 0; b < kBatch; ++b) {
+      const int g = first + b;
+      if (g >= last) continue;
+      const int kind = g < p.groups_q ? 0 : g < p.groups_q + p.groups_k ? 1 : 2;
+      const int head = (g - (kind == 0 ? 0 : kind == 1 ? p.groups_q : p.groups_q + p.groups_k)) * rows + sub;
+      const bool has = head < (kind == 0 ? p.q_heads : p.kv_heads);
+      if (kind < 2) {
+        float lo[CH], hi[CH];
+        x0[b].get(lo), x1[b].get(hi);
+        const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : p.k_weight);
+        if (weight) {
+          Chunk<T, CH> w0, w1;
+          w0.zero(), w1.zero();
+          if (on0) w0.load(weight + e0);
+          if (on1) w1.load(weight + e1);
+          float sum = 0.0f;
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int g = g0 + b;
-        if (g >= last) continue;
-        const int kind = g < p.groups_q ? 0 : g < p.groups_q + p.groups_k ? 1 : 2;
-        const int head = (g - (kind == 0 ? 0 : kind == 1 ? p.groups_q : p.groups_q + p.groups_k)) * rows + sub;
-        const bool has = head < (kind == 0 ? p.q_heads : p.kv_heads);
-        if (kind < 2) {
-          float lo[CH], hi[CH];
-          x0[b].get(lo), x1[b].get(hi);
-          const T* weight = static_cast<const T*>(kind == 0 ? p.q_weight : p.k_weight);
-          if (weight) {
-            float sum = 0.0f;
+          for (int i = 0; i < CH; ++i) sum += lo[i] * lo[i] + hi[i] * hi[i];
+          const float r = rsqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
+          float f0[CH], f1[CH];
+          w0.get(f0), w1.get(f1);
 #pragma unroll
-            for (int i = 0; i < CH; ++i) sum += lo[i] * lo[i] + hi[i] * hi[i];
-            const float r = rsqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
-            Chunk<T, CH> w0, w1;
-            float f0[CH], f1[CH];
-            w0.zero(), w1.zero();
-            if (on0) w0.load(weight + e0);
-            if (on1) w1.load(weight + e1);
-            w0.get(f0), w1.get(f1);
-#pragma unroll
-            for (int i = 0; i < CH; ++i) lo[i] = lo[i] * r * f0[i], hi[i] = hi[i] * r * f1[i];
-          }
-          rotate<CH, PAIRS, 1>(lo, hi, ang);
-          x0[b].set(lo), x1[b].set(hi);
+          for (int i = 0; i < CH; ++i) lo[i] = lo[i] * r * f0[i], hi[i] = hi[i] * r * f1[i];
         }
-        T* dst;
-        bool put = has;
-        if (kind == 0) {
-          dst = static_cast<T*>(p.q_out) + token * p.qo_token + head * p.qo_head;
-        } else if (p.slots) {
-          put = put && cache_at >= 0;
-          dst = static_cast<T*>(kind == 1 ? p.k_cache : p.v_cache) + cache_at + head * p.cache_head;
-        } else {
-          dst = static_cast<T*>(p.k_out) + token * p.ko_token + head * p.ko_head;
-        }
-        if (put && on0) x0[b].store(dst + e0);
-        if (put && on1) x1[b].store(dst + e1);
+        rotate<CH, PAIRS, 1>(lo, hi, ang);
+        x0[b].set(lo), x1[b].set(hi);
       }
+      T* dst;
+      bool put = has;
+      if (kind == 0) {
+        dst = static_cast<T*>(p.q_out) + token * p.qo_token + head * p.qo_head;
+      } else if (p.slots) {
+        put = put && cache_at >= 0;
+        dst = static_cast<T*>(kind == 1 ? p.k_cache : p.v_cache) + cache_at + head * p.cache_head;
+      } else {
+        dst = static_cast<T*>(p.k_out) + token * p.ko_token + head * p.ko_head;
+      }
+      if (put && on0) x0[b].store(dst + e0);
+      if (put && on1) x1[b].store(dst + e1);
     }
   }
 }
@@ -276,112 +296,117 @@ __global__ void __launch_bounds__(kThreads) rope_any_kernel(const RopeParams p) 
 // they are joined over the warp's lane groups, over the CTA's warps, and (by
 // the second kernel) over the CTAs, each in a fixed order.
 
+// A warp has units of queries or of keys for its whole life, so one set of sums.
+constexpr int kGradRows = 2;  // rows of a lane group in flight, each with its gradient
+
 template <typename T, int CH, bool PAIRS>
-__global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rows = 32 / p.lanes;
   const int slot = lane & (p.lanes - 1), sub = lane / p.lanes;
   int e0, e1;
   chunk_places<CH>(p, PAIRS, slot, &e0, &e1);
   const bool on0 = e0 < p.head_dim, on1 = e1 < p.head_dim;
-  const int groups = p.groups_q + p.groups_k;
-  const uint32_t units = static_cast<uint32_t>(p.tokens) * p.parts;
-  float sums[2][2 * CH];
+  // the first key_ctas CTAs have the keys
+  const bool keys = static_cast<int>(blockIdx.x) < p.key_ctas;
+  const int ctas = keys ? p.key_ctas : gridDim.x - p.key_ctas, cta = keys ? blockIdx.x : blockIdx.x - p.key_ctas;
+  const int heads = keys ? p.kv_heads : p.q_heads, groups = keys ? p.groups_k : p.groups_q;
+  const T* weight = static_cast<const T*>(keys ? p.k_weight : p.q_weight);
+  const T* xs = static_cast<const T*>(keys ? p.k : p.q);
+  const T* ys = static_cast<const T*>(keys ? p.k_out : p.q_out);
+  T* ds = static_cast<T*>(keys ? p.dk : p.dq);
+  const int64_t x_token = keys ? p.k_token : p.q_token, x_head = keys ? p.k_head : p.q_head;
+  const int64_t y_token = keys ? p.ko_token : p.qo_token, y_head = keys ? p.ko_head : p.qo_head;
+  const int64_t d_token = keys ? p.dk_token : p.dq_token, d_head = keys ? p.dk_head : p.dq_head;
+  float sums[2 * CH];
 #pragma unroll
-  for (int i = 0; i < 2 * CH; ++i) sums[0][i] = sums[1][i] = 0.0f;
-  for (uint32_t unit = blockIdx.x * kWarps + warp; unit < units; unit += gridDim.x * kWarps) {
-    const int token = unit / p.parts;
-    const int first = static_cast<int>(unit % p.parts) * p.per_warp;
-    const int last = min(first + p.per_warp, groups);
+  for (int i = 0; i < 2 * CH; ++i) sums[i] = 0.0f;
+  // all groups of a token, or for few tokens a part of them
+  const int per_unit = keys ? p.per_warp_k : p.per_warp;
+  const int parts = (groups + per_unit - 1) / per_unit;
+  const uint32_t units = static_cast<uint32_t>(p.tokens) * parts, step = ctas * kWarps;
+  uint32_t unit = cta * kWarps + warp;
+  int64_t next_pos = unit < units ? position_of(p, unit / parts) : 0;
+  for (; unit < units; unit += step) {
+    const int token = unit / parts, from = static_cast<int>(unit % parts) * per_unit, to = min(from + per_unit, groups);
     Angles<CH> ang;
-    load_angles<CH>(p, token, slot, ang);
+    const int64_t pos = next_pos;
+    if (unit + step < units) next_pos = position_of(p, (unit + step) / parts);
+    for (int g0 = from; g0 < to; g0 += kGradRows) {
+      Chunk<T, CH> x0[kGradRows], x1[kGradRows], y0[kGradRows], y1[kGradRows];
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      const int base = kind ? p.groups_q : 0;
-      const int from = max(first, base), to = min(last, kind ? groups : p.groups_q);
-      const int heads = kind ? p.kv_heads : p.q_heads;
-      const T* weight = static_cast<const T*>(kind ? p.k_weight : p.q_weight);
-      const T* xs = static_cast<const T*>(kind ? p.k : p.q) + token * (kind ? p.k_token : p.q_token);
-      const T* ys = static_cast<const T*>(kind ? p.k_out : p.q_out) + token * (kind ? p.ko_token : p.qo_token);
-      T* ds = static_cast<T*>(kind ? p.dk : p.dq) + token * (kind ? p.dk_token : p.dq_token);
-      const int64_t x_head = kind ? p.k_head : p.q_head, y_head = kind ? p.ko_head : p.qo_head,
-                    d_head = kind ? p.dk_head : p.dq_head;
-      constexpr int kRows = 2;  // x and dy of two rows in flight
-      for (int g0 = from; g0 < to; g0 += kRows) {
-        Chunk<T, CH> x0[kRows], x1[kRows], y0[kRows], y1[kRows];
-#pragma unroll
-        for (int b = 0; b < kRows; ++b) {
-          const int head = (g0 + b - base) * rows + sub;
-          x0[b].zero(), x1[b].zero(), y0[b].zero(), y1[b].zero();
-          if (g0 + b >= to || head >= heads) continue;
-          if (on0) y0[b].load(ys + head * y_head + e0);
-          if (on1) y1[b].load(ys + head * y_head + e1);
-          if (weight) {
-            if (on0) x0[b].load(xs + head * x_head + e0);
-            if (on1) x1[b].load(xs + head * x_head + e1);
-          }
+      for (int b = 0; b < kGradRows; ++b) {
+        const int head = (g0 + b) * rows + sub;
+        x0[b].zero(), x1[b].zero(), y0[b].zero(), y1[b].zero();
+        if (g0 + b >= to || head >= heads) continue;
+        const T* y = ys + token * y_token + head * y_head;
+        if (on0) y0[b].load(y + e0);
+        if (on1) y1[b].load(y + e1);
+        if (weight) {
+          const T* x = xs + token * x_token + head * x_head;
+          if (on0) x0[b].load(x + e0);
+          if (on1) x1[b].load(x + e1);
         }
+      }
+      if (g0 == from) load_angles<CH>(p, pos, slot, ang);
 #pragma unroll
-        for (int b = 0; b < kRows; ++b) {
-          if (g0 + b >= to) continue;
-          const int head = (g0 + b - base) * rows + sub;
-          float lo[CH], hi[CH];
-          y0[b].get(lo), y1[b].get(hi);
-          rotate<CH, PAIRS, -1>(lo, hi, ang);
-          if (weight) {
-            float h0[CH], h1[CH], f0[CH], f1[CH];
-            x0[b].get(h0), x1[b].get(h1);
-            float sum = 0.0f;
+      for (int b = 0; b < kGradRows; ++b) {
+        if (g0 + b >= to) continue;
+        const int head = (g0 + b) * rows + sub;
+        float lo[CH], hi[CH];
+        y0[b].get(lo), y1[b].get(hi);
+        rotate<CH, PAIRS, -1>(lo, hi, ang);
+        if (weight) {
+          float h0[CH], h1[CH], f0[CH], f1[CH];
+          x0[b].get(h0), x1[b].get(h1);
+          float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) sum += h0[i] * h0[i] + h1[i] * h1[i];
-            float r = rsqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
-            // a lane group past the last head holds zeros and adds none
-            if (head >= heads) r = 0.0f;
-            Chunk<T, CH> w0, w1;
-            w0.zero(), w1.zero();
-            if (on0) w0.load(weight + e0);
-            if (on1) w1.load(weight + e1);
-            w0.get(f0), w1.get(f1);
-            float dot = 0.0f;
+          for (int i = 0; i < CH; ++i) sum += h0[i] * h0[i] + h1[i] * h1[i];
+          float r = rsqrtf(group_sum(sum, p.lanes) * p.inv_dim + p.eps);
+          // a lane group past the last head holds zeros and adds none
+          if (head >= heads) r = 0.0f;
+          Chunk<T, CH> w0, w1;
+          w0.zero(), w1.zero();
+          if (on0) w0.load(weight + e0);
+          if (on1) w1.load(weight + e1);
+          w0.get(f0), w1.get(f1);
+          float dot = 0.0f;
 #pragma unroll
-            for (int i = 0; i < CH; ++i) {
-              h0[i] *= r, h1[i] *= r;
-              sums[kind][i] += lo[i] * h0[i];
-              sums[kind][CH + i] += hi[i] * h1[i];
-              lo[i] *= f0[i], hi[i] *= f1[i];
-              dot += lo[i] * h0[i] + hi[i] * h1[i];
-            }
-            const float mean = group_sum(dot, p.lanes) * p.inv_dim;
-#pragma unroll
-            for (int i = 0; i < CH; ++i) lo[i] = r * (lo[i] - h0[i] * mean), hi[i] = r * (hi[i] - h1[i] * mean);
+          for (int i = 0; i < CH; ++i) {
+            h0[i] *= r, h1[i] *= r;
+            sums[i] += lo[i] * h0[i];
+            sums[CH + i] += hi[i] * h1[i];
+            lo[i] *= f0[i], hi[i] *= f1[i];
+            dot += lo[i] * h0[i] + hi[i] * h1[i];
           }
-          if (head >= heads) continue;
-          y0[b].set(lo), y1[b].set(hi);
-          if (on0) y0[b].store(ds + head * d_head + e0);
-          if (on1) y1[b].store(ds + head * d_head + e1);
+          const float mean = group_sum(dot, p.lanes) * p.inv_dim;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) lo[i] = r * (lo[i] - h0[i] * mean), hi[i] = r * (hi[i] - h1[i] * mean);
         }
+        if (head >= heads) continue;
+        y0[b].set(lo), y1[b].set(hi);
+        T* d = ds + token * d_token + head * d_head;
+        if (on0) y0[b].store(d + e0);
+        if (on1) y1[b].store(d + e1);
       }
     }
   }
   if (!p.partial) return;
   // over the warp's lane groups, then over the warps
-  __shared__ float shared[kWarps][2][256 + 32];
+  __shared__ float shared[kWarps][256 + 32];
 #pragma unroll
-  for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-    for (int i = 0; i < 2 * CH; ++i) {
-      float v = sums[kind][i];
-      for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      const int e = i < CH ? e0 + i : e1 + i - CH;
-      if (sub == 0 && e < p.head_dim) shared[warp][kind][e] = v;
-    }
+  for (int i = 0; i < 2 * CH; ++i) {
+    float v = sums[i];
+    for (int o = p.lanes; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    const int e = i < CH ? e0 + i : e1 + i - CH;
+    if (sub == 0 && e < p.head_dim) shared[warp][e] = v;
+  }
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.head_dim; i += kThreads) {
-    const int kind = i / p.head_dim, e = i % p.head_dim;
+  for (int e = threadIdx.x; e < p.head_dim; e += kThreads) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += shared[w][kind][e];
-    p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + kind) * p.head_dim + e] = v;
+    for (int w = 0; w < kWarps; ++w) v += shared[w][e];
+    p.partial[static_cast<int64_t>(blockIdx.x) * p.head_dim + e] = v;
   }
 }
 
@@ -389,19 +414,18 @@ __global__ void __launch_bounds__(kThreads) rope_backward_kernel(const RopeParam
 template <typename T>
 __global__ void __launch_bounds__(kThreads) rope_backward_any_kernel(const RopeParams p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int heads = p.q_heads + p.kv_heads;
   const int half = p.rot_dim >> 1;
   const bool pairs = p.lanes != 0;
-  float sums[2][8];
+  const bool kind = static_cast<int>(blockIdx.x) < p.key_ctas;
+  const int ctas = kind ? p.key_ctas : gridDim.x - p.key_ctas, cta = kind ? blockIdx.x : blockIdx.x - p.key_ctas;
+  const int heads = kind ? p.kv_heads : p.q_heads;
+  float sums[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[0][i] = sums[1][i] = 0.0f;
+  for (int i = 0; i < 8; ++i) sums[i] = 0.0f;
   const int64_t units = static_cast<int64_t>(p.tokens) * heads;
-  for (int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + warp; unit < units;
-       unit += static_cast<int64_t>(gridDim.x) * kWarps) {
+  for (int64_t unit = static_cast<int64_t>(cta) * kWarps + warp; unit < units; unit += static_cast<int64_t>(ctas) * kWarps) {
     const int token = static_cast<int>(unit / heads);
-    const int at_head = static_cast<int>(unit % heads);
-    const int kind = at_head < p.q_heads ? 0 : 1;
-    const int head = at_head - (kind ? p.q_heads : 0);
+    const int head = static_cast<int>(unit % heads);
     const T* x = static_cast<const T*>(kind ? p.k : p.q) + token * (kind ? p.k_token : p.q_token) + head * (kind ? p.k_head : p.q_head);
     const T* dy = static_cast<const T*>(kind ? p.k_out : p.q_out) + token * (kind ? p.ko_token : p.qo_token) +
                   head * (kind ? p.ko_head : p.qo_head);
@@ -435,8 +459,7 @@ __global__ void __launch_bounds__(kThreads) rope_backward_any_kernel(const RopeP
         const int e = lane + 32 * i;
         if (e >= p.head_dim) continue;
         h[i] *= r;
-        if (kind) sums[1][i] += g[i] * h[i];
-        else sums[0][i] += g[i] * h[i];
+        sums[i] += g[i] * h[i];
         g[i] *= El<T>::to_float(weight[e]);
         dot += g[i] * h[i];
       }
@@ -452,38 +475,41 @@ __global__ void __launch_bounds__(kThreads) rope_backward_any_kernel(const RopeP
     }
   }
   if (!p.partial) return;
-  __shared__ float shared[kWarps][2][256];
+  __shared__ float shared[kWarps][256];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) shared[warp][0][lane + 32 * i] = sums[0][i], shared[warp][1][lane + 32 * i] = sums[1][i];
+  for (int i = 0; i < 8; ++i) shared[warp][lane + 32 * i] = sums[i];
   __syncthreads();
-  for (int i = threadIdx.x; i < 2 * p.head_dim; i += kThreads) {
-    const int kind = i / p.head_dim, e = i % p.head_dim;
+  for (int e = threadIdx.x; e < p.head_dim; e += kThreads) {
     float v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += shared[w][kind][e];
-    p.partial[(static_cast<int64_t>(blockIdx.x) * 2 + kind) * p.head_dim + e] = v;
+    for (int w = 0; w < kWarps; ++w) v += shared[w][e];
+    p.partial[static_cast<int64_t>(blockIdx.x) * p.head_dim + e] = v;
   }
 }
 
-// dw[kind][e] = sum over CTAs of the partial sums: one CTA for 32 elements,
-// each warp a fixed share of the rows.
-__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* partial, int ctas, int head_dim, float* dq_weight,
-                                                           float* dk_weight) {
+// dw[e] = sum over the CTAs that have queries (or keys) of their sums: one CTA
+// for 32 elements of one weight, each warp a fixed share of the rows.
+__global__ void __launch_bounds__(1024) rope_weight_kernel(const float* partial, int ctas, int key_ctas, int head_dim,
+                                                           float* dq_weight, float* dk_weight) {
   griddep_wait();
   __shared__ float shared[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int column = blockIdx.x * 32 + lane;
+  const bool keys = blockIdx.y != 0;
+  const int from = keys ? 0 : key_ctas, to = keys ? key_ctas : ctas;
+  float* out = keys ? dk_weight : dq_weight;
+  if (!out) return;
   float v = 0.0f;
-  if (column < 2 * head_dim)
-    for (int c = warp; c < ctas; c += 32) v += partial[static_cast<int64_t>(c) * 2 * head_dim + column];
+  if (column < head_dim)
+#pragma unroll 8
+    for (int c = from + warp; c < to; c += 32) v += partial[static_cast<int64_t>(c) * head_dim + column];
   shared[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && column < 2 * head_dim) {
+  if (warp == 0 && column < head_dim) {
     v = 0.0f;
 #pragma unroll
     for (int w = 0; w < 32; ++w) v += shared[w][lane];
-    float* out = column < head_dim ? dq_weight : dk_weight;
-    if (out) out[column < head_dim ? column : column - head_dim] = v;
+    out[column] = v;
   }
 }
 
@@ -567,10 +593,9 @@ bool chunks_fit(const eg_rope_args& a, int ch, std::initializer_list<const void*
   return true;
 }
 
-// Lanes of a row's group and the split of a token's rows over warps.  A warp
-// takes all rows of a token (its angles are then read once); where that leaves
-// fewer than four warps a scheduler, the rows are split into batches.
-void plan_rows(RopeParams* p, int ch, bool append, int sms) {
+// Lanes of a row's group, row groups, and the units of a token: `kBatch`
+// groups each.
+void plan_rows(RopeParams* p, int ch, bool append) {
   const int slots = (p->head_dim / ch + 1) / 2;
   p->lanes = 1;
   while (p->lanes < slots) p->lanes *= 2;
@@ -579,12 +604,18 @@ void plan_rows(RopeParams* p, int ch, bool append, int sms) {
   p->groups_k = (p->kv_heads + rows - 1) / rows;
   p->groups_v = append ? p->groups_k : 0;
   const int groups = p->groups_q + p->groups_k + p->groups_v;
-  const int64_t want = static_cast<int64_t>(sms) * 16;
-  int64_t parts = p->tokens ? (want + p->tokens - 1) / p->tokens : 1;
-  const int most = (groups + kBatch - 1) / kBatch;
-  parts = std::min<int64_t>(std::max<int64_t>(parts, 1), std::max(most, 1));
-  p->per_warp = std::max(1, static_cast<int>((groups + parts - 1) / parts));
+  p->parts = std::max(1, (groups + kBatch - 1) / kBatch);
+  p->per_warp = std::max(1, (groups + p->parts - 1) / p->parts);
   p->parts = std::max(1, (groups + p->per_warp - 1) / p->per_warp);
+  p->wide_table = ch % 4 == 0 && p->rot_dim % 8 == 0 && reinterpret_cast<uintptr_t>(p->cos_sin) % 16 == 0;
+}
+
+// The gradient's units: all row groups of a token, or where there are few
+// tokens for the warps a part of them (at least what is in flight at once).
+int grad_groups(int64_t tokens, int groups, int warps) {
+  if (groups == 0) return 1;
+  const int64_t parts = tokens ? std::max<int64_t>(1, warps / tokens) : 1;
+  return static_cast<int>(std::max<int64_t>(kGradRows, (groups + parts - 1) / parts));
 }
 
 template <typename T, int CH>
@@ -601,7 +632,7 @@ void launch_backward(const RopeParams& p, bool pairs, int grid, cudaStream_t st)
 
 eg_status forward(const eg_rope_args& a, RopeParams p, int ch, bool append, int sms, cudaStream_t st) {
   if (ch) {
-    plan_rows(&p, ch, append, sms);
+    plan_rows(&p, ch, append);
     const int64_t ctas = (static_cast<int64_t>(p.tokens) * p.parts + kWarps - 1) / kWarps;
     const int grid = static_cast<int>(std::min<int64_t>(ctas, 1 << 20));
     if (a.dtype == EG_EL_F32) launch_rows<float, 4>(p, a.pairs, grid, st);
@@ -621,10 +652,15 @@ eg_status forward(const eg_rope_args& a, RopeParams p, int ch, bool append, int 
   return e == cudaSuccess ? EG_OK : host_cuda_fail(e, append ? "launching kv_append" : "launching qk_norm_rope");
 }
 
-// CTAs of the gradient kernels: each leaves one row of partial sums.
-int backward_ctas(const eg_rope_args& a, int sms) {
+// CTAs of the gradient kernels (each leaves one row of partial sums) and how
+// many of them have keys: as the heads are divided.
+int backward_ctas(const eg_rope_args& a, int sms, int* key_ctas) {
   const int64_t rows = a.tokens * (a.q_heads + a.kv_heads);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>((rows + kWarps - 1) / kWarps, sms * 3)));
+  int ctas = static_cast<int>(std::max<int64_t>(2, std::min<int64_t>((rows + kWarps - 1) / kWarps, sms * 2)));
+  const int heads = a.q_heads + a.kv_heads;
+  int keys = heads ? static_cast<int>((static_cast<int64_t>(ctas) * a.kv_heads + heads / 2) / heads) : 1;
+  *key_ctas = std::min(ctas - 1, std::max(1, keys));
+  return ctas;
 }
 
 }  // namespace
@@ -701,9 +737,9 @@ eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache, const
 eg_status eg_qk_norm_rope_workspace_bytes(const eg_rope_args* fwd, size_t* out) {
   EG_TRY(check_args(fwd));
   if (!out) return host_fail(EG_ERR_INVALID_ARG, "out is NULL");
-  int dev = 0, sms = 0;
+  int dev = 0, sms = 0, key_ctas = 0;
   EG_TRY(host_check_device(&dev, &sms));
-  *out = (fwd->q_weight || fwd->k_weight) ? static_cast<size_t>(backward_ctas(*fwd, sms)) * 2 * fwd->head_dim * 4 : 0;
+  *out = (fwd->q_weight || fwd->k_weight) ? static_cast<size_t>(backward_ctas(*fwd, sms, &key_ctas)) * fwd->head_dim * 4 : 0;
   return EG_OK;
 }
 
@@ -724,17 +760,19 @@ eg_status eg_qk_norm_rope_backward(const eg_rope_args* fwd, const eg_rope_grads*
   float* dkw = a.k_weight ? d.dk_weight : nullptr;
   int dev = 0, sms = 0;
   EG_TRY(host_check_device(&dev, &sms));
-  const int ctas = backward_ctas(a, sms);
+  int key_ctas = 0;
+  const int ctas = backward_ctas(a, sms, &key_ctas);
   if (dqw || dkw) {
     if (!d.workspace || reinterpret_cast<uintptr_t>(d.workspace) % 16)
       return host_fail(EG_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
-    if (d.workspace_bytes < static_cast<size_t>(ctas) * 2 * a.head_dim * 4)
+    if (d.workspace_bytes < static_cast<size_t>(ctas) * a.head_dim * 4)
       return host_fail(EG_ERR_INVALID_ARG, "workspace holds %zu bytes of %zu", d.workspace_bytes,
-                       static_cast<size_t>(ctas) * 2 * a.head_dim * 4);
+                       static_cast<size_t>(ctas) * a.head_dim * 4);
   }
   RopeParams p = base_params(a);
   p.dq = d.dq, p.dk = d.dk;
   p.dq_token = d.dq_token, p.dq_head = d.dq_head, p.dk_token = d.dk_token, p.dk_head = d.dk_head;
+  p.key_ctas = key_ctas;
   p.partial = dqw || dkw ? static_cast<float*>(d.workspace) : nullptr;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int64_t on = a.q_heads ? 1 : 0, kon = a.kv_heads ? 1 : 0;
@@ -749,7 +787,9 @@ eg_status eg_qk_norm_rope_backward(const eg_rope_args* fwd, const eg_rope_grads*
       ch = c;
   }
   if (ch) {
-    plan_rows(&p, ch, false, sms);
+    plan_rows(&p, ch, false);
+    p.per_warp = grad_groups(a.tokens, p.groups_q, (ctas - key_ctas) * kWarps);
+    p.per_warp_k = grad_groups(a.tokens, p.groups_k, key_ctas * kWarps);
     if (a.dtype == EG_EL_F32) launch_backward<float, 4>(p, a.pairs, ctas, st);
     else if (a.dtype == EG_EL_BF16 && ch == 8) launch_backward<__nv_bfloat16, 8>(p, a.pairs, ctas, st);
     else if (a.dtype == EG_EL_BF16) launch_backward<__nv_bfloat16, 4>(p, a.pairs, ctas, st);
@@ -764,8 +804,17 @@ eg_status eg_qk_norm_rope_backward(const eg_rope_args* fwd, const eg_rope_grads*
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return host_cuda_fail(e, "launching the gradient of qk_norm_rope");
   if (dqw || dkw) {
-    rope_weight_kernel<<<(2 * a.head_dim + 31) / 32, 1024, 0, st>>>(p.partial, ctas, a.head_dim, dqw, dkw);
-    if ((e = cudaGetLastError()) != cudaSuccess) return host_cuda_fail(e, "launching the sum of the weights' gradients");
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((a.head_dim + 31) / 32), 2);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, rope_weight_kernel, static_cast<const float*>(p.partial), ctas, key_ctas, static_cast<int>(a.head_dim), dqw, dkw);
+    if (e != cudaSuccess) return host_cuda_fail(e, "launching the sum of the weights' gradients");
   }
   return EG_OK;
 }
