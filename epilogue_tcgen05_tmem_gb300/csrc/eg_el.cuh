@@ -9,6 +9,41 @@
 
 namespace eg {
 
+// Two float32 values in one 64-bit register, and the instructions on both.
+__device__ __forceinline__ uint64_t pk(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ float2 unpk(uint64_t v) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+  return f;
+}
+__device__ __forceinline__ uint64_t pk_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t pk_mul(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pk_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t pk_swap(uint64_t v) {
+  const float2 f = unpk(v);
+  return pk(f.y, f.x);
+}
+__device__ __forceinline__ float pk_sum(uint64_t v) {
+  const float2 f = unpk(v);
+  return f.x + f.y;
+}
+
 template <typename T>
 struct El;
 
@@ -83,6 +118,27 @@ struct Chunk {
         const float2 v = El<T>::unpack2(w[i]);
         f[2 * i] = v.x, f[2 * i + 1] = v.y;
       }
+    }
+  }
+  // the elements in pairs
+  __device__ __forceinline__ void get(uint64_t (&f)[CH / 2]) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < CH / 2; ++i) f[i] = pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        const float2 v = El<T>::unpack2(w[i]);
+        f[i] = pk(v.x, v.y);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const uint64_t (&f)[CH / 2]) {
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) {
+      const float2 v = unpk(f[i]);
+      if constexpr (sizeof(T) == 4) w[2 * i] = __float_as_uint(v.x), w[2 * i + 1] = __float_as_uint(v.y);
+      else w[i] = El<T>::pack2(v.x, v.y);
     }
   }
   __device__ __forceinline__ void set(const float (&f)[CH]) {
