@@ -9,40 +9,14 @@
 
 namespace eg {
 
-// Two float32 values in one 64-bit register, and the instructions on both.
-__device__ __forceinline__ uint64_t pk(float lo, float hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
-  return v;
-}
-__device__ __forceinline__ float2 unpk(uint64_t v) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-  return f;
-}
-__device__ __forceinline__ uint64_t pk_fma(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t pk_mul(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pk_add(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-__device__ __forceinline__ uint64_t pk_swap(uint64_t v) {
-  const float2 f = unpk(v);
-  return pk(f.y, f.x);
-}
-__device__ __forceinline__ float pk_sum(uint64_t v) {
-  const float2 f = unpk(v);
-  return f.x + f.y;
-}
+// Two float32 values.
+using pk_t = float2;
+__device__ __forceinline__ pk_t pk(float lo, float hi) { return make_float2(lo, hi); }
+__device__ __forceinline__ float2 unpk(pk_t v) { return v; }
+__device__ __forceinline__ pk_t pk_fma(pk_t a, pk_t b, pk_t c) { return make_float2(fmaf(a.x, b.x, c.x), fmaf(a.y, b.y, c.y)); }
+__device__ __forceinline__ pk_t pk_mul(pk_t a, pk_t b) { return make_float2(a.x * b.x, a.y * b.y); }
+__device__ __forceinline__ pk_t pk_swap(pk_t v) { return make_float2(v.y, v.x); }
+__device__ __forceinline__ float pk_sum(pk_t v) { return v.x + v.y; }
 
 template <typename T>
 struct El;
@@ -121,7 +95,7 @@ struct Chunk {
     }
   }
   // the elements in pairs
-  __device__ __forceinline__ void get(uint64_t (&f)[CH / 2]) const {
+  __device__ __forceinline__ void get(pk_t (&f)[CH / 2]) const {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int i = 0; i < CH / 2; ++i) f[i] = pk(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
@@ -133,7 +107,7 @@ struct Chunk {
       }
     }
   }
-  __device__ __forceinline__ void set(const uint64_t (&f)[CH / 2]) {
+  __device__ __forceinline__ void set(const pk_t (&f)[CH / 2]) {
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) {
       const float2 v = unpk(f[i]);

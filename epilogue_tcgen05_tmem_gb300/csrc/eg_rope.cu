@@ -66,7 +66,7 @@ struct RopeParams {
 // with neighbouring pairs the first half serves the first chunk.
 template <int CH>
 struct Angles {
-  uint64_t c[CH / 2], s[CH / 2];
+  pk_t c[CH / 2], s[CH / 2];
 };
 
 // 8 or 16 bytes to shared memory, in the background.
@@ -131,18 +131,40 @@ __device__ __forceinline__ void copy_angles(const RopeParams& p, int64_t pos, co
 
 template <int CH>
 __device__ __forceinline__ void read_angles(const RopeParams& p, int64_t pos, const AnglePlace& at, const float* from, Angles<CH>& a) {
-  const bool ok = pos >= 0 && pos < p.max_positions;
   const int half = p.rot_dim >> 1;
-  const float bad = __int_as_float(0x7FC00000);
+  if (p.wide_table) {
 #pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    if (!(k ? at.t1 : at.t0)) continue;
-    const int e = k ? at.a1 : at.a0;
+    for (int k = 0; k < 2; ++k) {
+      if (!(k ? at.t1 : at.t0)) continue;
+      const float* c = from + (k ? at.a1 : at.a0);
 #pragma unroll
-    for (int i = 0; i < CH / 2; i += 2) {
-      a.c[k * (CH / 4) + i / 2] = ok ? pk(from[e + i], from[e + i + 1]) : pk(bad, bad);
-      a.s[k * (CH / 4) + i / 2] = ok ? pk(from[half + e + i], from[half + e + i + 1]) : pk(bad, bad);
+      for (int i = 0; i < CH / 2; i += 4) {
+        if constexpr (CH == 8) {
+          const float4 u = *reinterpret_cast<const float4*>(c), v = *reinterpret_cast<const float4*>(c + half);
+          a.c[2 * k] = pk(u.x, u.y), a.c[2 * k + 1] = pk(u.z, u.w);
+          a.s[2 * k] = pk(v.x, v.y), a.s[2 * k + 1] = pk(v.z, v.w);
+        } else {
+          a.c[k] = *reinterpret_cast<const float2*>(c);
+          a.s[k] = *reinterpret_cast<const float2*>(c + half);
+        }
+      }
     }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (!(k ? at.t1 : at.t0)) continue;
+      const int e = k ? at.a1 : at.a0;
+#pragma unroll
+      for (int i = 0; i < CH / 2; i += 2) {
+        a.c[k * (CH / 4) + i / 2] = pk(from[e + i], from[e + i + 1]);
+        a.s[k * (CH / 4) + i / 2] = pk(from[half + e + i], from[half + e + i + 1]);
+      }
+    }
+  }
+  if (pos < 0 || pos >= p.max_positions) {
+    const float bad = __int_as_float(0x7FC00000);
+#pragma unroll
+    for (int i = 0; i < CH / 2; ++i) a.c[i] = a.s[i] = pk(bad, bad);
   }
 }
 __device__ __forceinline__ int64_t position_of(const RopeParams& p, int token) {
@@ -178,9 +200,9 @@ constexpr int kBatch = 2;
 // with x' the members exchanged and the sine's sign in s.
 template <int CH, bool PAIRS>
 struct Turn {
-  uint64_t c0[CH / 2], c1[CH / 2], s0[CH / 2], s1[CH / 2];
+  pk_t c0[CH / 2], c1[CH / 2], s0[CH / 2], s1[CH / 2];
 
-  __device__ __forceinline__ void form(const Angles<CH>& a, const uint64_t (&w0)[CH / 2], const uint64_t (&w1)[CH / 2], const AnglePlace& at) {
+  __device__ __forceinline__ void form(const Angles<CH>& a, const pk_t (&w0)[CH / 2], const pk_t (&w1)[CH / 2], const AnglePlace& at) {
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) c0[i] = w0[i], c1[i] = w1[i];
     if (at.t0) {
@@ -209,7 +231,7 @@ struct Turn {
   }
   // (x0, x1) of a lane times the weight and turned, without the factor r; a
   // chunk that is not rotated has only its weight in c
-  __device__ __forceinline__ void apply(uint64_t (&x0)[CH / 2], uint64_t (&x1)[CH / 2], const AnglePlace& at) const {
+  __device__ __forceinline__ void apply(pk_t (&x0)[CH / 2], pk_t (&x1)[CH / 2], const AnglePlace& at) const {
     if constexpr (PAIRS) {
 #pragma unroll
       for (int i = 0; i < CH / 2; ++i) {
@@ -221,7 +243,7 @@ struct Turn {
     } else if (at.t0) {
 #pragma unroll
       for (int i = 0; i < CH / 2; ++i) {
-        const uint64_t a = x0[i], b = x1[i];
+        const pk_t a = x0[i], b = x1[i];
         x0[i] = pk_fma(a, c0[i], pk_mul(b, s1[i]));
         x1[i] = pk_fma(b, c1[i], pk_mul(a, s0[i]));
       }
@@ -274,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const RopeParams p) {
   if (weight && on0) w0.load(weight + e0);
   if (weight && on1) w1.load(weight + e1);
   if (!weight) {
-    uint64_t one[CH / 2];
+    pk_t one[CH / 2];
 #pragma unroll
     for (int i = 0; i < CH / 2; ++i) one[i] = pk(1.0f, 1.0f);
     w0.set(one), w1.set(one);
@@ -325,7 +347,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const RopeParams p) {
     if (works) {
       Angles<CH> ang;
       read_angles<CH>(p, its_pos, place, now.table(), ang);
-      uint64_t f0[CH / 2], f1[CH / 2];
+      pk_t f0[CH / 2], f1[CH / 2];
       w0.get(f0), w1.get(f1);
       turn.form(ang, f0, f1, place);
     }
@@ -338,18 +360,18 @@ __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const RopeParams p) {
       if (has && on0) x0 = now.read(2 * b);
       if (has && on1) x1 = now.read(2 * b + 1);
       if (works) {
-        uint64_t lo[CH / 2], hi[CH / 2];
+        pk_t lo[CH / 2], hi[CH / 2];
         x0.get(lo), x1.get(hi);
         float r = 1.0f;
         if (weight) {
-          uint64_t sum = 0;
+          pk_t sum = pk(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) sum = pk_fma(lo[i], lo[i], sum), sum = pk_fma(hi[i], hi[i], sum);
           r = rsqrtf(group_sum(pk_sum(sum), p.lanes) * p.inv_dim + p.eps);
         }
         turn.apply(lo, hi, place);
         if (weight) {
-          const uint64_t r2 = pk(r, r);
+          const pk_t r2 = pk(r, r);
 #pragma unroll
           for (int i = 0; i < CH / 2; ++i) lo[i] = pk_mul(lo[i], r2), hi[i] = pk_mul(hi[i], r2);
         }
@@ -445,8 +467,8 @@ constexpr int kGradRows = 2;  // row groups of one work unit, each with its grad
 
 // A lane's gradients turned back: (a c + b s, b c - a s).
 template <int CH, bool PAIRS>
-__device__ __forceinline__ void turn_back(uint64_t (&x0)[CH / 2], uint64_t (&x1)[CH / 2], const Angles<CH>& a, const AnglePlace& at) {
-  const uint64_t minus = pk(-1.0f, -1.0f);
+__device__ __forceinline__ void turn_back(pk_t (&x0)[CH / 2], pk_t (&x1)[CH / 2], const Angles<CH>& a, const AnglePlace& at) {
+  const pk_t minus = pk(-1.0f, -1.0f);
 #pragma unroll
   for (int i = 0; i < CH / 2; ++i) {
     if constexpr (PAIRS) {
@@ -455,11 +477,11 @@ __device__ __forceinline__ void turn_back(uint64_t (&x0)[CH / 2], uint64_t (&x1)
         if (!(k ? at.t1 : at.t0)) continue;
         const float2 c = unpk(a.c[k * (CH / 4) + i / 2]), s = unpk(a.s[k * (CH / 4) + i / 2]);
         const float c_ = i & 1 ? c.y : c.x, s_ = i & 1 ? s.y : s.x;
-        uint64_t& x = k ? x1[i] : x0[i];
+        pk_t& x = k ? x1[i] : x0[i];
         x = pk_fma(x, pk(c_, c_), pk_mul(pk_swap(x), pk(s_, -s_)));
       }
     } else if (at.t0) {
-      const uint64_t u = x0[i], v = x1[i];
+      const pk_t u = x0[i], v = x1[i];
       x0[i] = pk_fma(u, a.c[i], pk_mul(v, a.s[i]));
       x1[i] = pk_fma(v, a.c[i], pk_mul(pk_mul(u, minus), a.s[i]));
     }
@@ -488,9 +510,9 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(const RopePa
   const T* xs = static_cast<const T*>(keys ? p.k : p.q) + head0 * x_head;
   const T* ys = static_cast<const T*>(keys ? p.k_out : p.q_out) + head0 * y_head;
   T* ds = static_cast<T*>(keys ? p.dk : p.dq) + head0 * d_head;
-  uint64_t sums[CH];
+  pk_t sums[CH];
 #pragma unroll
-  for (int i = 0; i < CH; ++i) sums[i] = 0;
+  for (int i = 0; i < CH; ++i) sums[i] = pk(0.0f, 0.0f);
   Chunk<T, CH> w0, w1;
   w0.zero(), w1.zero();
   if (weight && on0) w0.load(weight + e0);
@@ -538,13 +560,13 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(const RopePa
       y0.zero(), y1.zero(), x0.zero(), x1.zero();
       if (has && on0) y0 = now.read(4 * b);
       if (has && on1) y1 = now.read(4 * b + 1);
-      uint64_t lo[CH / 2], hi[CH / 2];
+      pk_t lo[CH / 2], hi[CH / 2];
       y0.get(lo), y1.get(hi);
       turn_back<CH, PAIRS>(lo, hi, ang, place);
       if (weight) {
         if (has && on0) x0 = now.read(4 * b + 2);
         if (has && on1) x1 = now.read(4 * b + 3);
-        uint64_t h0[CH / 2], h1[CH / 2], f0[CH / 2], f1[CH / 2], sum = 0;
+        pk_t h0[CH / 2], h1[CH / 2], f0[CH / 2], f1[CH / 2], sum = pk(0.0f, 0.0f);
         x0.get(h0), x1.get(h1);
         w0.get(f0), w1.get(f1);
 #pragma unroll
@@ -552,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(const RopePa
         float r = rsqrtf(group_sum(pk_sum(sum), p.lanes) * p.inv_dim + p.eps);
         // a lane group past the last head holds zeros and adds none
         if (!has) r = 0.0f;
-        const uint64_t r2 = pk(r, r);
-        uint64_t dot = 0;
+        const pk_t r2 = pk(r, r);
+        pk_t dot = pk(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i) {
           h0[i] = pk_mul(h0[i], r2), h1[i] = pk_mul(h1[i], r2);
@@ -563,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 2) rope_backward_kernel(const RopePa
           dot = pk_fma(lo[i], h0[i], dot), dot = pk_fma(hi[i], h1[i], dot);
         }
         const float mean = -group_sum(pk_sum(dot), p.lanes) * p.inv_dim;
-        const uint64_t mean2 = pk(mean, mean);
+        const pk_t mean2 = pk(mean, mean);
 #pragma unroll
         for (int i = 0; i < CH / 2; ++i)
           lo[i] = pk_mul(r2, pk_fma(h0[i], mean2, lo[i])), hi[i] = pk_mul(r2, pk_fma(h1[i], mean2, hi[i]));
