@@ -565,6 +565,9 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
         for (int u = 0; u < kUnroll; ++u)
           if (u * kThreads >= left) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
       }
+      // The copy that fills this place again writes through another proxy: the
+      // reads above have to be done for it before the place is given back.
+      fence_proxy_async_smem();
       __syncwarp();
       if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.empty[slot]);
       if (++slot == kStages) slot = 0, ++turns;

@@ -68,6 +68,19 @@ def test_forward(dtype, rows, vocab, top):
     _check(eg.token_logprobs(x.cuda(), tokens.cuda(), top=top), x, tokens, top)
 
 
+@pytest.mark.parametrize("dtype,rows,vocab", [("bf16", 4000, 130000), ("f32", 2500, 20011), ("f16", 9000, 1003)])
+def test_many_rows_are_the_same_every_time(dtype, rows, vocab):
+    """More rows than CTAs: each takes several, and the next one's loads overlap the end of the one before."""
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x = (torch.randn(rows, vocab, generator=g, device="cuda") * 2.5).to(H.DT[dtype])
+    tokens = torch.randint(0, vocab, (rows,), generator=g, device="cuda")
+    first = eg.token_logprobs(x, tokens, top=20)
+    ref = torch.cat([torch.logsumexp(part.double(), 1) for part in x.split(500)])
+    assert ((first.lse.double() - ref).abs() <= 2.0 ** -19 * (1 + ref)).all()
+    for _ in range(30):
+        assert all(torch.equal(a, b) for a, b in zip(eg.token_logprobs(x, tokens, top=20), first))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("order", ["rising", "falling", "equal", "two values", "few"])
 def test_top_of_ordered_and_equal_logits(dtype, order):
