@@ -184,24 +184,34 @@ def _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, page,
     tokens, heads, dim = shape = _heads("k", k)
     dtype, device = k.dtype, k.device
     kp, kt, kh = _rows("k", k, shape, dtype, device)
-    qp = qt = qh = hq = 0
+    qp = qt = qh = hq = vp = vt = vh = table = count = rot = at = qw = kw = 0
     if q is not None:
         hq = _heads("q", q)[1]
         qp, qt, qh = _rows("q", q, (tokens, hq, dim), dtype, device)
-    vp = vt = vh = 0
     if v is not None:
         vp, vt, vh = _rows("v", v, shape, dtype, device)
-    table = count = rot = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2 or cos_sin.dtype is not _b.f32 or not cos_sin.is_contiguous() or cos_sin.device != device:
             raise ValueError("cos_sin must be a contiguous float32 tensor [positions, rot_dim] on the tensors' device")
         table = cos_sin.data_ptr()
         count, rot = cos_sin.shape
+    if positions is not None:
+        at = _side("positions", positions, _b.i64, (tokens,), device)
+    if q_weight is not None:
+        qw = _side("q_weight", q_weight, dtype, (dim,), device)
+    if k_weight is not None:
+        kw = _side("k_weight", k_weight, dtype, (dim,), device)
     return (tokens, hq, heads, dim, rot, _code(k), 1 if pairs else 0, eps, page, table, count,
-            0 if positions is None else _side("positions", positions, _b.i64, (tokens,), device),
-            0 if q_weight is None else _side("q_weight", q_weight, dtype, (dim,), device),
-            0 if k_weight is None else _side("k_weight", k_weight, dtype, (dim,), device),
-            qp, kp, vp, qt, qh, kt, kh, vt, vh)
+            at, qw, kw, qp, kp, vp, qt, qh, kt, kh, vt, vh)
+
+
+def _out(name, given, like, stream):
+    """(tensor, pointer, token stride, head stride) of an output like `like`."""
+    if given is not None:
+        return (given, *_rows(name, given, like.shape, like.dtype, like.device))
+    shape = like.shape
+    new = like.new_empty(shape) if stream is None else _new(shape, like.dtype, like.device, stream)
+    return new, new.data_ptr(), shape[1] * shape[2], shape[2]
 
 
 def qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, eps=1e-6, pairs=False,
@@ -215,13 +225,8 @@ def qk_norm_rope(q, k, cos_sin, positions=None, q_weight=None, k_weight=None, ep
         _b.load()
     st = _stream_of(k, stream)
     fields = _rope_fields(q, k, cos_sin, positions, q_weight, k_weight, eps, pairs, 0, None)
-    dtype, device = k.dtype, k.device
-    if q_out is None:
-        q_out = _new(q.shape, dtype, device, stream)
-    if k_out is None:
-        k_out = _new(k.shape, dtype, device, stream)
-    qo, qot, qoh = _rows("q_out", q_out, q.shape, dtype, device)
-    ko, kot, koh = _rows("k_out", k_out, k.shape, dtype, device)
+    q_out, qo, qot, qoh = _out("q_out", q_out, q, stream)
+    k_out, ko, kot, koh = _out("k_out", k_out, k, stream)
     status = _b.qk_norm_rope(_pack_rope(*fields, qo, ko, qot, qoh, kot, koh), st)
     if status:
         _fail(status)
@@ -241,12 +246,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, cos_sin, positions=None, q_weigh
     qo, qot, qoh = _rows("dq_out", dq_out, q.shape, dtype, device)
     ko, kot, koh = _rows("dk_out", dk_out, k.shape, dtype, device)
     args = _pack_rope(*fields, qo, ko, qot, qoh, kot, koh)
-    if dq is None:
-        dq = _new(q.shape, dtype, device, stream)
-    if dk is None:
-        dk = _new(k.shape, dtype, device, stream)
-    pq, qt, qh = _rows("dq", dq, q.shape, dtype, device)
-    pk, kt, kh = _rows("dk", dk, k.shape, dtype, device)
+    dq, pq, qt, qh = _out("dq", dq, q, stream)
+    dk, pk, kt, kh = _out("dk", dk, k, stream)
     dqw = dkw = work = None
     need = ctypes.c_size_t(0)
     if q_weight is not None or k_weight is not None:
@@ -293,9 +294,7 @@ def kv_append(k, v, k_cache, v_cache, slots, q=None, cos_sin=None, positions=Non
     cache = _cache(k_cache, v_cache, (page, fields[2], fields[3]), dtype, device)
     qo = qot = qoh = 0
     if q is not None:
-        if q_out is None:
-            q_out = _new(q.shape, dtype, device, stream)
-        qo, qot, qoh = _rows("q_out", q_out, q.shape, dtype, device)
+        q_out, qo, qot, qoh = _out("q_out", q_out, q, stream)
     else:
         q_out = None
     status = _b.kv_append(_pack_rope(*fields, qo, 0, qot, qoh, 0, 0), cache, _side("slots", slots, _b.i64, (fields[0],), device), st)
@@ -358,9 +357,7 @@ class TreeAttention:
             words = mask.shape[1]
             # a mask without words is refused for their number, not taken for none
             at_mask = _side("mask", mask, _b.i32, (tokens, words), device) or 4
-        if out is None:
-            out = _new(shape, dtype, device, stream)
-        op, ot, oh = _rows("out", out, shape, dtype, device)
+        out, op, ot, oh = _out("out", out, q, stream)
         args = _pack_tree(batch, tokens, qp, op, qt, qh, ot, oh, table, width,
                           _side("context_lens", context_lens, _b.i32, (batch,), device),
                           _side("q_start", q_start, _b.i32, (batch + 1,), device), at_mask, words,
@@ -425,17 +422,18 @@ def token_logprobs(logits, tokens=None, top=0, stream=None) -> TokenLogProbs:
     rows, vocab = logits.shape
     device, f32 = logits.device, _b.f32
     given = 0 if tokens is None else _side("tokens", tokens, _b.i64, (rows,), device)
-    logprob, lse, entropy = _new(rows, f32, device, stream), _new(rows, f32, device, stream), _new(rows, f32, device, stream)
+    per_row = _new((3, rows), f32, device, stream)
+    at = per_row.data_ptr()
     ids = best = None
     at_ids = at_best = 0
     if top:
         ids, best = _new((rows, top), _b.i64, device, stream), _new((rows, top), f32, device, stream)
         at_ids, at_best = ids.data_ptr(), best.data_ptr()
-    status = _b.token_logprobs(_pack_score(rows, vocab, _code(logits), top, x, stride, given, logprob.data_ptr(), lse.data_ptr(),
-                                           entropy.data_ptr(), at_ids, at_best), st)
+    status = _b.token_logprobs(_pack_score(rows, vocab, _code(logits), top, x, stride, given, at, at + 4 * rows, at + 8 * rows, at_ids,
+                                           at_best), st)
     if status:
         _fail(status)
-    return TokenLogProbs(logprob, lse, entropy, ids, best)
+    return TokenLogProbs(*per_row.unbind(0), ids, best)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, d_logprob=None, d_entropy=None, out=None, stream=None):
