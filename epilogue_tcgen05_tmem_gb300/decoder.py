@@ -210,7 +210,7 @@ def _out(name, given, like, stream):
     if given is not None:
         return (given, *_rows(name, given, like.shape, like.dtype, like.device))
     shape = like.shape
-    new = like.new_empty(shape) if stream is None else _new(shape, like.dtype, like.device, stream)
+    new = _new(shape, like.dtype, like.device, stream)
     return new, new.data_ptr(), shape[1] * shape[2], shape[2]
 
 
@@ -422,18 +422,17 @@ def token_logprobs(logits, tokens=None, top=0, stream=None) -> TokenLogProbs:
     rows, vocab = logits.shape
     device, f32 = logits.device, _b.f32
     given = 0 if tokens is None else _side("tokens", tokens, _b.i64, (rows,), device)
-    per_row = _new((3, rows), f32, device, stream)
-    at = per_row.data_ptr()
+    logprob, lse, entropy = _new(rows, f32, device, stream), _new(rows, f32, device, stream), _new(rows, f32, device, stream)
     ids = best = None
     at_ids = at_best = 0
     if top:
         ids, best = _new((rows, top), _b.i64, device, stream), _new((rows, top), f32, device, stream)
         at_ids, at_best = ids.data_ptr(), best.data_ptr()
-    status = _b.token_logprobs(_pack_score(rows, vocab, _code(logits), top, x, stride, given, at, at + 4 * rows, at + 8 * rows, at_ids,
-                                           at_best), st)
+    status = _b.token_logprobs(_pack_score(rows, vocab, _code(logits), top, x, stride, given, logprob.data_ptr(), lse.data_ptr(),
+                                           entropy.data_ptr(), at_ids, at_best), st)
     if status:
         _fail(status)
-    return TokenLogProbs(*per_row.unbind(0), ids, best)
+    return TokenLogProbs(logprob, lse, entropy, ids, best)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, d_logprob=None, d_entropy=None, out=None, stream=None):
