@@ -24,10 +24,7 @@ namespace eg {
 
 namespace {
 
-constexpr int kThreads = 256;     // that look at values; one more warp loads
-constexpr int kWarps = kThreads / 32;
 constexpr int kUnroll = 4;        // 16-byte vectors of a thread and batch
-constexpr int kBatchBytes = kThreads * kUnroll * 16;
 constexpr int kStages = 2;        // batches in flight of a CTA
 constexpr int kMostTop = 32;
 constexpr int kWaiting = 1024;    // room for candidates of one selection
@@ -44,16 +41,9 @@ struct ScoreParams {
   int32_t top;
 };
 
-// Barrier of the threads that look at values.
-__device__ __forceinline__ void sync_lookers() { asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory"); }
-__device__ __forceinline__ bool sync_lookers_or(bool v) {
-  uint32_t any;
-  asm volatile("{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %1, 0;\n\tbar.red.or.pred b, 1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-               : "=r"(any)
-               : "r"(static_cast<uint32_t>(v)), "n"(kThreads)
-               : "memory");
-  return any != 0;
-}
+// N threads of a CTA look at values (one more warp loads them); a barrier of these.
+template <int N>
+__device__ __forceinline__ void sync_lookers() { asm volatile("bar.sync 1, %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -114,25 +104,27 @@ __device__ __forceinline__ Sums join(const Sums& a, const Sums& b) {
   return r;
 }
 
+template <int N>
 struct TopShared {
   alignas(16) uint64_t waiting[kWaiting];  // candidates
-  alignas(16) uint64_t bests[kThreads];    // the best one of each thread
+  alignas(16) uint64_t bests[N];    // the best one of each thread
   alignas(16) uint64_t kept[kMostTop];     // the best, in order; 0: none
   alignas(16) float groups[2][32];         // maxima of 32 groups of threads
   uint64_t least;            // a value has to reach this to be a candidate
   int count;                 // candidates that asked for a place
   int lost;                  // some candidates or notes found none
   int flood;                 // a warp has more notes than two for a thread
-  int2 queue[kWarps][kQueue];  // a thread's batches above the bar: the first vector, and the largest value
+  int2 queue[N / 32][kQueue];  // a thread's batches above the bar: the first vector, and the largest value
 };
 
+template <int N>
 struct RowShared {
-  alignas(16) uint8_t ring[kStages][kBatchBytes];
+  alignas(16) uint8_t ring[kStages][N * kUnroll * 16];
   uint64_t full[kStages], empty[kStages];
   int abort;
-  Sums warps[kWarps];
+  Sums warps[N / 32];
   Sums cta;
-  TopShared top;
+  TopShared<N> top;
 };
 
 // How many of list[0, n) are better than `mine`; the list is zero up to the
@@ -151,35 +143,39 @@ __device__ __forceinline__ int better_than(const uint64_t* list, int n, uint64_t
 
 // The best `top` of the candidates into kept, in order.  All threads, after a
 // barrier that follows the last candidate (`waiting` is zero behind it); the
-// place of each is the number of better ones.  Ends with a barrier.
-__device__ __forceinline__ void select_top(TopShared& sh, int top) {
+// place of each is the number of better ones.  Ends with a barrier; returns
+// the number of candidates.
+template <int N>
+__device__ __forceinline__ int select_top(TopShared<N>& sh, int top) {
   const int n = min(sh.count, kWaiting);
   if (static_cast<int>(threadIdx.x) >= n && threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
   uint64_t least = 0;
-  if (n > kThreads) {
+  if (n > N) {
     // more than one for a thread: only what reaches the `top`-th of the
     // threads' best is placed
     uint64_t best = 0;
-    for (int at = threadIdx.x; at < n; at += kThreads) best = max(best, sh.waiting[at]);
+    for (int at = threadIdx.x; at < n; at += N) best = max(best, sh.waiting[at]);
     sh.bests[threadIdx.x] = best;
     if (threadIdx.x == 0) sh.least = 0;
-    sync_lookers();
-    if (better_than(sh.bests, kThreads, best) == top - 1) sh.least = best;
-    sync_lookers();
+    sync_lookers<N>();
+    if (better_than(sh.bests, N, best) == top - 1) sh.least = best;
+    sync_lookers<N>();
     least = sh.least;
   }
-  for (int at = threadIdx.x; at < n; at += kThreads) {
+  for (int at = threadIdx.x; at < n; at += N) {
     const uint64_t mine = sh.waiting[at];
     if (mine < least) continue;
     const int place = better_than(sh.waiting, n, mine);
     if (place < top) sh.kept[place] = mine;
   }
-  sync_lookers();
+  sync_lookers<N>();
+  return n;
 }
 
-// Ready for the next row's candidates; a barrier has to come before the first.
-__device__ __forceinline__ void clear_top(TopShared& sh) {
-  for (int i = threadIdx.x; i < kWaiting; i += kThreads) sh.waiting[i] = 0;
+// Ready for the next row's candidates, of which there were `used`; a barrier has to come before the first.
+template <int N>
+__device__ __forceinline__ void clear_top(TopShared<N>& sh, int used) {
+  for (int i = threadIdx.x; i < used; i += N) sh.waiting[i] = 0;
   if (threadIdx.x == 0) sh.count = sh.lost = sh.flood = 0;
 }
 
@@ -222,33 +218,33 @@ __device__ __forceinline__ Sums warp_join(Sums v, int lanes) {
 
 // A row whose maximum is so low, so high or so infinite that the pass above
 // does not hold: its statistics from the definition, by one CTA.
-template <typename T>
+template <typename T, int N>
 __device__ __noinline__ void plain_row(const T* x, int64_t vocab, float* red, float* lse, float* entropy) {
   float m = -CUDART_INF_F;
-  for (int64_t i = threadIdx.x; i < vocab; i += kThreads) m = max_nan(m, El<T>::to_float(x[i]));
+  for (int64_t i = threadIdx.x; i < vocab; i += N) m = max_nan(m, El<T>::to_float(x[i]));
   red[threadIdx.x] = m;
-  sync_lookers();
-  for (int o = kThreads / 2; o > 0; o >>= 1) {
+  sync_lookers<N>();
+  for (int o = N / 2; o > 0; o >>= 1) {
     if (threadIdx.x < o) red[threadIdx.x] = max_nan(red[threadIdx.x], red[threadIdx.x + o]);
-    sync_lookers();
+    sync_lookers<N>();
   }
   m = red[0];
-  sync_lookers();
+  sync_lookers<N>();
   float s = 0.0f, t = 0.0f;
   if (fabsf(m) < CUDART_INF_F)
-    for (int64_t i = threadIdx.x; i < vocab; i += kThreads) {
+    for (int64_t i = threadIdx.x; i < vocab; i += N) {
       const float d = El<T>::to_float(x[i]) - m, e = expf(d);
       if (e > 0.0f) s += e, t += e * d;
     }
   for (int k = 0; k < 2; ++k) {
     red[threadIdx.x] = k ? t : s;
-    sync_lookers();
-    for (int o = kThreads / 2; o > 0; o >>= 1) {
+    sync_lookers<N>();
+    for (int o = N / 2; o > 0; o >>= 1) {
       if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-      sync_lookers();
+      sync_lookers<N>();
     }
     (k ? t : s) = red[0];
-    sync_lookers();
+    sync_lookers<N>();
   }
   if (m == -CUDART_INF_F) *lse = m, *entropy = 0.0f;
   else if (!(fabsf(m) < CUDART_INF_F)) *lse = m, *entropy = __int_as_float(0x7FC00000);
@@ -316,7 +312,8 @@ struct Part {
 };
 
 // Take a value for a candidate.
-__device__ __forceinline__ void offer_top(TopShared& sh, uint64_t least, float f, int32_t id) {
+template <int N>
+__device__ __forceinline__ void offer_top(TopShared<N>& sh, uint64_t least, float f, int32_t id) {
   const uint64_t c = candidate(f, static_cast<uint32_t>(id));
   if (c < least) return;
   const int place = atomicAdd(&sh.count, 1);
@@ -327,30 +324,31 @@ __device__ __forceinline__ void offer_top(TopShared& sh, uint64_t least, float f
 // A value that `top` of 32 groups of threads have reached, from each thread's
 // largest so far: at least `top` values reach it, and few more do.  One
 // barrier, after which every warp finds it by itself; `turn` counts the calls.
-__device__ __forceinline__ float group_bar(TopShared& sh, float most, int top, int turn) {
+template <int N>
+__device__ __forceinline__ float group_bar(TopShared<N>& sh, float most, int top, int turn) {
 #pragma unroll
-  for (int o = kThreads / 64; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int o = N / 64; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
   float* groups = sh.groups[turn & 1];
-  if ((threadIdx.x & (kThreads / 32 - 1)) == 0) groups[threadIdx.x / (kThreads / 32)] = most;
-  sync_lookers();
+  if (threadIdx.x % (N / 32) == 0) groups[threadIdx.x / (N / 32)] = most;
+  sync_lookers<N>();
   const float g = groups[threadIdx.x & 31];
-  int better = 0, equal = 0;
+  int better = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float4 f = reinterpret_cast<const float4*>(groups)[j];
     better += (f.x > g) + (f.y > g) + (f.z > g) + (f.w > g);
-    equal += (f.x == g) + (f.y == g) + (f.z == g) + (f.w == g);
   }
-  const uint32_t is = __ballot_sync(0xffffffffu, better < top && better + equal >= top);
-  return __shfl_sync(0xffffffffu, g, __ffs(is) - 1);
+  // the smallest of those with fewer than `top` better ones
+  const uint32_t least = __reduce_min_sync(0xffffffffu, better < top ? static_cast<uint32_t>(candidate(g, 0) >> 32) : 0xFFFFFFFFu);
+  return candidate_value(static_cast<uint64_t>(least) << 32);
 }
 
 // The candidates among the values of the vectors that this warp noted: those
 // that reach the last bar.  Where there is no bar, or many were noted (many
 // equal values, a short row), a better bound first: each thread has a best
 // candidate, and `top` of those reach the `top`-th of them.
-template <typename T>
-__device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, int queued, float bar, int top) {
+template <typename T, int N>
+__device__ __forceinline__ void open_queue(const Part<T>& part, TopShared<N>& sh, int queued, float bar, int top) {
   constexpr int V = kVec<T>;
   const int2* queue = sh.queue[threadIdx.x >> 5];
   const int lane = threadIdx.x & 31;
@@ -360,7 +358,7 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
   auto open = [&](const int2& note, Chunk<T, V> (&c)[kUnroll]) {
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int32_t v = note.x + u * kThreads;
+      const int32_t v = note.x + u * N;
       if (v < part.to) c[u].load(part.body + static_cast<int64_t>(v) * V);
       else c[u].w[0] = c[u].w[1] = c[u].w[2] = c[u].w[3] = kNothing<T>;
     }
@@ -375,7 +373,7 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
       for (int u = 0; u < kUnroll; ++u) {
         float f[V];
         c[0].get(f);
-        const int32_t v = queue[i].x + u * kThreads;
+        const int32_t v = queue[i].x + u * N;
         if (v < part.to)
 #pragma unroll
           for (int j = 0; j < V; ++j) best = max(best, candidate(f[j], static_cast<uint32_t>(part.head + v * V + j)));
@@ -384,11 +382,11 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
       }
     }
     sh.bests[threadIdx.x] = best;
-    sync_lookers();
+    sync_lookers<N>();
     // only the first threads have any in a short row
-    const int teams = min(kThreads, (part.to - part.from + 31) & ~31);
+    const int teams = min(N, (part.to - part.from + 31) & ~31);
     if (best && better_than(sh.bests, teams, best) == top - 1) sh.least = best;
-    sync_lookers();
+    sync_lookers<N>();
     least = max(least, sh.least);
   }
   for (int i = lane; i < queued; i += 32) {
@@ -399,7 +397,7 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
 #pragma unroll 1
     for (int u = 0; u < kUnroll; ++u) {
       const uint32_t high = word_max<T>(word_max<T>(c[0].w[0], c[0].w[1]), word_max<T>(c[0].w[2], c[0].w[3]));
-      const int32_t v = note.x + u * kThreads;
+      const int32_t v = note.x + u * N;
       if (v < part.to && !(word_top<T>(high) < bar)) {
         float f[V];
         c[0].get(f);
@@ -416,29 +414,31 @@ __device__ __forceinline__ void open_queue(const Part<T>& part, TopShared& sh, i
 // The best of a part, when more vectors or candidates came than there is room
 // for (values that rise along the row): some vectors at a time, with a
 // selection after each lot.
-template <typename T>
-__device__ __noinline__ void careful_top(const Part<T>& part, TopShared& sh, int top) {
+template <typename T, int N>
+__device__ __noinline__ int careful_top(const Part<T>& part, TopShared<N>& sh, int top) {
   constexpr int V = kVec<T>;
-  constexpr int kLot = (kWaiting - kMostTop - 16) / V < kThreads ? (kWaiting - kMostTop - 16) / V : kThreads;
-  sync_lookers();
+  constexpr int kLot = (kWaiting - kMostTop - 16) / V < N ? (kWaiting - kMostTop - 16) / V : N;
+  sync_lookers<N>();
+  int used = 0;
   if (threadIdx.x < kMostTop) sh.kept[threadIdx.x] = 0;
   for (int32_t at = part.from; at < part.to || at == part.from; at += kLot) {
-    sync_lookers();
-    clear_top(sh);
-    sync_lookers();
+    sync_lookers<N>();
+    clear_top(sh, kWaiting);
+    sync_lookers<N>();
     const uint64_t last = sh.kept[top - 1];
     if (threadIdx.x < top) sh.waiting[threadIdx.x] = sh.kept[threadIdx.x];
     if (threadIdx.x == 0) sh.count = top;
-    sync_lookers();
+    sync_lookers<N>();
     // a zero among the kept ones is no candidate: nothing is worse
     const uint64_t least = last + 1;
     const int32_t v = at + static_cast<int32_t>(threadIdx.x);
     if (at == part.from && part.odd_id >= 0) offer_top(sh, least, part.odd, part.odd_id);
     if (static_cast<int>(threadIdx.x) < kLot && v < part.to)
       for (int i = 0; i < V; ++i) offer_top(sh, least, El<T>::to_float(part.body[static_cast<int64_t>(v) * V + i]), part.head + v * V + i);
-    sync_lookers();
-    select_top(sh, top);
+    sync_lookers<N>();
+    used = select_top(sh, top);
   }
+  return used;
 }
 
 // Where the row's vectors start, and which of them this CTA of `ranks` has.
@@ -451,6 +451,10 @@ __device__ __forceinline__ Part<T> part_of(const T* x, int64_t vocab, uint32_t r
   part.body = x + part.head;
   return part;
 }
+
+// CTAs of an SM, as many as the ring and the registers allow.
+template <int N>
+constexpr int kCtas = N == 256 ? 4 : 7;
 
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -473,33 +477,33 @@ __device__ __forceinline__ bool wait_batch(uint64_t* bar, uint32_t phase, int* a
 // A CTA takes rows (or its part of a cluster's row) one after the other.  The
 // loading warp streams them into a ring of batches and runs ahead into the
 // next row, so the memory stays busy while a row is being finished.
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads + 32, 4) score_kernel(const ScoreParams p) {
+template <typename T, bool TOP, int N>
+__global__ void __launch_bounds__(N + 32, kCtas<N>) score_kernel(const ScoreParams p) {
   constexpr int V = kVec<T>;
   constexpr int W = 4;  // words of a vector
   extern __shared__ __align__(128) uint8_t raw[];
-  RowShared& sh = *reinterpret_cast<RowShared*>(raw);
+  RowShared<N>& sh = *reinterpret_cast<RowShared<N>*>(raw);
   uint32_t ranks, rank;
   asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ranks));
   rank = cluster_ctarank();
   const int64_t first_row = blockIdx.x / ranks, row_step = gridDim.x / ranks;
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], kWarps);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], N / 32);
     fence_mbar_init();
     sh.abort = 0;
   }
-  if (TOP && threadIdx.x < kThreads) clear_top(sh.top);
+  if (TOP && threadIdx.x < N) clear_top(sh.top, kWaiting);
   __syncthreads();
-  if (threadIdx.x >= kThreads) {
-    if (threadIdx.x == kThreads) {
+  if (threadIdx.x >= N) {
+    if (threadIdx.x == N) {
       uint32_t n = 0;  // batches so far
       bool ok = true;
       for (int64_t row = first_row; ok && row < p.rows; row += row_step) {
         const Part<T> part = part_of(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab, rank, ranks);
-        for (int32_t at = part.from; at < part.to; at += kUnroll * kThreads) {
+        for (int32_t at = part.from; at < part.to; at += kUnroll * N) {
           const int slot = n % kStages;
           if (!(ok = wait_batch(&sh.empty[slot], n / kStages + 1, &sh.abort))) break;
-          const uint32_t bytes = static_cast<uint32_t>(min(part.to - at, kUnroll * kThreads)) * 16u;
+          const uint32_t bytes = static_cast<uint32_t>(min(part.to - at, kUnroll * N)) * 16u;
           mbar_arrive_expect_tx(&sh.full[slot], bytes);
           asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                            smem_u32(sh.ring[slot])),
@@ -548,22 +552,22 @@ __global__ void __launch_bounds__(kThreads + 32, 4) score_kernel(const ScorePara
   int turn = 0, queued = 0;   // bars so far; vectors this warp has noted
   uint32_t batch = 0;
   bool gave_up = false;  // a load never came
-  for (int32_t at = part.from; at < part.to || batch == 0; at += kUnroll * kThreads, ++batch) {
+  for (int32_t at = part.from; at < part.to || batch == 0; at += kUnroll * N, ++batch) {
     uint32_t now[kUnroll][W];
     if (part.from < part.to) {
       if (!wait_batch(&sh.full[slot], turns, &sh.abort)) gave_up = true;
       const uint4* vec = reinterpret_cast<const uint4*>(sh.ring[slot]);
-const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
+      const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
-        const uint4 q = vec[u * kThreads + threadIdx.x];
+        const uint4 q = vec[u * N + threadIdx.x];
         now[u][0] = q.x, now[u][1] = q.y, now[u][2] = q.z, now[u][3] = q.w;
       }
-      if (part.to - at < kUnroll * kThreads) {
+      if (part.to - at < kUnroll * N) {
         // past the end: -infinity, which adds nothing
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u)
-          if (u * kThreads >= left) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
+          if (u * N >= left) now[u][0] = now[u][1] = now[u][2] = now[u][3] = kNothing<T>;
       }
       // The copy that fills this place again writes through another proxy: the
       // reads above have to be done for it before the place is given back.
@@ -598,7 +602,7 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
         queued += __popc(all);
       }
       // raise the bar after 4, 16, 64, ... batches
-      if (batch && ((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * kThreads < part.to)
+      if (batch && ((batch + 1) & batch) == 0 && ((batch + 1) & 0x55555555u) && at + kUnroll * N < part.to)
         bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
     }
     const float m = max_nan(acc.m, most);
@@ -646,17 +650,18 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
   if (TOP) {
     if (queued > kQueue) sh.top.lost = 1;
     if (queued > 64) sh.top.flood = 1;
-    bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
+    if (batch > 1) bar = fmaxf(bar, group_bar(sh.top, seen, p.top, turn++));
+    else sync_lookers<N>();
   } else {
-    sync_lookers();
+    sync_lookers<N>();
   }
-  Sums all = warp_join(sh.warps[threadIdx.x % kWarps], kWarps);
+  int used = 0;  // candidates of the row
+  Sums all = warp_join(sh.warps[threadIdx.x % (N / 32)], N / 32);
   if (TOP) {
     if (part.odd_id >= 0 && !(part.odd < bar)) offer_top(sh.top, candidate(bar, 0xFFFFFFFFu), part.odd, part.odd_id);
     open_queue(part, sh.top, queued, bar, p.top);
-    sync_lookers();
-    if (sh.top.lost) careful_top(part, sh.top, p.top);
-    else select_top(sh.top, p.top);
+    sync_lookers<N>();
+    used = sh.top.lost ? careful_top(part, sh.top, p.top) : select_top(sh.top, p.top);
   }
   if (ranks > 1) {
     if (threadIdx.x == 0) sh.cta = all;
@@ -672,8 +677,8 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
       }
       if (TOP) {
         // at most 8 x 32 candidates of the row's CTAs
-        clear_top(sh.top);
-        sync_lookers();
+        clear_top(sh.top, used);
+        sync_lookers<N>();
         if (threadIdx.x < ranks * p.top) {
           const uint32_t a = cluster_map(smem_u32(&sh.top.kept[threadIdx.x % p.top]), threadIdx.x / p.top);
           uint64_t c;
@@ -681,7 +686,7 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
           sh.top.waiting[threadIdx.x] = c;
         }
         if (threadIdx.x == 0) sh.top.count = static_cast<int>(ranks) * p.top;
-        sync_lookers();
+        sync_lookers<N>();
         select_top(sh.top, p.top);
       }
     }
@@ -690,18 +695,20 @@ const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
   }
   const bool nan_row = all.m != all.m;
   float lse, entropy;
-  if (nan_row) {
-    lse = entropy = __int_as_float(0x7FC00000);
-  } else if (all.m > low + 1024.0f && all.m < -low) {
-    const float l = log2f(all.s);
-    lse = (reference(all.m) + l) * kLn2;
-    entropy = (l - all.t / all.s) * kLn2;
-  } else {
-    plain_row(x, p.vocab, reinterpret_cast<float*>(sh.top.bests), &lse, &entropy);
+  const bool plain = !nan_row && !(all.m > low + 1024.0f && all.m < -low);
+  if (plain) plain_row<T, N>(x, p.vocab, reinterpret_cast<float*>(sh.top.bests), &lse, &entropy);
+  if (threadIdx.x < 32) {
+    if (nan_row) {
+      lse = entropy = __int_as_float(0x7FC00000);
+    } else if (!plain) {
+      const float l = log2f(all.s);
+      lse = (reference(all.m) + l) * kLn2;
+      entropy = (l - all.t / all.s) * kLn2;
+    }
+    write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept : nullptr);
   }
-  write_row(p, row, lse, entropy, logit, given, nan_row, TOP ? sh.top.kept : nullptr);
-  if (TOP) clear_top(sh.top);
-  else if (ranks == 1) sync_lookers();  // before the next row's sums
+  if (TOP) clear_top(sh.top, used);
+  else if (ranks == 1) sync_lookers<N>();  // before the next row's sums
   }
 }
 
@@ -783,6 +790,14 @@ __global__ void __launch_bounds__(kGradThreads) score_backward_kernel(const Grad
 
 // ------------------------------------------------------------------- host --
 
+// Many rows of up to this many bytes go to CTAs of 128, of which seven share
+// an SM: a row's end is barriers and one warp's work, and less stands idle
+// meanwhile (20 alternatives, bf16, CTAs of 256 and of 128: 8192 x 1000 145 and
+// 57 us, 8192 x 32000 170 and 135 us; longer rows need the larger batch: 4096 x
+// 131072 224 and 255 us; and rows that all run at once the more threads: 300 x
+// 32000 15.0 and 16.7 us).
+constexpr int64_t kShortRow = 65536;
+
 int el_bytes(int dtype) { return dtype == EG_EL_F32 ? 4 : 2; }
 
 eg_status check_score(const eg_score_args* a) {
@@ -803,20 +818,20 @@ eg_status check_score(const eg_score_args* a) {
   return EG_OK;
 }
 
-template <typename T, bool TOP>
+template <typename T, bool TOP, int N>
 eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
   cudaLaunchConfig_t cfg{};
-  auto kernel = score_kernel<T, TOP>;
-  const eg_status s = host_allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(sizeof(RowShared)), dev, &done);
+  auto kernel = score_kernel<T, TOP, N>;
+  const eg_status s = host_allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(sizeof(RowShared<N>)), dev, &done);
   if (s != EG_OK) return s;
-  // four CTAs an SM take rows in turn (4096 x 131072 bf16, 20 alternatives:
-  // three with a ring of three batches 250 us, four with two 231 us, two with
-  // four 267 us); a cluster takes one
-  const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, 4 * sms);
+  // four CTAs of 256 an SM take rows in turn (4096 x 131072 bf16, 20
+  // alternatives: three with a ring of three batches 250 us, four with two
+  // 231 us, two with four 267 us); a cluster takes one
+  const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, kCtas<N> * sms);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
-  cfg.blockDim = dim3(kThreads + 32);
-  cfg.dynamicSmemBytes = sizeof(RowShared);
+  cfg.blockDim = dim3(N + 32);
+  cfg.dynamicSmemBytes = sizeof(RowShared<N>);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -830,7 +845,9 @@ eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaSt
 
 template <typename T>
 eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaStream_t st) {
-  return p.top ? launch_score<T, true>(p, ranks, dev, sms, st) : launch_score<T, false>(p, ranks, dev, sms, st);
+  const bool small = p.rows > kCtas<256> * sms && p.vocab * static_cast<int64_t>(sizeof(T)) <= kShortRow;
+  if (p.top) return small ? launch_score<T, true, 128>(p, ranks, dev, sms, st) : launch_score<T, true, 256>(p, ranks, dev, sms, st);
+  return small ? launch_score<T, false, 128>(p, ranks, dev, sms, st) : launch_score<T, false, 256>(p, ranks, dev, sms, st);
 }
 
 }  // namespace

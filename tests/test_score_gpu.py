@@ -82,6 +82,24 @@ def test_many_rows_are_the_same_every_time(dtype, rows, vocab):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("vocab,top", [(1, 1), (37, 32), (1003, 20), (1003, 0), (14001, 32)])
+def test_many_short_rows(dtype, vocab, top):
+    """As many rows as fill the machine several times, ordinary ones and such as make every value a candidate or none."""
+    rows = 1500
+    g = torch.Generator().manual_seed(vocab)
+    x = H.rand(g, rows, vocab, dtype=dtype, scale=2.5)
+    at = torch.arange(vocab, dtype=torch.float32).to(x.dtype)
+    x[7::50] = at / 64
+    x[8::50] = -at / 64
+    x[9::50] = 3.0
+    x[10::50] = torch.finfo(x.dtype).min
+    x[11::50] = -INF
+    x[12::50, : vocab // 2] = -INF
+    tokens = torch.randint(-1, vocab + 1, (rows,), generator=g)
+    _check(eg.token_logprobs(x.cuda(), tokens.cuda(), top=top), x, tokens, top)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("order", ["rising", "falling", "equal", "two values", "few"])
 def test_top_of_ordered_and_equal_logits(dtype, order):
     """Values that would all be candidates: the selection runs often, and ties go to the lowest id."""
