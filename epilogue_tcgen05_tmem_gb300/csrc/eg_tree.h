@@ -13,7 +13,8 @@ namespace eg {
 // unit belongs to.
 struct TreeMeta {
   int64_t from;         // the CTA's first unit
-  int64_t begin, end;   // the units of the item that holds it
+  int64_t begin;        // the first unit of the item that holds it,
+  int64_t lead, last;   // and the first units of that item's first and last tile
   int64_t total;        // units of the run
   int32_t ctas;         // CTAs that have units
   int32_t start, rows, row0, head;  // the item's first packed row, rows, first row in the sequence, cached head

@@ -132,7 +132,8 @@ struct TreeSeq {
   int32_t start, n;    // packed rows
   int32_t ctx, keys;   // cached places, with the drafted tokens
   int32_t tiles;       // key tiles
-  int32_t groups;      // row groups
+  int32_t groups;      // row groups: items of a cached head
+  int32_t lots;        // costs of those items together
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int32_t start, int32_t n, int32_t ctx) {
@@ -142,6 +143,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int32_t start, 
   s.keys = min(ctx + n, room);
   s.tiles = (s.keys + static_cast<int32_t>(kTreeKeys) - 1) >> 7;
   s.groups = (n * p.group + p.item_rows - 1) / p.item_rows;
+  s.lots = s.groups * p.q_tiles;
+  if (p.q_tiles == 2 && s.groups > 0 && n * p.group - (s.groups - 1) * p.item_rows <= p.tile_rows) --s.lots;
   return s;
 }
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
@@ -150,12 +153,47 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   const int32_t start = min(max(from, 0), p.tokens);
   return tree_seq(p, start, min(min(max(to, start), p.tokens) - start, p.max_tree), min(max(ctx, 0), room));
 }
-// Units of one item: its key tiles, and kTreeFixed for what an item costs
-// beside them (queries, the first and the last tile's latency, the result).
+// Units.  A key tile of an item costs one, or two where the item has two row
+// tiles: that takes 1.8 times as long (16 sequences of 24 to 48 tokens, 64
+// query heads, 8 cached, 3800 to 8200 places: 181 us when both count the same,
+// 159 us so; 32 to 64 tokens: 182 and 172 us).  An item has kTreeFixed more
+// tiles' units for what it costs beside them: queries, the first and the last
+// tile's latency, the result (2, 3, 4 and 6: 189, 182, 180 and 183 us with 32
+// to 64 tokens, 116, 103, 102 and 105 us for 24 sequences of 7 to 13 tokens and
+// up to 9001 places).  A tile belongs to the CTA that has its first unit.
 constexpr int32_t kTreeFixed = 4;
-__device__ __forceinline__ int32_t tree_item_units(const TreeSeq& s) { return s.tiles + kTreeFixed; }
 __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& s) {
-  return static_cast<int64_t>(tree_item_units(s)) * (s.groups * p.kv_heads);
+  return static_cast<int64_t>(s.tiles + kTreeFixed) * (s.lots * p.kv_heads);
+}
+
+// The item that has unit `idx` of a sequence.
+struct TreeItem {
+  int32_t head, row0, rows;
+  int32_t cost;        // units of a tile
+  int32_t in, units;   // the unit's place in the item, and how many that has
+};
+__device__ __forceinline__ TreeItem tree_item(const TreeParams& p, const TreeSeq& s, int64_t idx) {
+  TreeItem item;
+  const int32_t each = s.tiles + kTreeFixed;
+  const int64_t of_head = static_cast<int64_t>(each) * s.lots;
+  int32_t g;
+  if ((of_head * p.kv_heads) >> 32) {
+    item.head = static_cast<int32_t>(idx / of_head);
+    const int64_t rest = idx - item.head * of_head, most = static_cast<int64_t>(each) * p.q_tiles;
+    g = min(static_cast<int32_t>(rest / most), s.groups - 1);
+    item.in = static_cast<int32_t>(rest - g * most);
+  } else {
+    const uint32_t most = static_cast<uint32_t>(each) * p.q_tiles;
+    item.head = static_cast<int32_t>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(of_head));
+    const uint32_t rest = static_cast<uint32_t>(idx) - item.head * static_cast<uint32_t>(of_head);
+    g = min(static_cast<int32_t>(rest / most), s.groups - 1);
+    item.in = static_cast<int32_t>(rest - g * most);
+  }
+  item.row0 = g * p.item_rows;
+  item.rows = min(s.n * p.group - item.row0, p.item_rows);
+  item.cost = item.rows > p.tile_rows ? 2 : 1;
+  item.units = each * item.cost;
+  return item;
 }
 
 // The first unit of CTA c, and the CTA that has unit u, when `total` units are
@@ -181,6 +219,7 @@ struct TreeWalk {
   int64_t at, to;
   // the segment
   int32_t head, row0, rows, first, count;
+  int32_t cost;
   int64_t begin;       // the first unit of its item
 
   const int32_t (*near_)[4];  // start, n, ctx of the sequences from near_b on
@@ -200,20 +239,16 @@ struct TreeWalk {
         load(p);
         units = tree_units(p, seq);
       }
-      const int64_t idx = at - before;
-      const int32_t each = tree_item_units(seq);
-      const int32_t item = units >> 32 ? static_cast<int32_t>(idx / each) : static_cast<int32_t>(static_cast<uint32_t>(idx) / static_cast<uint32_t>(each));
-      const int32_t in = static_cast<int32_t>(idx - static_cast<int64_t>(item) * each);
-      const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(each - in), to - at));
-      begin = at - in;
+      const TreeItem item = tree_item(p, seq, at - before);
+      const int32_t take = static_cast<int32_t>(min(static_cast<int64_t>(item.units - item.in), to - at));
+      begin = at - item.in;
       at += take;
-      // units 0..kTreeFixed-1 of an item stand for no tile
-      first = max(in - kTreeFixed, 0);
-      count = in + take - kTreeFixed - first;
+      cost = item.cost;
+      // tiles whose first unit is here; the first kTreeFixed stand for none
+      first = max((item.in + cost - 1) / cost - kTreeFixed, 0);
+      count = (item.in + take + cost - 1) / cost - kTreeFixed - first;
       if (count <= 0) continue;
-      head = item / seq.groups;
-      row0 = (item - head * seq.groups) * p.item_rows;
-      rows = min(seq.n * p.group - row0, p.item_rows);
+      head = item.head, row0 = item.row0, rows = item.rows;
       return true;
     }
   }
@@ -329,7 +364,9 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     if (w < warp) base += sh.warps[0][w];
     total += sh.warps[0][w];
   }
-  const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), total));
+  // a range is no shorter than a tile's units, so that a CTA between the first
+  // and the last of an item has a tile of it
+  const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), p.q_tiles == 2 ? total >> 1 : total));
   if (static_cast<int32_t>(blockIdx.x) >= ctas) {
     if (blockIdx.x == 0 && tid == 0) p.meta[0].ctas = 0;
     return;
@@ -544,13 +581,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       // what the joining kernel has to know of this CTA's first item
       TreeMeta m;
       m.from = from;
-      const int64_t idx = from - sh.before;
-      const int32_t each = tree_item_units(walk.seq);
-      m.begin = from - idx % each, m.end = m.begin + each, m.total = total;
-      m.ctas = ctas;
-      const int32_t item = static_cast<int32_t>(idx / each), head = item / walk.seq.groups;
-      m.start = walk.seq.start, m.row0 = (item - head * walk.seq.groups) * p.item_rows, m.head = head;
-      m.rows = min(walk.seq.n * p.group - m.row0, p.item_rows), m.pad = 0;
+      const TreeItem item = tree_item(p, walk.seq, from - sh.before);
+      m.begin = from - item.in, m.total = total, m.ctas = ctas;
+      m.lead = m.begin + kTreeFixed * item.cost, m.last = m.begin + item.units - item.cost;
+      m.start = walk.seq.start, m.row0 = item.row0, m.head = item.head, m.rows = item.rows, m.pad = 0;
       p.meta[blockIdx.x] = m;
     }
     if (warp == 10) {
@@ -828,8 +862,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       tc_fence_after();
       if (!whole && p.arrivals) {
         // the CTA that leaves the last part of the item joins all of them
-        const int32_t lead = tree_owner(total, ctas, walk.begin + kTreeFixed);
-        const int32_t last = tree_owner(total, ctas, walk.begin + tree_item_units(walk.seq) - 1);
+        const int32_t lead = tree_owner(total, ctas, walk.begin + kTreeFixed * walk.cost);
+        const int32_t last = tree_owner(total, ctas, walk.begin + (walk.seq.tiles + kTreeFixed - 1) * walk.cost);
         if (tid == 0) {
           const int before = atomicAdd(p.arrivals + lead, 1);
           sh.joins = before == last - lead;
@@ -876,7 +910,7 @@ __global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
   if (cut >= ctas || m.from <= m.begin || from_before > m.begin) return;
   // the CTAs with the item's first tile and with its last: those between them
   // have some too
-  const int lead = tree_owner(m.total, ctas, m.begin + kTreeFixed), last = tree_owner(m.total, ctas, m.end - 1);
+  const int lead = tree_owner(m.total, ctas, m.lead), last = tree_owner(m.total, ctas, m.last);
   if (lead == last) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + (lane & 7);
