@@ -3,16 +3,21 @@
 // cache (include/eg_decoder.h has the formulas).
 //
 // All of it is bound by memory (each value is read once and written once), and
-// behind that by how much of it a warp keeps in flight.  A row (one
-// head of one token) is held in registers by a group of lanes, each with two
-// chunks of CH consecutive elements chosen so that both members of every
-// rotated pair are in the same lane: with pairs (i, i + rot/2) chunk j and the
-// chunk rot/2 elements later, else any two; lanes lie side by side in both.  The norm's sum is
-// then the only exchange between lanes.  A warp has the same heads of one kind
-// (queries, keys or values) for its whole life and walks the tokens: addresses
-// step and weights stay in registers.  The next token's rows and angles come in
-// by asynchronous copies to shared memory while this one's are worked on; a
-// lane copies what it will read itself, so the rows need no barrier.
+// behind that by how much of it a warp keeps in flight and by some 330
+// instructions for 512 values.  bf16, 32 + 8 heads of 128: 8191 tokens forward
+// 37 us (4.7 TB/s, much of it in L2), 16384 tokens' gradient 96 us (5.3 TB/s);
+// fp16, 24593 tokens appended 96 us (6.4 TB/s of the 6.8 that a copy reaches).
+//
+// A row (one head of one token) is held in registers by a group of lanes, each
+// with two chunks of CH consecutive elements chosen so that both members of
+// every rotated pair are in the same lane: with pairs (i, i + rot/2) chunk j
+// and the chunk rot/2 elements later, else any two; lanes lie side by side in
+// both.  The norm's sum is then the only exchange between lanes.  A warp has
+// the same heads of one kind (queries, keys or values) for its whole life and
+// walks the tokens: addresses step and weights stay in registers.  The next
+// token's rows and angles come in by asynchronous copies to shared memory while
+// this one's are worked on; a lane copies what it will read itself, so the rows
+// need no barrier.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -788,7 +793,10 @@ RopeParams base_params(const eg_rope_args& a) {
 }
 
 // Whether chunks of `ch` elements serve this call: every address a chunk
-// starts at is a multiple of its size, and a lane's pairs are all rotated or none.
+// starts at is a multiple of its size, and a lane's pairs are all rotated or
+// none.  8 where they do (float32: 4, the same 16 bytes), else 4, else single
+// elements: the three take 39, 55 and 245 us for 8191 tokens of 32 + 8 heads of
+// 128 in bf16, and 109, 129 and 1102 us for 16384 tokens' gradient.
 bool chunks_fit(const eg_rope_args& a, int ch, std::initializer_list<const void*> ptrs,
                 std::initializer_list<int64_t> strides) {
   if (a.head_dim % ch) return false;

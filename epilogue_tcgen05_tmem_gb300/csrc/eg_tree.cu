@@ -158,7 +158,10 @@ eg_status set_up(eg_tree_plan* pl) {
   pl->hd = p.head_dim <= 64 ? 64 : 128;
   const int group = p.q_heads / p.kv_heads;
   pl->tile_rows = 128 / row_box(group) * row_box(group);
-  // two tiles of rows share each key tile where a tree can have more than one
+  // two tiles of rows share each key tile where a tree can have more than one;
+  // with one the second tile's shared memory is a stage of the ring (16
+  // sequences of 32 to 64 tokens of 64 heads over 8 cached: two 173 us, one at a
+  // time 206 us)
   pl->q_tiles = p.max_tree * group > pl->tile_rows ? 2 : 1;
   const uint32_t tile = pl->hd == 64 ? TreeSmem<64>::kTileBytes : TreeSmem<128>::kTileBytes;
   const uint32_t extra = TreeSmem<64>::kExtra;
@@ -178,8 +181,12 @@ eg_status set_up(eg_tree_plan* pl) {
     return host_cuda_fail(e, "cudaFuncSetAttribute");
   pl->wait_limit_ns = host_wait_limit_ns();
   // One CTA reads at most the parts of the most CTAs that share an item (those
-  // of a single sequence: the grid over the cached heads): up to 256 KB is
-  // quicker than a second kernel.
+  // of a single sequence: the grid over the cached heads).  Up to 256 KB are
+  // joined by the last of them, which spares a second kernel (32 query heads
+  // over 8 cached ones, one token after 517 and after 8000: 19.1 and 27.3 us,
+  // with the second kernel 21.2 and 31.5 us); above, the second kernel joins
+  // with the whole GPU (32 tokens after 8000: 32.4 us, 72.4 us by the last; 16
+  // sequences of 32 to 64 tokens of 64 heads: 172 and 198 us).
   const int64_t parts = pl->grid / p.kv_heads + 2;
   pl->joins_itself = parts * rows_of(*pl) * pl->hd * 4 <= 256 * 1024;
   return EG_OK;

@@ -23,6 +23,19 @@
 // on the key tiles and are joined at the end of the range; with more rows
 // each has 128 of them and K and V tiles are used twice.  So while one
 // warpgroup forms weights the tensor cores work for the other.
+//
+// Measured, and what bounds it.  Two sequences of 98304 and 131072 places, 32
+// query heads over 8 cached, one token each: 155 us, 6.1 TB/s of the 6.8 that a
+// copy reaches; CTAs get uneven shares of the bandwidth, and the last decides.
+// 24 sequences of up to 13 tokens and 9001 places: 100 us, 4.2 TB/s; a CTA has
+// 2.3 segments, and each costs some 4 us beside its tiles.  16 sequences of 32
+// to 64 tokens, 64 query heads, 3800 to 8200 places: 172 us, 790 TFLOP/s of the
+// 1922 of a plain product.  There a tile's two products take 1050 cycles of
+// the tensor cores and its weights 1480 of their warpgroup (read and maximum
+// 380, exponentials 680, store and signal 320), so a warpgroup's turn is 1700
+// cycles where two full overlaps would be 1050.  Two warpgroups for each row
+// tile, half the keys each, were slower (202 us: 104 registers a thread spill),
+// and so was a signal after half the weights (198 us).
 #pragma once
 #include <math_constants.h>
 
@@ -272,8 +285,7 @@ struct TreeShared {
 };
 static_assert(sizeof(TreeShared) <= TreeSmem<64>::kExtra, "fits the room after the tiles");
 
-// Position of a tile's load in the ring's order: K0, K1, V0, K2, V1, ...
-__device__ __forceinline__ uint32_t tree_pos_k(uint32_t i) { return i == 0 ? 0 : 2 * i - 1; }
+// Position of a tile's values in the ring's order: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ uint32_t tree_pos_v(uint32_t i, uint32_t count) { return i + 1 < count ? 2 * i + 2 : 2 * count - 1; }
 
 // Four columns of one row of an item that CTAs lead..last have parts of, joined

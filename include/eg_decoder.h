@@ -125,7 +125,8 @@ EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache
  * A plan owns the partial results of sequences that it splits over the GPU;
  * runs of one plan must not overlap on the GPU. */
 typedef struct {
-  int32_t q_heads, kv_heads;    /* q_heads a multiple of kv_heads */
+  int32_t q_heads, kv_heads;    /* q_heads a multiple of kv_heads: 1..16 times as many, or another
+                                   number whose least common multiple with 8 is at most 128 */
   int32_t head_dim;             /* a multiple of 8, 8..128 */
   int32_t dtype;                /* EG_EL_BF16 or EG_EL_F16 (q, cache and o) */
   int32_t page_size;            /* a multiple of 8 */
@@ -156,7 +157,8 @@ EG_API eg_status eg_tree_plan_workspace_bytes(const eg_tree_plan* plan, size_t* 
 EG_API eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args,
                                   const eg_kv_cache* cache, void* stream);
 /* Synchronise the plan's device and report a wait in its kernels that ran past
- * its limit (EG_ERR_DEVICE_TIMEOUT, then cleared). */
+ * its limit (EG_ERR_DEVICE_TIMEOUT, then cleared; what the plan's runs wrote
+ * since the wait is not to be used). */
 EG_API eg_status eg_tree_plan_device_status(eg_tree_plan* plan);
 /* Testing hook for failure detection, as eg_plan_set_test_stall: limit the
  * kernels' waits to `wait_limit_ns` (0: the default) and, with
