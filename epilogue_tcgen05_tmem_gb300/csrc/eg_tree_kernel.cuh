@@ -223,18 +223,21 @@ __device__ __forceinline__ int32_t tree_owner(int64_t total, int32_t ctas, int64
 
 constexpr int kTreeNear = 16;  // sequences whose lengths a CTA keeps in shared memory
 
-// A walk over a CTA's range: one segment (consecutive key tiles of one item)
-// at a time.
-struct TreeWalk {
+// Consecutive key tiles of one item.
+struct TreeSegment {
   TreeSeq seq;
   int32_t b;
-  int64_t before;      // units of the sequences before b
-  int64_t at, to;
-  // the segment
   int32_t head, row0, rows, first, count;
   int32_t cost;
+  int32_t more;        // 0: there is none
   int64_t begin;       // the first unit of its item
+  __device__ __forceinline__ bool whole() const { return first == 0 && count == seq.tiles; }
+};
 
+// A walk over a CTA's range, one segment at a time.
+struct TreeWalk : TreeSegment {
+  int64_t before;      // units of the sequences before b
+  int64_t at, to;
   const int32_t (*near_)[4];  // start, n, ctx of the sequences from near_b on
   int32_t near_b;
 
@@ -265,7 +268,6 @@ struct TreeWalk {
       return true;
     }
   }
-  __device__ __forceinline__ bool whole() const { return first == 0 && count == seq.tiles; }
 };
 
 // Shared state after the tiles.
@@ -273,6 +275,7 @@ struct TreeShared {
   uint64_t full[12], empty[12];   // ring stages
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t q_full, q_empty, exchange, drained;
+  uint64_t told[2], done[2];      // segments for the softmax warpgroups
   uint32_t tmem;
   int32_t abort;
   int32_t poisoned[2];            // the last segment (counted from 1) that found a value that is not finite
@@ -281,6 +284,7 @@ struct TreeShared {
   int64_t before;
   int64_t warps[2][12];
   int32_t near_[kTreeNear][4];
+  TreeSegment segments[2];
   float2 stats[2][128];           // a warpgroup's row references and weights
 };
 static_assert(sizeof(TreeShared) <= TreeSmem<64>::kExtra, "fits the room after the tiles");
@@ -361,6 +365,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   if (tid == 0) {
     for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_done[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.told[i], 1), mbar_init(&sh.done[i], 8);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_empty, 1);
     mbar_init(&sh.exchange, 256);
@@ -423,11 +428,6 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
-  TreeWalk walk;
-  walk.b = near_b, walk.before = sh.before, walk.at = from, walk.to = to;
-  walk.near_ = sh.near_, walk.near_b = near_b;
-  walk.load(p);
-
   // Bounded wait: false once any wait of the CTA has run past its limit.
   volatile int32_t* abort = &sh.abort;
   auto wait = [&](uint64_t* bar, uint32_t phase) {
@@ -456,6 +456,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
   // block was launched with (384 x 168).
   if (warp >= 8) {
   setmaxnreg_dec<88>();
+  TreeWalk walk;
+  walk.b = near_b, walk.before = sh.before, walk.at = from, walk.to = to;
+  walk.near_ = sh.near_, walk.near_b = near_b;
+  walk.load(p);
   if (warp == 8) {
     // ------------------------------------------------------- producer ----
     uint32_t pos = 0;  // loads so far
@@ -599,6 +603,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       m.start = walk.seq.start, m.row0 = item.row0, m.head = item.head, m.rows = item.rows, m.pad = 0;
       p.meta[blockIdx.x] = m;
     }
+    if (warp == 11) {
+      // the walk for the warpgroups below, whose registers have no room for it
+      bool more = true;
+      for (uint32_t n = 0; more; ++n) {
+        if (!wait_all(&sh.done[n & 1], (n >> 1) + 1)) break;
+        more = walk.next(p);
+        walk.more = more;
+        if (lane == 0) {
+          sh.segments[n & 1] = walk;
+          mbar_arrive(&sh.told[n & 1]);
+        }
+      }
+    }
     if (warp == 10) {
       // a box is `box_tokens` tokens by the heads that share a cached one;
       // lane i has box i of each tile
@@ -632,17 +649,19 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
     uint32_t base = 0, uses = 0, exchanges = 0;
     int32_t segment = 0;
     bool ok = true;
-    while (ok && walk.next(p)) {
+    for (;;) {
+      const TreeSegment& walk = sh.segments[segment & 1];
+      if (!(ok = wait_all(&sh.told[segment & 1], segment >> 1)) || !walk.more) break;
       ++segment;
       const bool pair = walk.rows > p.tile_rows;
-      const int count = walk.count;
+      const int count = walk.count, first = walk.first, ctx = walk.seq.ctx, keys = walk.seq.keys;
       const int r = (pair ? s * p.tile_rows : 0) + row_in;
       const bool valid = row_in < p.tile_rows && r < walk.rows;
       const bool busy = __any_sync(0xffffffffu, valid);  // the warp has a row
       const int t = (walk.row0 + r) / p.group;
       const int64_t packed = walk.seq.start + t;
       const int head = walk.head * p.group + (walk.row0 + r) - t * p.group;
-      const int drafted = walk.seq.keys - walk.seq.ctx;  // drafted keys that exist
+      const int drafted = keys - ctx;  // drafted keys that exist
       // 32 bits of the row's mask from drafted token u on
       auto drafted_bits = [&](int u) -> uint32_t {
         const int left = drafted - u;
@@ -661,8 +680,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       float m = -CUDART_INF_F, l = 0.0f;  // m: the reference (log2), before the shift
       bool fresh = true;                  // no tile of this segment yet
       for (int i = pair ? 0 : s; ok && i < count; i += pair ? 1 : 2) {
-        const int key0 = (walk.first + i) * static_cast<int>(kTreeKeys);
-        const bool edge = key0 + static_cast<int>(kTreeKeys) > walk.seq.ctx;
+        const int key0 = (first + i) * static_cast<int>(kTreeKeys);
+        const bool edge = key0 + static_cast<int>(kTreeKeys) > ctx;
         if (!(ok = wait_all(&sh.s_full[s], uses))) break;
         tc_fence_after();
         if (busy) {
@@ -676,7 +695,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
             // row does not attend to
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              const int d = walk.seq.ctx - (key0 + 32 * w);  // context places of this word
+              const int d = ctx - (key0 + 32 * w);  // context places of this word
               const uint32_t bits = d >= 32  ? 0xFFFFFFFFu
                                     : d <= 0 ? drafted_bits(-d)
                                              : ((1u << d) - 1u) | (drafted_bits(0) << d);
@@ -734,7 +753,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           tmem_st_wait();
         }
         fresh = false;
-        const bool cut = walk.seq.keys < key0 + static_cast<int>(kTreeKeys), scan = p.mask || drafted > 1;
+        const bool cut = keys < key0 + static_cast<int>(kTreeKeys), scan = p.mask || drafted > 1;
         if (edge && (cut || scan)) {
           // values of places past the end become zero, and so do drafted
           // values that are not finite: a weight of zero times one would
@@ -744,10 +763,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           if (!(ok = wait_all(&sh.full[slot], at / stages))) break;
           const int key = key0 + row_in;
           uint8_t* v_row = ring + slot * kTile + row_in * 128;
-          if (key >= walk.seq.keys) {
+          if (key >= keys) {
 #pragma unroll 4
             for (int j = 0; j < kChunks * 8; ++j) *reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
-          } else if (scan && key >= walk.seq.ctx) {
+          } else if (scan && key >= ctx) {
             constexpr uint32_t kInf = El<T>::kBf16 ? 0x7F80u : 0x7C00u;
             bool found = false;
 #pragma unroll 1
@@ -800,6 +819,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       const bool whole = walk.whole();
       if (busy) {
         // a pair's warpgroup writes its rows, else each writes half the columns
+        constexpr int kCols = HD / 2;  // at a time
         const int from_col = pair ? 0 : s * (HD / 2), to_col = pair ? HD : from_col + HD / 2;
         const float f0 = (pair || s == 0 ? f_own : f_other), f1 = (s == 0 ? f_other : f_own);
         const float scale = whole ? (weight == 0.0f ? 0.0f : 1.0f / weight) : 1.0f;
@@ -810,24 +830,28 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         // [slot][4 columns][row][column]: a warp's rows are stored side by side
         float* part = p.partial + slot * part_rows * HD + r * 4;
 #pragma unroll 1
-        for (int j = from_col; j < to_col; j += 32) {
-          uint32_t a[32];
-          tmem_ld32p(t_o + (pair ? s * 128 : 0) + j, a);
-          tmem_ld_wait();
-          reg_fence<32>(a);
+        for (int j = from_col; j < to_col; j += kCols) {
+          uint32_t a[kCols];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * f0);
+          for (int k = 0; k < kCols; k += 32) tmem_ld32p(t_o + (pair ? s * 128 : 0) + j + k, a + k);
           if (!pair && tiles1 > 0) {
-            uint32_t b[32];
-            tmem_ld32p(t_o + 128 + j, b);
-            tmem_ld_wait();
-            reg_fence<32>(b);
+            uint32_t b[kCols];
 #pragma unroll
-            for (int k = 0; k < 32; ++k) a[k] = __float_as_uint(fmaf(__uint_as_float(b[k]), f1, __uint_as_float(a[k])));
+            for (int k = 0; k < kCols; k += 32) tmem_ld32p(t_o + 128 + j + k, b + k);
+            tmem_ld_wait();
+            reg_fence<kCols>(a), reg_fence<kCols>(b);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+              a[k] = __float_as_uint(fmaf(__uint_as_float(b[k]), f1, __uint_as_float(a[k]) * f0));
+          } else {
+            tmem_ld_wait();
+            reg_fence<kCols>(a);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * f0);
           }
           if (!valid) continue;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
+          for (int k = 0; k < kCols; k += 8) {
             if (j + k >= p.head_dim) continue;
             float y[8];
 #pragma unroll
@@ -895,6 +919,8 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
         }
       }
       base += 2 * count;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.done[(segment - 1) & 1]);
     }
   }
   __syncwarp();

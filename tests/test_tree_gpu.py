@@ -145,6 +145,11 @@ CASES = [
     ("bf16", 32, 4, 128, 32, [3000], [256], True, False),
     ("f16", 2, 1, 72, 40, list(range(0, 400, 7)), [1 + i % 4 for i in range(58)], False, False),
     ("bf16", 64, 8, 128, 16, [17000], [1], True, False),
+    # items of two row tiles and of one side by side, each over several CTAs
+    ("bf16", 32, 2, 128, 16, [6000, 0, 2500, 77], [17, 24, 9, 8], False, False),
+    ("f16", 40, 1, 64, 32, [9000, 4000], [30, 3], False, False),
+    # more sequences than a CTA has threads
+    ("bf16", 4, 2, 64, 8, [37 * i % 300 for i in range(900)], [i % 3 for i in range(900)], False, False),
 ]
 
 
@@ -300,6 +305,15 @@ def test_nothing_to_do():
     e = plan.run(d["q"][:0], d["k_cache"], d["v_cache"], d["block_table"][:0], d["context_lens"][:0], d["q_start"][:1])
     assert e.shape == (0, 4, 64)
     plan.close()
+
+
+def test_heads_that_do_not_fit_a_tile_are_refused():
+    for group in (17, 19, 136):
+        with pytest.raises(eg.EgError, match="do not fit a tile") as e:
+            eg.TreeAttention(group, 1, 64)
+        assert e.value.status == eg.EG_ERR_UNSUPPORTED
+    for group in (16, 18, 40, 128):
+        eg.TreeAttention(group, 1, 64).close()
 
 
 def test_refusals():
