@@ -9,33 +9,34 @@
 // product (their error, 2^-9 or 2^-12 of each weight, is the output type's own);
 // l sums them before that rounding, in float32 as S, O and m are.
 //
-// Work.  Every item has as many units as key tiles; all items' units in a row
-// are cut into equal ranges, one for each CTA (one CTA an SM), on the device
-// from the sequences' lengths.  An item that a cut divides leaves float32
-// partial results that a second small kernel joins in a fixed order, so equal
-// inputs give equal bits.
+// Work.  Every item has units for its key tiles (see kTreeFixed); all items'
+// units in a row are cut into equal ranges, one for each CTA (one CTA an SM),
+// on the device from the sequences' lengths.  An item that a cut divides leaves
+// float32 partial results that its last CTA or a second small kernel joins in a
+// fixed order, so equal inputs give equal bits.
 //
 // One CTA: a producer warp (TMA boxes of pages into a ring of 128-key tiles,
-// K and V alike), one issuing thread (tcgen05.mma), two softmax warpgroups
-// and two warps that fetch queries.  S and O of both warpgroups fill tensor
-// memory (4 x 128 columns); P overwrites S as 16-bit values and feeds the
-// second product from there.  With at most 128 rows the warpgroups take turns
-// on the key tiles and are joined at the end of the range; with more rows
-// each has 128 of them and K and V tiles are used twice.  So while one
-// warpgroup forms weights the tensor cores work for the other.
+// K and V alike), one issuing thread (tcgen05.mma), two softmax warpgroups, a
+// warp that fetches queries and one that walks the range for the softmax
+// warpgroups (who spill registers when they do it: 173 against 167 us).  S and
+// O of both warpgroups fill tensor memory (4 x 128 columns); P overwrites S as
+// 16-bit values and feeds the second product from there.  With at most 128 rows
+// the warpgroups take turns on the key tiles and are joined at the end of the
+// range; with more rows each has 128 of them and K and V tiles are used twice.
+// So while one warpgroup forms weights the tensor cores work for the other.
 //
 // Measured, and what bounds it.  Two sequences of 98304 and 131072 places, 32
-// query heads over 8 cached, one token each: 155 us, 6.1 TB/s of the 6.8 that a
+// query heads over 8 cached, one token each: 152 us, 6.2 TB/s of the 6.8 that a
 // copy reaches; CTAs get uneven shares of the bandwidth, and the last decides.
-// 24 sequences of up to 13 tokens and 9001 places: 100 us, 4.2 TB/s; a CTA has
-// 2.3 segments, and each costs some 4 us beside its tiles.  16 sequences of 32
-// to 64 tokens, 64 query heads, 3800 to 8200 places: 172 us, 790 TFLOP/s of the
+// 24 sequences of up to 13 tokens and 9001 places: 97 us, 4.3 TB/s; a CTA has
+// 2.1 segments, and each costs some 4 us beside its tiles.  16 sequences of 32
+// to 64 tokens, 64 query heads, 3800 to 8200 places: 166 us, 816 TFLOP/s of the
 // 1922 of a plain product.  There a tile's two products take 1050 cycles of
 // the tensor cores and its weights 1480 of their warpgroup (read and maximum
 // 380, exponentials 680, store and signal 320), so a warpgroup's turn is 1700
 // cycles where two full overlaps would be 1050.  Two warpgroups for each row
-// tile, half the keys each, were slower (202 us: 104 registers a thread spill),
-// and so was a signal after half the weights (198 us).
+// tile, half the keys each, were slower (202 against 172 us: 104 registers a
+// thread spill), and so was a signal after half the weights (171 against 167).
 #pragma once
 #include <math_constants.h>
 
