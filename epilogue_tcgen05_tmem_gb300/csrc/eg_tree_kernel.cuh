@@ -806,13 +806,10 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
       if (!(ok = wait_all(&sh.exchange, exchanges))) break;
       ++exchanges;
       tc_fence_after();
-      bool repair;
-      if (pair) {
-        repair = *reinterpret_cast<volatile int32_t*>(&sh.poisoned[s]) == segment;
-      } else {
-        other = sh.stats[s ^ 1][row_in];
-        repair = *reinterpret_cast<volatile int32_t*>(&sh.poisoned[0]) == segment || *reinterpret_cast<volatile int32_t*>(&sh.poisoned[1]) == segment;
-      }
+      if (!pair) other = sh.stats[s ^ 1][row_in];
+      // either warpgroup may have met the value first
+      const bool repair = *reinterpret_cast<volatile int32_t*>(&sh.poisoned[0]) == segment ||
+                          *reinterpret_cast<volatile int32_t*>(&sh.poisoned[1]) == segment;
       const float both = fmaxf(own.x, other.x);
       const float ref = both == -CUDART_INF_F ? 0.0f : both;
       const float f_own = tree_ex2(own.x - ref), f_other = tree_ex2(other.x - ref);

@@ -223,6 +223,18 @@ def test_infinite_values_of_seen_places_reach_the_result():
     assert (o[:, :2, 5] == INF).all() and (o[1:, 2:, 6] == -INF).all() and torch.isfinite(o[0, 2:]).all()
 
 
+def test_infinite_drafted_values_reach_the_rows_of_both_tiles():
+    """More rows than one tile: the tiles share the drafted keys, one comes to them after the other, and the rows of each that attend to
+    the value get it."""
+    many, ctx = 200, 900
+    c = Case("bf16", 8, 1, 128, 16, [ctx] * many, [32] * many, True, seed=9)
+    for b in range(many):
+        c.kv[1][c.table[b, (ctx + 2) // 16], (ctx + 2) % 16, 0, 7] = INF  # drafted token 2
+    o, _ = _run(c)
+    o = o.cpu().view(many, 32, 8, 128)
+    assert (o[:, 2:, :, 7] == INF).all() and torch.isfinite(o[:, :2]).all() and torch.isfinite(o[..., :7]).all()
+
+
 def test_same_every_time_and_on_another_stream():
     c = Case("bf16", 32, 8, 128, 16, [3000, 20, 0, 911], [5, 1, 3, 8], False, seed=9)
     d, plan = c.device(), c.plan()
