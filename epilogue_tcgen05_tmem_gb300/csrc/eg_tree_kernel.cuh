@@ -36,7 +36,9 @@
 // 380, exponentials 680, store and signal 320), so a warpgroup's turn is 1700
 // cycles where two full overlaps would be 1050.  Two warpgroups for each row
 // tile, half the keys each, were slower (202 against 172 us: 104 registers a
-// thread spill), and so was a signal after half the weights (171 against 167).
+// thread spill), and so were a signal after half the weights (171 against 167)
+// and scores in halves of 64 keys, each formed while the other's weights are
+// (208: products of 64 columns take the tensor cores nearly as long as 128).
 #pragma once
 #include <math_constants.h>
 
