@@ -149,9 +149,17 @@ int rows_of(const eg_tree_plan& pl) {
   return std::min(pl.tile_rows * pl.q_tiles, pl.prob.max_tree * (pl.prob.q_heads / pl.prob.kv_heads));
 }
 
+// Clear the plan's words from `at` on, and wait for it: the clear is queued on
+// the legacy stream, which a run on a non-blocking stream does not wait for.
+eg_status clear_words(eg_tree_plan* pl, size_t at, const char* what) {
+  cudaError_t e = cudaMemset(pl->ws + at, 0, pl->ws_bytes - at);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, what);
+}
+
 eg_status set_up(eg_tree_plan* pl) {
   int sms = 0;
-  const eg_status s = host_check_device(&pl->device, &sms);
+  eg_status s = host_check_device(&pl->device, &sms);
   if (s != EG_OK) return s;
   cudaError_t e = cudaSuccess;
   const eg_tree_problem& p = pl->prob;
@@ -175,7 +183,7 @@ eg_status set_up(eg_tree_plan* pl) {
   pl->status_at = pl->arrivals_at + (pl->grid * 4 + 15) / 16 * 16;
   pl->ws_bytes = pl->status_at + 16;
   if ((e = cudaMalloc(&pl->ws, pl->ws_bytes)) != cudaSuccess) return host_cuda_fail(e, "allocating the plan's workspace");
-  if ((e = cudaMemset(pl->ws + pl->meta_at, 0, pl->ws_bytes - pl->meta_at)) != cudaSuccess) return host_cuda_fail(e, "clearing the plan's workspace");
+  if ((s = clear_words(pl, pl->meta_at, "clearing the plan's workspace")) != EG_OK) return s;
   if ((e = cudaFuncSetAttribute(reinterpret_cast<const void*>(main_kernel(*pl)), cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(pl->smem))) != cudaSuccess)
     return host_cuda_fail(e, "cudaFuncSetAttribute");
@@ -282,8 +290,8 @@ eg_status eg_tree_plan_device_status(eg_tree_plan* plan) {
     return host_cuda_fail(e, "reading the plan's status");
   if (status == 0) return EG_OK;
   // a CTA that gave up leaves items half counted
-  if ((e = cudaMemset(plan->ws + plan->arrivals_at, 0, plan->ws_bytes - plan->arrivals_at)) != cudaSuccess)
-    return host_cuda_fail(e, "clearing the plan's status");
+  const eg_status s = clear_words(plan, plan->arrivals_at, "clearing the plan's status");
+  if (s != EG_OK) return s;
   return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the tree attention kernel ran past its limit");
 }
 

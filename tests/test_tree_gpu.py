@@ -249,6 +249,39 @@ def test_same_every_time_and_on_another_stream():
     plan.close()
 
 
+def test_a_new_plan_is_ready_for_any_stream():
+    """A plan made while the default stream is busy, with its first run on a stream that does not wait for that one: its counters are clear
+    by then (the items are split over CTAs, and a count left over would leave them unjoined)."""
+    c = Case("bf16", 8, 2, 128, 16, [5000, 900], [1, 1], True, seed=14)
+    d = c.device()
+    out, lse = torch.zeros_like(d["q"]), torch.zeros(2, 8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s of the default stream
+    plan = c.plan()
+    assert torch.cuda.default_stream().query()
+    plan.run(**d, out=out, lse=lse, stream=s.cuda_stream)
+    s.synchronize()
+    _check(c, out, lse)
+    plan.close()
+
+
+def test_a_reported_plan_is_ready_for_any_stream():
+    """The same for the clear that follows a report."""
+    c = Case("bf16", 8, 2, 128, 16, [5000, 900], [1, 1], True, seed=15)
+    d, plan = c.device(), c.plan()
+    out, s = torch.zeros_like(d["q"]), torch.cuda.Stream()
+    plan.set_test_stall(5_000_000, 1)
+    plan.run(**d, out=out)
+    assert plan.device_status() == eg.EG_ERR_DEVICE_TIMEOUT
+    plan.set_test_stall(0, 0)
+    plan.run(**d, out=out, stream=s.cuda_stream)
+    s.synchronize()
+    _check(c, out)
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
 def test_graph_replays_with_new_lengths():
     """Lengths, tables and queries are read on the device: one captured graph serves later steps."""
     a = Case("bf16", 16, 4, 128, 16, [600, 31], [2, 2], True, seed=10)
