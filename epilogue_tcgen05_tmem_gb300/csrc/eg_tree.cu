@@ -149,6 +149,16 @@ int rows_of(const eg_tree_plan& pl) {
   return std::min(pl.tile_rows * pl.q_tiles, pl.prob.max_tree * (pl.prob.q_heads / pl.prob.kv_heads));
 }
 
+// A plan's memory and its kernels' settings are on the device that it was made on.
+eg_status check_current(const eg_tree_plan* plan) {
+  int dev = -1;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return host_cuda_fail(e, "cudaGetDevice");
+  if (dev != plan->device)
+    return host_fail(EG_ERR_INVALID_ARG, "the plan was made on device %d, and device %d is the current one", plan->device, dev);
+  return EG_OK;
+}
+
 // Clear the plan's words from `at` on, and wait for it: the clear is queued on
 // the legacy stream, which a run on a non-blocking stream does not wait for.
 eg_status clear_words(eg_tree_plan* pl, size_t at, const char* what) {
@@ -233,6 +243,7 @@ eg_status eg_tree_plan_workspace_bytes(const eg_tree_plan* plan, size_t* out) {
 eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const eg_kv_cache* cache, void* stream) {
   if (!plan) return host_fail(EG_ERR_INVALID_ARG, "plan is NULL");
   eg_status s = check_run(plan, args, cache);
+  if (s == EG_OK) s = check_current(plan);
   if (s != EG_OK) return s;
   const eg_tree_problem& b = plan->prob;
   const eg_tree_args& a = *args;
@@ -283,6 +294,8 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
 
 eg_status eg_tree_plan_device_status(eg_tree_plan* plan) {
   if (!plan) return host_fail(EG_ERR_INVALID_ARG, "plan is NULL");
+  eg_status s = check_current(plan);
+  if (s != EG_OK) return s;
   cudaError_t e = cudaDeviceSynchronize();
   if (e != cudaSuccess) return host_cuda_fail(e, "synchronising the plan's device");
   int32_t status = 0;
@@ -290,8 +303,7 @@ eg_status eg_tree_plan_device_status(eg_tree_plan* plan) {
     return host_cuda_fail(e, "reading the plan's status");
   if (status == 0) return EG_OK;
   // a CTA that gave up leaves items half counted
-  const eg_status s = clear_words(plan, plan->arrivals_at, "clearing the plan's status");
-  if (s != EG_OK) return s;
+  if ((s = clear_words(plan, plan->arrivals_at, "clearing the plan's status")) != EG_OK) return s;
   return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the tree attention kernel ran past its limit");
 }
 
@@ -305,8 +317,12 @@ eg_status eg_tree_plan_set_test_stall(eg_tree_plan* plan, uint64_t wait_limit_ns
 
 eg_status eg_tree_plan_destroy(eg_tree_plan* plan) {
   if (!plan) return EG_OK;
+  int dev = plan->device;
+  cudaGetDevice(&dev);
+  if (dev != plan->device) cudaSetDevice(plan->device);
   cudaDeviceSynchronize();
   cudaFree(plan->ws);
+  if (dev != plan->device) cudaSetDevice(dev);
   delete plan;
   return EG_OK;
 }

@@ -123,7 +123,9 @@ EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache
  * them, and table entries outside [0, num_pages) read as zero keys and values.
  *
  * A plan owns the partial results of sequences that it splits over the GPU;
- * runs of one plan must not overlap on the GPU. */
+ * runs of one plan must not overlap on the GPU.  It belongs to the device that
+ * is current when it is made: runs and status calls with another one current
+ * are refused (EG_ERR_INVALID_ARG); destroying it is not. */
 typedef struct {
   int32_t q_heads, kv_heads;    /* q_heads a multiple of kv_heads: 1..16 times as many, or another
                                    number whose least common multiple with 8 is at most 128 */

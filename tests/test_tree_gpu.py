@@ -1,5 +1,6 @@
 """Attention of drafted trees over a paged cache on the GPU against the 64-bit
 definition."""
+import ctypes
 import math
 
 import numpy as np
@@ -7,6 +8,7 @@ import pytest
 import torch
 
 import epilogue_tcgen05_tmem_gb300 as eg
+from epilogue_tcgen05_tmem_gb300 import decoder
 from tests import _decoder_helpers as H
 
 pytestmark = pytest.mark.gpu
@@ -339,6 +341,27 @@ def test_a_wait_that_runs_out_is_reported():
     assert plan.device_status() == eg.EG_ERR_DEVICE_TIMEOUT
     assert plan.device_status() == eg.EG_OK  # reported once
     plan.set_test_stall(0, 0)
+    _check(c, plan.run(**d))
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
+def test_a_plan_of_another_device_is_refused():
+    """Found on the host: the plan's record of its device (after its problem) is set to another one, and nothing is launched."""
+    c = Case("bf16", 4, 2, 64, 16, [30], [2], True)
+    d, plan = c.device(), c.plan()
+    problem = decoder.eg_tree_problem.from_address(plan.handle)
+    assert (problem.q_heads, problem.page_size, problem.max_tree) == (4, 16, 2)
+    its = ctypes.c_int.from_address(plan.handle + ctypes.sizeof(problem))
+    assert its.value == torch.cuda.current_device()
+    its.value += 1
+    try:
+        with pytest.raises(eg.EgError, match="device") as e:
+            plan.run(**d)
+        assert e.value.status == eg.EG_ERR_INVALID_ARG
+        assert plan.device_status() == eg.EG_ERR_INVALID_ARG
+    finally:
+        its.value -= 1
     _check(c, plan.run(**d))
     assert plan.device_status() == eg.EG_OK
     plan.close()
