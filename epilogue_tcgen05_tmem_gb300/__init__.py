@@ -20,7 +20,7 @@ import threading
 
 from . import decoder
 from .decoder import (TokenLogProbs, TreeAttention, kv_append, qk_norm_rope,  # noqa: F401
-                      qk_norm_rope_backward, token_logprobs, token_logprobs_backward)
+                      qk_norm_rope_backward, token_logprobs, token_logprobs_backward, token_logprobs_device_status)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libeg.so")

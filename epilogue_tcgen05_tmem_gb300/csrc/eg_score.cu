@@ -42,7 +42,13 @@ struct ScoreParams {
   float *logprob, *lse, *entropy, *top_logprobs;
   int64_t* top_ids;
   int32_t top;
+  int32_t stall;           // test hook: the loading warp loads nothing
+  uint64_t wait_limit_ns;
 };
+
+// Set when a wait of score_kernel ran past its limit (one for each device);
+// eg_token_logprobs_device_status reads it.
+__device__ int32_t g_score_status;
 
 // N threads of a CTA look at values (one more warp loads them); a barrier of these.
 template <int N>
@@ -459,18 +465,17 @@ __device__ __forceinline__ Part<T> part_of(const T* x, int64_t vocab, uint32_t r
 template <int N>
 constexpr int kCtas = N == 256 ? 4 : 7;
 
-constexpr uint64_t kWaitNs = 2000000000ull;
-
 // Bounded wait; gives up at once after any wait of the CTA has run out.
-__device__ __forceinline__ bool wait_batch(uint64_t* bar, uint32_t phase, int* abort) {
+__device__ __forceinline__ bool wait_batch(uint64_t* bar, uint32_t phase, int* abort, uint64_t limit_ns) {
   if (mbar_try_wait(bar, phase & 1)) return true;
   const uint64_t t0 = global_timer_ns();
-  for (uint32_t it = 1;; ++it) {
+  for (uint32_t it = 0;; ++it) {
     if (mbar_try_wait(bar, phase & 1)) return true;
     if ((it & 63u) == 0) {
       if (*reinterpret_cast<volatile int*>(abort)) return false;
-      if (global_timer_ns() - t0 > kWaitNs) {
+      if (global_timer_ns() - t0 > limit_ns) {
         *reinterpret_cast<volatile int*>(abort) = 1;
+        *reinterpret_cast<volatile int32_t*>(&g_score_status) = 1;
         return false;
       }
     }
@@ -498,14 +503,14 @@ __global__ void __launch_bounds__(N + 32, kCtas<N>) score_kernel(const ScorePara
   if (TOP && threadIdx.x < N) clear_top(sh.top, kWaiting);
   __syncthreads();
   if (threadIdx.x >= N) {
-    if (threadIdx.x == N) {
+    if (threadIdx.x == N && !p.stall) {
       uint32_t n = 0;  // batches so far
       bool ok = true;
       for (int64_t row = first_row; ok && row < p.rows; row += row_step) {
         const Part<T> part = part_of(static_cast<const T*>(p.logits) + row * p.row_stride, p.vocab, rank, ranks);
         for (int32_t at = part.from; at < part.to; at += kUnroll * N) {
           const int slot = n % kStages;
-          if (!(ok = wait_batch(&sh.empty[slot], n / kStages + 1, &sh.abort))) break;
+          if (!(ok = wait_batch(&sh.empty[slot], n / kStages + 1, &sh.abort, p.wait_limit_ns))) break;
           const uint32_t bytes = static_cast<uint32_t>(min(part.to - at, kUnroll * N)) * 16u;
           mbar_arrive_expect_tx(&sh.full[slot], bytes);
           asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -516,7 +521,7 @@ __global__ void __launch_bounds__(N + 32, kCtas<N>) score_kernel(const ScorePara
         }
       }
       // leave no copy in flight behind
-      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, kWaitNs);
+      for (uint32_t i = n > kStages ? n - kStages : 0; i < n; ++i) mbar_wait(&sh.full[i % kStages], (i / kStages) & 1, p.wait_limit_ns);
     }
     __syncwarp();
     if (ranks > 1) {  // as often as the other warps below: a cluster has one row
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(N + 32, kCtas<N>) score_kernel(const ScorePara
   for (int32_t at = part.from; at < part.to || batch == 0; at += kUnroll * N, ++batch) {
     uint32_t now[kUnroll][W];
     if (part.from < part.to) {
-      if (!wait_batch(&sh.full[slot], turns, &sh.abort)) gave_up = true;
+      if (!wait_batch(&sh.full[slot], turns, &sh.abort, p.wait_limit_ns)) gave_up = true;
       const uint4* vec = reinterpret_cast<const uint4*>(sh.ring[slot]);
       const int32_t left = part.to - at - static_cast<int32_t>(threadIdx.x);
 #pragma unroll
@@ -821,6 +826,10 @@ eg_status check_score(const eg_score_args* a) {
   return EG_OK;
 }
 
+// What eg_token_logprobs_set_test_stall set: the limit of a wait (0: the default).
+std::atomic<uint64_t> g_limit_ns{0};
+std::atomic<int32_t> g_stall{0};
+
 template <typename T, bool TOP, int N>
 eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaStream_t st) {
   static std::atomic<uint64_t> done{0};
@@ -879,6 +888,8 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   p.logprob = a.logprob, p.lse = a.lse, p.entropy = a.entropy;
   p.top = a.top_ids || a.top_logprobs ? a.top : 0;
   p.top_ids = a.top_ids, p.top_logprobs = a.top_logprobs;
+  p.wait_limit_ns = g_limit_ns.load(std::memory_order_relaxed), p.stall = g_stall.load(std::memory_order_relaxed);
+  if (p.wait_limit_ns == 0) p.wait_limit_ns = host_wait_limit_ns();
   // a cluster for a row while that still leaves every CTA an SM of its own
   // and 16 KB of logits (float32, 50021 of them, five alternatives: 5 rows 13.0
   // us, 17.1 us by one CTA each; 32 rows 14.9 and 17.6 us)
@@ -888,6 +899,29 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   return a.dtype == EG_EL_F32    ? launch_score<float>(p, ranks, dev, sms, st)
          : a.dtype == EG_EL_BF16 ? launch_score<__nv_bfloat16>(p, ranks, dev, sms, st)
                                  : launch_score<__half>(p, ranks, dev, sms, st);
+}
+
+eg_status eg_token_logprobs_device_status(void) {
+  int dev = 0;
+  const eg_status s = host_check_device(&dev);
+  if (s != EG_OK) return s;
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return host_cuda_fail(e, "synchronising the current device");
+  int32_t status = 0;
+  if ((e = cudaMemcpyFromSymbol(&status, g_score_status, 4)) != cudaSuccess) return host_cuda_fail(e, "reading the status of token_logprobs");
+  if (status == 0) return EG_OK;
+  status = 0;
+  e = cudaMemcpyToSymbol(g_score_status, &status, 4);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // later calls may be on streams that do not wait for this one
+  if (e != cudaSuccess) return host_cuda_fail(e, "clearing the status of token_logprobs");
+  return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the token_logprobs kernel ran past its limit");
+}
+
+eg_status eg_token_logprobs_set_test_stall(uint64_t wait_limit_ns, int32_t stall_loader) {
+  if (stall_loader != 0 && stall_loader != 1) return host_fail(EG_ERR_INVALID_ARG, "stall_loader must be 0 or 1");
+  g_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
+  g_stall.store(stall_loader, std::memory_order_relaxed);
+  return EG_OK;
 }
 
 eg_status eg_token_logprobs_backward(const eg_score_args* args, const eg_score_grads* grads, void* stream) {

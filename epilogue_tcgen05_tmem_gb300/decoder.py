@@ -22,7 +22,8 @@ EXPORTED = ("eg_qk_norm_rope", "eg_qk_norm_rope_backward", "eg_qk_norm_rope_work
             "eg_kv_append", "eg_tree_plan_create", "eg_tree_plan_workspace_bytes",
             "eg_tree_plan_run", "eg_tree_plan_device_status", "eg_tree_plan_set_test_stall",
             "eg_tree_plan_destroy",
-            "eg_token_logprobs", "eg_token_logprobs_backward")
+            "eg_token_logprobs", "eg_token_logprobs_backward", "eg_token_logprobs_device_status",
+            "eg_token_logprobs_set_test_stall")
 
 _i64, _i32, _f32, _p = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p
 
@@ -97,6 +98,8 @@ def declare(L: ctypes.CDLL) -> None:
                        ("eg_tree_plan_set_test_stall", [_p, ctypes.c_uint64, _i32]),
                        ("eg_tree_plan_destroy", [_p]),
                        ("eg_token_logprobs", [_p, _p]),
+                       ("eg_token_logprobs_device_status", []),
+                       ("eg_token_logprobs_set_test_stall", [ctypes.c_uint64, _i32]),
                        ("eg_token_logprobs_backward", [_p, _p, _p])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, ctypes.c_int
@@ -433,6 +436,23 @@ def token_logprobs(logits, tokens=None, top=0, stream=None) -> TokenLogProbs:
     if status:
         _fail(status)
     return TokenLogProbs(logprob, lse, entropy, ids, best)
+
+
+def token_logprobs_device_status() -> int:
+    """Synchronises the current device: EG_ERR_DEVICE_TIMEOUT, once, when a wait of ``token_logprobs`` on it ran past its limit
+    (EG_WAIT_CAP_MS) since the last call; the rows concerned are NaN."""
+    if not _b.ready:
+        _b.load()
+    return _b.token_logprobs_device_status()
+
+
+def token_logprobs_set_test_stall(wait_limit_ns: int, stall_loader: int):
+    """Testing hook for failure detection (see include/eg_decoder.h)."""
+    if not _b.ready:
+        _b.load()
+    status = _b.token_logprobs_set_test_stall(wait_limit_ns, int(stall_loader))
+    if status:
+        _fail(status)
 
 
 def token_logprobs_backward(logits, tokens, lse, entropy, d_logprob=None, d_entropy=None, out=None, stream=None):

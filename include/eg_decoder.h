@@ -198,6 +198,16 @@ typedef struct {
 } eg_score_args;
 
 EG_API eg_status eg_token_logprobs(const eg_score_args* args, void* stream);
+/* Synchronise the current device and report a wait of eg_token_logprobs on it
+ * that ran past its limit since the last report (EG_ERR_DEVICE_TIMEOUT, then
+ * cleared).  A row whose logits never came has NaN everywhere and ids -1, as
+ * one with a NaN among its logits: this call tells them apart. */
+EG_API eg_status eg_token_logprobs_device_status(void);
+/* Testing hook for failure detection, for the calls that follow in this
+ * process: limit the kernel's waits to `wait_limit_ns` (0: the default) and,
+ * with `stall_loader` 1, have no logits loaded, so that the first wait for
+ * some runs out. */
+EG_API eg_status eg_token_logprobs_set_test_stall(uint64_t wait_limit_ns, int32_t stall_loader);
 
 /* The gradient to the logits, from the rows' lse and entropy (as
  * eg_token_logprobs gave them) and the given gradients of logprob and entropy

@@ -140,3 +140,9 @@ def test_tree_null_arguments(L):
     assert L.eg_tree_plan_device_status(None) == eg.EG_ERR_INVALID_ARG
     assert L.eg_tree_plan_set_test_stall(None, 0, 0) == eg.EG_ERR_INVALID_ARG
     assert L.eg_tree_plan_destroy(None) == eg.EG_OK
+
+
+def test_score_hook_refusals(L):
+    for bad in (-1, 2):
+        assert L.eg_token_logprobs_set_test_stall(0, bad) == eg.EG_ERR_INVALID_ARG
+    assert L.eg_token_logprobs_set_test_stall(0, 0) == eg.EG_OK

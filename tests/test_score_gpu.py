@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import epilogue_tcgen05_tmem_gb300 as eg
+from epilogue_tcgen05_tmem_gb300 import decoder
 from tests import _decoder_helpers as H
 
 pytestmark = pytest.mark.gpu
@@ -133,6 +134,46 @@ def test_infinite_and_undefined_logits():
     assert r.top_ids[0].tolist() == [5, 0]
     for row in (1, 2):
         assert all(torch.isnan(t[row]).all() for t in (r.lse, r.logprob, r.entropy, r.top_logprobs)) and (r.top_ids[row] == -1).all()
+
+
+@pytest.mark.parametrize("rows,vocab,top", [(5, 50021, 5), (700, 9000, 3), (2, 200, 0), (1500, 1000, 20)])
+def test_a_wait_that_runs_out_is_reported(rows, vocab, top):
+    """By a cluster for a row, CTAs of either size and short rows; not to be taken for a NaN among the logits."""
+    g = torch.Generator().manual_seed(rows)
+    x = H.rand(g, rows, vocab, dtype="f32", scale=2.5)
+    tokens = torch.randint(0, vocab, (rows,), generator=g)
+    xd, td = x.cuda(), tokens.cuda()
+    decoder.token_logprobs_set_test_stall(5_000_000, 1)
+    try:
+        r = eg.token_logprobs(xd, td, top=top)
+        torch.cuda.synchronize()
+        assert eg.token_logprobs_device_status() == eg.EG_ERR_DEVICE_TIMEOUT
+        assert eg.token_logprobs_device_status() == eg.EG_OK  # reported once
+    finally:
+        decoder.token_logprobs_set_test_stall(0, 0)
+    assert all(torch.isnan(t).all() for t in (r.lse, r.logprob, r.entropy))
+    if top:
+        assert torch.isnan(r.top_logprobs).all() and (r.top_ids == -1).all()
+    x[0, 7] = math.nan
+    _check(eg.token_logprobs(xd, td, top=top), xd.cpu(), tokens, top)
+    assert torch.isnan(eg.token_logprobs(x.cuda(), td, top=top).lse[0]) and eg.token_logprobs_device_status() == eg.EG_OK
+
+
+@pytest.mark.parametrize("hook", [False, True])
+def test_the_limit_of_a_wait(hook, monkeypatch):
+    """From the hook or from EG_WAIT_CAP_MS, as the other kernels have it."""
+    x, tokens = torch.zeros(2, 5000, device="cuda"), torch.zeros(2, dtype=torch.int64, device="cuda")
+    monkeypatch.setenv("EG_WAIT_CAP_MS", "40" if not hook else "4000")
+    decoder.token_logprobs_set_test_stall(40_000_000 if hook else 0, 1)
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    try:
+        begin.record()
+        eg.token_logprobs(x, tokens)
+        end.record()
+        assert eg.token_logprobs_device_status() == eg.EG_ERR_DEVICE_TIMEOUT
+    finally:
+        decoder.token_logprobs_set_test_stall(0, 0)
+    assert 30 < begin.elapsed_time(end) < 1000
 
 
 def test_rows_of_a_wider_tensor():
