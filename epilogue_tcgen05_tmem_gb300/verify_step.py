@@ -37,6 +37,8 @@ def pack_trees(parents, context_lens, block_table, page_size, max_tree, device="
     words = (max_tree + 31) // 32
     start, masks, positions, slots = [0], [], [], []
     for b, tree in enumerate(parents):
+        if len(tree) > max_tree:
+            raise ValueError(f"tree {b} has {len(tree)} drafts, more than max_tree={max_tree}")
         seen, depth = [], []
         for i, parent in enumerate(tree):
             if not -1 <= parent < i:

@@ -25,6 +25,14 @@ def test_a_draft_before_its_parent_is_refused():
         V.pack_trees([[1, -1]], [0], [[0]], page_size=4, max_tree=2, device="cpu")
 
 
+def test_a_tree_of_more_drafts_than_the_plan_takes_is_refused():
+    """Its last rows would not be attended (and their mask bits would be lost)."""
+    V.pack_trees([[-1, 0]], [0], [[0]], page_size=4, max_tree=2, device="cpu")
+    for drafts, most in ((3, 2), (40, 33), (33, 32)):
+        with pytest.raises(ValueError, match="max_tree"):
+            V.pack_trees([[-1], list(range(-1, drafts - 1))], [0, 0], [[0], [1]], page_size=64, max_tree=most, device="cpu")
+
+
 def _step_in_64_bits(layer, hidden, parents, ctx, table, page, cache):
     """Log probabilities from the definitions; the projections' outputs are rounded to 16 bits, as the layer's are."""
     d = torch.float64
