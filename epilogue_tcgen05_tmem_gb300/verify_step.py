@@ -94,6 +94,13 @@ class VerifyLayer:
         of next_tokens (int64 [tokens], -1: none) and the ``top`` alternatives;
         the cache [pages, page_size, kv_heads, head_dim] has the drafts' keys
         and values afterwards."""
+        # the linear plans take pointers: their row count is the plan's
+        like = self.states
+        if hidden.shape != like.shape or hidden.dtype is not like.dtype or hidden.device != like.device or hidden.stride(1) != 1:
+            raise ValueError(f"hidden must be {like.dtype} {tuple(like.shape)} on {like.device} with a contiguous last dimension: got "
+                             f"{hidden.dtype} {tuple(hidden.shape)} on {hidden.device}")
+        if trees.slots.shape[0] != like.shape[0]:
+            raise ValueError(f"the layer's steps have {like.shape[0]} drafts, not {trees.slots.shape[0]}")
         self.qkv.run(hidden, self.w_qkv, self.projected)
         heads = self.projected.view(-1, self.q_heads + 2 * self.kv_heads, self.head_dim)
         q, k, v = heads.split([self.q_heads, self.kv_heads, self.kv_heads], 1)

@@ -100,6 +100,23 @@ def test_step(branching):
 
 
 @pytest.mark.gpu
+def test_states_that_are_not_the_plans_are_refused():
+    """Before any launch: fewer rows, another type or another layout would be read out of range."""
+    layer = V.VerifyLayer(6, 256, 8, 2, 64, 1000, 16, 2, 3, max_positions=64)
+    cache = [torch.zeros(2, 16, 2, 64, device="cuda").bfloat16() for _ in range(2)]
+    parents = [[-1, 0, 1], [-1, 0, 0]]
+    trees = V.pack_trees(parents, [5, 7], [[0], [1]], 16, 3)
+    hidden = torch.zeros(6, 256, device="cuda").bfloat16()
+    for bad in (hidden[:5], hidden[:, :128], hidden.float(), hidden.cpu(), torch.zeros(256, 6, device="cuda").bfloat16().t(), hidden.flatten()):
+        with pytest.raises(ValueError, match="hidden must be"):
+            layer.run(bad, trees, *cache)
+    with pytest.raises(ValueError, match="6 drafts"):
+        layer.run(hidden, V.pack_trees(parents[:1], [5], [[0]], 16, 3), *cache)
+    torch.cuda.synchronize()
+    assert all((c == 0).all() for c in cache)
+
+
+@pytest.mark.gpu
 def test_a_captured_step_replays_with_new_inputs():
     parents, page = [[-1, 0, 1], [-1, 0, 0]], 16
     table = [[0, 1, 2, 3], [4, 5, 6, 7]]
