@@ -345,7 +345,9 @@ class TreeAttention:
         [tokens, words] (None: each token sees the drafted ones up to itself).
         The drafted tokens' own keys and values are in the cache already, after
         the context.  ``scale``: of the scores, 1 / sqrt(head_dim) when None.
-        Returns o like q; lse float32 [tokens, q_heads] is written where given."""
+        Returns o like q; lse float32 [tokens, q_heads] is written where given.
+        Rows that are no sequence's (from q_start[batch] on, a sequence's past
+        max_tree) are left as they were in ``out`` and lse, undefined in a new o."""
         st = _stream_of(q, stream)
         tokens = _heads("q", q)[0]
         shape, dtype, device = (tokens, self.q_heads, self.head_dim), self._dtype, q.device

@@ -121,6 +121,8 @@ EG_API eg_status eg_kv_append(const eg_rope_args* args, const eg_kv_cache* cache
  * lengths are read on the device, so a captured graph replays with new ones;
  * lengths beyond the plan's limits, the table or the packed rows are cut to
  * them, and table entries outside [0, num_pages) read as zero keys and values.
+ * Rows of o and lse that are no sequence's (before q_start[0], from
+ * q_start[batch] on, and a sequence's past max_tree) are not written.
  *
  * A plan owns the partial results of sequences that it splits over the GPU;
  * runs of one plan must not overlap on the GPU.  It belongs to the device that

@@ -332,6 +332,26 @@ def test_lengths_beyond_the_limits_are_cut():
     plan.close()
 
 
+@pytest.mark.parametrize("ctx", [3, 6000])
+def test_rows_of_no_sequence_are_left_as_they_were(ctx):
+    """Before the first sequence, after the last, and past max_tree; the others are as without them."""
+    c = Case("bf16", 8, 2, 64, 16, [ctx, 40, 0], [4, 7, 3], True, seed=16, max_tree=5)
+    d, plan = c.device(), c.plan()
+    d["q_start"][0] = 2                  # its rows 0 and 1 are no sequence's: the other two are tokens 0 and 1
+    d["q_start"][3] = 13                 # row 13 neither
+    out, lse = torch.full_like(d["q"], 7.0), torch.full((14, 8), 7.0, device="cuda")
+    plan.run(**d, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert plan.device_status() == eg.EG_OK
+    left = [0, 1, 9, 10, 13]             # 9 and 10: past max_tree of the second sequence
+    assert (out[left] == 7).all() and (lse[left] == 7).all()
+    own = [2, 3, 4, 5, 6, 7, 8, 11, 12]
+    alone = Case("bf16", 8, 2, 64, 16, [ctx, 40, 0], [2, 5, 2], True, seed=16, max_tree=5)
+    alone.q, alone.kv, alone.table = c.q[own], c.kv, c.table
+    _check(alone, out[own], lse[own])
+    plan.close()
+
+
 def test_a_wait_that_runs_out_is_reported():
     c = Case("bf16", 8, 2, 128, 16, [900, 0], [5, 2], False, seed=13)
     d, plan = c.device(), c.plan()
