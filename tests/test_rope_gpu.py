@@ -221,6 +221,22 @@ def test_append_on_another_stream():
     assert torch.equal(vc.view(64, 2, 128).cpu(), v)
 
 
+def test_append_on_a_stream_that_waits_for_its_inputs():
+    """Every input, the slots too, is made before the stream waits for it, and is kept until the stream is done."""
+    g = torch.Generator().manual_seed(9)
+    k, v, q = H.rand(g, 64, 2, 128), H.rand(g, 64, 2, 128), H.rand(g, 64, 8, 128)
+    slots, tab = torch.randperm(64, generator=g), H.table(64, 128)
+    kc, vc = (torch.zeros(8, 8, 2, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    a = [x.cuda() for x in (k, v, q, tab, slots)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    y = eg.kv_append(a[0], a[1], kc, vc, a[4], q=a[2], cos_sin=a[3], stream=s.cuda_stream)
+    s.synchronize()
+    H.assert_rounded(y, H.norm_rope(q, None, tab, torch.arange(64), False, EPS))
+    H.assert_rounded(kc.view(64, 2, 128)[a[4]], H.norm_rope(k, None, tab, torch.arange(64), False, EPS))
+    assert torch.equal(vc.view(64, 2, 128).cpu()[slots], v)
+
+
 def test_refusals():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16, device="cuda")
     tab = H.table(16, 64).cuda()
