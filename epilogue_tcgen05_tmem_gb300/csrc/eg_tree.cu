@@ -256,7 +256,7 @@ eg_status eg_tree_plan_run(eg_tree_plan* plan, const eg_tree_args* args, const e
   p.q_tiles = plan->q_tiles, p.stages = plan->stages;
   p.box_tokens = row_box(p.group) / p.group, p.tile_rows = plan->tile_rows, p.item_rows = plan->tile_rows * plan->q_tiles;
   p.batch = a.batch, p.tokens = a.tokens;
-  p.q = a.q, p.o = a.o, p.q_token = a.q_token, p.q_head = a.q_head, p.o_token = a.o_token, p.o_head = a.o_head;
+  p.o = a.o, p.o_token = a.o_token, p.o_head = a.o_head;
   p.block_table = a.block_table, p.table_stride = a.table_stride, p.context_lens = a.context_lens, p.q_start = a.q_start;
   p.mask = a.mask, p.mask_stride = a.mask_stride, p.scale_log2 = a.scale * 1.4426950408889634f, p.lse = a.lse;
   p.v = cache->v, p.num_pages = cache->num_pages;

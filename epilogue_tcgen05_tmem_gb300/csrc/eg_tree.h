@@ -33,9 +33,8 @@ struct TreeParams {
   int32_t stages;
   // the run
   int32_t batch, tokens;
-  const void* q;
   void* o;
-  int64_t q_token, q_head, o_token, o_head;
+  int64_t o_token, o_head;
   const int32_t* block_table;
   int64_t table_stride;
   const int32_t* context_lens;
@@ -62,7 +61,6 @@ template <int HD>
 struct TreeSmem {
   static constexpr uint32_t kTileBytes = 128u * HD * 2u;  // 128 rows of queries, keys or values
   static constexpr uint32_t kExtra = 3072u;               // barriers, schedule, exchange of row statistics
-  static uint32_t bytes(int q_tiles, int stages) { return (q_tiles + stages) * kTileBytes + kExtra; }
 };
 
 }  // namespace eg
