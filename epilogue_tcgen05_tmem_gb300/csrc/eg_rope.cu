@@ -2,11 +2,13 @@
 // in the same pass, its gradient, and appending keys and values to a paged
 // cache (include/eg_decoder.h has the formulas).
 //
-// All of it is bound by memory (each value is read once and written once), and
-// behind that by how much of it a warp keeps in flight and by some 330
-// instructions for 512 values.  bf16, 32 + 8 heads of 128: 8191 tokens forward
-// 37 us (4.7 TB/s, much of it in L2), 16384 tokens' gradient 96 us (5.3 TB/s);
-// fp16, 24593 tokens appended 96 us (6.4 TB/s of the 6.8 that a copy reaches).
+// Each value is read once and written once.  In succession, bf16, 32 + 8 heads
+// of 128: 8191 tokens forward 37 us (4.7 TB/s, much of it in L2), 16384 tokens'
+// gradient 96 us (5.3 TB/s); fp16, 24593 tokens appended 96 us (6.4 TB/s of the
+// 6.8 that a copy reaches, its bound).  Forward and gradient are bound by
+// latency before that: with 16 warps an SM and one token's rows in flight in
+// each, neither DRAM (42 and 62 %) nor the issue slots (57 and 64 %; some 330
+// instructions for 512 values) are full.
 //
 // A row (one head of one token) is held in registers by a group of lanes, each
 // with two chunks of CH consecutive elements chosen so that both members of
@@ -195,7 +197,7 @@ __device__ __forceinline__ float group_sum(float v, int lanes) {
 }
 
 // Row groups of one work unit: two of 512 elements (8191 tokens of 32 + 8 heads of
-// 128 in bf16: two 37.5 us, four 52.9 us; a third CTA an SM spills, 60 us).
+// 128 in bf16, cold L2: two 40 us, four 58 us; a third CTA an SM spills, 82 us).
 constexpr int kBatch = 2;
 
 // The factors of one lane for one token: y_a = r (x_a ca + x_b sb) and
@@ -795,8 +797,8 @@ RopeParams base_params(const eg_rope_args& a) {
 // Whether chunks of `ch` elements serve this call: every address a chunk
 // starts at is a multiple of its size, and a lane's pairs are all rotated or
 // none.  8 where they do (float32: 4, the same 16 bytes), else 4, else single
-// elements: the three take 39, 55 and 245 us for 8191 tokens of 32 + 8 heads of
-// 128 in bf16, and 109, 129 and 1102 us for 16384 tokens' gradient.
+// elements: the three take 40, 55 and 244 us for 8191 tokens of 32 + 8 heads of
+// 128 in bf16, and 110, 137 and 1103 us for 16384 tokens' gradient (cold L2).
 bool chunks_fit(const eg_rope_args& a, int ch, std::initializer_list<const void*> ptrs,
                 std::initializer_list<int64_t> strides) {
   if (a.head_dim % ch) return false;

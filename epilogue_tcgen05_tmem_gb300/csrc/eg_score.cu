@@ -2,10 +2,11 @@
 // alternatives, and their gradient (include/eg_decoder.h has the formulas).
 //
 // Both are bound by memory: the logits are read once (and their gradient
-// written once).  4096 x 131072 in bf16 take 175 us (6.1 TB/s of the 6.8 that a
-// copy reaches), with 20 alternatives 216 us, the rest being instructions and
-// the barriers at a row's end; the gradient of 2048 x 100003 in float32 246 us
-// (6.6 TB/s).  Forward: a CTA, or a cluster of CTAs where there are few
+// written once).  Single calls with cold L2: 4096 x 131072 in bf16 take 175 us
+// (6.1 TB/s of the 6.8 that a copy reaches), with 20 alternatives 217 us (207 us
+// in succession), the rest being instructions and the barriers at a row's end;
+// the gradient of 2048 x 100003 in float32 246 us (6.6 TB/s; 240 us in
+// succession).  Forward: a CTA, or a cluster of CTAs where there are few
 // rows, takes one row.  A thread keeps the maximum m of what it saw and, to
 // that reference, s = sum 2^y and t = sum 2^y y with y = (x - m) log2 e; then
 // lse = (m log2 e + log2 s) ln 2 and entropy = (log2 s - t / s) ln 2.  The top
@@ -800,10 +801,10 @@ __global__ void __launch_bounds__(kGradThreads) score_backward_kernel(const Grad
 
 // Many rows of up to this many bytes go to CTAs of 128, of which seven share
 // an SM: a row's end is barriers and one warp's work, and less stands idle
-// meanwhile (20 alternatives, bf16, CTAs of 256 and of 128: 8192 x 1000 145 and
-// 57 us, 8192 x 32000 170 and 135 us; longer rows need the larger batch: 4096 x
-// 131072 224 and 255 us; and rows that all run at once the more threads: 300 x
-// 32000 15.0 and 16.7 us).
+// meanwhile (20 alternatives, bf16, cold L2, CTAs of 256 and of 128: 8192 x 1000
+// 124 and 57 us, 8192 x 32000 179 and 159 us; longer rows need the larger batch:
+// 4096 x 131072 217 and 254 us; and rows that all run at once the more threads:
+// 300 x 32000 17.0 and 20.8 us).
 constexpr int64_t kShortRow = 65536;
 
 int el_bytes(int dtype) { return dtype == EG_EL_F32 ? 4 : 2; }
@@ -838,8 +839,8 @@ eg_status launch_score(const ScoreParams& p, int ranks, int dev, int sms, cudaSt
   const eg_status s = host_allow_smem(reinterpret_cast<const void*>(kernel), static_cast<int>(sizeof(RowShared<N>)), dev, &done);
   if (s != EG_OK) return s;
   // four CTAs of 256 an SM take rows in turn (4096 x 131072 bf16, 20
-  // alternatives: three with a ring of three batches 250 us, four with two
-  // 231 us, two with four 267 us); a cluster takes one
+  // alternatives: three with a ring of three batches 233 us, four with two
+  // 217 us, two with four 253 us); a cluster takes one
   const int64_t clusters = ranks > 1 ? p.rows : std::min<int64_t>(p.rows, kCtas<N> * sms);
   cfg.gridDim = dim3(static_cast<unsigned>(clusters * ranks));
   cfg.blockDim = dim3(N + 32);
@@ -891,8 +892,8 @@ eg_status eg_token_logprobs(const eg_score_args* args, void* stream) {
   p.wait_limit_ns = g_limit_ns.load(std::memory_order_relaxed), p.stall = g_stall.load(std::memory_order_relaxed);
   if (p.wait_limit_ns == 0) p.wait_limit_ns = host_wait_limit_ns();
   // a cluster for a row while that still leaves every CTA an SM of its own
-  // and 16 KB of logits (float32, 50021 of them, five alternatives: 5 rows 13.0
-  // us, 17.1 us by one CTA each; 32 rows 14.9 and 17.6 us)
+  // and 16 KB of logits (float32, 50021 of them, five alternatives: 5 rows 13.9
+  // us, 17.0 us by one CTA each; 32 rows 15.0 and 17.3 us)
   int ranks = 1;
   while (ranks < 8 && a.rows * ranks * 2 <= sms && a.vocab * el_bytes(a.dtype) / (ranks * 2) >= 16384) ranks *= 2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -946,8 +947,8 @@ eg_status eg_token_logprobs_backward(const eg_score_args* args, const eg_score_g
   p.lse = g.lse, p.entropy = g.entropy, p.d_logprob = g.d_logprob, p.d_entropy = g.d_entropy;
   // A CTA for each 32 KB of a row, or 16 KB, which is one batch of each thread,
   // where that many CTAs run at once or nearly so (float32, 64, 32, 16 and 8
-  // KB: 2048 x 100003 259, 246, 252 and 296 us; 4 x 100003 12.9, 10.9, 8.8 and
-  // 8.8 us; one CTA for a row 287 and 32 us)
+  // KB: 2048 x 100003 259, 246, 255 and 300 us; 4 x 100003 13.0, 10.4, 8.8 and
+  // 8.8 us; one CTA for a row 289 and 33 us)
   const int64_t bytes = a.vocab * el_bytes(a.dtype);
   const int64_t parts = std::max<int64_t>(1, bytes / (a.rows * (bytes / 16384) <= 16 * sms ? 16384 : 32768));
   if (a.rows * parts > INT32_MAX) return host_fail(EG_ERR_UNSUPPORTED, "too many logits for one call");

@@ -6,8 +6,10 @@
 // with c = scale log2 e and m a row reference at least the row maximum less 8:
 // O and l are only brought to a new reference when the maximum grew by more
 // than 2^8, which few tiles do.  Weights are rounded to 16 bits for the second
-// product (their error, 2^-9 or 2^-12 of each weight, is the output type's own);
-// l sums them before that rounding, in float32 as S, O and m are.
+// product, whose operands are: at most 2^-8 (bf16) or 2^-11 (fp16) of each
+// weight, the output type's own rounding, which makes the error against 64 bits
+// up to 1.4 times that of weights in float32.  l sums them before that
+// rounding, in float32 as S, O and m are.
 //
 // Work.  Every item has units for its key tiles (see kTreeFixed); all items'
 // units in a row are cut into equal ranges, one for each CTA (one CTA an SM),
@@ -18,27 +20,28 @@
 // One CTA: a producer warp (TMA boxes of pages into a ring of 128-key tiles,
 // K and V alike), one issuing thread (tcgen05.mma), two softmax warpgroups, a
 // warp that fetches queries and one that walks the range for the softmax
-// warpgroups (who spill registers when they do it: 173 against 167 us).  S and
+// warpgroups (who spill registers when they do it: 4 % slower in the wide case below).  S and
 // O of both warpgroups fill tensor memory (4 x 128 columns); P overwrites S as
 // 16-bit values and feeds the second product from there.  With at most 128 rows
 // the warpgroups take turns on the key tiles and are joined at the end of the
 // range; with more rows each has 128 of them and K and V tiles are used twice.
 // So while one warpgroup forms weights the tensor cores work for the other.
 //
-// Measured, and what bounds it.  Two sequences of 98304 and 131072 places, 32
-// query heads over 8 cached, one token each: 152 us, 6.2 TB/s of the 6.8 that a
-// copy reaches; CTAs get uneven shares of the bandwidth, and the last decides.
+// Measured in succession, and what bounds it.  Two sequences of 98304 and
+// 131072 places, 32 query heads over 8 cached, one token each: 151 us, 6.2 TB/s
+// of the 6.8 that a copy reaches; CTAs get uneven shares of the bandwidth, and
+// the last decides.
 // 24 sequences of up to 13 tokens and 9001 places: 97 us, 4.3 TB/s; a CTA has
 // 2.1 segments, and each costs some 4 us beside its tiles.  16 sequences of 32
-// to 64 tokens, 64 query heads, 3800 to 8200 places: 166 us, 816 TFLOP/s of the
-// 1922 of a plain product.  There a tile's two products take 1050 cycles of
+// to 64 tokens, 64 query heads, 3800 to 8200 places: 167 us, 812 TFLOP/s of the
+// 1954 of a plain product.  There a tile's two products take 1050 cycles of
 // the tensor cores and its weights 1480 of their warpgroup (read and maximum
 // 380, exponentials 680, store and signal 320), so a warpgroup's turn is 1700
 // cycles where two full overlaps would be 1050.  Two warpgroups for each row
-// tile, half the keys each, were slower (202 against 172 us: 104 registers a
-// thread spill), and so were a signal after half the weights (171 against 167)
-// and scores in halves of 64 keys, each formed while the other's weights are
-// (208: products of 64 columns take the tensor cores nearly as long as 128).
+// tile, half the keys each, were 17 % slower (104 registers a thread spill), and
+// so were a signal after half the weights (2 %) and scores in halves of 64 keys,
+// each formed while the other's weights are (25 %: products of 64 columns take
+// the tensor cores nearly as long as 128).
 #pragma once
 #include <math_constants.h>
 
@@ -171,11 +174,11 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 }
 // Units.  A key tile of an item costs one, or two where the item has two row
 // tiles: that takes 1.8 times as long (16 sequences of 24 to 48 tokens, 64
-// query heads, 8 cached, 3800 to 8200 places: 181 us when both count the same,
-// 159 us so; 32 to 64 tokens: 182 and 172 us).  An item has kTreeFixed more
+// query heads, 8 cached, 3800 to 8200 places, cold L2: 177 us when both count the
+// same, 155 us so; 32 to 64 tokens: 176 and 163 us).  An item has kTreeFixed more
 // tiles' units for what it costs beside them: queries, the first and the last
-// tile's latency, the result (2, 3, 4 and 6: 189, 182, 180 and 183 us with 32
-// to 64 tokens, 116, 103, 102 and 105 us for 24 sequences of 7 to 13 tokens and
+// tile's latency, the result (2, 3, 4 and 6: 168, 164, 163 and 167 us with 32
+// to 64 tokens, 98, 100, 101 and 105 us for 24 sequences of 7 to 13 tokens and
 // up to 9001 places).  A tile belongs to the CTA that has its first unit.
 constexpr int32_t kTreeFixed = 4;
 __device__ __forceinline__ int64_t tree_units(const TreeParams& p, const TreeSeq& s) {

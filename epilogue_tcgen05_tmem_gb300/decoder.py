@@ -8,7 +8,8 @@ by their strides (the last dimension contiguous), so parts of one projection's
 output are passed as they are.  ``TreeAttention`` is a plan for attention of
 drafted token trees (or single tokens) over that cache.  ``token_logprobs`` and its gradient take logits
 [rows, vocab].  Every call runs on the current stream unless ``stream`` gives
-another.
+another.  None records autograd, as the linear plans do not: gradients come
+from the ``_backward`` calls.
 """
 from __future__ import annotations
 
