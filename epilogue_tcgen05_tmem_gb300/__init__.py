@@ -9,7 +9,8 @@ epilogue_tcgen05_tmem_gb300._build``).
 Names follow the C ABI: ``eg_plan_create``, ``eg_plan_run``,
 ``eg_plan_run_unfused``, ``eg_plan_destroy``, ... and a small ``Plan`` class
 that takes torch tensors and passes their device pointers.  The operators
-between the linear layers (``include/eg_decoder.h``) are in ``decoder`` and
+between the linear layers (``include/eg_decoder.h``) are in ``decoder``, those
+that take in a prompt (``include/eg_prompt.h``) in ``prompt``; both are
 re-exported here.
 """
 from __future__ import annotations
@@ -18,9 +19,10 @@ import ctypes
 import os
 import threading
 
-from . import decoder
+from . import decoder, prompt
 from .decoder import (TokenLogProbs, TreeAttention, kv_append, qk_norm_rope,  # noqa: F401
                       qk_norm_rope_backward, token_logprobs, token_logprobs_backward, token_logprobs_device_status)
+from .prompt import NormResult, add_rms_norm, add_rms_norm_backward  # noqa: F401
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libeg.so")
@@ -133,6 +135,7 @@ def lib() -> ctypes.CDLL:
             L.eg_last_error_detail.argtypes = []
             L.eg_last_error_detail.restype = ctypes.c_char_p
             decoder.declare(L)
+            prompt.declare(L)
             _lib = L
     return _lib
 

@@ -37,7 +37,7 @@ def _sources():
 
 def _headers():
     hs = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h", ".inc"))]
-    hs += [os.path.join(INCLUDE, f) for f in ("eg.h", "eg_decoder.h")]
+    hs += [os.path.join(INCLUDE, f) for f in ("eg.h", "eg_decoder.h", "eg_prompt.h")]
     return hs
 
 

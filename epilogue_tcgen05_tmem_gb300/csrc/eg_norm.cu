@@ -1,0 +1,591 @@
+// eg_norm.cu -- addition to the residual stream with the root-mean-square norm
+// and the codes and scales that a linear plan takes, in one pass, and the
+// gradient (include/eg_prompt.h has the formulas).
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <initializer_list>
+
+#include "../../include/eg_prompt.h"
+#include "eg_el.cuh"
+#include "eg_host.h"
+#include "eg_ptx.cuh"
+
+namespace eg {
+
+namespace {
+
+#define EG_TRY(call)              \
+  do {                            \
+    eg_status s_ = (call);        \
+    if (s_ != EG_OK) return s_;   \
+  } while (0)
+
+struct NormParams {
+  int32_t rows, width, quant;
+  float eps, inv_width;
+  const void *x, *residual, *weight;
+  int64_t x_row, residual_row;
+  void *sum, *out;
+  int64_t sum_row, out_row;
+  uint8_t* codes;
+  int64_t codes_row;
+  float* scales;
+};
+
+struct NormGradParams {
+  int32_t rows, width;
+  float eps, inv_width;
+  const void *d_out, *sum, *weight, *d_sum;
+  int64_t d_out_row, sum_row, d_sum_row;
+  void* dx;
+  int64_t dx_row;
+  float* partial;  // [CTAs][width] sums of d_weight, or NULL
+};
+
+// The scale of values whose largest magnitude has the bits `most` (a NaN's are
+// above all numbers').
+__device__ __forceinline__ float scale_of(uint32_t most, float top) {
+  const float s = __fdiv_rn(__uint_as_float(most), top);
+  return s == 0.0f ? 1.0f : s;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ uint32_t code_of(float h, float scale) {
+  const float t = __fdiv_rn(h, scale);  // IEEE division, as the definition states
+  if constexpr (E4M3) {
+    return __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+  } else {
+    const int r = __float2int_rn(t);
+    return static_cast<uint8_t>(static_cast<int8_t>(r > 127 ? 127 : r < -127 ? -127 : r));
+  }
+}
+
+// Sum, or largest bits, over the threads of a row: a warp, or the whole CTA.
+template <bool WARP>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if constexpr (WARP) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < (blockDim.x >> 5) ? red[lane] : 0.0f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <bool WARP>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if constexpr (WARP) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < (blockDim.x >> 5) ? red[lane] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
+// Rows whose vectors of CH elements are aligned.  A thread keeps V vectors of
+// its row; WARP: a row is a warp's, else a CTA's.
+template <typename T, int CH, int V, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParams p) {
+  // a linear plan launched as this kernel's dependent may stream its weights
+  griddep_launch_dependents();
+  __shared__ float red_sum[32];
+  __shared__ uint32_t red_max[32];
+  const int row = WARP ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
+  if (WARP && row >= p.rows) return;
+  const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
+  const int vectors = p.width / CH;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_row;
+  Chunk<T, CH> c[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * step + tid;
+    if (v < vectors) c[i].load(x + v * CH);
+    else c[i].zero();
+  }
+  if (p.residual) {
+    const T* r = static_cast<const T*>(p.residual) + row * p.residual_row;
+    T* s = static_cast<T*>(p.sum) + row * p.sum_row;
+    Chunk<T, CH> d[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      if (v < vectors) d[i].load(r + v * CH);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      if (v >= vectors) continue;
+      float a[CH], b[CH];
+      c[i].get(a), d[i].get(b);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) a[e] += b[e];
+      c[i].set(a);
+      c[i].store(s + v * CH);
+    }
+  }
+  float square = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float a[CH];
+    c[i].get(a);
+#pragma unroll
+    for (int e = 0; e < CH; ++e) square = fmaf(a[e], a[e], square);
+  }
+  square = row_sum<WARP>(square, red_sum);
+  const float r = rsqrtf(fmaf(square, p.inv_width, p.eps));
+  const T* w = static_cast<const T*>(p.weight);
+  // h of one vector
+  auto normed = [&](int i, int v, float (&h)[CH]) {
+    Chunk<T, CH> wc;
+    wc.load(w + v * CH);
+    float f[CH];
+    wc.get(f), c[i].get(h);
+#pragma unroll
+    for (int e = 0; e < CH; ++e) h[e] = h[e] * r * f[e];
+  };
+  uint32_t most[V], top = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * step + tid;
+    most[i] = 0;
+    if (v >= vectors) continue;
+    float h[CH];
+    normed(i, v, h);
+    if (p.out) {
+      Chunk<T, CH> o;
+      o.set(h);
+      o.store(static_cast<T*>(p.out) + row * p.out_row + v * CH);
+    }
+#pragma unroll
+    for (int e = 0; e < CH; ++e) most[i] = max(most[i], __float_as_uint(h[e]) & 0x7FFFFFFFu);
+    top = max(top, most[i]);
+  }
+  if (p.quant == EG_NORM_PLAIN) return;
+  float scale = 1.0f;
+  if (p.quant != EG_NORM_E4M3_BLOCK) {
+    scale = scale_of(row_max<WARP>(top, red_max), p.quant == EG_NORM_INT8 ? 127.0f : 448.0f);
+    if (tid == 0) p.scales[row] = scale;
+  }
+  uint8_t* codes = p.codes + row * p.codes_row;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * step + tid;
+    if (p.quant == EG_NORM_E4M3_BLOCK) {
+      // a block is 128 / CH neighbouring lanes; the lanes past the row's end hold zeros of no block
+#pragma unroll
+      for (int o = 64 / CH; o > 0; o >>= 1) most[i] = max(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+      scale = scale_of(most[i], 448.0f);
+      if (v < vectors && v % (128 / CH) == 0) p.scales[static_cast<int64_t>(row) * (p.width >> 7) + v / (128 / CH)] = scale;
+    }
+    if (v >= vectors) continue;
+    float h[CH];
+    normed(i, v, h);
+    uint32_t word[2] = {0u, 0u};
+#pragma unroll
+    for (int e = 0; e < CH; ++e)
+      word[e >> 2] |= (p.quant == EG_NORM_INT8 ? code_of<false>(h[e], scale) : code_of<true>(h[e], scale)) << (8 * (e & 3));
+    if constexpr (CH == 8) *reinterpret_cast<uint2*>(codes + v * CH) = make_uint2(word[0], word[1]);
+    else *reinterpret_cast<uint32_t*>(codes + v * CH) = word[0];
+  }
+}
+
+// Any width and alignment: element by element, the row read again from the
+// cache after each reduction.
+constexpr int kAnyThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams p) {
+  griddep_launch_dependents();
+  __shared__ float red_sum[32];
+  __shared__ uint32_t red_max[32];
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const T* x = static_cast<const T*>(p.x) + row * p.x_row;
+  const T* w = static_cast<const T*>(p.weight);
+  float square = 0.0f;
+  if (p.residual) {
+    const T* r = static_cast<const T*>(p.residual) + row * p.residual_row;
+    T* s = static_cast<T*>(p.sum) + row * p.sum_row;
+    for (int k = tid; k < p.width; k += kAnyThreads) {
+      const T v = El<T>::from_float(El<T>::to_float(x[k]) + El<T>::to_float(r[k]));
+      s[k] = v;
+      const float f = El<T>::to_float(v);
+      square = fmaf(f, f, square);
+    }
+    x = s;
+  } else {
+    for (int k = tid; k < p.width; k += kAnyThreads) {
+      const float f = El<T>::to_float(x[k]);
+      square = fmaf(f, f, square);
+    }
+  }
+  square = row_sum<false>(square, red_sum);
+  const float r = rsqrtf(fmaf(square, p.inv_width, p.eps));
+  auto normed = [&](int k) { return El<T>::to_float(x[k]) * r * El<T>::to_float(w[k]); };
+  uint8_t* codes = p.codes + row * p.codes_row;
+  if (p.quant == EG_NORM_E4M3_BLOCK) {
+    // a warp has a block of 128 columns, four a lane
+    for (int b = tid >> 5; b < p.width >> 7; b += kAnyThreads / 32) {
+      float h[4];
+      uint32_t most = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        h[e] = normed(b * 128 + e * 32 + (tid & 31));
+        most = max(most, __float_as_uint(h[e]) & 0x7FFFFFFFu);
+      }
+      const float scale = scale_of(__reduce_max_sync(0xffffffffu, most), 448.0f);
+      if ((tid & 31) == 0) p.scales[static_cast<int64_t>(row) * (p.width >> 7) + b] = scale;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) codes[b * 128 + e * 32 + (tid & 31)] = static_cast<uint8_t>(code_of<true>(h[e], scale));
+    }
+  } else if (p.quant != EG_NORM_PLAIN) {
+    uint32_t most = 0;
+    for (int k = tid; k < p.width; k += kAnyThreads) most = max(most, __float_as_uint(normed(k)) & 0x7FFFFFFFu);
+    const float scale = scale_of(row_max<false>(most, red_max), p.quant == EG_NORM_INT8 ? 127.0f : 448.0f);
+    if (tid == 0) p.scales[row] = scale;
+    for (int k = tid; k < p.width; k += kAnyThreads)
+      codes[k] = static_cast<uint8_t>(p.quant == EG_NORM_INT8 ? code_of<false>(normed(k), scale) : code_of<true>(normed(k), scale));
+  }
+  if (p.out) {
+    if (p.quant == EG_NORM_E4M3_BLOCK) __syncthreads();  // out may be x: every block has been read
+    T* o = static_cast<T*>(p.out) + row * p.out_row;
+    for (int k = tid; k < p.width; k += kAnyThreads) o[k] = El<T>::from_float(normed(k));
+  }
+}
+
+// The gradient.  A CTA walks rows; a thread has the same columns of each, so
+// the weight's gradient adds up in its registers.
+__device__ __forceinline__ float2 cta_sum2(float2 v, float2* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) red[threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < (blockDim.x >> 5) ? red[lane] : make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v.x += __shfl_xor_sync(0xffffffffu, v.x, o), v.y += __shfl_xor_sync(0xffffffffu, v.y, o);
+  return v;
+}
+
+template <typename T, int CH, int V>
+__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormGradParams p) {
+  griddep_launch_dependents();
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x, step = blockDim.x, vectors = p.width / CH;
+  float dw[V][CH];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int e = 0; e < CH; ++e) dw[i][e] = 0.0f;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const T* d_row = static_cast<const T*>(p.d_out) + row * p.d_out_row;
+    const T* z_row = static_cast<const T*>(p.sum) + row * p.sum_row;
+    Chunk<T, CH> d[V], z[V], add[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      if (v < vectors) d[i].load(d_row + v * CH), z[i].load(z_row + v * CH);
+      else d[i].zero(), z[i].zero();
+      add[i].zero();
+      if (p.d_sum && v < vectors) add[i].load(static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH);
+    }
+    float2 both = make_float2(0.0f, 0.0f);  // sums of z^2 and of g z
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      if (v >= vectors) continue;
+      Chunk<T, CH> wc;
+      wc.load(static_cast<const T*>(p.weight) + v * CH);
+      float a[CH], b[CH], w[CH];
+      d[i].get(a), z[i].get(b), wc.get(w);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) both.x = fmaf(b[e], b[e], both.x), both.y = fmaf(a[e] * w[e], b[e], both.y);
+    }
+    both = cta_sum2(both, red[turn]);
+    const float r = rsqrtf(fmaf(both.x, p.inv_width, p.eps));
+    const float back = r * r * (both.y * p.inv_width) * r;
+    T* dx = static_cast<T*>(p.dx) + row * p.dx_row;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      if (v >= vectors) continue;
+      Chunk<T, CH> wc, o;
+      wc.load(static_cast<const T*>(p.weight) + v * CH);
+      float a[CH], b[CH], w[CH], s[CH], y[CH];
+      d[i].get(a), z[i].get(b), wc.get(w), add[i].get(s);
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        y[e] = fmaf(a[e] * w[e], r, fmaf(-back, b[e], s[e]));
+        dw[i][e] = fmaf(a[e], b[e] * r, dw[i][e]);
+      }
+      o.set(y);
+      o.store(dx + v * CH);
+    }
+  }
+  if (!p.partial) return;
+  float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.width;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * step + tid;
+    if (v >= vectors) continue;
+#pragma unroll
+    for (int e = 0; e < CH; e += 4) *reinterpret_cast<float4*>(out + v * CH + e) = make_float4(dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]);
+  }
+}
+
+// The same for any width and alignment; the sums of the weight's gradient stay
+// in the workspace, each column its thread's.
+template <typename T>
+__global__ void __launch_bounds__(kAnyThreads) norm_backward_any_kernel(const NormGradParams p) {
+  griddep_launch_dependents();
+  __shared__ float2 red[2][32];
+  const int tid = threadIdx.x;
+  const T* w = static_cast<const T*>(p.weight);
+  float* mine = p.partial ? p.partial + static_cast<int64_t>(blockIdx.x) * p.width : nullptr;
+  int turn = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    const T* d = static_cast<const T*>(p.d_out) + row * p.d_out_row;
+    const T* z = static_cast<const T*>(p.sum) + row * p.sum_row;
+    const T* add = p.d_sum ? static_cast<const T*>(p.d_sum) + row * p.d_sum_row : nullptr;
+    T* dx = static_cast<T*>(p.dx) + row * p.dx_row;
+    float2 both = make_float2(0.0f, 0.0f);
+    for (int k = tid; k < p.width; k += kAnyThreads) {
+      const float a = El<T>::to_float(d[k]), b = El<T>::to_float(z[k]);
+      both.x = fmaf(b, b, both.x), both.y = fmaf(a * El<T>::to_float(w[k]), b, both.y);
+    }
+    both = cta_sum2(both, red[turn]);
+    const float r = rsqrtf(fmaf(both.x, p.inv_width, p.eps));
+    const float back = r * r * (both.y * p.inv_width) * r;
+    for (int k = tid; k < p.width; k += kAnyThreads) {
+      const float a = El<T>::to_float(d[k]), b = El<T>::to_float(z[k]);
+      const float s = add ? El<T>::to_float(add[k]) : 0.0f;
+      if (mine) mine[k] = fmaf(a, b * r, row == blockIdx.x ? 0.0f : mine[k]);
+      dx[k] = El<T>::from_float(fmaf(a * El<T>::to_float(w[k]), r, fmaf(-back, b, s)));
+    }
+  }
+}
+
+// Sums of the CTAs' parts, in their order: a warp has 32 columns of every 32nd.
+__global__ void __launch_bounds__(1024) norm_weight_kernel(const float* partial, int ctas, int width, float* out) {
+  griddep_wait();
+  __shared__ float shared[32][33];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int column = blockIdx.x * 32 + lane;
+  float v = 0.0f;
+  if (column < width)
+#pragma unroll 8
+    for (int c = warp; c < ctas; c += 32) v += partial[static_cast<int64_t>(c) * width + column];
+  shared[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && column < width) {
+    v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v += shared[i][lane];
+    out[column] = v;
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+int el_bytes(int dtype) { return dtype == EG_EL_F32 ? 4 : 2; }
+
+eg_status check_shape(int64_t rows, int64_t width, int32_t dtype, float eps) {
+  if (rows < 0 || width < 0) return host_fail(EG_ERR_INVALID_ARG, "negative size (rows=%lld width=%lld)", (long long)rows, (long long)width);
+  if (dtype != EG_EL_BF16 && dtype != EG_EL_F16 && dtype != EG_EL_F32) return host_fail(EG_ERR_INVALID_ARG, "unknown dtype %d", dtype);
+  if (rows > (1 << 24)) return host_fail(EG_ERR_UNSUPPORTED, "at most 2^24 rows a call (got %lld)", (long long)rows);
+  if (width < 1 || width > 65536) return host_fail(EG_ERR_UNSUPPORTED, "width must be in 1..65536 (got %lld)", (long long)width);
+  if (!(eps >= 0.0f)) return host_fail(EG_ERR_INVALID_ARG, "eps must not be negative");
+  return EG_OK;
+}
+
+eg_status check_rows(const char* name, const void* ptr, int64_t stride, int64_t rows, int64_t width, int bytes) {
+  if (rows == 0) return EG_OK;
+  if (!ptr) return host_fail(EG_ERR_INVALID_ARG, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(ptr) % bytes) return host_fail(EG_ERR_INVALID_ARG, "%s is not aligned to its elements", name);
+  if (rows > 1 && stride < width) return host_fail(EG_ERR_INVALID_ARG, "the rows of %s are %lld apart, less than their width", name, (long long)stride);
+  return EG_OK;
+}
+
+// Inputs may be broadcast over the rows (stride 0), outputs may not.
+eg_status check_input(const char* name, const void* ptr, int64_t stride, int64_t rows, int64_t width, int bytes) {
+  return check_rows(name, ptr, stride == 0 ? width : stride, rows, width, bytes);
+}
+
+struct Operand {
+  const void* ptr;
+  int64_t stride;
+};
+
+// Whether every row starts on a vector of `ch` elements of `bytes` bytes.
+bool vectors_fit(int64_t width, int64_t rows, int ch, int bytes, std::initializer_list<Operand> operands) {
+  if (width % ch) return false;
+  for (const Operand& o : operands)
+    if (o.ptr && (reinterpret_cast<uintptr_t>(o.ptr) % (ch * bytes) || (rows > 1 && o.stride % ch))) return false;
+  return true;
+}
+
+// Vectors a thread holds of a row of `vectors`, and the threads of a row.
+void split_row(int vectors, int want, int* v, int* threads) {
+  *v = want;
+  while (*v < 8 && (vectors + *v - 1) / *v > 1024) *v *= 2;
+  *threads = std::max(32, ((vectors + *v - 1) / *v + 31) / 32 * 32);
+}
+
+template <typename T, int CH>
+void launch_norm(const NormParams& p, int v, int threads, cudaStream_t st) {
+  if (threads == 32) {
+    // four rows a CTA
+    const unsigned grid = static_cast<unsigned>((p.rows + 3) / 4);
+    if (v == 1) norm_kernel<T, CH, 1, true><<<grid, 128, 0, st>>>(p);
+    else if (v == 2) norm_kernel<T, CH, 2, true><<<grid, 128, 0, st>>>(p);
+    else norm_kernel<T, CH, 4, true><<<grid, 128, 0, st>>>(p);
+    return;
+  }
+  if (v == 1) norm_kernel<T, CH, 1, false><<<p.rows, threads, 0, st>>>(p);
+  else if (v == 2) norm_kernel<T, CH, 2, false><<<p.rows, threads, 0, st>>>(p);
+  else if (v == 4) norm_kernel<T, CH, 4, false><<<p.rows, threads, 0, st>>>(p);
+  else norm_kernel<T, CH, 8, false><<<p.rows, threads, 0, st>>>(p);
+}
+
+template <typename T, int CH>
+void launch_backward(const NormGradParams& p, int v, int threads, int grid, cudaStream_t st) {
+  if (v == 1) norm_backward_kernel<T, CH, 1><<<grid, threads, 0, st>>>(p);
+  else if (v == 2) norm_backward_kernel<T, CH, 2><<<grid, threads, 0, st>>>(p);
+  else norm_backward_kernel<T, CH, 4><<<grid, threads, 0, st>>>(p);
+}
+
+// Most CTAs of the gradient: each leaves a row of sums.
+int backward_ctas(int sms, int64_t rows) { return static_cast<int>(std::min<int64_t>(std::max<int64_t>(rows, 1), sms * 4)); }
+
+eg_status check_grads(const eg_norm_grads* a) {
+  if (!a) return host_fail(EG_ERR_INVALID_ARG, "args is NULL");
+  return check_shape(a->rows, a->width, a->dtype, a->eps);
+}
+
+}  // namespace
+}  // namespace eg
+
+using namespace eg;
+
+extern "C" {
+
+eg_status eg_add_rms_norm(const eg_norm_args* args, void* stream) {
+  if (!args) return host_fail(EG_ERR_INVALID_ARG, "args is NULL");
+  const eg_norm_args& a = *args;
+  EG_TRY(check_shape(a.rows, a.width, a.dtype, a.eps));
+  if (a.quant < EG_NORM_PLAIN || a.quant > EG_NORM_E4M3_BLOCK) return host_fail(EG_ERR_INVALID_ARG, "unknown quant mode %d", a.quant);
+  if (a.quant == EG_NORM_E4M3_BLOCK && a.width % 128)
+    return host_fail(EG_ERR_UNSUPPORTED, "block scales need a width that is a multiple of 128 (got %lld)", (long long)a.width);
+  const int bytes = el_bytes(a.dtype);
+  EG_TRY(check_input("x", a.x, a.x_row, a.rows, a.width, bytes));
+  EG_TRY(check_input("weight", a.weight, 0, a.rows, a.width, bytes));
+  if (a.residual) {
+    EG_TRY(check_input("residual", a.residual, a.residual_row, a.rows, a.width, bytes));
+    EG_TRY(check_rows("sum", a.sum, a.sum_row, a.rows, a.width, bytes));
+  }
+  if (a.out || a.quant == EG_NORM_PLAIN) EG_TRY(check_rows("out", a.out, a.out_row, a.rows, a.width, bytes));
+  if (a.quant != EG_NORM_PLAIN) {
+    EG_TRY(check_rows("codes", a.codes, a.codes_row, a.rows, a.width, 1));
+    EG_TRY(check_rows("scales", a.scales, 1, std::min<int64_t>(a.rows, 1), 1, 4));
+  }
+  if (a.rows == 0) return EG_OK;
+  int dev = 0;
+  EG_TRY(host_check_device(&dev));
+  NormParams p{};
+  p.rows = static_cast<int32_t>(a.rows), p.width = static_cast<int32_t>(a.width), p.quant = a.quant;
+  p.eps = a.eps, p.inv_width = 1.0f / static_cast<float>(a.width);
+  p.x = a.x, p.residual = a.residual, p.weight = a.weight, p.x_row = a.x_row, p.residual_row = a.residual_row;
+  p.sum = a.sum, p.out = a.out, p.sum_row = a.sum_row, p.out_row = a.out_row;
+  p.codes = static_cast<uint8_t*>(a.codes), p.codes_row = a.codes_row, p.scales = a.scales;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const int ch = 16 / bytes;
+  const bool quant = a.quant != EG_NORM_PLAIN;
+  const bool fits = a.width / ch <= 8 * 1024 && vectors_fit(a.width, a.rows, ch, bytes, {{a.x, a.x_row}, {a.residual, a.residual_row}, {a.residual ? a.sum : nullptr, a.sum_row}, {a.out, a.out_row}, {a.weight, 0}}) &&
+                    (!quant || vectors_fit(a.width, a.rows, ch, 1, {{a.codes, a.codes_row}}));
+  if (fits) {
+    int v = 0, threads = 0;
+    split_row(p.width / ch, 4, &v, &threads);
+    if (a.dtype == EG_EL_F32) launch_norm<float, 4>(p, v, threads, st);
+    else if (a.dtype == EG_EL_BF16) launch_norm<__nv_bfloat16, 8>(p, v, threads, st);
+    else launch_norm<__half, 8>(p, v, threads, st);
+  } else if (a.dtype == EG_EL_F32) norm_any_kernel<float><<<p.rows, kAnyThreads, 0, st>>>(p);
+  else if (a.dtype == EG_EL_BF16) norm_any_kernel<__nv_bfloat16><<<p.rows, kAnyThreads, 0, st>>>(p);
+  else norm_any_kernel<__half><<<p.rows, kAnyThreads, 0, st>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching add_rms_norm");
+}
+
+eg_status eg_add_rms_norm_workspace_bytes(const eg_norm_grads* args, size_t* out) {
+  EG_TRY(check_grads(args));
+  if (!out) return host_fail(EG_ERR_INVALID_ARG, "out is NULL");
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
+  *out = static_cast<size_t>(backward_ctas(sms, args->rows)) * args->width * 4;
+  return EG_OK;
+}
+
+eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream) {
+  EG_TRY(check_grads(args));
+  const eg_norm_grads& a = *args;
+  const int bytes = el_bytes(a.dtype);
+  EG_TRY(check_input("d_out", a.d_out, a.d_out_row, a.rows, a.width, bytes));
+  EG_TRY(check_input("sum", a.sum, a.sum_row, a.rows, a.width, bytes));
+  EG_TRY(check_input("weight", a.weight, 0, a.rows, a.width, bytes));
+  if (a.d_sum) EG_TRY(check_input("d_sum", a.d_sum, a.d_sum_row, a.rows, a.width, bytes));
+  EG_TRY(check_rows("dx", a.dx, a.dx_row, a.rows, a.width, bytes));
+  if (reinterpret_cast<uintptr_t>(a.d_weight) % 4) return host_fail(EG_ERR_INVALID_ARG, "d_weight is not aligned to its elements");
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a.rows == 0) {
+    if (!a.d_weight) return EG_OK;
+    const cudaError_t e = cudaMemsetAsync(a.d_weight, 0, static_cast<size_t>(a.width) * 4, st);
+    return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "clearing the weight's gradient");
+  }
+  const int grid = backward_ctas(sms, a.rows);
+  if (a.d_weight) {
+    const size_t need = static_cast<size_t>(grid) * a.width * 4;
+    if (!a.workspace || reinterpret_cast<uintptr_t>(a.workspace) % 16)
+      return host_fail(EG_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
+    if (a.workspace_bytes < need) return host_fail(EG_ERR_INVALID_ARG, "workspace holds %zu bytes of %zu", a.workspace_bytes, need);
+  }
+  NormGradParams p{};
+  p.rows = static_cast<int32_t>(a.rows), p.width = static_cast<int32_t>(a.width);
+  p.eps = a.eps, p.inv_width = 1.0f / static_cast<float>(a.width);
+  p.d_out = a.d_out, p.sum = a.sum, p.weight = a.weight, p.d_sum = a.d_sum;
+  p.d_out_row = a.d_out_row, p.sum_row = a.sum_row, p.d_sum_row = a.d_sum_row;
+  p.dx = a.dx, p.dx_row = a.dx_row;
+  p.partial = a.d_weight ? static_cast<float*>(a.workspace) : nullptr;
+  const int ch = 16 / bytes;
+  const bool fits = a.width / ch <= 4 * 1024 && vectors_fit(a.width, a.rows, ch, bytes, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.weight, 0}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}});
+  if (fits) {
+    int v = 0, threads = 0;
+    split_row(p.width / ch, 1, &v, &threads);
+    if (a.dtype == EG_EL_F32) launch_backward<float, 4>(p, v, threads, grid, st);
+    else if (a.dtype == EG_EL_BF16) launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, st);
+    else launch_backward<__half, 8>(p, v, threads, grid, st);
+  } else if (a.dtype == EG_EL_F32) norm_backward_any_kernel<float><<<grid, kAnyThreads, 0, st>>>(p);
+  else if (a.dtype == EG_EL_BF16) norm_backward_any_kernel<__nv_bfloat16><<<grid, kAnyThreads, 0, st>>>(p);
+  else norm_backward_any_kernel<__half><<<grid, kAnyThreads, 0, st>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return host_cuda_fail(e, "launching the gradient of add_rms_norm");
+  if (!a.d_weight) return EG_OK;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>((a.width + 31) / 32));
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, norm_weight_kernel, static_cast<const float*>(p.partial), grid, static_cast<int>(a.width), a.d_weight);
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching the sum of the weight's gradient");
+}
+
+}  // extern "C"

@@ -121,7 +121,7 @@ class _Bound:
         cls.raw_stream, cls.current = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
         cls.f32, cls.i32, cls.i64 = torch.float32, torch.int32, torch.int64
         cls.code = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-        for name in EXPORTED:
+        for name in EXPORTED + eg.prompt.EXPORTED:
             setattr(cls, name[3:], staticmethod(getattr(lib, name)))
         cls.ready = True
 

@@ -1,0 +1,148 @@
+"""The operators that take in a prompt: thin Python binding of
+``include/eg_prompt.h``.
+
+``add_rms_norm`` adds to the residual stream and norms it, with an output in 16
+bits or as the codes and scales that an 8-bit linear plan takes;
+``add_rms_norm_backward`` is its gradient.  All take torch CUDA tensors by their
+row strides (the last dimension contiguous).  Every call runs on the current
+stream unless ``stream`` gives another.  None records autograd, as the linear
+plans do not.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+from .decoder import _b, _code, _fail, _new, _packer, _side, _stream_of
+
+EXPORTED = ("eg_add_rms_norm", "eg_add_rms_norm_backward", "eg_add_rms_norm_workspace_bytes")
+
+_i64, _i32, _f32, _p, _size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
+
+
+class eg_norm_args(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("width", _i64), ("dtype", _i32), ("quant", _i32), ("eps", _f32), ("x", _p), ("residual", _p),
+                ("weight", _p), ("x_row", _i64), ("residual_row", _i64), ("sum", _p), ("out", _p), ("sum_row", _i64),
+                ("out_row", _i64), ("codes", _p), ("codes_row", _i64), ("scales", _p)]
+
+
+class eg_norm_grads(ctypes.Structure):
+    _fields_ = [("rows", _i64), ("width", _i64), ("dtype", _i32), ("eps", _f32), ("d_out", _p), ("sum", _p), ("weight", _p),
+                ("d_sum", _p), ("d_out_row", _i64), ("sum_row", _i64), ("d_sum_row", _i64), ("dx", _p), ("dx_row", _i64),
+                ("d_weight", _p), ("workspace", _p), ("workspace_bytes", _size)]
+
+
+_pack_norm, _pack_norm_grads = _packer(eg_norm_args), _packer(eg_norm_grads)
+
+
+def declare(L: ctypes.CDLL) -> None:
+    """Argument and result types of the entry points."""
+    for name, args in (("eg_add_rms_norm", [_p, _p]),
+                       ("eg_add_rms_norm_backward", [_p, _p]),
+                       ("eg_add_rms_norm_workspace_bytes", [_p, ctypes.POINTER(_size)])):
+        f = getattr(L, name)
+        f.argtypes, f.restype = args, ctypes.c_int
+
+
+def _matrix(name, t, shape, dtype, device):
+    """(pointer, row stride) of a [rows, width] tensor."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} with a contiguous last dimension: got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr(), t.stride(0)
+
+
+def _result(name, given, shape, dtype, device, stream):
+    """(tensor, pointer, row stride) of an output."""
+    if given is not None:
+        return (given, *_matrix(name, given, shape, dtype, device))
+    new = _new(shape, dtype, device, stream)
+    return new, new.data_ptr(), shape[1]
+
+
+# ------------------------------------------------------- norm of the sum ---
+
+QUANT = {None: 0, "e4m3": 1, "int8": 2, "e4m3_block": 3}
+
+
+class NormResult(NamedTuple):
+    """out [rows, width] (None where not wanted), the new residual stream, and
+    the codes [rows, width] (uint8 E4M3 codes or int8) with their scales."""
+    out: "torch.Tensor | None"      # noqa: F821
+    sum: "torch.Tensor"             # noqa: F821
+    codes: "torch.Tensor | None"    # noqa: F821
+    scales: "torch.Tensor | None"   # noqa: F821  float32 [rows] or [rows, width / 128]
+
+
+def add_rms_norm(x, weight, residual=None, eps=1e-6, quant=None, keep_out=False, out=None, sum_out=None, stream=None) -> NormResult:
+    """x [rows, width] plus ``residual``, and the sum's root-mean-square norm
+    times weight [width].  ``quant``: "e4m3", "int8" (a scale for each row) or
+    "e4m3_block" (one for each 128 columns) gives the norm as codes and scales
+    that a linear plan takes for A and s_a; the norm in x's type comes without
+    ``quant``, and with ``keep_out`` or ``out`` beside the codes.  ``sum_out``
+    may be x or residual; without a residual the sum is x itself."""
+    if not _b.ready:
+        _b.load()
+    st = _stream_of(x, stream)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows, width]")
+    rows, width = shape = x.shape
+    dtype, device = x.dtype, x.device
+    code = _code(x)
+    try:
+        mode = QUANT[quant]
+    except KeyError:
+        raise ValueError(f"quant must be one of {tuple(QUANT)}: got {quant!r}") from None
+    px, x_row = _matrix("x", x, shape, dtype, device)
+    w = _side("weight", weight, dtype, (width,), device)
+    pr = r_row = ps = s_row = po = o_row = pc = c_row = pz = 0
+    total = x
+    if residual is not None:
+        pr, r_row = _matrix("residual", residual, shape, dtype, device)
+        total, ps, s_row = _result("sum_out", sum_out, shape, dtype, device, stream)
+    elif sum_out is not None:
+        raise ValueError("sum_out without a residual: the sum is x")
+    if mode == 0 or keep_out or out is not None:
+        out, po, o_row = _result("out", out, shape, dtype, device, stream)
+    codes = scales = None
+    if mode:
+        codes = _new(shape, _b.torch.int8 if mode == 2 else _b.torch.uint8, device, stream)
+        scales = _new((rows, width // 128) if mode == 3 else rows, _b.f32, device, stream)
+        pc, c_row, pz = codes.data_ptr(), width, scales.data_ptr()
+    status = _b.add_rms_norm(_pack_norm(rows, width, code, mode, eps, px, pr, w, x_row, r_row, ps, po, s_row, o_row, pc, c_row, pz), st)
+    if status:
+        _fail(status)
+    return NormResult(out, total, codes, scales)
+
+
+def add_rms_norm_backward(d_out, sum, weight, eps=1e-6, d_sum=None, dx=None, stream=None):
+    """Gradients of ``add_rms_norm`` from that of its norm and, where given, of
+    its sum: (dx, d_weight).  dx [rows, width] is the gradient of x and of the
+    residual alike (it may be d_out or d_sum), d_weight float32 [width]."""
+    if not _b.ready:
+        _b.load()
+    st = _stream_of(sum, stream)
+    if sum.dim() != 2:
+        raise ValueError("sum must be [rows, width]")
+    rows, width = shape = sum.shape
+    dtype, device = sum.dtype, sum.device
+    code = _code(sum)
+    pz, z_row = _matrix("sum", sum, shape, dtype, device)
+    pd, d_row = _matrix("d_out", d_out, shape, dtype, device)
+    w = _side("weight", weight, dtype, (width,), device)
+    pa = a_row = 0
+    if d_sum is not None:
+        pa, a_row = _matrix("d_sum", d_sum, shape, dtype, device)
+    dx, px, x_row = _result("dx", dx, shape, dtype, device, stream)
+    need = _size(0)
+    status = _b.add_rms_norm_workspace_bytes(_pack_norm_grads(rows, width, code, eps, pd, pz, w, pa, d_row, z_row, a_row, px, x_row, 0, 0, 0),
+                                             ctypes.byref(need))
+    if status:
+        _fail(status)
+    work = _new(need.value // 4, _b.f32, device, stream)
+    dw = _new(width, _b.f32, device, stream)
+    status = _b.add_rms_norm_backward(_pack_norm_grads(rows, width, code, eps, pd, pz, w, pa, d_row, z_row, a_row, px, x_row, dw.data_ptr(),
+                                                       work.data_ptr(), need.value), st)
+    if status:
+        _fail(status)
+    return dx, dw
