@@ -43,107 +43,13 @@
 // each formed while the other's weights are (25 %: products of 64 columns take
 // the tensor cores nearly as long as 128).
 #pragma once
-#include <math_constants.h>
-
-#include "eg_el.cuh"
-#include "eg_ptx.cuh"
+#include "eg_attn.cuh"
 #include "eg_tree.h"
 
 namespace eg {
 
 constexpr int kTreeThreads = 384;
 constexpr uint32_t kTreeKeys = 128;
-
-// 4-D tiled bulk-tensor load global -> shared.
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z,
-                                            int32_t w) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
-      : "memory");
-}
-
-// 3-D tiled bulk-tensor load global -> shared.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y, int32_t z) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
-      : "memory");
-}
-
-// Matrix descriptor of an operand whose M or N index is the contiguous one,
-// in 128-byte swizzled rows: 64 columns of 8 keys are 1024 bytes, the next 8
-// keys follow (stride byte offset), the next 64 columns are `next` bytes on
-// (leading byte offset).
-__device__ __forceinline__ uint64_t sdesc_mn_sw128(uint32_t saddr, uint32_t next) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>(next >> 4) << 16;
-  d |= static_cast<uint64_t>(1024 >> 4) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  d |= static_cast<uint64_t>(2) << 61;
-  return d;
-}
-
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// One lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
-  return p != 0;
-}
-// The products with an accumulator that is added to (the predicate is a
-// constant here: no instruction for it).
-__device__ __forceinline__ void umma_f16_add(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc)
-      : "memory");
-}
-__device__ __forceinline__ void umma_f16_ts_add(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc)
-      : "memory");
-}
-
-// Two float32 lanes in one instruction.
-__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
-  uint64_t v;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
-  return v;
-}
-__device__ __forceinline__ void unpack64(uint64_t v, float* lo, float* hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-__device__ __forceinline__ float tree_ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // One sequence's lengths, cut to what the table, the packed rows and the plan
 // hold.
@@ -294,42 +200,6 @@ struct TreeShared {
   float2 stats[2][128];           // a warpgroup's row references and weights
 };
 static_assert(sizeof(TreeShared) <= TreeSmem<64>::kExtra, "fits the room after the tiles");
-
-// Position of a tile's values in the ring's order: K0, K1, V0, K2, V1, ...
-__device__ __forceinline__ uint32_t tree_pos_v(uint32_t i, uint32_t count) { return i + 1 < count ? 2 * i + 2 : 2 * count - 1; }
-
-// Four columns of one row of an item that CTAs lead..last have parts of, joined
-// in the order of the CTAs.
-template <typename T, int HD>
-__device__ __forceinline__ void tree_join_piece(const TreeParams& p, int lead, int last, int r, int col, int64_t packed, int head) {
-  constexpr float kShift = El<T>::kBf16 ? 0.0f : 7.0f;
-  const int64_t rows = static_cast<int64_t>(128) * p.q_tiles;
-  const float2* ml = reinterpret_cast<const float2*>(p.partial_ml) + r;
-  const float* part = p.partial + static_cast<int64_t>(col) * rows + r * 4;
-  // both to the reference of the largest maximum so far
-  float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float top = -CUDART_INF_F, weight = 0.0f;
-#pragma unroll 4
-  for (int c = lead; c <= last; ++c) {
-    const int64_t slot = (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * rows;
-    const float2 w = __ldcg(ml + slot);
-    const float4 x = __ldcg(reinterpret_cast<const float4*>(part + slot * HD));
-    const float next = fmaxf(top, w.x);
-    const float ref = next == -CUDART_INF_F ? 0.0f : next;
-    const float f_old = tree_ex2(top - ref), f = tree_ex2(w.x - ref);
-    top = next;
-    weight = weight * f_old + w.y * f;
-    y.x *= f_old, y.y *= f_old, y.z *= f_old, y.w *= f_old;
-    if (w.y != 0.0f) y.x = fmaf(x.x, f, y.x), y.y = fmaf(x.y, f, y.y), y.z = fmaf(x.z, f, y.z), y.w = fmaf(x.w, f, y.w);
-  }
-  const float scale = weight == 0.0f ? 0.0f : 1.0f / weight;
-  if (col < p.head_dim) {
-    T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head + col;
-    *reinterpret_cast<uint2*>(o) = make_uint2(El<T>::pack2(y.x * scale, y.y * scale), El<T>::pack2(y.z * scale, y.w * scale));
-  }
-  if (p.lse && col == 0)
-    p.lse[packed * p.q_heads + head] = weight == 0.0f ? -CUDART_INF_F : (top - kShift + __log2f(weight)) * 0.6931471805599453f;
-}
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kTreeThreads, 1)
@@ -724,7 +594,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           } else if (__any_sync(0xffffffffu, high > m + kGrow)) {
             // bring this row's sums to its new maximum
             const float next = fmaxf(m, high);
-            const float f = next == m ? 1.0f : tree_ex2(m - next);
+            const float f = next == m ? 1.0f : attn_ex2(m - next);
             if (!(ok = wait_all(&sh.o_done[s], uses - 1))) break;
             tc_fence_after();
 #pragma unroll 1
@@ -747,7 +617,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           for (int j = 0; j < 64; ++j) {
             float a, b;
             unpack64(fma2(pack64(x[2 * j], x[2 * j + 1]), c2, ref2), &a, &b);
-            a = tree_ex2(a), b = tree_ex2(b);
+            a = attn_ex2(a), b = attn_ex2(b);
             sum2[j & 1] = add2(sum2[j & 1], pack64(__float_as_uint(a), __float_as_uint(b)));
             x[j] = El<T>::pack2(a, b);
           }
@@ -765,7 +635,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           // values that are not finite: a weight of zero times one would
           // reach rows that do not attend to it (`repair` adds it to those
           // that do)
-          const uint32_t at = base + tree_pos_v(i, count), slot = at % stages;
+          const uint32_t at = base + attn_pos_v(i, count), slot = at % stages;
           if (!(ok = wait_all(&sh.full[slot], at / stages))) break;
           const int key = key0 + row_in;
           uint8_t* v_row = ring + slot * kTile + row_in * 128;
@@ -817,7 +687,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
                           *reinterpret_cast<volatile int32_t*>(&sh.poisoned[1]) == segment;
       const float both = fmaxf(own.x, other.x);
       const float ref = both == -CUDART_INF_F ? 0.0f : both;
-      const float f_own = tree_ex2(own.x - ref), f_other = tree_ex2(other.x - ref);
+      const float f_own = attn_ex2(own.x - ref), f_other = attn_ex2(other.x - ref);
       const float weight = own.y * f_own + other.y * f_other;
       const bool whole = walk.whole();
       if (busy) {
@@ -916,7 +786,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int pieces = walk.rows * (HD / 4);
           for (int i = tid; i < pieces; i += 256) {
             const int r_ = i % walk.rows, t_ = (walk.row0 + r_) / p.group;
-            tree_join_piece<T, HD>(p, lead, last, r_, i / walk.rows * 4, walk.seq.start + t_,
+            attn_join_piece<T, HD>(p, lead, last, r_, i / walk.rows * 4, walk.seq.start + t_,
                                    walk.head * p.group + (walk.row0 + r_) - t_ * p.group);
           }
         }
@@ -957,7 +827,7 @@ __global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
   const int r = blockIdx.y * 8 + (lane & 7);
   if (r >= m.rows) return;
   const int t = (m.row0 + r) / p.group;
-  tree_join_piece<T, HD>(p, lead, last, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
+  attn_join_piece<T, HD>(p, lead, last, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
 }
 
 }  // namespace eg

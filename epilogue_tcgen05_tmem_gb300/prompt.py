@@ -3,7 +3,9 @@
 
 ``add_rms_norm`` adds to the residual stream and norms it, with an output in 16
 bits or as the codes and scales that an 8-bit linear plan takes;
-``add_rms_norm_backward`` is its gradient.  All take torch CUDA tensors by their
+``add_rms_norm_backward`` is its gradient.  ``ChunkAttention`` is a plan for
+attention of chunks of new tokens over a paged cache, all of it or a sliding
+window and the first places.  All take torch CUDA tensors by their
 row strides (the last dimension contiguous).  Every call runs on the current
 stream unless ``stream`` gives another.  None records autograd, as the linear
 plans do not.
@@ -13,9 +15,11 @@ from __future__ import annotations
 import ctypes
 from typing import NamedTuple
 
-from .decoder import _b, _code, _fail, _new, _packer, _side, _stream_of
+from .decoder import EL_DTYPES, _b, _cache, _code, _fail, _heads, _new, _out, _packer, _rows, _side, _stream_of
 
-EXPORTED = ("eg_add_rms_norm", "eg_add_rms_norm_backward", "eg_add_rms_norm_workspace_bytes")
+EXPORTED = ("eg_add_rms_norm", "eg_add_rms_norm_backward", "eg_add_rms_norm_workspace_bytes",
+            "eg_chunk_plan_create", "eg_chunk_plan_workspace_bytes", "eg_chunk_plan_run", "eg_chunk_plan_device_status",
+            "eg_chunk_plan_set_test_stall", "eg_chunk_plan_destroy")
 
 _i64, _i32, _f32, _p, _size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -32,14 +36,32 @@ class eg_norm_grads(ctypes.Structure):
                 ("d_weight", _p), ("workspace", _p), ("workspace_bytes", _size)]
 
 
+class eg_chunk_problem(ctypes.Structure):
+    _fields_ = [("q_heads", _i32), ("kv_heads", _i32), ("head_dim", _i32), ("dtype", _i32), ("page_size", _i32), ("max_batch", _i32),
+                ("max_chunk", _i32)]
+
+
+class eg_chunk_args(ctypes.Structure):
+    _fields_ = [("batch", _i32), ("tokens", _i32), ("q", _p), ("o", _p), ("q_token", _i64), ("q_head", _i64), ("o_token", _i64),
+                ("o_head", _i64), ("block_table", _p), ("table_stride", _i64), ("context_lens", _p), ("q_start", _p), ("window", _i32),
+                ("sinks", _i32), ("scale", _f32), ("lse", _p)]
+
+
 _pack_norm, _pack_norm_grads = _packer(eg_norm_args), _packer(eg_norm_grads)
+_pack_chunk = _packer(eg_chunk_args)
 
 
 def declare(L: ctypes.CDLL) -> None:
     """Argument and result types of the entry points."""
     for name, args in (("eg_add_rms_norm", [_p, _p]),
                        ("eg_add_rms_norm_backward", [_p, _p]),
-                       ("eg_add_rms_norm_workspace_bytes", [_p, ctypes.POINTER(_size)])):
+                       ("eg_add_rms_norm_workspace_bytes", [_p, ctypes.POINTER(_size)]),
+                       ("eg_chunk_plan_create", [_p, ctypes.POINTER(_p)]),
+                       ("eg_chunk_plan_workspace_bytes", [_p, ctypes.POINTER(_size)]),
+                       ("eg_chunk_plan_run", [_p, _p, _p, _p]),
+                       ("eg_chunk_plan_device_status", [_p]),
+                       ("eg_chunk_plan_set_test_stall", [_p, ctypes.c_uint64, _i32]),
+                       ("eg_chunk_plan_destroy", [_p])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, ctypes.c_int
 
@@ -146,3 +168,86 @@ def add_rms_norm_backward(d_out, sum, weight, eps=1e-6, d_sum=None, dx=None, str
     if status:
         _fail(status)
     return dx, dw
+
+
+# ------------------------------------------------------ chunk attention ---
+
+class ChunkAttention:
+    """A plan for causal attention of chunks of new tokens over a paged cache:
+    ``max_batch`` sequences of up to ``max_chunk`` new tokens each (1: ordinary
+    decoding).  It owns the workspace for sequences split over the GPU; its runs
+    must not overlap on the GPU."""
+
+    def __init__(self, q_heads, kv_heads, head_dim, dtype="bf16", page_size=16, max_batch=1, max_chunk=1):
+        if not _b.ready:
+            _b.load()
+        self.handle = None
+        self.q_heads, self.kv_heads, self.head_dim, self.page_size = q_heads, kv_heads, head_dim, page_size
+        self.max_batch, self.max_chunk = max_batch, max_chunk
+        h = _p()
+        problem = eg_chunk_problem(q_heads, kv_heads, head_dim, EL_DTYPES[dtype], page_size, max_batch, max_chunk)
+        status = _b.chunk_plan_create(ctypes.addressof(problem), ctypes.byref(h))
+        if status:
+            _fail(status)
+        self.handle = h.value
+        self._dtype = {"bf16": _b.torch.bfloat16, "f16": _b.torch.float16}[dtype]
+        self._place = (page_size, kv_heads, head_dim)
+
+    @property
+    def workspace_bytes(self) -> int:
+        n = _size()
+        status = _b.chunk_plan_workspace_bytes(self.handle, ctypes.byref(n))
+        if status:
+            _fail(status)
+        return n.value
+
+    def run(self, q, k_cache, v_cache, block_table, context_lens, q_start, window=0, sinks=0, scale=None, out=None, lse=None, stream=None):
+        """Packed queries q [tokens, q_heads, head_dim] of the sequences' new
+        tokens (rows q_start[b] .. q_start[b + 1]) over the cache [pages,
+        page_size, kv_heads, head_dim]; block_table int32 [batch, pages of a
+        sequence], context_lens int32 [batch] (places before the chunk), q_start
+        int32 [batch + 1].  The new tokens' own keys and values are in the cache
+        already, after the context.  A token sees the places up to its own: with
+        ``window`` only the last ``window`` of them and the first ``sinks``.
+        ``scale``: of the scores, 1 / sqrt(head_dim) when None.  Returns o like
+        q; lse float32 [tokens, q_heads] is written where given.  Rows that are
+        no sequence's (from q_start[batch] on, a sequence's past max_chunk) are
+        left as they were in ``out`` and lse, undefined in a new o."""
+        st = _stream_of(q, stream)
+        tokens = _heads("q", q)[0]
+        shape, dtype, device = (tokens, self.q_heads, self.head_dim), self._dtype, q.device
+        qp, qt, qh = _rows("q", q, shape, dtype, device)
+        if k_cache.dim() != 4:
+            raise ValueError("the cache must be [pages, page_size, kv_heads, head_dim]")
+        cache = _cache(k_cache, v_cache, self._place, dtype, device)
+        batch, width = block_table.shape
+        table = _side("block_table", block_table, _b.i32, (batch, width), device)
+        out, op, ot, oh = _out("out", out, q, stream)
+        args = _pack_chunk(batch, tokens, qp, op, qt, qh, ot, oh, table, width,
+                           _side("context_lens", context_lens, _b.i32, (batch,), device),
+                           _side("q_start", q_start, _b.i32, (batch + 1,), device), window, sinks,
+                           self.head_dim ** -0.5 if scale is None else scale,
+                           0 if lse is None else _side("lse", lse, _b.f32, (tokens, self.q_heads), device))
+        status = _b.chunk_plan_run(self.handle, args, cache, st)
+        if status:
+            _fail(status)
+        return out
+
+    def device_status(self) -> int:
+        return _b.chunk_plan_device_status(self.handle)
+
+    def set_test_stall(self, wait_limit_ns: int, stall_producer: int):
+        status = _b.chunk_plan_set_test_stall(self.handle, wait_limit_ns, int(stall_producer))
+        if status:
+            _fail(status)
+
+    def close(self):
+        if getattr(self, "handle", None):
+            _b.chunk_plan_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass

@@ -1,6 +1,7 @@
 /*
  * eg_prompt.h -- C ABI of the operators that take in a prompt (sm_103a): the
- * residual stream's addition and norm with an output in 8 bits.  Conventions as in eg_decoder.h:
+ * residual stream's addition and norm with an output in 8 bits, and attention
+ * of chunks of new tokens over a paged cache.  Conventions as in eg_decoder.h:
  * every call returns an eg_status, argument errors are found before any device
  * work is queued, eg_last_error_detail() describes the last failure of this
  * thread, the caller owns every tensor and keeps it alive until the stream has
@@ -82,6 +83,66 @@ typedef struct {
 
 EG_API eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream);
 EG_API eg_status eg_add_rms_norm_workspace_bytes(const eg_norm_grads* args, size_t* out);
+
+/* ---------------------- attention of chunks of new tokens over the cache --
+ *
+ * Sequence b has context_lens[b] cached tokens and n_b = q_start[b + 1] -
+ * q_start[b] new ones (0 or more; 1 for ordinary decoding), whose keys and
+ * values follow the context in the same cache: place j of the sequence is in
+ * page block_table[b][j / page_size], place j % page_size.  New token t
+ * (packed row q_start[b] + t of q) stands at place i = context_lens[b] + t and
+ * attends to the places j <= i with i - j < window or j < sinks; to all j <= i
+ * where window is 0.  For query head h, with the cached head
+ * h / (q_heads / kv_heads):
+ *
+ *   o = sum_j softmax_j(scale q . k_j) v_j,  lse = log sum_j exp(scale q . k_j)
+ *
+ * Places that a token does not attend to, slots of the cache past a sequence's
+ * end and table entries past its pages have no part, whatever they hold.
+ * Sequence lengths are read on the device, so a captured graph replays with
+ * new ones; lengths beyond the plan's limits, the table or the packed rows are
+ * cut to them, and table entries outside [0, num_pages) read as zero keys and
+ * values.  Rows of o and lse that are no sequence's (before q_start[0], from
+ * q_start[batch] on, and a sequence's past max_chunk) are not written.
+ *
+ * A plan owns the partial results of sequences that it splits over the GPU;
+ * runs of one plan must not overlap on the GPU.  It belongs to the device that
+ * is current when it is made, as an eg_tree_plan does. */
+typedef struct {
+  int32_t q_heads, kv_heads;    /* as in eg_tree_problem */
+  int32_t head_dim;             /* a multiple of 8, 8..128 */
+  int32_t dtype;                /* EG_EL_BF16 or EG_EL_F16 (q, cache and o) */
+  int32_t page_size;            /* a multiple of 8 */
+  int32_t max_batch;            /* sequences of a run, 1..65536 */
+  int32_t max_chunk;            /* new tokens of a sequence, 1..2^20 */
+} eg_chunk_problem;
+
+typedef struct {
+  int32_t batch;
+  int32_t tokens;               /* rows of q and o */
+  const void* q;                /* [tokens][q_heads][head_dim] by the strides, 16-byte aligned rows */
+  void* o;
+  int64_t q_token, q_head, o_token, o_head;
+  const int32_t* block_table;   /* [batch][table_stride], table_stride entries of each may be read */
+  int64_t table_stride;
+  const int32_t* context_lens;  /* [batch] */
+  const int32_t* q_start;       /* [batch + 1], rising */
+  int32_t window, sinks;        /* 0 or more; sinks only with a window */
+  float scale;                  /* positive */
+  float* lse;                   /* [tokens][q_heads], or NULL */
+} eg_chunk_args;
+
+typedef struct eg_chunk_plan eg_chunk_plan;
+
+EG_API eg_status eg_chunk_plan_create(const eg_chunk_problem* problem, eg_chunk_plan** out);
+EG_API eg_status eg_chunk_plan_workspace_bytes(const eg_chunk_plan* plan, size_t* out);
+EG_API eg_status eg_chunk_plan_run(eg_chunk_plan* plan, const eg_chunk_args* args,
+                                   const eg_kv_cache* cache, void* stream);
+/* As eg_tree_plan_device_status and eg_tree_plan_set_test_stall. */
+EG_API eg_status eg_chunk_plan_device_status(eg_chunk_plan* plan);
+EG_API eg_status eg_chunk_plan_set_test_stall(eg_chunk_plan* plan, uint64_t wait_limit_ns,
+                                              int32_t stall_producer);
+EG_API eg_status eg_chunk_plan_destroy(eg_chunk_plan* plan);
 
 #ifdef __cplusplus
 }

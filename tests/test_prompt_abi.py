@@ -90,3 +90,28 @@ def test_null_arguments(L):
 
 def test_no_rows_is_no_work(L):
     assert L.eg_add_rms_norm(ctypes.addressof(_norm(rows=0, x=None, sum=None, out=None, codes=None, scales=None)), None) == eg.EG_OK
+
+
+def _chunk_problem(**kw):
+    return _set(prompt.eg_chunk_problem(q_heads=4, kv_heads=2, head_dim=64, dtype=0, page_size=16, max_batch=1, max_chunk=1), kw)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q_heads=0), BAD), (dict(q_heads=5), BAD), (dict(head_dim=0), NOT), (dict(head_dim=132), NOT), (dict(dtype=2), NOT), (dict(dtype=-1), BAD),
+    (dict(page_size=20), NOT), (dict(max_batch=0), NOT), (dict(max_batch=65537), NOT), (dict(max_chunk=0), NOT), (dict(max_chunk=2 ** 20 + 1), NOT),
+    (dict(q_heads=2048), NOT), (dict(q_heads=34), NOT)])
+def test_chunk_refusals_before_device(L, kw, status):
+    h = ctypes.c_void_p()
+    assert L.eg_chunk_plan_create(ctypes.addressof(_chunk_problem(**kw)), ctypes.byref(h)) == status and not h.value
+    assert eg.last_error_detail()
+
+
+def test_chunk_null_arguments(L):
+    h = ctypes.c_void_p()
+    assert L.eg_chunk_plan_create(None, ctypes.byref(h)) == BAD
+    assert L.eg_chunk_plan_create(None, None) == BAD
+    assert L.eg_chunk_plan_run(None, None, None, None) == BAD
+    assert L.eg_chunk_plan_workspace_bytes(None, None) == BAD
+    assert L.eg_chunk_plan_device_status(None) == BAD
+    assert L.eg_chunk_plan_set_test_stall(None, 0, 0) == BAD
+    assert L.eg_chunk_plan_destroy(None) == eg.EG_OK
