@@ -22,7 +22,8 @@ import threading
 from . import decoder, prompt
 from .decoder import (TokenLogProbs, TreeAttention, kv_append, qk_norm_rope,  # noqa: F401
                       qk_norm_rope_backward, token_logprobs, token_logprobs_backward, token_logprobs_device_status)
-from .prompt import (ChunkAttention, NormResult, add_rms_norm, add_rms_norm_backward)  # noqa: F401
+from .prompt import (ChunkAttention, NormResult, add_rms_norm, add_rms_norm_backward, lora,  # noqa: F401
+                     lora_device_status)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libeg.so")

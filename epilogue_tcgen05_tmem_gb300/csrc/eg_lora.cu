@@ -1,0 +1,687 @@
+// eg_lora.cu -- low-rank adapters of many requests beside a shared projection
+// (include/eg_prompt.h has the formula).
+//
+// Two kernels over tiles of up to 128 rows of one sequence, so of one adapter.
+// The first forms h = x A^T: a cluster shares a tile's columns of x, each CTA
+// streams its part of x and A through a ring of TMA boxes into tcgen05.mma, and
+// the parts are added through distributed shared memory in the cluster's order.
+// The second, launched as the first's dependent, streams B in tiles of 128
+// outputs, forms h B^T and adds base in its epilogue.  h goes between them as
+// two 16-bit parts: h / 2^e = hi + lo with 2^e the row's size, so that the
+// second product's operands lose nothing that shows next to the output's own
+// rounding (fp16 needs the common size for its range); hi and lo are side by
+// side along its inner dimension, against the same tile of B.
+//
+// Tiles of at most 16 rows (single tokens) take the second product the other
+// way round: 128 outputs are the rows of tensor memory and the tokens its
+// columns, so that one product covers 128 outputs with no idle rows and a warp
+// writes neighbouring outputs of a token.
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <math_constants.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/eg_prompt.h"
+#include "eg_el.cuh"
+#include "eg_host.h"
+#include "eg_ptx.cuh"
+
+namespace eg {
+
+namespace {
+
+#define EG_TRY(call)              \
+  do {                            \
+    eg_status s_ = (call);        \
+    if (s_ != EG_OK) return s_;   \
+  } while (0)
+
+constexpr int kTileRows = 128;  // rows of a tile, and outputs of one of the second product
+constexpr int kBox = 16;        // rows of one TMA box of x and h; tiles of at most as many are small
+constexpr int kInnerThreads = 192, kOuterThreads = 320;
+constexpr uint32_t kRowTile = 128u * 128u;  // bytes of 128 rows of 64 elements
+
+struct LoraParams {
+  int32_t rows, sequences, adapters, outputs, rank;
+  int32_t rank16;       // rank rounded up to the products' step of 16
+  int32_t chunks;       // columns of x, in 64s
+  int32_t splits;       // CTAs of a cluster that share them
+  int32_t subs;         // tiles of 128 outputs
+  int32_t subs_each;    // those of one CTA of the second kernel
+  int32_t stages;       // of the first kernel's ring
+  int32_t stages_out;   // of the second's
+  const int32_t *seq_start, *adapter;
+  const float* scales;
+  const void* base;
+  int64_t base_row;
+  void* out;
+  int64_t out_row;
+  void* h;              // [rows][2 rank16]
+  float* row_scale;     // [rows]: 2^e times the adapter's scale
+  uint64_t wait_limit_ns;
+  int32_t stall;        // test hook: the loading warps load nothing
+};
+
+// Set when a wait of either kernel ran past its limit (one for each device).
+__device__ int32_t g_lora_status;
+
+struct LoraTile {
+  int32_t row0, rows, adapter;  // rows 0: there is no such tile
+};
+
+struct LoraShared {
+  uint64_t full[8], empty[8];
+  uint64_t acc_full[2], acc_empty[2], h_full, done, drained;
+  uint32_t tmem;
+  int32_t abort;
+  LoraTile tile;
+  int32_t warps[2][12];
+};
+
+// Bounded wait: false once any wait of the CTA has run past its limit.
+__device__ __forceinline__ bool lora_wait(LoraShared& sh, uint64_t* bar, uint32_t phase, uint64_t limit_ns) {
+  if (mbar_try_wait(bar, phase & 1)) return true;
+  volatile int32_t* abort = &sh.abort;
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, phase & 1)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (global_timer_ns() - t0 > limit_ns) {
+        *abort = 1;
+        *reinterpret_cast<volatile int32_t*>(&g_lora_status) = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// The tile of number `index`, found by the whole CTA.
+template <int THREADS>
+__device__ __forceinline__ LoraTile find_tile(const LoraParams& p, LoraShared& sh, int index) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh.tile.rows = 0;
+  int before = 0;
+  for (int b0 = 0, turn = 0; b0 < p.sequences && before <= index; b0 += THREADS, turn ^= 1) {
+    const int b = b0 + tid;
+    int start = 0, n = 0;
+    if (b < p.sequences) {
+      start = min(max(__ldg(p.seq_start + b), 0), p.rows);
+      n = min(max(__ldg(p.seq_start + b + 1), start), p.rows) - start;
+    }
+    const int tiles = (n + kTileRows - 1) / kTileRows;
+    int upto = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += x;
+    }
+    if (lane == 31) sh.warps[turn][warp] = upto;
+    __syncthreads();
+    int base = before;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      if (w < warp) base += sh.warps[turn][w];
+      before += sh.warps[turn][w];
+    }
+    const int first = base + upto - tiles;
+    if (first <= index && index < first + tiles) {
+      const int row0 = (index - first) * kTileRows;
+      int a = __ldg(p.adapter + b);
+      if (a < 0 || a >= p.adapters) a = -1;
+      sh.tile = LoraTile{start + row0, min(n - row0, kTileRows), a};
+    }
+  }
+  __syncthreads();
+  return sh.tile;
+}
+
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
+// Products in flight have to end before tensor memory is freed.
+__device__ __forceinline__ void drain(LoraShared& sh, uint64_t limit_ns) {
+  if (elected()) umma_commit(&sh.drained);
+  __syncwarp();
+  if (!mbar_wait(&sh.drained, 0, limit_ns)) mbar_wait(&sh.drained, 0, 8 * limit_ns);
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// ------------------------------------------------------ h = x A^T ---------
+
+template <typename T>
+__global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_x,
+                                                                   const __grid_constant__ CUtensorMap map_a) {
+  constexpr uint32_t kFmt = El<T>::kBf16 ? 1u : 0u;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t a_bytes = p.rank16 * 128u, stage_bytes = kRowTile + (a_bytes + 1023u) / 1024u * 1024u;
+  LoraShared& sh = *reinterpret_cast<LoraShared*>(smem + p.stages * stage_bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int index = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
+  if (tid == 0) {
+    for (int i = 0; i < p.stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    mbar_init(&sh.done, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  const LoraTile tile = find_tile<kInnerThreads>(p, sh, index);
+  // the whole cluster has the same tile
+  if (tile.rows == 0 || tile.adapter < 0) return;
+  if (warp == 1) tmem_alloc(&sh.tmem, 128);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // not before every CTA has its tensor memory: the second kernel's CTAs hold
+  // theirs while they wait for this kernel
+  griddep_launch_dependents();
+  const uint32_t tmem = sh.tmem;
+  const int from = p.chunks * part / p.splits, to = p.chunks * (part + 1) / p.splits;
+  const int count = to - from;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- loads ----
+    const int boxes = (tile.rows + kBox - 1) / kBox;
+    const uint32_t bytes = boxes * kBox * 128u + p.rank * 128u;
+    int i = 0;
+    for (; i < count; ++i) {
+      const int slot = i % p.stages;
+      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], i / p.stages + 1, p.wait_limit_ns))) break;
+      if (p.stall) continue;
+      uint8_t* stage = smem + slot * stage_bytes;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+      __syncwarp();
+      if (lane < boxes) tma_load_2d(stage + lane * kBox * 128, &map_x, &sh.full[slot], (from + i) * 64, tile.row0 + lane * kBox);
+      if (lane == 31) tma_load_2d(stage + kRowTile, &map_a, &sh.full[slot], (from + i) * 64, tile.adapter * p.rank);
+    }
+    // no copy in flight is left behind
+    if (!p.stall)
+      for (int j = max(i - p.stages, 0); j < i; ++j)
+        if (!mbar_wait(&sh.full[j % p.stages], (j / p.stages) & 1, p.wait_limit_ns)) break;
+  } else if (warp == 1) {
+    // ---------------------------------------------------- products ----
+    const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, p.rank16);
+    for (int i = 0; i < count; ++i) {
+      const int slot = i % p.stages;
+      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], i / p.stages, p.wait_limit_ns))) break;
+      tc_fence_after();
+      const uint64_t x = sdesc_k_sw128(smem_u32(smem + slot * stage_bytes)), a = sdesc_k_sw128(smem_u32(smem + slot * stage_bytes + kRowTile));
+      if (elected()) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) umma_f16(tmem, x + k * 2, a + k * 2, idesc, i > 0 || k > 0);
+        umma_commit(&sh.empty[slot]);
+        if (i + 1 == count) umma_commit(&sh.done);
+      }
+      __syncwarp();
+    }
+    drain(sh, p.wait_limit_ns);
+  }
+  __syncwarp();
+  // ------------------------------------------------------- the sum ----
+  const int pitch = p.rank16 + 4;  // floats: rows start on different banks
+  float* mine = reinterpret_cast<float*>(smem);
+  bool ok = true;
+  if (warp >= 2) {
+    // the ring has been read when the products are done: it takes this CTA's part of h
+    ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.done, 0, p.wait_limit_ns));
+    tc_fence_after();
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    if (ok && quarter * 32 < tile.rows) {
+      for (int c = 0; c < p.rank16; c += 16) {
+        uint32_t v[16];
+        tmem_ld16(tmem + (static_cast<uint32_t>(quarter) << 21) + c, v);
+        tmem_ld_wait();
+        reg_fence<16>(v);
+        if (row < tile.rows)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4)
+            *reinterpret_cast<float4*>(mine + row * pitch + c + j) =
+                make_float4(__uint_as_float(v[j]), __uint_as_float(v[j + 1]), __uint_as_float(v[j + 2]), __uint_as_float(v[j + 3]));
+      }
+    }
+  }
+  __syncwarp();
+  if (p.splits > 1) cluster_sync_all();
+  else __syncthreads();
+  if (warp >= 2 && ok) {
+    // rows in turn over the cluster's CTAs and their warps; a lane has four columns
+    const float scale = p.scales ? __ldg(p.scales + tile.adapter) : 1.0f;
+    const int col = lane * 4;
+    for (int row = part * 4 + warp - 2; row < tile.rows; row += p.splits * 4) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (col < p.rank) {
+        const uint32_t at = smem_u32(mine + row * pitch + col);
+        for (int c = 0; c < p.splits; ++c) {
+          const float4 w = p.splits > 1 ? ld_cluster4(cluster_map(at, c)) : *reinterpret_cast<const float4*>(mine + row * pitch + col);
+          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        }
+      }
+      // bits of the largest magnitude: a NaN's are above infinity's
+      uint32_t most = max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
+                          max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
+      most = __reduce_max_sync(0xffffffffu, most);
+      // 2^e of the largest, at most 2^126 either way so that its inverse is normal too
+      const int e = most >= 0x7F800000u || most == 0 ? 127 : min(max(static_cast<int>(most >> 23), 1), 253);
+      const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23), up = __uint_as_float(static_cast<uint32_t>(e) << 23);
+      if (lane == 0) p.row_scale[tile.row0 + row] = up * scale;
+      if (col < p.rank16) {
+        const float y[4] = {v.x * down, v.y * down, v.z * down, v.w * down};
+        float hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = El<T>::to_float(El<T>::from_float(y[j]));
+          lo[j] = fabsf(hi[j]) < CUDART_INF_F ? y[j] - hi[j] : 0.0f;
+        }
+        T* out = static_cast<T*>(p.h) + static_cast<int64_t>(tile.row0 + row) * (2 * p.rank16) + col;
+        *reinterpret_cast<uint2*>(out) = make_uint2(El<T>::pack2(hi[0], hi[1]), El<T>::pack2(hi[2], hi[3]));
+        *reinterpret_cast<uint2*>(out + p.rank16) = make_uint2(El<T>::pack2(lo[0], lo[1]), El<T>::pack2(lo[2], lo[3]));
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  if (p.splits > 1) cluster_sync_all();  // no CTA's shared memory goes while it is read
+  else __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 128);
+  }
+}
+
+// ---------------------------------------------- out = base + h B^T --------
+
+// 16 outputs of one row: out = base + acc * scale (base may be NULL).
+template <typename T>
+__device__ __forceinline__ void add_store16(T* out, const uint4 (&base)[2], const uint32_t* acc, float scale) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    Chunk<T, 8> b, o;
+    b.w[0] = base[j].x, b.w[1] = base[j].y, b.w[2] = base[j].z, b.w[3] = base[j].w;
+    float f[8];
+    b.get(f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(acc[j * 8 + e]), scale, f[e]);
+    o.set(f);
+    o.store(out + j * 8);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_h,
+                                                                      const __grid_constant__ CUtensorMap map_b) {
+  constexpr uint32_t kFmt = El<T>::kBf16 ? 1u : 0u;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int parts = (p.rank16 + 63) / 64;            // 64-column parts of a tile of B
+  const int h_parts = (2 * p.rank16 + 63) / 64;      // and of h
+  const uint32_t b_bytes = parts * kRowTile;
+  uint8_t* h_smem = smem;
+  uint8_t* ring = smem + h_parts * kRowTile;
+  LoraShared& sh = *reinterpret_cast<LoraShared*>(ring + p.stages_out * b_bytes);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
+  const int index = blockIdx.x / groups, sub0 = blockIdx.x % groups * p.subs_each;
+  const int count = min(p.subs - sub0, p.subs_each);
+  if (tid == 0) {
+    for (int i = 0; i < p.stages_out; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
+    mbar_init(&sh.h_full, 1);
+    mbar_init(&sh.drained, 1);
+    fence_mbar_init();
+    sh.abort = 0;
+  }
+  const LoraTile tile = find_tile<kOuterThreads>(p, sh, index);
+  if (tile.rows == 0) {
+    griddep_wait();  // this kernel does not end before the first
+    return;
+  }
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  if (tile.adapter < 0) {
+    // nothing is added
+    griddep_wait();
+    if (base == out) return;
+    const int width = min(p.outputs - sub0 * kTileRows, count * kTileRows) / 8;
+    for (int i = tid; i < tile.rows * width; i += kOuterThreads) {
+      const int64_t row = tile.row0 + i / width;
+      const int col = sub0 * kTileRows + i % width * 8;
+      const uint4 v = base ? *reinterpret_cast<const uint4*>(base + row * p.base_row + col) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(out + row * p.out_row + col) = v;
+    }
+    return;
+  }
+  if (warp == 1) tmem_alloc(&sh.tmem, 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const bool small = tile.rows <= kBox;
+
+  if (warp == 0) {
+    // ------------------------------------------------------- loads ----
+    // B does not wait for the first kernel, whose h follows the ring's first filling
+    const int ahead = min(count, p.stages_out);
+    const int boxes = (tile.rows + kBox - 1) / kBox;
+    int i = 0;
+    bool ok = true, h_sent = false;
+    for (; ok && i <= count; ++i) {
+      if (i == ahead) {
+        griddep_wait();
+        if (!p.stall) {
+          if (lane == 0) mbar_arrive_expect_tx(&sh.h_full, boxes * kBox * 128u * h_parts);
+          __syncwarp();
+          for (int j = lane; j < boxes * h_parts; j += 32) {
+            const int part = j / boxes, box = j % boxes;
+            tma_load_2d(h_smem + part * kRowTile + box * kBox * 128, &map_h, &sh.h_full, part * 64, tile.row0 + box * kBox);
+          }
+          h_sent = true;
+        }
+      }
+      if (i == count) break;
+      const int slot = i % p.stages_out;
+      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], i / p.stages_out + 1, p.wait_limit_ns));
+      if (!ok || p.stall) continue;
+      const int n0 = (sub0 + i) * kTileRows;
+      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], b_bytes);
+      __syncwarp();
+      // rows past the adapter's last output are the next one's, or zeros: their products are not stored
+      if (lane < parts) tma_load_2d(ring + slot * b_bytes + lane * kRowTile, &map_b, &sh.full[slot], lane * 64, tile.adapter * p.outputs + n0);
+    }
+    if (!p.stall) {
+      const int sent = min(i, count);
+      for (int j = max(sent - p.stages_out, 0); j < sent; ++j)
+        if (!mbar_wait(&sh.full[j % p.stages_out], (j / p.stages_out) & 1, p.wait_limit_ns)) break;
+      if (h_sent) mbar_wait(&sh.h_full, 0, p.wait_limit_ns);
+    }
+  } else if (warp == 1) {
+    // ---------------------------------------------------- products ----
+    const uint32_t idesc = small ? idesc_f32acc(kFmt, kFmt, 128, kBox) : idesc_f32acc(kFmt, kFmt, 128, kTileRows);
+    const int steps = p.rank16 / 16;
+    const uint64_t h0 = sdesc_k_sw128(smem_u32(h_smem));
+    bool ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_full, 0, p.wait_limit_ns));
+    for (int i = 0; ok && i < count; ++i) {
+      const int slot = i % p.stages_out, buf = i & 1;
+      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], i / p.stages_out, p.wait_limit_ns)) &&
+           __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_empty[buf], i / 2 + 1, p.wait_limit_ns));
+      if (!ok) break;
+      tc_fence_after();
+      const uint64_t b0 = sdesc_k_sw128(smem_u32(ring + slot * b_bytes));
+      if (elected()) {
+        for (int k = 0; k < 2 * steps; ++k) {
+          // step k of h against step k of B, again from its first for the low parts
+          const int kb = k < steps ? k : k - steps;
+          const uint64_t hk = h0 + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = b0 + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
+          if (small) umma_f16(tmem + buf * 128, bk, hk, idesc, k > 0);
+          else umma_f16(tmem + buf * 128, hk, bk, idesc, k > 0);
+        }
+        umma_commit(&sh.empty[slot]);
+        umma_commit(&sh.acc_full[buf]);
+      }
+      __syncwarp();
+    }
+    drain(sh, p.wait_limit_ns);
+  } else {
+    // ---------------------------------------------------- epilogue ----
+    // two warpgroups, a buffer each
+    const int group = (warp - 2) >> 2, quarter = warp & 3;
+    const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + group * 128;
+    griddep_wait();  // before row_scale is read
+    const int row = quarter * 32 + lane;
+    const bool busy = quarter * 32 < tile.rows;
+    const bool valid = row < tile.rows;
+    const float scale = !small && valid ? p.row_scale[tile.row0 + row] : 0.0f;
+    const int64_t at = tile.row0 + row;
+    uint32_t turn = 0;
+    for (int i = group; i < count; i += 2, ++turn) {
+      const int n0 = (sub0 + i) * kTileRows;
+      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns))) break;
+      tc_fence_after();
+      if (small) {
+        uint32_t v[16];
+        tmem_ld16(acc, v);
+        tmem_ld_wait();
+        reg_fence<16>(v);
+        const int n = n0 + row;
+        if (n < p.outputs) {
+#pragma unroll
+          for (int t = 0; t < kBox; ++t) {
+            if (t >= tile.rows) break;
+            const int64_t r = tile.row0 + t;
+            const float b = base ? El<T>::to_float(base[r * p.base_row + n]) : 0.0f;
+            out[r * p.out_row + n] = El<T>::from_float(fmaf(__uint_as_float(v[t]), p.row_scale[r], b));
+          }
+        }
+      } else if (busy) {
+        const int width = min(p.outputs - n0, kTileRows);
+#pragma unroll 1
+        for (int c = 0; c < width; c += 32) {
+          uint4 b[2][2] = {};
+          if (valid && base) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (c + j * 8 < width) b[j >> 1][j & 1] = *reinterpret_cast<const uint4*>(base + at * p.base_row + n0 + c + j * 8);
+          }
+          uint32_t v[32];
+          tmem_ld32(acc + c, v);
+          tmem_ld_wait();
+          reg_fence<32>(v);
+          if (!valid) continue;
+          T* o = out + at * p.out_row + n0 + c;
+          if (c + 32 <= width) {
+            add_store16<T>(o, b[0], v, scale);
+            add_store16<T>(o + 16, b[1], v + 16, scale);
+          } else {
+            for (int j = 0; j < 4; ++j) {
+              if (c + j * 8 >= width) break;
+#pragma unroll
+              for (int jj = 0; jj < 4; ++jj) {
+                if (jj != j) continue;
+                Chunk<T, 8> bc, oc;
+                const uint4 w = b[jj >> 1][jj & 1];
+                bc.w[0] = w.x, bc.w[1] = w.y, bc.w[2] = w.z, bc.w[3] = w.w;
+                float f[8];
+                bc.get(f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[jj * 8 + e]), scale, f[e]);
+                oc.set(f);
+                oc.store(o + jj * 8);
+              }
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    tmem_relinquish();
+    tmem_dealloc(tmem, 256);
+  }
+}
+
+// ------------------------------------------------------------------- host --
+
+std::atomic<uint64_t> g_limit_ns{0};
+std::atomic<int32_t> g_stall{0};
+
+bool multiple16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+int rank16_of(const eg_lora_args& a) { return (a.rank + 15) / 16 * 16; }
+size_t h_bytes(const eg_lora_args& a) { return static_cast<size_t>(a.rows) * 2 * rank16_of(a) * 2; }
+size_t workspace_of(const eg_lora_args& a) { return h_bytes(a) + (static_cast<size_t>(a.rows) * 4 + 15) / 16 * 16; }
+
+eg_status check_shape(const eg_lora_args* a) {
+  if (!a) return host_fail(EG_ERR_INVALID_ARG, "args is NULL");
+  if (a->rows < 0 || a->sequences < 0 || a->adapters < 0)
+    return host_fail(EG_ERR_INVALID_ARG, "negative size (rows=%d sequences=%d adapters=%d)", a->rows, a->sequences, a->adapters);
+  if (a->dtype != EG_EL_BF16 && a->dtype != EG_EL_F16)
+    return host_fail(a->dtype == EG_EL_F32 ? EG_ERR_UNSUPPORTED : EG_ERR_INVALID_ARG, "dtype must be bf16 or fp16 (got %d)", a->dtype);
+  if (a->rows > (1 << 24) || a->sequences > 65536) return host_fail(EG_ERR_UNSUPPORTED, "at most 2^24 rows and 65536 sequences a call");
+  for (int n : {a->inputs, a->outputs})
+    if (n < 8 || n % 8 || n > (1 << 20)) return host_fail(EG_ERR_UNSUPPORTED, "inputs and outputs must be multiples of 8 in 8..2^20 (got %d and %d)", a->inputs, a->outputs);
+  if (a->rank < 8 || a->rank % 8 || a->rank > 128) return host_fail(EG_ERR_UNSUPPORTED, "rank must be a multiple of 8 in 8..128 (got %d)", a->rank);
+  if (static_cast<int64_t>(a->adapters) * std::max(a->outputs, a->rank) > INT32_MAX)
+    return host_fail(EG_ERR_UNSUPPORTED, "%d adapters of %d outputs exceed 2^31 rows", a->adapters, a->outputs);
+  return EG_OK;
+}
+
+eg_status check_matrix(const char* name, const void* p, int64_t stride, int width, int rows, bool output) {
+  if (!p || !multiple16(p)) return host_fail(EG_ERR_INVALID_ARG, "%s is NULL or not 16-byte aligned", name);
+  if (rows > 1 && (stride % 8 || stride < (output ? width : 8) || stride > (1ll << 38)))
+    return host_fail(EG_ERR_INVALID_ARG, "the rows of %s must be a positive multiple of 8 elements apart%s (got %lld)", name,
+                     output ? ", their width at least" : "", (long long)stride);
+  return EG_OK;
+}
+
+eg_status encode(const eg_lora_args& a, const void* base, uint64_t cols, uint64_t rows, uint64_t row_elements, uint32_t box_rows, CUtensorMap* map) {
+  EncodeTiledFn fn = host_encode_tiled();
+  if (!fn) return host_fail(EG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t dims[2] = {cols, rows};
+  const cuuint64_t strides[1] = {row_elements * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t steps[2] = {1, 1};
+  const CUresult r = fn(map, a.dtype == EG_EL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(base), dims,
+                        strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? EG_OK : host_fail(EG_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d)", static_cast<int>(r));
+}
+
+template <typename T>
+eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed_inner{0}, allowed_outer{0};
+  CUtensorMap map_x, map_a, map_h, map_b;
+  EG_TRY(encode(a, a.x, a.inputs, a.rows, a.rows > 1 ? a.x_row : a.inputs, kBox, &map_x));
+  // nothing is read of an empty bank, but a map has to have some place
+  const uint64_t bank = std::max(a.adapters, 1);
+  EG_TRY(encode(a, a.adapters ? a.a : a.x, a.inputs, bank * a.rank, a.inputs, a.rank, &map_a));
+  EG_TRY(encode(a, p.h, 2 * p.rank16, a.rows, 2 * p.rank16, kBox, &map_h));
+  EG_TRY(encode(a, a.adapters ? a.b : a.x, a.rank, bank * a.outputs, a.rank, kTileRows, &map_b));
+
+  // Two CTAs an SM in either kernel, where their shared memory lets them.
+  const int room = 113 * 1024 - static_cast<int>(sizeof(LoraShared));
+  const int stage = static_cast<int>(kRowTile) + (p.rank16 * 128 + 1023) / 1024 * 1024;
+  p.stages = std::min(8, room / stage);
+  const int inner_bytes = p.stages * stage + static_cast<int>(sizeof(LoraShared));
+  // CTAs for two an SM, at least four columns of 64 each
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= sms * 2 && p.chunks >= p.splits * 8) p.splits *= 2;
+  const int h_tile = (2 * p.rank16 + 63) / 64 * static_cast<int>(kRowTile), b_tile = (p.rank16 + 63) / 64 * static_cast<int>(kRowTile);
+  p.stages_out = std::min(8, (room - h_tile) / b_tile);
+  if (p.stages_out < 2) p.stages_out = std::min(8, (226 * 1024 - static_cast<int>(sizeof(LoraShared)) - h_tile) / b_tile);
+  const int outer_bytes = h_tile + p.stages_out * b_tile + static_cast<int>(sizeof(LoraShared));
+  p.subs = (a.outputs + kTileRows - 1) / kTileRows;
+  const int each = std::max(1, sms * 2 / tiles);  // CTAs that share a tile's outputs
+  p.subs_each = (p.subs + each - 1) / each;
+  const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
+
+  auto inner = lora_inner_kernel<T>;
+  auto outer = lora_outer_kernel<T>;
+  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(inner), 114 * 1024, dev, &allowed_inner));
+  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(outer), 227 * 1024, dev, &allowed_outer));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * p.splits);
+  cfg.blockDim = dim3(kInnerThreads);
+  cfg.dynamicSmemBytes = inner_bytes;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = p.splits, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, inner, p, map_x, map_a);
+  if (e != cudaSuccess) return host_cuda_fail(e, "launching lora's first product");
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * groups);
+  cfg.blockDim = dim3(kOuterThreads);
+  cfg.dynamicSmemBytes = outer_bytes;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  e = cudaLaunchKernelEx(&cfg, outer, p, map_h, map_b);
+  return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching lora's second product");
+}
+
+}  // namespace
+}  // namespace eg
+
+using namespace eg;
+
+extern "C" {
+
+eg_status eg_lora_workspace_bytes(const eg_lora_args* args, size_t* out) {
+  EG_TRY(check_shape(args));
+  if (!out) return host_fail(EG_ERR_INVALID_ARG, "out is NULL");
+  *out = workspace_of(*args);
+  return EG_OK;
+}
+
+eg_status eg_lora(const eg_lora_args* args, void* stream) {
+  EG_TRY(check_shape(args));
+  const eg_lora_args& a = *args;
+  if (a.rows == 0 || a.sequences == 0) return EG_OK;
+  EG_TRY(check_matrix("out", a.out, a.out_row, a.outputs, a.rows, true));
+  if (a.base) EG_TRY(check_matrix("base", a.base, a.base_row, a.outputs, a.rows, false));
+  if (a.base == a.out && a.rows > 1 && a.base_row != a.out_row)
+    return host_fail(EG_ERR_INVALID_ARG, "out is base with another stride");
+  EG_TRY(check_matrix("x", a.x, a.x_row, a.inputs, a.rows, false));
+  if (a.adapters > 0 && (!a.a || !a.b || !multiple16(a.a) || !multiple16(a.b)))
+    return host_fail(EG_ERR_INVALID_ARG, "a or b is NULL or not 16-byte aligned");
+  if (!a.seq_start || !a.adapter) return host_fail(EG_ERR_INVALID_ARG, "seq_start or adapter is NULL");
+  for (const void* x : {static_cast<const void*>(a.seq_start), static_cast<const void*>(a.adapter), static_cast<const void*>(a.scales)})
+    if (reinterpret_cast<uintptr_t>(x) % 4) return host_fail(EG_ERR_INVALID_ARG, "a side tensor is not aligned to its elements");
+  if (!a.workspace || !multiple16(a.workspace)) return host_fail(EG_ERR_INVALID_ARG, "workspace is NULL or not 16-byte aligned");
+  if (a.workspace_bytes < workspace_of(a)) return host_fail(EG_ERR_INVALID_ARG, "workspace holds %zu bytes of %zu", a.workspace_bytes, workspace_of(a));
+  int dev = 0, sms = 0;
+  EG_TRY(host_check_device(&dev, &sms));
+  LoraParams p{};
+  p.rows = a.rows, p.sequences = a.sequences, p.adapters = a.adapters, p.outputs = a.outputs, p.rank = a.rank, p.rank16 = rank16_of(a);
+  p.chunks = (a.inputs + 63) / 64;
+  p.seq_start = a.seq_start, p.adapter = a.adapter, p.scales = a.scales;
+  p.base = a.base, p.base_row = a.base_row, p.out = a.out, p.out_row = a.out_row;
+  p.h = a.workspace, p.row_scale = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + h_bytes(a));
+  const uint64_t limit = g_limit_ns.load(std::memory_order_relaxed);
+  p.wait_limit_ns = limit ? limit : host_wait_limit_ns();
+  p.stall = g_stall.load(std::memory_order_relaxed);
+  // tiles that the sequences can have at most: one more each than whole ones
+  const int tiles = a.rows / kTileRows + std::min(a.sequences, a.rows);
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return a.dtype == EG_EL_BF16 ? launch<__nv_bfloat16>(a, p, tiles, sms, dev, st) : launch<__half>(a, p, tiles, sms, dev, st);
+}
+
+eg_status eg_lora_device_status(void) {
+  int dev = 0;
+  EG_TRY(host_check_device(&dev));
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e != cudaSuccess) return host_cuda_fail(e, "synchronising the current device");
+  int32_t status = 0;
+  if ((e = cudaMemcpyFromSymbol(&status, g_lora_status, 4)) != cudaSuccess) return host_cuda_fail(e, "reading the status of lora");
+  if (status == 0) return EG_OK;
+  status = 0;
+  e = cudaMemcpyToSymbol(g_lora_status, &status, 4);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(nullptr);  // later calls may be on streams that do not wait for this one
+  if (e != cudaSuccess) return host_cuda_fail(e, "clearing the status of lora");
+  return host_fail(EG_ERR_DEVICE_TIMEOUT, "a wait of the lora kernels ran past its limit");
+}
+
+eg_status eg_lora_set_test_stall(uint64_t wait_limit_ns, int32_t stall_loader) {
+  if (stall_loader != 0 && stall_loader != 1) return host_fail(EG_ERR_INVALID_ARG, "stall_loader must be 0 or 1");
+  g_limit_ns.store(wait_limit_ns, std::memory_order_relaxed);
+  g_stall.store(stall_loader, std::memory_order_relaxed);
+  return EG_OK;
+}
+
+}  // extern "C"

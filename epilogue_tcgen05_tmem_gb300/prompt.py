@@ -5,7 +5,8 @@
 bits or as the codes and scales that an 8-bit linear plan takes;
 ``add_rms_norm_backward`` is its gradient.  ``ChunkAttention`` is a plan for
 attention of chunks of new tokens over a paged cache, all of it or a sliding
-window and the first places.  All take torch CUDA tensors by their
+window and the first places.  ``lora`` adds the low-rank adapters of many
+requests to a shared projection's output.  All take torch CUDA tensors by their
 row strides (the last dimension contiguous).  Every call runs on the current
 stream unless ``stream`` gives another.  None records autograd, as the linear
 plans do not.
@@ -19,7 +20,8 @@ from .decoder import EL_DTYPES, _b, _cache, _code, _fail, _heads, _new, _out, _p
 
 EXPORTED = ("eg_add_rms_norm", "eg_add_rms_norm_backward", "eg_add_rms_norm_workspace_bytes",
             "eg_chunk_plan_create", "eg_chunk_plan_workspace_bytes", "eg_chunk_plan_run", "eg_chunk_plan_device_status",
-            "eg_chunk_plan_set_test_stall", "eg_chunk_plan_destroy")
+            "eg_chunk_plan_set_test_stall", "eg_chunk_plan_destroy",
+            "eg_lora", "eg_lora_workspace_bytes", "eg_lora_device_status", "eg_lora_set_test_stall")
 
 _i64, _i32, _f32, _p, _size = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_void_p, ctypes.c_size_t
 
@@ -47,8 +49,14 @@ class eg_chunk_args(ctypes.Structure):
                 ("sinks", _i32), ("scale", _f32), ("lse", _p)]
 
 
+class eg_lora_args(ctypes.Structure):
+    _fields_ = [("rows", _i32), ("sequences", _i32), ("adapters", _i32), ("inputs", _i32), ("outputs", _i32), ("rank", _i32), ("dtype", _i32),
+                ("x", _p), ("x_row", _i64), ("a", _p), ("b", _p), ("scales", _p), ("seq_start", _p), ("adapter", _p), ("base", _p),
+                ("base_row", _i64), ("out", _p), ("out_row", _i64), ("workspace", _p), ("workspace_bytes", _size)]
+
+
 _pack_norm, _pack_norm_grads = _packer(eg_norm_args), _packer(eg_norm_grads)
-_pack_chunk = _packer(eg_chunk_args)
+_pack_chunk, _pack_lora = _packer(eg_chunk_args), _packer(eg_lora_args)
 
 
 def declare(L: ctypes.CDLL) -> None:
@@ -61,7 +69,11 @@ def declare(L: ctypes.CDLL) -> None:
                        ("eg_chunk_plan_run", [_p, _p, _p, _p]),
                        ("eg_chunk_plan_device_status", [_p]),
                        ("eg_chunk_plan_set_test_stall", [_p, ctypes.c_uint64, _i32]),
-                       ("eg_chunk_plan_destroy", [_p])):
+                       ("eg_chunk_plan_destroy", [_p]),
+                       ("eg_lora", [_p, _p]),
+                       ("eg_lora_workspace_bytes", [_p, ctypes.POINTER(_size)]),
+                       ("eg_lora_device_status", []),
+                       ("eg_lora_set_test_stall", [ctypes.c_uint64, _i32])):
         f = getattr(L, name)
         f.argtypes, f.restype = args, ctypes.c_int
 
@@ -251,3 +263,66 @@ class ChunkAttention:
             self.close()
         except Exception:
             pass
+
+
+# --------------------------------------------------- low-rank adapters ----
+
+def lora(x, a, b, seq_start, adapter, scales=None, base=None, out=None, stream=None):
+    """Low-rank adapters of many requests beside a shared projection: for the
+    rows seq_start[i] .. seq_start[i + 1] of x [rows, inputs], with the adapter
+    n = adapter[i] (int32; none where it is outside the bank),
+
+        out = base + scales[n] * (x @ a[n].T) @ b[n].T
+
+    a [adapters, rank, inputs] and b [adapters, outputs, rank] are the bank
+    (adapters of a lower rank padded with zeros), scales float32 [adapters]
+    (None: 1), base [rows, outputs] the projection's output (None: 0; give it as
+    ``out`` too to add in place).  Without a base the result is what a linear
+    plan takes as its residual before the activation.  Rows that no sequence has
+    are left as they were in ``out``, undefined in a new one."""
+    if not _b.ready:
+        _b.load()
+    st = _stream_of(x, stream)
+    if x.dim() != 2 or a.dim() != 3 or b.dim() != 3:
+        raise ValueError("x must be [rows, inputs], a [adapters, rank, inputs] and b [adapters, outputs, rank]")
+    rows, inputs = x.shape
+    adapters, rank = a.shape[:2]
+    outputs = b.shape[1]
+    dtype, device = x.dtype, x.device
+    px, x_row = _matrix("x", x, x.shape, dtype, device)
+    pa, pb = _side("a", a, dtype, (adapters, rank, inputs), device), _side("b", b, dtype, (adapters, outputs, rank), device)
+    sequences = adapter.shape[0]
+    start = _side("seq_start", seq_start, _b.i32, (sequences + 1,), device)
+    which = _side("adapter", adapter, _b.i32, (sequences,), device)
+    ps = _side("scales", scales, _b.f32, (adapters,), device)
+    pbase = base_row = 0
+    if base is not None:
+        pbase, base_row = _matrix("base", base, (rows, outputs), dtype, device)
+    out, po, out_row = _result("out", out, (rows, outputs), dtype, device, stream)
+    head = (rows, sequences, adapters, inputs, outputs, rank, _code(x), px, x_row, pa, pb, ps, start, which, pbase, base_row, po, out_row)
+    need = _size(0)
+    status = _b.lora_workspace_bytes(_pack_lora(*head, 0, 0), ctypes.byref(need))
+    if status:
+        _fail(status)
+    work = _new(need.value, _b.torch.uint8, device, stream)
+    status = _b.lora(_pack_lora(*head, work.data_ptr(), need.value), st)
+    if status:
+        _fail(status)
+    return out
+
+
+def lora_device_status() -> int:
+    """Synchronises the current device: EG_ERR_DEVICE_TIMEOUT, once, when a wait of ``lora`` on it ran past its limit (EG_WAIT_CAP_MS) since
+    the last call; what the calls since then wrote is not to be used."""
+    if not _b.ready:
+        _b.load()
+    return _b.lora_device_status()
+
+
+def lora_set_test_stall(wait_limit_ns: int, stall_loader: int):
+    """Testing hook for failure detection (see include/eg_prompt.h)."""
+    if not _b.ready:
+        _b.load()
+    status = _b.lora_set_test_stall(wait_limit_ns, int(stall_loader))
+    if status:
+        _fail(status)

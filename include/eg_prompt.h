@@ -1,7 +1,8 @@
 /*
  * eg_prompt.h -- C ABI of the operators that take in a prompt (sm_103a): the
- * residual stream's addition and norm with an output in 8 bits, and attention
- * of chunks of new tokens over a paged cache.  Conventions as in eg_decoder.h:
+ * residual stream's addition and norm with an output in 8 bits, low-rank
+ * adapters of many requests beside a shared projection, and attention of
+ * chunks of new tokens over a paged cache.  Conventions as in eg_decoder.h:
  * every call returns an eg_status, argument errors are found before any device
  * work is queued, eg_last_error_detail() describes the last failure of this
  * thread, the caller owns every tensor and keeps it alive until the stream has
@@ -83,6 +84,50 @@ typedef struct {
 
 EG_API eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream);
 EG_API eg_status eg_add_rms_norm_workspace_bytes(const eg_norm_grads* args, size_t* out);
+
+/* --------------------------------- low-rank adapters of many requests -----
+ *
+ * Sequence b is rows seq_start[b] .. seq_start[b + 1] of x and has adapter
+ * a = adapter[b].  For each of its rows, with A_a [rank][inputs] and
+ * B_a [outputs][rank]:
+ *
+ *   out = base + scales[a] * (x A_a^T) B_a^T
+ *
+ * (base 0 where NULL; scales 1 where NULL; nothing is added where a is outside
+ * [0, adapters)).  x A_a^T is kept to float32 sums and enters the second
+ * product as two 16-bit parts, some 2^-16 of its row's largest value off.
+ * seq_start and adapter are read on the device, so a captured graph replays
+ * with new ones; seq_start rises, and is cut to the rows there are.  Rows that
+ * no sequence has are not written.  An adapter of a lower rank than the bank's
+ * is padded with zeros.  out may be base (same stride). */
+typedef struct {
+  int32_t rows, sequences;      /* of x; up to 2^24 rows, 65536 sequences */
+  int32_t adapters;
+  int32_t inputs, outputs;      /* multiples of 8, 8..2^20 */
+  int32_t rank;                 /* a multiple of 8, 8..128 */
+  int32_t dtype;                /* EG_EL_BF16 or EG_EL_F16 of x, a, b, base and out */
+  const void* x;                /* [rows][inputs] by the stride */
+  int64_t x_row;
+  const void *a, *b;            /* [adapters][rank][inputs], [adapters][outputs][rank], contiguous */
+  const float* scales;          /* [adapters] */
+  const int32_t* seq_start;     /* [sequences + 1] */
+  const int32_t* adapter;       /* [sequences] */
+  const void* base;             /* [rows][outputs] by the stride */
+  int64_t base_row;
+  void* out;
+  int64_t out_row;              /* x, a, b, base, out and their rows: multiples of 16 bytes */
+  void* workspace;              /* at least eg_lora_workspace_bytes(), 16-byte aligned, not shared by calls that overlap */
+  size_t workspace_bytes;
+} eg_lora_args;
+
+EG_API eg_status eg_lora(const eg_lora_args* args, void* stream);
+EG_API eg_status eg_lora_workspace_bytes(const eg_lora_args* args, size_t* out);
+/* Synchronise the current device and report a wait of eg_lora on it that ran
+ * past its limit since the last report (EG_ERR_DEVICE_TIMEOUT, then cleared):
+ * what the calls since then wrote is not to be used. */
+EG_API eg_status eg_lora_device_status(void);
+/* Testing hook for failure detection, as eg_token_logprobs_set_test_stall. */
+EG_API eg_status eg_lora_set_test_stall(uint64_t wait_limit_ns, int32_t stall_loader);
 
 /* ---------------------- attention of chunks of new tokens over the cache --
  *

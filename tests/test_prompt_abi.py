@@ -115,3 +115,33 @@ def test_chunk_null_arguments(L):
     assert L.eg_chunk_plan_device_status(None) == BAD
     assert L.eg_chunk_plan_set_test_stall(None, 0, 0) == BAD
     assert L.eg_chunk_plan_destroy(None) == eg.EG_OK
+
+
+def _lora(**kw):
+    return _set(prompt.eg_lora_args(rows=4, sequences=2, adapters=3, inputs=64, outputs=128, rank=16, dtype=0, x=16, x_row=64, a=16, b=16, scales=16,
+                                    seq_start=16, adapter=16, base=32, base_row=128, out=16, out_row=128, workspace=16, workspace_bytes=1 << 20), kw)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(rows=-1), BAD), (dict(sequences=-1), BAD), (dict(adapters=-1), BAD), (dict(rows=(1 << 24) + 1), NOT), (dict(sequences=65537), NOT),
+    (dict(inputs=0), NOT), (dict(inputs=68), NOT), (dict(outputs=4), NOT), (dict(inputs=(1 << 20) + 8), NOT), (dict(rank=0), NOT), (dict(rank=12), NOT),
+    (dict(rank=136), NOT), (dict(dtype=2), NOT), (dict(dtype=9), BAD), (dict(adapters=1 << 30), NOT), (dict(x=None), BAD), (dict(x=24), BAD),
+    (dict(x_row=0), BAD), (dict(x_row=65), BAD), (dict(a=None), BAD), (dict(b=8), BAD), (dict(scales=18), BAD), (dict(seq_start=None), BAD),
+    (dict(adapter=None), BAD), (dict(adapter=17), BAD), (dict(base=40), BAD), (dict(base_row=4), BAD), (dict(out=None), BAD), (dict(out_row=120), BAD),
+    (dict(base=16, base_row=256), BAD), (dict(workspace=None), BAD), (dict(workspace=24), BAD), (dict(workspace_bytes=100), BAD)])
+def test_lora_refusals_before_device(L, kw, status):
+    assert L.eg_lora(ctypes.addressof(_lora(**kw)), None) == status
+    assert eg.last_error_detail()
+
+
+def test_lora_without_work_and_hooks(L):
+    assert L.eg_lora(None, None) == BAD
+    assert L.eg_lora_workspace_bytes(None, None) == BAD
+    assert L.eg_lora_workspace_bytes(ctypes.addressof(_lora()), None) == BAD
+    n = ctypes.c_size_t()
+    assert L.eg_lora_workspace_bytes(ctypes.addressof(_lora(rows=5)), ctypes.byref(n)) == eg.EG_OK and n.value == 5 * 2 * 16 * 2 + 32
+    assert L.eg_lora(ctypes.addressof(_lora(rows=0, x=None, out=None)), None) == eg.EG_OK
+    assert L.eg_lora(ctypes.addressof(_lora(sequences=0, seq_start=None)), None) == eg.EG_OK
+    for bad in (-1, 2):
+        assert L.eg_lora_set_test_stall(0, bad) == BAD
+    assert L.eg_lora_set_test_stall(0, 0) == eg.EG_OK
