@@ -231,7 +231,7 @@ struct ChunkShared {
   uint64_t told[2], done[2];      // segments for the softmax warpgroups
   uint32_t tmem;
   int32_t abort;
-  int32_t poisoned[2];            // the last segment (counted from 1) that found a value that is not finite
+  int32_t poisoned[2][2];         // a warpgroup's last odd and even segment (counted from 1) that found a value that is not finite
   int32_t b;
   int32_t joins;                  // this CTA has the last part of an item
   int64_t before;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     sh.abort = 0;
-    sh.poisoned[0] = sh.poisoned[1] = 0;
+    for (int i = 0; i < 4; ++i) sh.poisoned[i >> 1][i & 1] = 0;
   }
   __syncthreads();
   int64_t total = 0, base = 0;
@@ -563,6 +563,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
     const uint32_t t_s = tmem + lanes + s * 128, t_o = tmem + lanes + 256;
     const float c = p.scale_log2;
+    const uint64_t c2 = pack64(__float_as_uint(c), __float_as_uint(c));
     uint32_t base = 0, uses = 0, exchanges = 0;
     int32_t segment = 0;
     bool ok = true;
@@ -585,6 +586,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       // what every row of the warpgroup's tile attends to
       const int all_to = min(walk.seq.ctx + (walk.item.row0 + tile_row0) / p.group + 1, hi);
       const int all_from = p.window ? walk.seq.ctx + (walk.item.row0 + min(tile_row0 + p.tile_rows, walk.item.rows) - 1) / p.group - p.window + 1 : 0;
+      // and what every row of the item does
+      const int item_to = min(walk.seq.ctx + walk.item.row0 / p.group + 1, hi);
+      const int item_from = p.window ? walk.seq.ctx + (walk.item.row0 + walk.item.rows - 1) / p.group - p.window + 1 : 0;
       // 32 bits of which places from `place` on this row attends to
       auto seen_bits = [&](int place) -> uint32_t {
         auto first_bits = [](int n) { return n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1u; };
@@ -597,105 +601,152 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int key0 = walk.place(i);
         const int key1 = key0 + static_cast<int>(kChunkKeys);
         const bool edge = key1 > all_to || (key0 < all_from && key1 > sinks);
-        if (!(ok = wait_all(&sh.s_full[s], uses))) break;
-        tc_fence_after();
-        if (busy) {
-          uint32_t x[128];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32p(t_s + j * 32, x + j * 32);
-          tmem_ld_wait();
-          reg_fence<128>(x);
-          if (edge) {
-            // -infinity where the row does not attend to
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = seen_bits(key0 + 32 * w);
-              if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) continue;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(bits >> j & 1u)) x[w * 32 + j] = 0xFF800000u;
-            }
-          }
-          float top[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top[j] = __uint_as_float(x[j]);
-#pragma unroll
-          for (int j = 4; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], __uint_as_float(x[j]));
-          float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          high = high == -CUDART_INF_F ? high : high * c;
-          if (!valid) high = -CUDART_INF_F;
-          if (fresh) {
-            m = high;
-          } else if (__any_sync(0xffffffffu, high > m + kGrow)) {
-            // bring this row's sums to its new maximum
-            const float next = fmaxf(m, high);
-            const float f = next == m ? 1.0f : attn_ex2(m - next);
-            if (!(ok = wait_all(&sh.o_done[s], uses - 1))) break;
-            tc_fence_after();
-#pragma unroll 1
-            for (int j = 0; j < HD; j += 16) {
-              uint32_t y[16];
-              tmem_ld16(t_o + s * 128 + j, y);
-              tmem_ld_wait();
-              reg_fence<16>(y);
-#pragma unroll
-              for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
-              tmem_st16(t_o + s * 128 + j, y);
-            }
-            l *= f;
-            m = next;
-          }
-          const float ref = m == -CUDART_INF_F ? 0.0f : kShift - m;
-          const uint64_t c2 = pack64(__float_as_uint(c), __float_as_uint(c)), ref2 = pack64(__float_as_uint(ref), __float_as_uint(ref));
-          uint64_t sum2[2] = {0, 0};
-#pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            float a, b;
-            unpack64(fma2(pack64(x[2 * j], x[2 * j + 1]), c2, ref2), &a, &b);
-            a = attn_ex2(a), b = attn_ex2(b);
-            sum2[j & 1] = add2(sum2[j & 1], pack64(__float_as_uint(a), __float_as_uint(b)));
-            x[j] = El<T>::pack2(a, b);
-          }
-          float sum_a, sum_b;
-          unpack64(add2(sum2[0], sum2[1]), &sum_a, &sum_b);
-          l += sum_a + sum_b;
-          tmem_st32(t_s, x);
-          tmem_st32(t_s + 32, x + 32);
-          tmem_st_wait();
-        }
-        fresh = false;
-        if (edge) {
-          // Values of places that no row attends to become zero, and so do
-          // other values that are not finite: a weight of zero times one would
-          // reach rows that do not attend to it (`repair` adds it to those
-          // that do).
+        if (key1 > item_to || (key0 < item_from && key1 > sinks)) {
+          // Before a pair's scores come: values of places that no row attends to
+          // become zero, and so do other values that are not finite: a weight
+          // of zero times one would reach rows that do not attend to it
+          // (`repair` adds it to those that do).  The flag is there before the
+          // zeros, for the other warpgroup that may find those.
+          // A wait for a turn of the ring needs the turn before to be over: a
+          // pair's warpgroup has used the keys of tile i - 1, which lie behind
+          // that in a ring of five or more; one that takes every other tile
+          // has to have the scores of this one, whose keys do in any.
+          if (!pair && !(ok = wait_all(&sh.s_full[s], uses))) break;
           const uint32_t at = base + attn_pos_v(i, count), slot = at % stages;
           if (!(ok = wait_all(&sh.full[slot], at / stages))) break;
           const int key = key0 + row_in;
           uint8_t* v_row = ring + slot * kTile + row_in * 128;
+          // a lane's pieces of its row, in an order that keeps lanes off each other's banks
+          auto piece = [&](int j) { return reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + ((j ^ lane) & 7) * 16); };
           if (key >= hi || (key < lo && key >= sinks)) {
-#pragma unroll 4
-            for (int j = 0; j < kChunks * 8; ++j) *reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16) = make_uint4(0, 0, 0, 0);
-          } else {
-            constexpr uint32_t kInf = El<T>::kBf16 ? 0x7F80u : 0x7C00u;
-            bool found = false;
-#pragma unroll 1
-            for (int j = 0; j < kChunks * 8; ++j) {
-              uint4* at_v = reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + (j & 7) * 16);
-              uint4 v = *at_v;
-              uint32_t* word = reinterpret_cast<uint32_t*>(&v);
-              bool here = false;
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                if ((word[k] & kInf) == kInf) word[k] &= 0xFFFF0000u, here = true;
-                if ((word[k] & (kInf << 16)) == (kInf << 16)) word[k] &= 0x0000FFFFu, here = true;
-              }
-              if (here) *at_v = v, found = true;
+            for (int j = 0; j < kChunks * 8; ++j) *piece(j) = make_uint4(0, 0, 0, 0);
+          } else {
+            // an exponent of ones carries into the sign's place
+            constexpr uint32_t kInf = El<T>::kBf16 ? 0x7F80u : 0x7C00u, kInf2 = kInf << 16 | kInf, kOne2 = 0x80008000u - kInf2;
+            uint32_t bad = 0;
+#pragma unroll
+            for (int j = 0; j < kChunks * 8; ++j) {
+              const uint4 v = *piece(j);
+              bad |= ((v.x & kInf2) + kOne2) | ((v.y & kInf2) + kOne2) | ((v.z & kInf2) + kOne2) | ((v.w & kInf2) + kOne2);
             }
-            if (found) *reinterpret_cast<volatile int32_t*>(&sh.poisoned[s]) = segment;
+            if (bad & 0x80008000u) {
+              *reinterpret_cast<volatile int32_t*>(&sh.poisoned[s][segment & 1]) = segment;
+              __threadfence_block();
+#pragma unroll 1
+              for (int j = 0; j < kChunks * 8; ++j) {
+                uint32_t* word = reinterpret_cast<uint32_t*>(piece(j));
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  if ((word[k] & kInf) == kInf) word[k] &= 0xFFFF0000u;
+                  if ((word[k] & (kInf << 16)) == (kInf << 16)) word[k] &= 0x0000FFFFu;
+                }
+              }
+            }
           }
           fence_proxy_async_smem();
         }
+        if (!(ok = wait_all(&sh.s_full[s], uses))) break;
+        tc_fence_after();
+        if (busy) {
+          uint32_t w[64];  // the weights, two 16-bit values a word
+          float high = -CUDART_INF_F, sum = 0.0f;
+          bool careful = edge || fresh;
+          if (!careful) {
+            // Weights against the reference at hand, their maximum beside
+            // them: where that turns out too high the tile is done again.
+            const float ref = m == -CUDART_INF_F ? 0.0f : kShift - m;
+            const uint64_t ref2 = pack64(__float_as_uint(ref), __float_as_uint(ref));
+            uint32_t x[2][32];
+            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+            uint64_t sum2[2] = {0, 0};
+            tmem_ld32p(t_s, x[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t* y = x[q & 1];
+              tmem_ld_wait();
+              reg_fence<32>(y);
+              if (q < 3) tmem_ld32p(t_s + (q + 1) * 32, x[(q + 1) & 1]);
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                top[j & 1] = max3(top[j & 1], __uint_as_float(y[2 * j]), __uint_as_float(y[2 * j + 1]));
+                float a, b;
+                unpack64(fma2(pack64(y[2 * j], y[2 * j + 1]), c2, ref2), &a, &b);
+                a = attn_ex2(a), b = attn_ex2(b);
+                sum2[j & 1] = add2(sum2[j & 1], pack64(__float_as_uint(a), __float_as_uint(b)));
+                w[q * 16 + j] = El<T>::pack2(a, b);
+              }
+            }
+            high = fmaxf(top[0], top[1]) * c;
+            float sum_a, sum_b;
+            unpack64(add2(sum2[0], sum2[1]), &sum_a, &sum_b);
+            sum = sum_a + sum_b;
+            careful = __any_sync(0xffffffffu, valid && high > m + kGrow);
+          }
+          if (careful) {
+            uint32_t x[128];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) tmem_ld32p(t_s + j * 32, x + j * 32);
+            tmem_ld_wait();
+            reg_fence<128>(x);
+            if (edge) {
+              // -infinity where the row does not attend to
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t bits = seen_bits(key0 + 32 * k);
+                if (__all_sync(0xffffffffu, bits == 0xFFFFFFFFu)) continue;
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                  if (!(bits >> j & 1u)) x[k * 32 + j] = 0xFF800000u;
+              }
+            }
+            float top[2] = {-CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) top[j & 1] = max3(top[j & 1], __uint_as_float(x[2 * j]), __uint_as_float(x[2 * j + 1]));
+            high = fmaxf(top[0], top[1]);
+            high = high == -CUDART_INF_F || !valid ? -CUDART_INF_F : high * c;
+            if (fresh) {
+              m = high;
+            } else if (__any_sync(0xffffffffu, high > m + kGrow)) {
+              // bring this row's sums to its new maximum
+              const float next = fmaxf(m, high);
+              const float f = next == m ? 1.0f : attn_ex2(m - next);
+              if (!(ok = wait_all(&sh.o_done[s], uses - 1))) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int j = 0; j < HD; j += 16) {
+                uint32_t y[16];
+                tmem_ld16(t_o + s * 128 + j, y);
+                tmem_ld_wait();
+                reg_fence<16>(y);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(__uint_as_float(y[k]) * f);
+                tmem_st16(t_o + s * 128 + j, y);
+              }
+              l *= f;
+              m = next;
+            }
+            const float ref = m == -CUDART_INF_F ? 0.0f : kShift - m;
+            const uint64_t ref2 = pack64(__float_as_uint(ref), __float_as_uint(ref));
+            uint64_t sum2[2] = {0, 0};
+#pragma unroll
+            for (int j = 0; j < 64; ++j) {
+              float a, b;
+              unpack64(fma2(pack64(x[2 * j], x[2 * j + 1]), c2, ref2), &a, &b);
+              a = attn_ex2(a), b = attn_ex2(b);
+              sum2[j & 1] = add2(sum2[j & 1], pack64(__float_as_uint(a), __float_as_uint(b)));
+              w[j] = El<T>::pack2(a, b);
+            }
+            float sum_a, sum_b;
+            unpack64(add2(sum2[0], sum2[1]), &sum_a, &sum_b);
+            sum = sum_a + sum_b;
+          }
+          l += sum;
+          tmem_st32(t_s, w);
+          tmem_st32(t_s + 32, w + 32);
+          tmem_st_wait();
+        }
+        fresh = false;
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.p_ready[s]);
@@ -708,17 +759,22 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (!(ok = wait_all(&sh.o_done[s], uses - 1))) break;
         tc_fence_after();
       }
+      // A pair's warpgroups have rows of their own and go on by themselves; else
+      // each has half the keys of all rows, and half the columns of the result.
       float2 own = make_float2(m, l), other = make_float2(-CUDART_INF_F, 0.0f);
-      sh.stats[s][row_in] = own;
-      tc_fence_before();
-      mbar_arrive(&sh.exchange);
-      if (!(ok = wait_all(&sh.exchange, exchanges))) break;
-      ++exchanges;
-      tc_fence_after();
-      if (!pair) other = sh.stats[s ^ 1][row_in];
+      if (!pair) {
+        sh.stats[s][row_in] = own;
+        tc_fence_before();
+        mbar_arrive(&sh.exchange);
+        if (!(ok = wait_all(&sh.exchange, exchanges))) break;
+        ++exchanges;
+        tc_fence_after();
+        other = sh.stats[s ^ 1][row_in];
+      }
       // either warpgroup may have met the value first
-      const bool repair = *reinterpret_cast<volatile int32_t*>(&sh.poisoned[0]) == segment ||
-                          *reinterpret_cast<volatile int32_t*>(&sh.poisoned[1]) == segment;
+      __threadfence_block();
+      const bool repair = *reinterpret_cast<volatile int32_t*>(&sh.poisoned[0][segment & 1]) == segment ||
+                          *reinterpret_cast<volatile int32_t*>(&sh.poisoned[1][segment & 1]) == segment;
       const float both = fmaxf(own.x, other.x);
       const float ref = both == -CUDART_INF_F ? 0.0f : both;
       const float f_own = attn_ex2(own.x - ref), f_other = attn_ex2(other.x - ref);
@@ -796,14 +852,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
         }
       }
-      // the other warpgroup's accumulator is read: it may be written again
-      if (!whole && p.arrivals) __threadfence();
+      const bool joining = !whole && p.arrivals;
+      if (joining) __threadfence();
       tc_fence_before();
-      mbar_arrive(&sh.exchange);
-      if (!(ok = wait_all(&sh.exchange, exchanges))) break;
-      ++exchanges;
+      if (!pair || joining) {
+        // the other warpgroup's accumulator is read: it may be written again
+        mbar_arrive(&sh.exchange);
+        if (!(ok = wait_all(&sh.exchange, exchanges))) break;
+        ++exchanges;
+      }
       tc_fence_after();
-      if (!whole && p.arrivals) {
+      if (joining) {
         // the CTA that leaves the last part of the item joins all of them
         const int32_t lead = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(0));
         const int32_t last = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(walk.item.tiles - 1));
