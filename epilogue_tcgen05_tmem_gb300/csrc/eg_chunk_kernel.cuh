@@ -228,6 +228,7 @@ struct ChunkShared {
   uint64_t full[12], empty[12];   // ring stages
   uint64_t s_full[2], p_ready[2], o_done[2];
   uint64_t q_full, q_empty, exchange, drained;
+  uint64_t turn[2];               // a pair's issuers issue in turn
   uint64_t told[2], done[2];      // segments for the softmax warpgroups
   uint32_t tmem;
   int32_t abort;
@@ -235,10 +236,12 @@ struct ChunkShared {
   int32_t b;
   int32_t joins;                  // this CTA has the last part of an item
   int64_t before;
-  int64_t warps[2][12];
   int32_t near_[kChunkNear][4];
   ChunkSegment segments[2];
-  float2 stats[2][128];           // a warpgroup's row references and weights
+  union {
+    float2 stats[2][128];         // a warpgroup's row references and weights
+    int64_t warps[2][12];         // before any: units of each warp's sequences
+  };
 };
 static_assert(sizeof(ChunkShared) <= ChunkSmem<64>::kExtra, "fits the room after the tiles");
 
@@ -280,13 +283,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   if (lane == 31) sh.warps[0][warp] = upto;
   if (tid == 0) {
-    for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 2);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_done[i], 1);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.told[i], 1), mbar_init(&sh.done[i], 8);
+    mbar_init(&sh.turn[0], 1), mbar_init(&sh.turn[1], 1);
     mbar_init(&sh.q_full, 1);
-    mbar_init(&sh.q_empty, 1);
+    mbar_init(&sh.q_empty, 2);
     mbar_init(&sh.exchange, 256);
-    mbar_init(&sh.drained, 1);
+    mbar_init(&sh.drained, 2);
     fence_mbar_init();
     sh.abort = 0;
     for (int i = 0; i < 4; ++i) sh.poisoned[i >> 1][i & 1] = 0;
@@ -429,17 +433,28 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (uint32_t i = pos > stages ? pos - stages : 0; i < pos; ++i)
         if (!mbar_wait(&sh.full[i % stages], (i / stages) & 1, p.wait_limit_ns)) break;
     }
-  } else if (warp == 9) {
-    // --------------------------------------------------------- issuer ----
-    // The whole warp walks, so that addresses stay in uniform registers; one
-    // elected lane issues.  What the tensor cores wait for most is this
-    // warp: positions in the ring are stepped, not divided out.
+  } else if (warp != 11) {
+    // -------------------------------------------------------- issuers ----
+    // One for each softmax warpgroup, so that what one of them waits for and
+    // computes between its products passes behind the other's.  For a pair
+    // they issue in turn: else the two fall into step, with both warpgroups at
+    // their weights while the tensor cores wait and the other way round.  The
+    // whole warp walks, so that addresses stay in uniform registers; one
+    // elected lane issues; places in the ring are stepped, not divided out.
     constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
     constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
+    const uint32_t s = warp - 9, w = tmem + s * 128, o = w + 256;
     const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
     const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
-    uint32_t segment = 0, used0 = 0, used1 = 0;  // segments, and tiles given to each warpgroup
-    uint32_t slot0 = 0, turn0 = 0;               // the segment's first place in the ring, and how often the ring was full
+    uint32_t segment = 0, used = 0;  // segments, and tiles given to the warpgroup
+    uint32_t turns = 0;              // of a pair
+    auto my_turn = [&]() { return wait_all(&sh.turn[s], s ? turns : turns + 1); };
+    auto pass = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.turn[s ^ 1]);
+      ++turns;
+    };
+    uint32_t slot0 = 0, turn0 = 0;   // the segment's first place in the ring, and how often the ring was full
     auto step = [&](uint32_t& slot, uint32_t& turn, uint32_t by) {
       slot += by;
       if (slot >= stages) slot -= stages, ++turn;
@@ -448,56 +463,80 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     while (ok && walk.next(p)) {
       const uint32_t count = walk.count;
       const bool pair = walk.item.cost == 2;
-      const uint32_t jobs = pair ? 2 * count : count;
+      // tiles begin at `first`, `stride` apart; the keys of tile i are 2 i - 1
+      // places on (those of tile 0 at none), its values 2 i + 2, the last
+      // tile's one less
+      const uint32_t first = pair ? 0 : s, stride = pair ? 1 : 2;
+      const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0);
       uint32_t slot_k = slot0, turn_k = turn0, slot_v = slot0, turn_v = turn0;
-      step(slot_v, turn_v, count == 1 ? 1 : 2);
+      step(slot_k, turn_k, first);
+      step(slot_v, turn_v, 2 * first + (first + 1 < count ? 2 : 1));
       if (!(ok = wait_all(&sh.q_full, segment))) break;
-      // job j is warpgroup j & 1's next tile; the scores of two jobs run
-      // ahead of the weighted sums
-      for (uint32_t j = 0; j < jobs + 2; ++j) {
-        const uint32_t s = j & 1;
-        const bool first_use = !pair || s == 0, last_use = !pair || s == 1;
-        if (j >= 2) {
-          // O += P V of job j - 2
-          if (first_use && !(ok = wait_all(&sh.full[slot_v], turn_v))) break;
-          if (!(ok = wait_all(&sh.p_ready[s], s ? used1 : used0))) break;
-          tc_fence_after();
-          const uint64_t v = v_desc + (slot_v * kTile >> 4);
-          const uint32_t o = tmem + 256 + s * 128, w = tmem + s * 128;
-          if (elect_one()) {
-            umma_f16_ts(o, w, v, kIdescO, j >= 4 ? 1 : 0);
+      // O += P V of tile i
+      auto sums = [&](uint32_t i) {
+        const uint64_t v = v_desc + (slot_v * kTile >> 4);
+        umma_f16_ts(o, w, v, kIdescO, i > first ? 1 : 0);
 #pragma unroll
-            for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2048 >> 4), kIdescO);
-            umma_commit(&sh.o_done[s]);
-            if (last_use) umma_commit(&sh.empty[slot_v]);
-          }
-          if (s) ++used1;
-          else ++used0;
-          // V of tile i is 2 i + 2 places on, the last one directly after the one before
-          if (last_use) {
-            const uint32_t i = pair ? (j - 2) >> 1 : j - 2;
-            step(slot_v, turn_v, i + 2 == count ? 1 : 2);
-          }
-        }
-        if (j < jobs) {
-          // S of job j
-          if (first_use && !(ok = wait_all(&sh.full[slot_k], turn_k))) break;
-          tc_fence_after();
-          const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0), key = k_desc + (slot_k * kTile >> 4);
-          const uint32_t d = tmem + s * 128;
-          if (elect_one()) {
-            umma_f16(d, q, key, kIdescS, 0);
+        for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2048 >> 4), kIdescO);
+        umma_commit(&sh.o_done[s]);
+        umma_commit(&sh.empty[slot_v]);
+        if (!pair) umma_commit(&sh.empty[slot_v]);  // for the other issuer too
+      };
+      // S = Q K^T of the next tile
+      auto scores = [&]() {
+        const uint64_t key = k_desc + (slot_k * kTile >> 4);
+        umma_f16(w, q, key, kIdescS, 0);
 #pragma unroll
-            for (int k = 1; k < HD / 16; ++k) {
-              const uint32_t at = ((k / 4) * kPart + (k % 4) * 32) >> 4;
-              umma_f16_add(d, q + at, key + at, kIdescS);
-            }
-            umma_commit(&sh.s_full[s]);
-            if (last_use) umma_commit(&sh.empty[slot_k]);
-            if (j + 1 == jobs) umma_commit(&sh.q_empty);
-          }
-          if (last_use) step(slot_k, turn_k, j < (pair ? 2 : 1) ? 1 : 2);
+        for (int k = 1; k < HD / 16; ++k) {
+          const uint32_t at = ((k / 4) * kPart + (k % 4) * 32) >> 4;
+          umma_f16_add(w, q + at, key + at, kIdescS);
         }
+        umma_commit(&sh.s_full[s]);
+        umma_commit(&sh.empty[slot_k]);
+        if (!pair) umma_commit(&sh.empty[slot_k]);
+      };
+      if (first < count) {
+        if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
+        if (pair && !(ok = my_turn())) break;
+        tc_fence_after();
+        if (elect_one()) scores();
+        if (pair) pass();
+        step(slot_k, turn_k, first == 0 ? 2 * stride - 1 : 2 * stride);
+      }
+      uint32_t i = first;
+      for (; i + stride < count; i += stride) {
+        // a pair's next keys are there when these values are; where keys and
+        // values come straight from memory the sums do not wait for the keys
+        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || wait_all(&sh.full[slot_k], turn_k)) && wait_all(&sh.p_ready[s], used))) break;
+        if (pair) {
+          if (!(ok = my_turn())) break;
+          tc_fence_after();
+          if (elect_one()) sums(i), scores();
+          pass();
+        } else {
+          tc_fence_after();
+          if (elect_one()) sums(i);
+          __syncwarp();
+          if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
+          tc_fence_after();
+          if (elect_one()) scores();
+        }
+        __syncwarp();
+        ++used;
+        step(slot_k, turn_k, 2 * stride);
+        step(slot_v, turn_v, i + stride + 1 < count ? 2 * stride : 2 * stride - 1);
+      }
+      if (!ok) break;
+      if (elect_one()) umma_commit(&sh.q_empty);
+      __syncwarp();
+      if (i < count) {
+        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && wait_all(&sh.p_ready[s], used))) break;
+        if (pair && !(ok = my_turn())) break;
+        tc_fence_after();
+        if (elect_one()) sums(i);
+        if (pair) pass();
+        __syncwarp();
+        ++used;
       }
       // the segment took 2 count places
       uint32_t places = 2 * count;
@@ -510,7 +549,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     __syncwarp();
     if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
   } else {
-    // -------------------------------------------------------- queries ----
+    // ---------------------------------- the walk's segments and queries ----
     if (tid == kChunkThreads - 1) {
       // what the joining kernel has to know of this CTA's first item
       ChunkMeta m;
@@ -520,40 +559,33 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       m.start = walk.seq.start, m.row0 = walk.item.row0, m.head = walk.head, m.rows = walk.item.rows, m.pad = 0;
       p.meta[blockIdx.x] = m;
     }
-    if (warp == 11) {
-      // the walk for the warpgroups below, whose registers have no room for it
-      bool more = true;
-      for (uint32_t n = 0; more; ++n) {
-        if (!wait_all(&sh.done[n & 1], (n >> 1) + 1)) break;
-        more = walk.next(p);
-        walk.more = more;
-        if (lane == 0) {
-          sh.segments[n & 1] = walk;
-          mbar_arrive(&sh.told[n & 1]);
-        }
+    // The walk for the softmax warpgroups, whose registers have no room for it,
+    // and the queries: a box is `box_tokens` tokens by the heads that share a
+    // cached one; lane i has box i of each tile.
+    const int box = p.box_tokens * p.group, boxes = p.tile_rows / box;
+    uint32_t segment = 0;
+    for (bool more = true; more; ) {
+      if (!wait_all(&sh.done[segment & 1], (segment >> 1) + 1)) break;
+      more = walk.next(p);
+      walk.more = more;
+      if (lane == 0) {
+        sh.segments[segment & 1] = walk;
+        mbar_arrive(&sh.told[segment & 1]);
       }
-    }
-    if (warp == 10) {
-      // a box is `box_tokens` tokens by the heads that share a cached one;
-      // lane i has box i of each tile
-      uint32_t segment = 0;
-      const int box = p.box_tokens * p.group, boxes = p.tile_rows / box;
-      while (walk.next(p)) {
-        if (!wait_all(&sh.q_empty, segment + 1)) break;
-        const int all = (walk.item.rows + box - 1) / box;  // boxes that hold a row
-        if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, all * box * 128u * kChunks);
-        __syncwarp();
-        for (int i = lane; i < all; i += 32) {
-          const int tile = i >= boxes ? 1 : 0, in = i - tile * boxes;
+      if (!more || !wait_all(&sh.q_empty, segment + 1)) break;
+      const int all = (walk.item.rows + box - 1) / box;  // boxes that hold a row
+      if (lane == 0) mbar_arrive_expect_tx(&sh.q_full, all * box * 128u * kChunks);
+      __syncwarp();
+      for (int i = lane; i < all; i += 32) {
+        const int tile = i >= boxes ? 1 : 0, in = i - tile * boxes;
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_3d(smem_u32(q_smem) + tile * kTile + c * kPart + in * box * 128u, &map_q, &sh.q_full, c * 64, walk.head * p.group,
-                        walk.seq.start + walk.item.row0 / p.group + i * p.box_tokens);
-        }
-        ++segment;
+        for (int c = 0; c < kChunks; ++c)
+          tma_load_3d(smem_u32(q_smem) + tile * kTile + c * kPart + in * box * 128u, &map_q, &sh.q_full, c * 64, walk.head * p.group,
+                      walk.seq.start + walk.item.row0 / p.group + i * p.box_tokens);
       }
-      if (segment > 0) mbar_wait(&sh.q_full, (segment - 1) & 1, p.wait_limit_ns);  // leaves no copy in flight behind
+      ++segment;
     }
+    if (segment > 0) mbar_wait(&sh.q_full, (segment - 1) & 1, p.wait_limit_ns);  // leaves no copy in flight behind
   }
   } else {
     // -------------------------------------------------------- softmax ----
