@@ -507,9 +507,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       for (; i + stride < count; i += stride) {
         // a pair's next keys are there when these values are; where keys and
         // values come straight from memory the sums do not wait for the keys
-        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || wait_all(&sh.full[slot_k], turn_k)) && wait_all(&sh.p_ready[s], used))) break;
+        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || (wait_all(&sh.full[slot_k], turn_k) && my_turn())) &&
+                   wait_all(&sh.p_ready[s], used)))
+          break;
         if (pair) {
-          if (!(ok = my_turn())) break;
           tc_fence_after();
           if (elect_one()) sums(i), scores();
           pass();
@@ -530,8 +531,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (elect_one()) umma_commit(&sh.q_empty);
       __syncwarp();
       if (i < count) {
-        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && wait_all(&sh.p_ready[s], used))) break;
-        if (pair && !(ok = my_turn())) break;
+        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || my_turn()) && wait_all(&sh.p_ready[s], used))) break;
         tc_fence_after();
         if (elect_one()) sums(i);
         if (pair) pass();
