@@ -50,7 +50,7 @@ struct LoraParams {
   int32_t splits;       // CTAs of a cluster that share them
   int32_t subs;         // tiles of 128 outputs
   int32_t subs_each;    // those of one CTA of the second kernel
-  int32_t stages;       // of the first kernel's ring
+  int32_t ring;         // bytes of the first kernel's ring
   int32_t stages_out;   // of the second's
   const int32_t *seq_start, *adapter;
   const float* scales;
@@ -71,9 +71,12 @@ struct LoraTile {
   int32_t row0, rows, adapter;  // rows 0: there is no such tile
 };
 
+constexpr int kStages = 12;  // of a ring, at most
+constexpr int kBuffers = 8;  // accumulators of a small tile
+
 struct LoraShared {
-  uint64_t full[8], empty[8];
-  uint64_t acc_full[2], acc_empty[2], h_full, done, drained;
+  uint64_t full[kStages], empty[kStages];
+  uint64_t acc_full[kBuffers], acc_empty[kBuffers], base_full[2], h_full, done, drained;
   uint32_t tmem;
   int32_t abort;
   LoraTile tile;
@@ -161,15 +164,14 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
 
 template <typename T>
 __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_x,
-                                                                   const __grid_constant__ CUtensorMap map_a) {
+                                                                   const __grid_constant__ CUtensorMap map_box, const __grid_constant__ CUtensorMap map_a) {
   constexpr uint32_t kFmt = El<T>::kBf16 ? 1u : 0u;
   extern __shared__ __align__(1024) uint8_t smem[];
-  const uint32_t a_bytes = p.rank16 * 128u, stage_bytes = kRowTile + (a_bytes + 1023u) / 1024u * 1024u;
-  LoraShared& sh = *reinterpret_cast<LoraShared*>(smem + p.stages * stage_bytes);
+  LoraShared& sh = *reinterpret_cast<LoraShared*>(smem + p.ring);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int index = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
   if (tid == 0) {
-    for (int i = 0; i < p.stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     mbar_init(&sh.done, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
@@ -188,34 +190,44 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   const uint32_t tmem = sh.tmem;
   const int from = p.chunks * part / p.splits, to = p.chunks * (part + 1) / p.splits;
   const int count = to - from;
+  // Rows come in one box of 128, or 16 a box where that is less to read.  A
+  // stage has the rows that come and A's; a product reads 128 rows of it, the
+  // idle ones from whatever follows, so that much follows the last stage too.
+  const int boxes = (tile.rows + kBox - 1) / kBox;
+  const bool big = boxes > 4;
+  const uint32_t x_bytes = big ? kRowTile : boxes * kBox * 128u, a_at = x_bytes;
+  const uint32_t stage_bytes = x_bytes + (p.rank16 * 128u + 1023u) / 1024u * 1024u;
+  const int stages = min(kStages, static_cast<int>((p.ring - max(stage_bytes, kRowTile)) / stage_bytes) + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------- loads ----
-    const int boxes = (tile.rows + kBox - 1) / kBox;
-    const uint32_t bytes = boxes * kBox * 128u + p.rank * 128u;
-    int i = 0;
+    const uint32_t bytes = x_bytes + p.rank * 128u;
+    int i = 0, slot = 0, turn = 0;
     for (; i < count; ++i) {
-      const int slot = i % p.stages;
-      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], i / p.stages + 1, p.wait_limit_ns))) break;
-      if (p.stall) continue;
+      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], turn + 1, p.wait_limit_ns))) break;
       uint8_t* stage = smem + slot * stage_bytes;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
-      __syncwarp();
-      if (lane < boxes) tma_load_2d(stage + lane * kBox * 128, &map_x, &sh.full[slot], (from + i) * 64, tile.row0 + lane * kBox);
-      if (lane == 31) tma_load_2d(stage + kRowTile, &map_a, &sh.full[slot], (from + i) * 64, tile.adapter * p.rank);
+      if (!p.stall) {
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
+        __syncwarp();
+        if (big ? lane == 0 : lane < boxes)
+          tma_load_2d(stage + lane * kBox * 128, big ? &map_x : &map_box, &sh.full[slot], (from + i) * 64, tile.row0 + lane * kBox);
+        if (lane == 31) tma_load_2d(stage + a_at, &map_a, &sh.full[slot], (from + i) * 64, tile.adapter * p.rank);
+      }
+      if (++slot == stages) slot = 0, ++turn;
     }
     // no copy in flight is left behind
     if (!p.stall)
-      for (int j = max(i - p.stages, 0); j < i; ++j)
-        if (!mbar_wait(&sh.full[j % p.stages], (j / p.stages) & 1, p.wait_limit_ns)) break;
+      for (int j = max(i - stages, 0); j < i; ++j)
+        if (!mbar_wait(&sh.full[j % stages], (j / stages) & 1, p.wait_limit_ns)) break;
   } else if (warp == 1) {
     // ---------------------------------------------------- products ----
     const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, p.rank16);
+    const uint64_t x0 = sdesc_k_sw128(smem_u32(smem)), a0 = sdesc_k_sw128(smem_u32(smem + a_at));
+    int slot = 0, turn = 0;
     for (int i = 0; i < count; ++i) {
-      const int slot = i % p.stages;
-      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], i / p.stages, p.wait_limit_ns))) break;
+      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], turn, p.wait_limit_ns))) break;
       tc_fence_after();
-      const uint64_t x = sdesc_k_sw128(smem_u32(smem + slot * stage_bytes)), a = sdesc_k_sw128(smem_u32(smem + slot * stage_bytes + kRowTile));
+      const uint64_t x = x0 + (slot * stage_bytes >> 4), a = a0 + (slot * stage_bytes >> 4);
       if (elected()) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) umma_f16(tmem, x + k * 2, a + k * 2, idesc, i > 0 || k > 0);
@@ -223,6 +235,7 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
         if (i + 1 == count) umma_commit(&sh.done);
       }
       __syncwarp();
+      if (++slot == stages) slot = 0, ++turn;
     }
     drain(sh, p.wait_limit_ns);
   }
@@ -261,9 +274,17 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (col < p.rank) {
         const uint32_t at = smem_u32(mine + row * pitch + col);
-        for (int c = 0; c < p.splits; ++c) {
-          const float4 w = p.splits > 1 ? ld_cluster4(cluster_map(at, c)) : *reinterpret_cast<const float4*>(mine + row * pitch + col);
-          v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+        if (p.splits == 1) {
+          v = *reinterpret_cast<const float4*>(mine + row * pitch + col);
+        } else {
+          // all on their way before the first is added
+          float4 w[8];
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < p.splits) w[c] = ld_cluster4(cluster_map(at, c));
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            if (c < p.splits) v.x += w[c].x, v.y += w[c].y, v.z += w[c].z, v.w += w[c].w;
         }
       }
       // bits of the largest magnitude: a NaN's are above infinity's
@@ -301,32 +322,21 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
 
 // ---------------------------------------------- out = base + h B^T --------
 
-// 16 outputs of one row: out = base + acc * scale (base may be NULL).
-template <typename T>
-__device__ __forceinline__ void add_store16(T* out, const uint4 (&base)[2], const uint32_t* acc, float scale) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    Chunk<T, 8> b, o;
-    b.w[0] = base[j].x, b.w[1] = base[j].y, b.w[2] = base[j].z, b.w[3] = base[j].w;
-    float f[8];
-    b.get(f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(acc[j * 8 + e]), scale, f[e]);
-    o.set(f);
-    o.store(out + j * 8);
-  }
-}
+// Barrier of the four warps of an epilogue group.
+__device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
 
 template <typename T>
-__global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_h,
-                                                                      const __grid_constant__ CUtensorMap map_b) {
+__global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_h,
+                                                                      const __grid_constant__ CUtensorMap map_b,
+                                                                      const __grid_constant__ CUtensorMap map_base) {
   constexpr uint32_t kFmt = El<T>::kBf16 ? 1u : 0u;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int parts = (p.rank16 + 63) / 64;            // 64-column parts of a tile of B
   const int h_parts = (2 * p.rank16 + 63) / 64;      // and of h
   const uint32_t b_bytes = parts * kRowTile;
   uint8_t* h_smem = smem;
-  uint8_t* ring = smem + h_parts * kRowTile;
+  uint8_t* staged = smem + h_parts * kRowTile;       // 128 rows of 128 outputs for each epilogue group
+  uint8_t* ring = staged + 2 * 2 * kRowTile;
   LoraShared& sh = *reinterpret_cast<LoraShared*>(ring + p.stages_out * b_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
@@ -334,7 +344,8 @@ __global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const Lora
   const int count = min(p.subs - sub0, p.subs_each);
   if (tid == 0) {
     for (int i = 0; i < p.stages_out; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
+    for (int i = 0; i < kBuffers; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
+    mbar_init(&sh.base_full[0], 1), mbar_init(&sh.base_full[1], 1);
     mbar_init(&sh.h_full, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
@@ -360,19 +371,14 @@ __global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const Lora
     }
     return;
   }
-  if (warp == 1) tmem_alloc(&sh.tmem, 256);
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = sh.tmem;
   const bool small = tile.rows <= kBox;
+  const int boxes = (tile.rows + kBox - 1) / kBox;
 
   if (warp == 0) {
     // ------------------------------------------------------- loads ----
     // B does not wait for the first kernel, whose h follows the ring's first filling
     const int ahead = min(count, p.stages_out);
-    const int boxes = (tile.rows + kBox - 1) / kBox;
-    int i = 0;
+    int i = 0, slot = 0, turn = 0;
     bool ok = true, h_sent = false;
     for (; ok && i <= count; ++i) {
       if (i == ahead) {
@@ -388,121 +394,167 @@ __global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const Lora
         }
       }
       if (i == count) break;
-      const int slot = i % p.stages_out;
-      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], i / p.stages_out + 1, p.wait_limit_ns));
-      if (!ok || p.stall) continue;
-      const int n0 = (sub0 + i) * kTileRows;
-      if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], b_bytes);
-      __syncwarp();
-      // rows past the adapter's last output are the next one's, or zeros: their products are not stored
-      if (lane < parts) tma_load_2d(ring + slot * b_bytes + lane * kRowTile, &map_b, &sh.full[slot], lane * 64, tile.adapter * p.outputs + n0);
+      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], turn + 1, p.wait_limit_ns));
+      if (ok && !p.stall) {
+        const int n0 = (sub0 + i) * kTileRows;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], b_bytes);
+        __syncwarp();
+        // rows past the adapter's last output are the next one's, or zeros: their products are not stored
+        if (lane < parts) tma_load_2d(ring + slot * b_bytes + lane * kRowTile, &map_b, &sh.full[slot], lane * 64, tile.adapter * p.outputs + n0);
+      }
+      if (++slot == p.stages_out) slot = 0, ++turn;
     }
     if (!p.stall) {
-      const int sent = min(i, count);
+      const int sent = ok ? count : i - 1;
       for (int j = max(sent - p.stages_out, 0); j < sent; ++j)
         if (!mbar_wait(&sh.full[j % p.stages_out], (j / p.stages_out) & 1, p.wait_limit_ns)) break;
       if (h_sent) mbar_wait(&sh.h_full, 0, p.wait_limit_ns);
     }
-  } else if (warp == 1) {
-    // ---------------------------------------------------- products ----
-    const uint32_t idesc = small ? idesc_f32acc(kFmt, kFmt, 128, kBox) : idesc_f32acc(kFmt, kFmt, 128, kTileRows);
-    const int steps = p.rank16 / 16;
-    const uint64_t h0 = sdesc_k_sw128(smem_u32(h_smem));
-    bool ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_full, 0, p.wait_limit_ns));
-    for (int i = 0; ok && i < count; ++i) {
-      const int slot = i % p.stages_out, buf = i & 1;
-      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], i / p.stages_out, p.wait_limit_ns)) &&
-           __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_empty[buf], i / 2 + 1, p.wait_limit_ns));
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t b0 = sdesc_k_sw128(smem_u32(ring + slot * b_bytes));
-      if (elected()) {
-        for (int k = 0; k < 2 * steps; ++k) {
-          // step k of h against step k of B, again from its first for the low parts
-          const int kb = k < steps ? k : k - steps;
-          const uint64_t hk = h0 + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = b0 + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
-          if (small) umma_f16(tmem + buf * 128, bk, hk, idesc, k > 0);
-          else umma_f16(tmem + buf * 128, hk, bk, idesc, k > 0);
-        }
-        umma_commit(&sh.empty[slot]);
-        umma_commit(&sh.acc_full[buf]);
-      }
-      __syncwarp();
-    }
-    drain(sh, p.wait_limit_ns);
   } else {
-    // ---------------------------------------------------- epilogue ----
-    // two warpgroups, a buffer each
-    const int group = (warp - 2) >> 2, quarter = warp & 3;
-    const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + group * 128;
-    griddep_wait();  // before row_scale is read
-    const int row = quarter * 32 + lane;
-    const bool busy = quarter * 32 < tile.rows;
-    const bool valid = row < tile.rows;
-    const float scale = !small && valid ? p.row_scale[tile.row0 + row] : 0.0f;
-    const int64_t at = tile.row0 + row;
-    uint32_t turn = 0;
-    for (int i = group; i < count; i += 2, ++turn) {
-      const int n0 = (sub0 + i) * kTileRows;
-      if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns))) break;
-      tc_fence_after();
-      if (small) {
-        uint32_t v[16];
-        tmem_ld16(acc, v);
-        tmem_ld_wait();
-        reg_fence<16>(v);
-        const int n = n0 + row;
-        if (n < p.outputs) {
-#pragma unroll
-          for (int t = 0; t < kBox; ++t) {
-            if (t >= tile.rows) break;
-            const int64_t r = tile.row0 + t;
-            const float b = base ? El<T>::to_float(base[r * p.base_row + n]) : 0.0f;
-            out[r * p.out_row + n] = El<T>::from_float(fmaf(__uint_as_float(v[t]), p.row_scale[r], b));
+    if (warp == 1) tmem_alloc(&sh.tmem, 256);
+    tc_fence_before();
+    asm volatile("bar.sync 3, %0;" ::"n"(kOuterThreads - 32) : "memory");  // all but the loading warp
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    // accumulators: 128 columns of outputs, or of a small tile's 16 rows
+    const int buffers = small ? kBuffers : 2, buffer_columns = small ? kBox : kTileRows;
+    if (warp == 1) {
+      // -------------------------------------------------- products ----
+      const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, buffer_columns);
+      const int steps = p.rank16 / 16;
+      const uint64_t h0 = sdesc_k_sw128(smem_u32(h_smem)), b0 = sdesc_k_sw128(smem_u32(ring));
+      int slot = 0, turn = 0, buf = 0, buf_turn = 0;
+      bool ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_full, 0, p.wait_limit_ns));
+      for (int i = 0; ok && i < count; ++i) {
+        ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_empty[buf], buf_turn + 1, p.wait_limit_ns) &&
+                                         lora_wait(sh, &sh.full[slot], turn, p.wait_limit_ns));
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t bs = b0 + (slot * b_bytes >> 4);
+        const uint32_t d = tmem + buf * buffer_columns;
+        if (elected()) {
+          for (int k = 0; k < 2 * steps; ++k) {
+            // step k of h against step k of B, again from its first for the low parts
+            const int kb = k < steps ? k : k - steps;
+            const uint64_t hk = h0 + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = bs + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
+            if (small) umma_f16(d, bk, hk, idesc, k > 0);
+            else umma_f16(d, hk, bk, idesc, k > 0);
           }
+          umma_commit(&sh.empty[slot]);
+          umma_commit(&sh.acc_full[buf]);
         }
-      } else if (busy) {
-        const int width = min(p.outputs - n0, kTileRows);
-#pragma unroll 1
-        for (int c = 0; c < width; c += 32) {
-          uint4 b[2][2] = {};
-          if (valid && base) {
+        __syncwarp();
+        if (++slot == p.stages_out) slot = 0, ++turn;
+        if (++buf == buffers) buf = 0, ++buf_turn;
+      }
+      drain(sh, p.wait_limit_ns);
+    } else {
+      // -------------------------------------------------- epilogue ----
+      // two groups of four warps take every other tile of outputs
+      const int group = (warp - 2) >> 2, quarter = warp & 3, in = tid - 64 - group * 128;
+      const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+      const int row = quarter * 32 + lane;
+      if (small) {
+        // lanes are outputs, columns rows; the next outputs of base are read
+        // while these are on their way
+        const int rows = tile.rows;
+        griddep_wait();  // before row_scale is read
+        float scale[kBox], held[kBox];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (c + j * 8 < width) b[j >> 1][j & 1] = *reinterpret_cast<const uint4*>(base + at * p.base_row + n0 + c + j * 8);
-          }
-          uint32_t v[32];
-          tmem_ld32(acc + c, v);
+        for (int t = 0; t < kBox; ++t) scale[t] = t < rows ? p.row_scale[tile.row0 + t] : 0.0f;
+        auto read = [&](int i) {
+          const int n = (sub0 + i) * kTileRows + row;
+#pragma unroll
+          for (int t = 0; t < kBox; ++t)
+            held[t] = base && t < rows && i < count && n < p.outputs ? El<T>::to_float(base[(tile.row0 + t) * p.base_row + n]) : 0.0f;
+        };
+        read(group);
+        int buf = group, turn = 0;
+        for (int i = group; i < count; i += 2) {
+          if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[buf], turn, p.wait_limit_ns))) break;
+          tc_fence_after();
+          uint32_t v[kBox];
+          tmem_ld16(tmem + lanes + buf * kBox, v);
           tmem_ld_wait();
-          reg_fence<32>(v);
-          if (!valid) continue;
-          T* o = out + at * p.out_row + n0 + c;
-          if (c + 32 <= width) {
-            add_store16<T>(o, b[0], v, scale);
-            add_store16<T>(o + 16, b[1], v + 16, scale);
-          } else {
-            for (int j = 0; j < 4; ++j) {
-              if (c + j * 8 >= width) break;
+          reg_fence<kBox>(v);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
+          const int n = (sub0 + i) * kTileRows + row;
+          if (n < p.outputs) {
 #pragma unroll
-              for (int jj = 0; jj < 4; ++jj) {
-                if (jj != j) continue;
-                Chunk<T, 8> bc, oc;
-                const uint4 w = b[jj >> 1][jj & 1];
-                bc.w[0] = w.x, bc.w[1] = w.y, bc.w[2] = w.z, bc.w[3] = w.w;
+            for (int t = 0; t < kBox; ++t)
+              if (t < rows) out[(tile.row0 + t) * p.out_row + n] = El<T>::from_float(fmaf(__uint_as_float(v[t]), scale[t], held[t]));
+          }
+          read(i + 2);
+          buf += 2;
+          if (buf >= kBuffers) buf -= kBuffers, ++turn;
+        }
+      } else {
+        // A lane has a row: base comes to shared memory in boxes, the sum
+        // replaces it there, and goes out a row of 256 bytes to half a warp.
+        uint8_t* mine = staged + group * 2 * kRowTile;
+        const bool busy = quarter * 32 < tile.rows;
+        auto fetch = [&](int i) {
+          if (!base || i >= count || p.stall) return;
+          if (in == 0) mbar_arrive_expect_tx(&sh.base_full[group], boxes * kBox * 256u);
+          __syncwarp();
+          if (in < 2 * boxes)
+            tma_load_2d(mine + (in & 1) * kRowTile + (in >> 1) * kBox * 128, &map_base, &sh.base_full[group], (sub0 + i) * kTileRows + (in & 1) * 64,
+                        tile.row0 + (in >> 1) * kBox);
+        };
+        if (in < 32) fetch(group);
+        griddep_wait();  // before row_scale is read
+        const float scale = row < tile.rows ? p.row_scale[tile.row0 + row] : 0.0f;
+        uint32_t turn = 0;
+        bool ok = true;
+        for (int i = group; i < count; i += 2, ++turn) {
+          if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns) &&
+                                                 (!base || lora_wait(sh, &sh.base_full[group], turn, p.wait_limit_ns)))))
+            break;
+          tc_fence_after();
+          if (busy) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tmem_ld32(tmem + lanes + group * kTileRows + c * 32, v);
+              tmem_ld_wait();
+              reg_fence<32>(v);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const int piece = c * 4 + j;  // of 8 outputs; in the order that the boxes are swizzled in
+                uint8_t* at = mine + (piece >> 3) * kRowTile + row * 128 + ((piece ^ row) & 7) * 16;
+                Chunk<T, 8> sum;
+                if (base) sum.load(reinterpret_cast<const T*>(at));
+                else sum.zero();
                 float f[8];
-                bc.get(f);
+                sum.get(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[jj * 8 + e]), scale, f[e]);
-                oc.set(f);
-                oc.store(o + jj * 8);
+                for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[j * 8 + e]), scale, f[e]);
+                sum.set(f);
+                sum.store(reinterpret_cast<T*>(at));
               }
             }
           }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
+          group_sync(group);
+          const int n0 = (sub0 + i) * kTileRows, pieces = min(p.outputs - n0, kTileRows) / 8;
+          for (int r = in >> 4; r < tile.rows; r += 8) {
+            const int piece = in & 15;
+            if (piece < pieces) {
+              const uint4 v = *reinterpret_cast<const uint4*>(mine + (piece >> 3) * kRowTile + r * 128 + ((piece ^ r) & 7) * 16);
+              *reinterpret_cast<uint4*>(out + (tile.row0 + r) * p.out_row + n0 + piece * 8) = v;
+            }
+          }
+          fence_proxy_async_smem();  // the next box of base goes where these reads and writes were
+          group_sync(group);
+          if (in < 32) fetch(i + 2);
         }
+        // no copy in flight is left behind
+        if (!ok && base && !p.stall) mbar_wait(&sh.base_full[group], turn & 1, p.wait_limit_ns);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
     }
   }
   __syncwarp();
@@ -510,6 +562,7 @@ __global__ void __launch_bounds__(kOuterThreads, 2) lora_outer_kernel(const Lora
   __syncthreads();
   tc_fence_after();
   if (warp == 1) {
+    const uint32_t tmem = sh.tmem;
     tmem_relinquish();
     tmem_dealloc(tmem, 256);
   }
@@ -565,28 +618,32 @@ eg_status encode(const eg_lora_args& a, const void* base, uint64_t cols, uint64_
 template <typename T>
 eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int dev, cudaStream_t st) {
   static std::atomic<uint64_t> allowed_inner{0}, allowed_outer{0};
-  CUtensorMap map_x, map_a, map_h, map_b;
-  EG_TRY(encode(a, a.x, a.inputs, a.rows, a.rows > 1 ? a.x_row : a.inputs, kBox, &map_x));
+  CUtensorMap map_x, map_box, map_a, map_h, map_b, map_base;
+  const uint64_t x_row = a.rows > 1 ? a.x_row : a.inputs;
+  EG_TRY(encode(a, a.x, a.inputs, a.rows, x_row, kTileRows, &map_x));
+  EG_TRY(encode(a, a.x, a.inputs, a.rows, x_row, kBox, &map_box));
   // nothing is read of an empty bank, but a map has to have some place
   const uint64_t bank = std::max(a.adapters, 1);
   EG_TRY(encode(a, a.adapters ? a.a : a.x, a.inputs, bank * a.rank, a.inputs, a.rank, &map_a));
   EG_TRY(encode(a, p.h, 2 * p.rank16, a.rows, 2 * p.rank16, kBox, &map_h));
   EG_TRY(encode(a, a.adapters ? a.b : a.x, a.rank, bank * a.outputs, a.rank, kTileRows, &map_b));
 
-  // Two CTAs an SM in either kernel, where their shared memory lets them.
-  const int room = 113 * 1024 - static_cast<int>(sizeof(LoraShared));
-  const int stage = static_cast<int>(kRowTile) + (p.rank16 * 128 + 1023) / 1024 * 1024;
-  p.stages = std::min(8, room / stage);
-  const int inner_bytes = p.stages * stage + static_cast<int>(sizeof(LoraShared));
-  // CTAs for two an SM, at least four columns of 64 each
+  if (a.base) EG_TRY(encode(a, a.base, a.outputs, a.rows, a.rows > 1 ? a.base_row : a.outputs, kBox, &map_base));
+  else map_base = map_h;  // not used
+
+  // First kernel: two CTAs an SM, CTAs for those, at least four columns of 64
+  // each.
+  p.ring = (113 * 1024 - static_cast<int>(sizeof(LoraShared))) / 1024 * 1024;
+  const int inner_bytes = p.ring + static_cast<int>(sizeof(LoraShared));
   p.splits = 1;
   while (p.splits < 8 && tiles * p.splits * 2 <= sms * 2 && p.chunks >= p.splits * 8) p.splits *= 2;
+  // Second kernel: one CTA an SM, whose tiles of outputs and of base come far ahead.
   const int h_tile = (2 * p.rank16 + 63) / 64 * static_cast<int>(kRowTile), b_tile = (p.rank16 + 63) / 64 * static_cast<int>(kRowTile);
-  p.stages_out = std::min(8, (room - h_tile) / b_tile);
-  if (p.stages_out < 2) p.stages_out = std::min(8, (226 * 1024 - static_cast<int>(sizeof(LoraShared)) - h_tile) / b_tile);
-  const int outer_bytes = h_tile + p.stages_out * b_tile + static_cast<int>(sizeof(LoraShared));
+  const int staged = 4 * static_cast<int>(kRowTile);
+  p.stages_out = std::min(kStages, (226 * 1024 - static_cast<int>(sizeof(LoraShared)) - h_tile - staged) / b_tile);
+  const int outer_bytes = h_tile + staged + p.stages_out * b_tile + static_cast<int>(sizeof(LoraShared));
   p.subs = (a.outputs + kTileRows - 1) / kTileRows;
-  const int each = std::max(1, sms * 2 / tiles);  // CTAs that share a tile's outputs
+  const int each = std::max(1, sms / tiles);  // CTAs that share a tile's outputs
   p.subs_each = (p.subs + each - 1) / each;
   const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
 
@@ -604,14 +661,14 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   attr[0].val.clusterDim.x = p.splits, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, inner, p, map_x, map_a);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, inner, p, map_x, map_box, map_a);
   if (e != cudaSuccess) return host_cuda_fail(e, "launching lora's first product");
   cfg.gridDim = dim3(static_cast<unsigned>(tiles) * groups);
   cfg.blockDim = dim3(kOuterThreads);
   cfg.dynamicSmemBytes = outer_bytes;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  e = cudaLaunchKernelEx(&cfg, outer, p, map_h, map_b);
+  e = cudaLaunchKernelEx(&cfg, outer, p, map_h, map_b, map_base);
   return e == cudaSuccess ? EG_OK : host_cuda_fail(e, "launching lora's second product");
 }
 
