@@ -435,109 +435,115 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     }
   } else if (warp != 11) {
     // -------------------------------------------------------- issuers ----
-    // One for each softmax warpgroup, so that what one of them waits for and
-    // computes between its products passes behind the other's.  For a pair
-    // they issue in turn: else the two fall into step, with both warpgroups at
-    // their weights while the tensor cores wait and the other way round.  The
-    // whole warp walks, so that addresses stay in uniform registers; one
-    // elected lane issues; places in the ring are stepped, not divided out.
+    // The first gives both softmax warpgroups their products where they take
+    // turns on the key tiles.  For a pair each has a warpgroup of its own, so
+    // that what one of them waits for and computes between its products passes
+    // behind the other's; they issue in turn: else the two fall into step, with
+    // both warpgroups at their weights while the tensor cores wait and the
+    // other way round.  The whole warp walks, so that addresses stay in uniform
+    // registers; one elected lane issues; places in the ring are stepped, not
+    // divided out.
+    //
+    // Loads need not end in their order, and a wait for a turn of the ring
+    // passes at once while the turn before is not over.  So whoever waits for
+    // a place has waited for the one a ring's length before, or knows of
+    // products that came after it.
     constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
     constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
-    const uint32_t s = warp - 9, w = tmem + s * 128, o = w + 256;
+    const uint32_t mine = warp - 9;
     const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
     const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
-    uint32_t segment = 0, used = 0;  // segments, and tiles given to the warpgroup
-    uint32_t turns = 0;              // of a pair
-    auto my_turn = [&]() { return wait_all(&sh.turn[s], s ? turns : turns + 1); };
-    auto pass = [&]() {
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.turn[s ^ 1]);
-      ++turns;
-    };
-    uint32_t slot0 = 0, turn0 = 0;   // the segment's first place in the ring, and how often the ring was full
+    uint32_t segment = 0, used0 = 0, used1 = 0;  // segments, and tiles given to each warpgroup
+    uint32_t slot0 = 0, turn0 = 0;               // the segment's first place in the ring, and how often the ring was full
+    uint32_t turns = 0;                          // of a pair
     auto step = [&](uint32_t& slot, uint32_t& turn, uint32_t by) {
       slot += by;
       if (slot >= stages) slot -= stages, ++turn;
+    };
+    auto my_turn = [&]() { return wait_all(&sh.turn[mine], mine ? turns : turns + 1); };
+    auto pass = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.turn[mine ^ 1]);
+      ++turns;
     };
     bool ok = true;
     while (ok && walk.next(p)) {
       const uint32_t count = walk.count;
       const bool pair = walk.item.cost == 2;
-      // tiles begin at `first`, `stride` apart; the keys of tile i are 2 i - 1
-      // places on (those of tile 0 at none), its values 2 i + 2, the last
-      // tile's one less
-      const uint32_t first = pair ? 0 : s, stride = pair ? 1 : 2;
-      const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0);
       uint32_t slot_k = slot0, turn_k = turn0, slot_v = slot0, turn_v = turn0;
-      step(slot_k, turn_k, first);
-      step(slot_v, turn_v, 2 * first + (first + 1 < count ? 2 : 1));
+      step(slot_v, turn_v, count == 1 ? 1 : 2);
       if (!(ok = wait_all(&sh.q_full, segment))) break;
-      // O += P V of tile i
-      auto sums = [&](uint32_t i) {
+      // O += P V of a warpgroup's tile
+      auto sums = [&](uint32_t s, bool add) {
         const uint64_t v = v_desc + (slot_v * kTile >> 4);
-        umma_f16_ts(o, w, v, kIdescO, i > first ? 1 : 0);
+        const uint32_t w = tmem + s * 128, o = w + 256;
+        umma_f16_ts(o, w, v, kIdescO, add ? 1 : 0);
 #pragma unroll
         for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2048 >> 4), kIdescO);
         umma_commit(&sh.o_done[s]);
         umma_commit(&sh.empty[slot_v]);
-        if (!pair) umma_commit(&sh.empty[slot_v]);  // for the other issuer too
+        if (!pair) umma_commit(&sh.empty[slot_v]);  // for the other issuer
       };
-      // S = Q K^T of the next tile
-      auto scores = [&]() {
-        const uint64_t key = k_desc + (slot_k * kTile >> 4);
-        umma_f16(w, q, key, kIdescS, 0);
+      // S = Q K^T of its next one
+      auto scores = [&](uint32_t s) {
+        const uint64_t q = q_desc + (pair && s ? kTile >> 4 : 0), key = k_desc + (slot_k * kTile >> 4);
+        const uint32_t d = tmem + s * 128;
+        umma_f16(d, q, key, kIdescS, 0);
 #pragma unroll
         for (int k = 1; k < HD / 16; ++k) {
           const uint32_t at = ((k / 4) * kPart + (k % 4) * 32) >> 4;
-          umma_f16_add(w, q + at, key + at, kIdescS);
+          umma_f16_add(d, q + at, key + at, kIdescS);
         }
         umma_commit(&sh.s_full[s]);
         umma_commit(&sh.empty[slot_k]);
         if (!pair) umma_commit(&sh.empty[slot_k]);
       };
-      if (first < count) {
-        if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
-        if (pair && !(ok = my_turn())) break;
-        tc_fence_after();
-        if (elect_one()) scores();
-        if (pair) pass();
-        step(slot_k, turn_k, first == 0 ? 2 * stride - 1 : 2 * stride);
-      }
-      uint32_t i = first;
-      for (; i + stride < count; i += stride) {
-        // a pair's next keys are there when these values are; where keys and
-        // values come straight from memory the sums do not wait for the keys
-        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || (wait_all(&sh.full[slot_k], turn_k) && my_turn())) &&
-                   wait_all(&sh.p_ready[s], used)))
-          break;
-        if (pair) {
+      // the keys of tile i are 2 i - 1 places on (those of tile 0 at none),
+      // its values 2 i + 2, the last tile's one less
+      auto next_k = [&](uint32_t i) { step(slot_k, turn_k, i == 0 ? 1 : 2); };
+      auto next_v = [&](uint32_t i) { step(slot_v, turn_v, i + 2 == count ? 1 : 2); };
+      if (pair) {
+        for (uint32_t i = 0; i <= count; ++i) {
+          // sums of tile i - 1, scores of tile i, whose keys came before those values
+          if (!(ok = (i == count || wait_all(&sh.full[slot_k], turn_k)) && (i == 0 || wait_all(&sh.full[slot_v], turn_v)) && my_turn() &&
+                     (i == 0 || wait_all(&sh.p_ready[mine], (mine ? used1 : used0) + i - 1))))
+            break;
           tc_fence_after();
-          if (elect_one()) sums(i), scores();
+          if (elect_one()) {
+            if (i > 0) sums(mine, i > 1);
+            if (i < count) scores(mine);
+            if (i + 1 == count) umma_commit(&sh.q_empty);
+          }
           pass();
-        } else {
-          tc_fence_after();
-          if (elect_one()) sums(i);
-          __syncwarp();
-          if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
-          tc_fence_after();
-          if (elect_one()) scores();
+          next_k(i);
+          if (i > 0) next_v(i - 1);
         }
-        __syncwarp();
-        ++used;
-        step(slot_k, turn_k, 2 * stride);
-        step(slot_v, turn_v, i + stride + 1 < count ? 2 * stride : 2 * stride - 1);
+        used0 += count, used1 += count;
+      } else if (mine == 0) {
+        // scores run two tiles ahead of the sums
+        for (uint32_t j = 0; j < count + 2; ++j) {
+          const uint32_t s = j & 1;
+          if (j >= 2) {
+            if (!(ok = wait_all(&sh.full[slot_v], turn_v) && wait_all(&sh.p_ready[s], (s ? used1 : used0) + (j >> 1) - 1))) break;
+            tc_fence_after();
+            if (elect_one()) sums(s, j >= 4);
+            __syncwarp();
+            next_v(j - 2);
+          }
+          if (j < count) {
+            if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              scores(s);
+              if (j + 1 == count) umma_commit(&sh.q_empty), umma_commit(&sh.q_empty);
+            }
+            __syncwarp();
+            next_k(j);
+          }
+        }
       }
       if (!ok) break;
-      if (elect_one()) umma_commit(&sh.q_empty);
-      __syncwarp();
-      if (i < count) {
-        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && (!pair || my_turn()) && wait_all(&sh.p_ready[s], used))) break;
-        tc_fence_after();
-        if (elect_one()) sums(i);
-        if (pair) pass();
-        __syncwarp();
-        ++used;
-      }
+      if (!pair) used0 += (count + 1) / 2, used1 += count / 2;
       // the segment took 2 count places
       uint32_t places = 2 * count;
       turn0 += places / stages;

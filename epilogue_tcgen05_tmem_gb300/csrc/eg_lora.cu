@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kTileRows = 128;  // rows of a tile, and outputs of one of the second product
 constexpr int kBox = 16;        // rows of one TMA box of x and h; tiles of at most as many are small
-constexpr int kInnerThreads = 192, kOuterThreads = 320;
+constexpr int kInnerThreads = 224, kOuterThreads = 320;
 constexpr uint32_t kRowTile = 128u * 128u;  // bytes of 128 rows of 64 elements
 
 struct LoraParams {
@@ -76,7 +76,7 @@ constexpr int kBuffers = 8;  // accumulators of a small tile
 
 struct LoraShared {
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[kBuffers], acc_empty[kBuffers], base_full[2], h_full, done, drained;
+  uint64_t acc_full[kBuffers], acc_empty[kBuffers], base_full[2][2], h_full, done, drained;
   uint32_t tmem;
   int32_t abort;
   LoraTile tile;
@@ -171,16 +171,16 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int index = blockIdx.x / p.splits, part = blockIdx.x % p.splits;
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-    mbar_init(&sh.done, 1);
-    mbar_init(&sh.drained, 1);
+    for (int i = 0; i < kStages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 2);
+    mbar_init(&sh.done, 2);
+    mbar_init(&sh.drained, 2);
     fence_mbar_init();
     sh.abort = 0;
   }
   const LoraTile tile = find_tile<kInnerThreads>(p, sh, index);
   // the whole cluster has the same tile
   if (tile.rows == 0 || tile.adapter < 0) return;
-  if (warp == 1) tmem_alloc(&sh.tmem, 128);
+  if (warp == 1) tmem_alloc(&sh.tmem, 256);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -219,24 +219,35 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
     if (!p.stall)
       for (int j = max(i - stages, 0); j < i; ++j)
         if (!mbar_wait(&sh.full[j % stages], (j / stages) & 1, p.wait_limit_ns)) break;
-  } else if (warp == 1) {
+  } else if (warp <= 2) {
     // ---------------------------------------------------- products ----
-    const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, p.rank16);
+    // Two issuers take every other stage, each to an accumulator of its own:
+    // what one waits for passes behind the other's products.  Each waits for
+    // every stage and gives every one back: loads need not end in their order,
+    // and a wait for a turn of a stage whose last turn is not over would pass
+    // at once.
+    const int which = warp - 1;
+    const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, p.rank16), d = tmem + which * 128;
     const uint64_t x0 = sdesc_k_sw128(smem_u32(smem)), a0 = sdesc_k_sw128(smem_u32(smem + a_at));
     int slot = 0, turn = 0;
     for (int i = 0; i < count; ++i) {
       if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.full[slot], turn, p.wait_limit_ns))) break;
-      tc_fence_after();
-      const uint64_t x = x0 + (slot * stage_bytes >> 4), a = a0 + (slot * stage_bytes >> 4);
-      if (elected()) {
+      if ((i & 1) == which) {
+        tc_fence_after();
+        const uint64_t x = x0 + (slot * stage_bytes >> 4), a = a0 + (slot * stage_bytes >> 4);
+        if (elected()) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) umma_f16(tmem, x + k * 2, a + k * 2, idesc, i > 0 || k > 0);
-        umma_commit(&sh.empty[slot]);
-        if (i + 1 == count) umma_commit(&sh.done);
+          for (int k = 0; k < 4; ++k) umma_f16(d, x + k * 2, a + k * 2, idesc, i >= 2 || k > 0);
+          umma_commit(&sh.empty[slot]);
+        }
+      } else if (lane == 0) {
+        mbar_arrive(&sh.empty[slot]);
       }
       __syncwarp();
       if (++slot == stages) slot = 0, ++turn;
     }
+    if (elected()) umma_commit(&sh.done);
+    __syncwarp();
     drain(sh, p.wait_limit_ns);
   }
   __syncwarp();
@@ -244,7 +255,7 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   const int pitch = p.rank16 + 4;  // floats: rows start on different banks
   float* mine = reinterpret_cast<float*>(smem);
   bool ok = true;
-  if (warp >= 2) {
+  if (warp >= 3) {
     // the ring has been read when the products are done: it takes this CTA's part of h
     ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.done, 0, p.wait_limit_ns));
     tc_fence_after();
@@ -253,8 +264,17 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
       for (int c = 0; c < p.rank16; c += 16) {
         uint32_t v[16];
         tmem_ld16(tmem + (static_cast<uint32_t>(quarter) << 21) + c, v);
-        tmem_ld_wait();
-        reg_fence<16>(v);
+        if (count > 1) {
+          uint32_t w[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(quarter) << 21) + 128 + c, w);
+          tmem_ld_wait();
+          reg_fence<16>(v), reg_fence<16>(w);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(w[j]));
+        } else {
+          tmem_ld_wait();
+          reg_fence<16>(v);
+        }
         if (row < tile.rows)
 #pragma unroll
           for (int j = 0; j < 16; j += 4)
@@ -266,11 +286,11 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   __syncwarp();
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
-  if (warp >= 2 && ok) {
+  if (warp >= 3 && ok) {
     // rows in turn over the cluster's CTAs and their warps; a lane has four columns
     const float scale = p.scales ? __ldg(p.scales + tile.adapter) : 1.0f;
     const int col = lane * 4;
-    for (int row = part * 4 + warp - 2; row < tile.rows; row += p.splits * 4) {
+    for (int row = part * 4 + warp - 3; row < tile.rows; row += p.splits * 4) {
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       if (col < p.rank) {
         const uint32_t at = smem_u32(mine + row * pitch + col);
@@ -316,7 +336,7 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   tc_fence_after();
   if (warp == 1) {
     tmem_relinquish();
-    tmem_dealloc(tmem, 128);
+    tmem_dealloc(tmem, 256);
   }
 }
 
@@ -324,6 +344,31 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
 
 // Barrier of the four warps of an epilogue group.
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+
+// D = h B^T of STEPS steps of 16 for the high parts, and as many for the low
+// ones against the same B.  SMALL: D^T.
+template <bool SMALL, int STEPS>
+__device__ __forceinline__ void outer_products(uint32_t d, uint64_t h, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int k = 0; k < 2 * STEPS; ++k) {
+    const int kb = k % STEPS;
+    const uint64_t hk = h + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = b + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
+    umma_f16(d, SMALL ? bk : hk, SMALL ? hk : bk, idesc, k > 0);
+  }
+}
+template <bool SMALL>
+__device__ __forceinline__ void outer_products(int steps, uint32_t d, uint64_t h, uint64_t b, uint32_t idesc) {
+  switch (steps) {
+    case 1: return outer_products<SMALL, 1>(d, h, b, idesc);
+    case 2: return outer_products<SMALL, 2>(d, h, b, idesc);
+    case 3: return outer_products<SMALL, 3>(d, h, b, idesc);
+    case 4: return outer_products<SMALL, 4>(d, h, b, idesc);
+    case 5: return outer_products<SMALL, 5>(d, h, b, idesc);
+    case 6: return outer_products<SMALL, 6>(d, h, b, idesc);
+    case 7: return outer_products<SMALL, 7>(d, h, b, idesc);
+    default: return outer_products<SMALL, 8>(d, h, b, idesc);
+  }
+}
 
 template <typename T>
 __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const LoraParams p, const __grid_constant__ CUtensorMap map_h,
@@ -345,7 +390,7 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
   if (tid == 0) {
     for (int i = 0; i < p.stages_out; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
     for (int i = 0; i < kBuffers; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
-    mbar_init(&sh.base_full[0], 1), mbar_init(&sh.base_full[1], 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.base_full[i >> 1][i & 1], 1);
     mbar_init(&sh.h_full, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
@@ -433,13 +478,8 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
         const uint64_t bs = b0 + (slot * b_bytes >> 4);
         const uint32_t d = tmem + buf * buffer_columns;
         if (elected()) {
-          for (int k = 0; k < 2 * steps; ++k) {
-            // step k of h against step k of B, again from its first for the low parts
-            const int kb = k < steps ? k : k - steps;
-            const uint64_t hk = h0 + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = bs + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
-            if (small) umma_f16(d, bk, hk, idesc, k > 0);
-            else umma_f16(d, hk, bk, idesc, k > 0);
-          }
+          if (small) outer_products<true>(steps, d, h0, bs, idesc);
+          else outer_products<false>(steps, d, h0, bs, idesc);
           umma_commit(&sh.empty[slot]);
           umma_commit(&sh.acc_full[buf]);
         }
@@ -491,39 +531,42 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
           if (buf >= kBuffers) buf -= kBuffers, ++turn;
         }
       } else {
-        // A lane has a row: base comes to shared memory in boxes, the sum
-        // replaces it there, and goes out a row of 256 bytes to half a warp.
+        // A lane has a row.  Base comes to shared memory in boxes of 64
+        // outputs, the sum replaces it there, and goes out a row of 128 bytes
+        // to eight lanes; the next tile's box is on its way while the other
+        // half is worked on.
         uint8_t* mine = staged + group * 2 * kRowTile;
         const bool busy = quarter * 32 < tile.rows;
-        auto fetch = [&](int i) {
+        auto fetch = [&](int i, int half) {
           if (!base || i >= count || p.stall) return;
-          if (in == 0) mbar_arrive_expect_tx(&sh.base_full[group], boxes * kBox * 256u);
+          if (in == 0) mbar_arrive_expect_tx(&sh.base_full[group][half], boxes * kBox * 128u);
           __syncwarp();
-          if (in < 2 * boxes)
-            tma_load_2d(mine + (in & 1) * kRowTile + (in >> 1) * kBox * 128, &map_base, &sh.base_full[group], (sub0 + i) * kTileRows + (in & 1) * 64,
-                        tile.row0 + (in >> 1) * kBox);
+          if (in < boxes)
+            tma_load_2d(mine + half * kRowTile + in * kBox * 128, &map_base, &sh.base_full[group][half], (sub0 + i) * kTileRows + half * 64,
+                        tile.row0 + in * kBox);
         };
-        if (in < 32) fetch(group);
+        if (in < 32) fetch(group, 0), fetch(group, 1);
         griddep_wait();  // before row_scale is read
         const float scale = row < tile.rows ? p.row_scale[tile.row0 + row] : 0.0f;
         uint32_t turn = 0;
         bool ok = true;
         for (int i = group; i < count; i += 2, ++turn) {
-          if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns) &&
-                                                 (!base || lora_wait(sh, &sh.base_full[group], turn, p.wait_limit_ns)))))
-            break;
+          if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns)))) break;
           tc_fence_after();
-          if (busy) {
+          const int n0 = (sub0 + i) * kTileRows;
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tmem_ld32(tmem + lanes + group * kTileRows + c * 32, v);
+          for (int half = 0; half < 2; ++half) {
+            uint8_t* box = mine + half * kRowTile;
+            if (base && !(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.base_full[group][half], turn, p.wait_limit_ns)))) break;
+            if (busy) {
+              uint32_t v[64];
+              tmem_ld32p(tmem + lanes + group * kTileRows + half * 64, v);
+              tmem_ld32p(tmem + lanes + group * kTileRows + half * 64 + 32, v + 32);
               tmem_ld_wait();
-              reg_fence<32>(v);
+              reg_fence<64>(v);
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const int piece = c * 4 + j;  // of 8 outputs; in the order that the boxes are swizzled in
-                uint8_t* at = mine + (piece >> 3) * kRowTile + row * 128 + ((piece ^ row) & 7) * 16;
+              for (int j = 0; j < 8; ++j) {
+                uint8_t* at = box + row * 128 + ((j ^ row) & 7) * 16;  // pieces of 8 outputs, in the order that boxes are swizzled in
                 Chunk<T, 8> sum;
                 if (base) sum.load(reinterpret_cast<const T*>(at));
                 else sum.zero();
@@ -535,25 +578,29 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
                 sum.store(reinterpret_cast<T*>(at));
               }
             }
-          }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
-          group_sync(group);
-          const int n0 = (sub0 + i) * kTileRows, pieces = min(p.outputs - n0, kTileRows) / 8;
-          for (int r = in >> 4; r < tile.rows; r += 8) {
-            const int piece = in & 15;
-            if (piece < pieces) {
-              const uint4 v = *reinterpret_cast<const uint4*>(mine + (piece >> 3) * kRowTile + r * 128 + ((piece ^ r) & 7) * 16);
-              *reinterpret_cast<uint4*>(out + (tile.row0 + r) * p.out_row + n0 + piece * 8) = v;
+            if (half == 1) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
             }
+            group_sync(group);
+            const int piece = in & 7, col = n0 + half * 64 + piece * 8;
+            if (col < p.outputs) {
+#pragma unroll 4
+              for (int r = in >> 3; r < tile.rows; r += 16) {
+                const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + ((piece ^ r) & 7) * 16);
+                *reinterpret_cast<uint4*>(out + (tile.row0 + r) * p.out_row + col) = v;
+              }
+            }
+            fence_proxy_async_smem();  // the next box of base goes where these reads and writes were
+            group_sync(group);
+            if (in < 32) fetch(i + 2, half);
           }
-          fence_proxy_async_smem();  // the next box of base goes where these reads and writes were
-          group_sync(group);
-          if (in < 32) fetch(i + 2);
+          if (!ok) break;
         }
         // no copy in flight is left behind
-        if (!ok && base && !p.stall) mbar_wait(&sh.base_full[group], turn & 1, p.wait_limit_ns);
+        if (!ok && base && !p.stall)
+          for (int half = 0; half < 2; ++half) mbar_wait(&sh.base_full[group][half], turn & 1, p.wait_limit_ns);
       }
     }
   }
@@ -636,7 +683,7 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   p.ring = (113 * 1024 - static_cast<int>(sizeof(LoraShared))) / 1024 * 1024;
   const int inner_bytes = p.ring + static_cast<int>(sizeof(LoraShared));
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= sms * 2 && p.chunks >= p.splits * 8) p.splits *= 2;
+  while (p.splits < 8 && tiles * p.splits * 2 <= sms * 5 / 2 && p.chunks >= p.splits * 8) p.splits *= 2;
   // Second kernel: one CTA an SM, whose tiles of outputs and of base come far ahead.
   const int h_tile = (2 * p.rank16 + 63) / 64 * static_cast<int>(kRowTile), b_tile = (p.rank16 + 63) / 64 * static_cast<int>(kRowTile);
   const int staged = 4 * static_cast<int>(kRowTile);
