@@ -18,6 +18,32 @@ __device__ __forceinline__ pk_t pk_mul(pk_t a, pk_t b) { return make_float2(a.x 
 __device__ __forceinline__ pk_t pk_swap(pk_t v) { return make_float2(v.y, v.x); }
 __device__ __forceinline__ float pk_sum(pk_t v) { return v.x + v.y; }
 
+// Two float32 in one register pair, for instructions that take both.
+__device__ __forceinline__ uint64_t pack64(uint32_t lo, uint32_t hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "r"(lo), "r"(hi));
+  return v;
+}
+__device__ __forceinline__ uint64_t pack64(float lo, float hi) { return pack64(__float_as_uint(lo), __float_as_uint(hi)); }
+__device__ __forceinline__ void unpack64(uint64_t v, float* lo, float* hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*lo), "=f"(*hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 template <typename T>
 struct El;
 
@@ -106,6 +132,20 @@ struct Chunk {
         f[i] = pk(v.x, v.y);
       }
     }
+  }
+  __device__ __forceinline__ uint64_t pair(int i) const {
+    if constexpr (sizeof(T) == 4) {
+      return pack64(w[2 * i], w[2 * i + 1]);
+    } else {
+      const float2 v = El<T>::unpack2(w[i]);
+      return pack64(v.x, v.y);
+    }
+  }
+  __device__ __forceinline__ void set_pair(int i, uint64_t v) {
+    float a, b;
+    unpack64(v, &a, &b);
+    if constexpr (sizeof(T) == 4) w[2 * i] = __float_as_uint(a), w[2 * i + 1] = __float_as_uint(b);
+    else w[i] = El<T>::pack2(a, b);
   }
   __device__ __forceinline__ void set(const pk_t (&f)[CH / 2]) {
 #pragma unroll

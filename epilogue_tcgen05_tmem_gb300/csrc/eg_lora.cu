@@ -49,7 +49,6 @@ struct LoraParams {
   int32_t chunks;       // columns of x, in 64s
   int32_t splits;       // CTAs of a cluster that share them
   int32_t subs;         // tiles of 128 outputs
-  int32_t subs_each;    // those of one CTA of the second kernel
   int32_t ring;         // bytes of the first kernel's ring
   int32_t stages_out;   // of the second's
   const int32_t *seq_start, *adapter;
@@ -72,27 +71,35 @@ struct LoraTile {
 };
 
 constexpr int kStages = 12;  // of a ring, at most
-constexpr int kBuffers = 8;  // accumulators of a small tile
+constexpr int kAhead = 8;    // boxes of base that a group has for a small tile
 
 struct LoraShared {
   uint64_t full[kStages], empty[kStages];
-  uint64_t acc_full[kBuffers], acc_empty[kBuffers], base_full[2][2], h_full, done, drained;
+  uint64_t acc_full[2], acc_empty[2], h_full, h_empty, done, drained;
+  uint64_t base_half[2][2], base_ahead[2][kAhead];
   uint32_t tmem;
   int32_t abort;
   LoraTile tile;
-  int32_t warps[2][12];
+  int32_t b;
+  int64_t before;
+  union {
+    int32_t warps[2][12];
+    int64_t units[12];
+  };
 };
 
 // Bounded wait: false once any wait of the CTA has run past its limit.
 __device__ __forceinline__ bool lora_wait(LoraShared& sh, uint64_t* bar, uint32_t phase, uint64_t limit_ns) {
   if (mbar_try_wait(bar, phase & 1)) return true;
   volatile int32_t* abort = &sh.abort;
-  const uint64_t t0 = global_timer_ns();
+  uint64_t t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, phase & 1)) return true;
     if ((it & 63u) == 0) {
       if (*abort) return false;
-      if (global_timer_ns() - t0 > limit_ns) {
+      const uint64_t now = global_timer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > limit_ns) {
         *abort = 1;
         *reinterpret_cast<volatile int32_t*>(&g_lora_status) = 1;
         return false;
@@ -254,10 +261,9 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   // ------------------------------------------------------- the sum ----
   const int pitch = p.rank16 + 4;  // floats: rows start on different banks
   float* mine = reinterpret_cast<float*>(smem);
-  bool ok = true;
   if (warp >= 3) {
     // the ring has been read when the products are done: it takes this CTA's part of h
-    ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.done, 0, p.wait_limit_ns));
+    const bool ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.done, 0, p.wait_limit_ns));
     tc_fence_after();
     const int quarter = warp & 3, row = quarter * 32 + lane;
     if (ok && quarter * 32 < tile.rows) {
@@ -286,18 +292,20 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   __syncwarp();
   if (p.splits > 1) cluster_sync_all();
   else __syncthreads();
-  if (warp >= 3 && ok) {
-    // rows in turn over the cluster's CTAs and their warps; a lane has four columns
+  {
+    // Rows in turn over the cluster's CTAs and all their warps; a lane has four
+    // columns, so half a warp has a row of rank 64 or less.
     const float scale = p.scales ? __ldg(p.scales + tile.adapter) : 1.0f;
-    const int col = lane * 4;
-    for (int row = part * 4 + warp - 3; row < tile.rows; row += p.splits * 4) {
+    const int width = p.rank16 <= 64 ? 16 : 32, sub = lane / width, col = lane % width * 4, at_once = 32 / width;
+    for (int row0 = (part * (kInnerThreads / 32) + warp) * at_once; row0 < tile.rows; row0 += p.splits * (kInnerThreads / 32) * at_once) {
+      const int row = row0 + sub;
       float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      if (col < p.rank) {
-        const uint32_t at = smem_u32(mine + row * pitch + col);
+      if (col < p.rank && row < tile.rows) {
         if (p.splits == 1) {
           v = *reinterpret_cast<const float4*>(mine + row * pitch + col);
         } else {
           // all on their way before the first is added
+          const uint32_t at = smem_u32(mine + row * pitch + col);
           float4 w[8];
 #pragma unroll
           for (int c = 0; c < 8; ++c)
@@ -310,12 +318,14 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
       // bits of the largest magnitude: a NaN's are above infinity's
       uint32_t most = max(max(__float_as_uint(v.x) & 0x7FFFFFFFu, __float_as_uint(v.y) & 0x7FFFFFFFu),
                           max(__float_as_uint(v.z) & 0x7FFFFFFFu, __float_as_uint(v.w) & 0x7FFFFFFFu));
-      most = __reduce_max_sync(0xffffffffu, most);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1)
+        if (o < width) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
       // 2^e of the largest, at most 2^126 either way so that its inverse is normal too
       const int e = most >= 0x7F800000u || most == 0 ? 127 : min(max(static_cast<int>(most >> 23), 1), 253);
       const float down = __uint_as_float(static_cast<uint32_t>(254 - e) << 23), up = __uint_as_float(static_cast<uint32_t>(e) << 23);
-      if (lane == 0) p.row_scale[tile.row0 + row] = up * scale;
-      if (col < p.rank16) {
+      if (row < tile.rows && col < p.rank16) {
+        if (col == 0) p.row_scale[tile.row0 + row] = up * scale;
         const float y[4] = {v.x * down, v.y * down, v.z * down, v.w * down};
         float hi[4], lo[4];
 #pragma unroll
@@ -344,6 +354,102 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
 
 // Barrier of the four warps of an epilogue group.
 __device__ __forceinline__ void group_sync(int group) { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); }
+
+// Work of the second kernel: every tile has units for its tiles of outputs, one
+// each where it is small, else kBigCost; all units in a row are cut into equal
+// ranges, one a CTA.  A tile of outputs belongs to the CTA that has its first.
+constexpr int kBigCost = 3;
+
+// Consecutive tiles of outputs of one tile of rows, and the walk over a CTA's range.
+struct LoraWalk {
+  LoraTile tile;
+  int32_t sub0, count;
+  int32_t b, start, n, k;  // the sequence, its rows, the tile in it
+  int64_t begin, at, to;   // the tile's first unit, the range that is left
+
+  __device__ __forceinline__ void load(const LoraParams& p) {
+    start = min(max(__ldg(p.seq_start + b), 0), p.rows);
+    n = min(max(__ldg(p.seq_start + b + 1), start), p.rows) - start;
+  }
+  __device__ __forceinline__ static int64_t units_of(const LoraParams& p, int n) {
+    const int tiles = (n + kTileRows - 1) / kTileRows, rest = n - (tiles - 1) * kTileRows;
+    return n == 0 ? 0 : static_cast<int64_t>(p.subs) * ((tiles - 1) * kBigCost + (rest <= kBox ? 1 : kBigCost));
+  }
+  __device__ __forceinline__ void start_at(const LoraParams& p, int b_, int64_t before, int64_t from, int64_t to_) {
+    b = b_, at = from, to = to_;
+    load(p);
+    k = static_cast<int32_t>((from - before) / (static_cast<int64_t>(p.subs) * kBigCost));
+    begin = before + static_cast<int64_t>(k) * p.subs * kBigCost;
+  }
+  __device__ __forceinline__ bool next(const LoraParams& p) {
+    while (at < to) {
+      const int rows = min(n - k * kTileRows, kTileRows), cost = rows <= kBox ? 1 : kBigCost;
+      const int64_t end = begin + static_cast<int64_t>(p.subs) * cost, upto = min(end, to);
+      sub0 = static_cast<int32_t>((at - begin + cost - 1) / cost);
+      count = static_cast<int32_t>((upto - begin + cost - 1) / cost) - sub0;
+      if (count > 0) {
+        const int a = __ldg(p.adapter + b);
+        tile = LoraTile{start + k * kTileRows, rows, a < 0 || a >= p.adapters ? -1 : a};
+      }
+      at = upto;
+      if (upto == end) {
+        begin = end;
+        if (++k * kTileRows >= n && at < to) {
+          k = 0;
+          do ++b, load(p);
+          while (n == 0);
+        }
+      }
+      if (count > 0) return true;
+    }
+    return false;
+  }
+};
+
+// The range of this CTA, found by all its threads: false where it has none.
+template <int THREADS>
+__device__ __forceinline__ bool find_range(const LoraParams& p, LoraShared& sh, LoraWalk* walk) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto units_at = [&](int b) -> int64_t {
+    if (b >= p.sequences) return 0;
+    const int start = min(max(__ldg(p.seq_start + b), 0), p.rows);
+    return LoraWalk::units_of(p, min(max(__ldg(p.seq_start + b + 1), start), p.rows) - start);
+  };
+  // the total, then the place: each thread has consecutive sequences
+  const int each = (p.sequences + THREADS - 1) / THREADS;
+  int64_t mine = 0;
+  for (int i = 0; i < each; ++i) mine += units_at(tid * each + i);
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.units[warp] = upto;
+  __syncthreads();
+  int64_t total = 0, before = upto - mine;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) {
+    if (w < warp) before += sh.units[w];
+    total += sh.units[w];
+  }
+  const int64_t ctas = min(static_cast<int64_t>(gridDim.x), total);
+  if (blockIdx.x >= ctas) return false;
+  const int64_t from = total * blockIdx.x / ctas, to = total * (blockIdx.x + 1) / ctas;
+  if (before <= from && from < before + mine) {
+    for (int i = 0; i < each; ++i) {
+      const int64_t units = units_at(tid * each + i);
+      if (from < before + units) {
+        sh.b = tid * each + i, sh.before = before;
+        break;
+      }
+      before += units;
+    }
+  }
+  __syncthreads();
+  walk->start_at(p, sh.b, sh.before, from, to);
+  return true;
+}
 
 // D = h B^T of STEPS steps of 16 for the high parts, and as many for the low
 // ones against the same B.  SMALL: D^T.
@@ -380,80 +486,73 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
   const int h_parts = (2 * p.rank16 + 63) / 64;      // and of h
   const uint32_t b_bytes = parts * kRowTile;
   uint8_t* h_smem = smem;
-  uint8_t* staged = smem + h_parts * kRowTile;       // 128 rows of 128 outputs for each epilogue group
+  uint8_t* staged = smem + h_parts * kRowTile;       // base and results: two boxes of 128 rows of 64 outputs for each epilogue group
   uint8_t* ring = staged + 2 * 2 * kRowTile;
   LoraShared& sh = *reinterpret_cast<LoraShared*>(ring + p.stages_out * b_bytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
-  const int index = blockIdx.x / groups, sub0 = blockIdx.x % groups * p.subs_each;
-  const int count = min(p.subs - sub0, p.subs_each);
   if (tid == 0) {
     for (int i = 0; i < p.stages_out; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 1);
-    for (int i = 0; i < kBuffers; ++i) mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.base_full[i >> 1][i & 1], 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.acc_full[i], 1), mbar_init(&sh.acc_empty[i], 4);
+      mbar_init(&sh.base_half[i][0], 1), mbar_init(&sh.base_half[i][1], 1);
+      for (int j = 0; j < kAhead; ++j) mbar_init(&sh.base_ahead[i][j], 1);
+    }
     mbar_init(&sh.h_full, 1);
+    mbar_init(&sh.h_empty, 1);
     mbar_init(&sh.drained, 1);
     fence_mbar_init();
     sh.abort = 0;
   }
-  const LoraTile tile = find_tile<kOuterThreads>(p, sh, index);
-  if (tile.rows == 0) {
+  LoraWalk walk;
+  if (!find_range<kOuterThreads>(p, sh, &walk)) {
     griddep_wait();  // this kernel does not end before the first
     return;
   }
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
-  if (tile.adapter < 0) {
-    // nothing is added
-    griddep_wait();
-    if (base == out) return;
-    const int width = min(p.outputs - sub0 * kTileRows, count * kTileRows) / 8;
-    for (int i = tid; i < tile.rows * width; i += kOuterThreads) {
-      const int64_t row = tile.row0 + i / width;
-      const int col = sub0 * kTileRows + i % width * 8;
-      const uint4 v = base ? *reinterpret_cast<const uint4*>(base + row * p.base_row + col) : make_uint4(0, 0, 0, 0);
-      *reinterpret_cast<uint4*>(out + row * p.out_row + col) = v;
-    }
-    return;
-  }
-  const bool small = tile.rows <= kBox;
-  const int boxes = (tile.rows + kBox - 1) / kBox;
 
   if (warp == 0) {
     // ------------------------------------------------------- loads ----
-    // B does not wait for the first kernel, whose h follows the ring's first filling
-    const int ahead = min(count, p.stages_out);
-    int i = 0, slot = 0, turn = 0;
-    bool ok = true, h_sent = false;
-    for (; ok && i <= count; ++i) {
-      if (i == ahead) {
-        griddep_wait();
-        if (!p.stall) {
-          if (lane == 0) mbar_arrive_expect_tx(&sh.h_full, boxes * kBox * 128u * h_parts);
-          __syncwarp();
-          for (int j = lane; j < boxes * h_parts; j += 32) {
-            const int part = j / boxes, box = j % boxes;
-            tma_load_2d(h_smem + part * kRowTile + box * kBox * 128, &map_h, &sh.h_full, part * 64, tile.row0 + box * kBox);
+    int slot = 0, turn = 0, sent = 0;
+    uint32_t segment = 0;
+    bool ok = true;
+    while (ok && walk.next(p)) {
+      const LoraTile& tile = walk.tile;
+      if (tile.adapter < 0) continue;
+      // B does not wait for the first kernel, whose h follows the ring's filling
+      const int ahead = min(walk.count, p.stages_out), boxes = (tile.rows + kBox - 1) / kBox;
+      for (int i = 0; i <= walk.count; ++i) {
+        if (i == ahead) {
+          if (segment == 0) griddep_wait();
+          if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_empty, segment + 1, p.wait_limit_ns)))) break;
+          if (!p.stall) {
+            if (lane == 0) mbar_arrive_expect_tx(&sh.h_full, boxes * kBox * 128u * h_parts);
+            __syncwarp();
+            for (int j = lane; j < boxes * h_parts; j += 32) {
+              const int part = j / boxes, box = j % boxes;
+              tma_load_2d(h_smem + part * kRowTile + box * kBox * 128, &map_h, &sh.h_full, part * 64, tile.row0 + box * kBox);
+            }
           }
-          h_sent = true;
+          ++segment;
         }
+        if (i == walk.count) break;
+        if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], turn + 1, p.wait_limit_ns)))) break;
+        if (!p.stall) {
+          const int n0 = (walk.sub0 + i) * kTileRows;
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], b_bytes);
+          __syncwarp();
+          // rows past the adapter's last output are the next one's, or zeros: their products are not stored
+          if (lane < parts) tma_load_2d(ring + slot * b_bytes + lane * kRowTile, &map_b, &sh.full[slot], lane * 64, tile.adapter * p.outputs + n0);
+        }
+        ++sent;
+        if (++slot == p.stages_out) slot = 0, ++turn;
       }
-      if (i == count) break;
-      ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], turn + 1, p.wait_limit_ns));
-      if (ok && !p.stall) {
-        const int n0 = (sub0 + i) * kTileRows;
-        if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], b_bytes);
-        __syncwarp();
-        // rows past the adapter's last output are the next one's, or zeros: their products are not stored
-        if (lane < parts) tma_load_2d(ring + slot * b_bytes + lane * kRowTile, &map_b, &sh.full[slot], lane * 64, tile.adapter * p.outputs + n0);
-      }
-      if (++slot == p.stages_out) slot = 0, ++turn;
     }
     if (!p.stall) {
-      const int sent = ok ? count : i - 1;
+      // no copy in flight is left behind
       for (int j = max(sent - p.stages_out, 0); j < sent; ++j)
         if (!mbar_wait(&sh.full[j % p.stages_out], (j / p.stages_out) & 1, p.wait_limit_ns)) break;
-      if (h_sent) mbar_wait(&sh.h_full, 0, p.wait_limit_ns);
+      if (segment > 0) mbar_wait(&sh.h_full, (segment - 1) & 1, p.wait_limit_ns);
     }
   } else {
     if (warp == 1) tmem_alloc(&sh.tmem, 256);
@@ -461,147 +560,179 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
     asm volatile("bar.sync 3, %0;" ::"n"(kOuterThreads - 32) : "memory");  // all but the loading warp
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    // accumulators: 128 columns of outputs, or of a small tile's 16 rows
-    const int buffers = small ? kBuffers : 2, buffer_columns = small ? kBox : kTileRows;
     if (warp == 1) {
       // -------------------------------------------------- products ----
-      const uint32_t idesc = idesc_f32acc(kFmt, kFmt, 128, buffer_columns);
       const int steps = p.rank16 / 16;
       const uint64_t h0 = sdesc_k_sw128(smem_u32(h_smem)), b0 = sdesc_k_sw128(smem_u32(ring));
-      int slot = 0, turn = 0, buf = 0, buf_turn = 0;
-      bool ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_full, 0, p.wait_limit_ns));
-      for (int i = 0; ok && i < count; ++i) {
-        ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_empty[buf], buf_turn + 1, p.wait_limit_ns) &&
-                                         lora_wait(sh, &sh.full[slot], turn, p.wait_limit_ns));
-        if (!ok) break;
-        tc_fence_after();
-        const uint64_t bs = b0 + (slot * b_bytes >> 4);
-        const uint32_t d = tmem + buf * buffer_columns;
-        if (elected()) {
-          if (small) outer_products<true>(steps, d, h0, bs, idesc);
-          else outer_products<false>(steps, d, h0, bs, idesc);
-          umma_commit(&sh.empty[slot]);
-          umma_commit(&sh.acc_full[buf]);
+      int slot = 0, turn = 0;
+      uint32_t segment = 0, used = 0;  // tiles of outputs so far: the two accumulators in turn
+      bool ok = true;
+      while (ok && walk.next(p)) {
+        if (walk.tile.adapter < 0) continue;
+        const bool small = walk.tile.rows <= kBox;
+        const uint32_t idesc = small ? idesc_f32acc(kFmt, kFmt, 128, kBox) : idesc_f32acc(kFmt, kFmt, 128, kTileRows);
+        if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_full, segment, p.wait_limit_ns)))) break;
+        ++segment;
+        for (int i = 0; i < walk.count; ++i, ++used) {
+          const uint32_t buf = used & 1;
+          ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_empty[buf], (used >> 1) + 1, p.wait_limit_ns) &&
+                                           lora_wait(sh, &sh.full[slot], turn, p.wait_limit_ns));
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t bs = b0 + (slot * b_bytes >> 4);
+          if (elected()) {
+            if (small) outer_products<true>(steps, tmem + buf * kTileRows, h0, bs, idesc);
+            else outer_products<false>(steps, tmem + buf * kTileRows, h0, bs, idesc);
+            umma_commit(&sh.empty[slot]);
+            umma_commit(&sh.acc_full[buf]);
+            if (i + 1 == walk.count) umma_commit(&sh.h_empty);
+          }
+          __syncwarp();
+          if (++slot == p.stages_out) slot = 0, ++turn;
         }
-        __syncwarp();
-        if (++slot == p.stages_out) slot = 0, ++turn;
-        if (++buf == buffers) buf = 0, ++buf_turn;
       }
       drain(sh, p.wait_limit_ns);
     } else {
       // -------------------------------------------------- epilogue ----
       // two groups of four warps take every other tile of outputs
       const int group = (warp - 2) >> 2, quarter = warp & 3, in = tid - 64 - group * 128;
-      const uint32_t lanes = static_cast<uint32_t>(quarter) << 21;
+      const uint32_t acc = tmem + (static_cast<uint32_t>(quarter) << 21) + group * kTileRows;
       const int row = quarter * 32 + lane;
-      if (small) {
-        // lanes are outputs, columns rows; the next outputs of base are read
-        // while these are on their way
-        const int rows = tile.rows;
-        griddep_wait();  // before row_scale is read
-        float scale[kBox], held[kBox];
-#pragma unroll
-        for (int t = 0; t < kBox; ++t) scale[t] = t < rows ? p.row_scale[tile.row0 + t] : 0.0f;
-        auto read = [&](int i) {
-          const int n = (sub0 + i) * kTileRows + row;
-#pragma unroll
-          for (int t = 0; t < kBox; ++t)
-            held[t] = base && t < rows && i < count && n < p.outputs ? El<T>::to_float(base[(tile.row0 + t) * p.base_row + n]) : 0.0f;
-        };
-        read(group);
-        int buf = group, turn = 0;
-        for (int i = group; i < count; i += 2) {
-          if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[buf], turn, p.wait_limit_ns))) break;
-          tc_fence_after();
-          uint32_t v[kBox];
-          tmem_ld16(tmem + lanes + buf * kBox, v);
-          tmem_ld_wait();
-          reg_fence<kBox>(v);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.acc_empty[buf]);
-          const int n = (sub0 + i) * kTileRows + row;
-          if (n < p.outputs) {
-#pragma unroll
-            for (int t = 0; t < kBox; ++t)
-              if (t < rows) out[(tile.row0 + t) * p.out_row + n] = El<T>::from_float(fmaf(__uint_as_float(v[t]), scale[t], held[t]));
+      uint8_t* mine = staged + group * 2 * kRowTile;
+      uint32_t used = 0;                   // tiles of outputs before this segment
+      uint32_t turn = 0, halves = 0, aheads = 0;  // this group's tiles; those with base in halves, and in small boxes
+      bool ok = true, waited = false;
+      while (ok && walk.next(p)) {
+        const LoraTile tile = walk.tile;
+        const int count = walk.count, sub0 = walk.sub0;
+        if (tile.adapter < 0) {
+          // nothing is added
+          if (base == out) continue;
+          const int width = (min(p.outputs, (sub0 + count) * kTileRows) - sub0 * kTileRows) / 8;
+          for (int i = tid - 64; i < tile.rows * width; i += 256) {
+            const int64_t r = tile.row0 + i / width;
+            const int col = sub0 * kTileRows + i % width * 8;
+            const uint4 v = base ? *reinterpret_cast<const uint4*>(base + r * p.base_row + col) : make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(out + r * p.out_row + col) = v;
           }
-          read(i + 2);
-          buf += 2;
-          if (buf >= kBuffers) buf -= kBuffers, ++turn;
+          continue;
         }
-      } else {
-        // A lane has a row.  Base comes to shared memory in boxes of 64
-        // outputs, the sum replaces it there, and goes out a row of 128 bytes
-        // to eight lanes; the next tile's box is on its way while the other
-        // half is worked on.
-        uint8_t* mine = staged + group * 2 * kRowTile;
-        const bool busy = quarter * 32 < tile.rows;
-        auto fetch = [&](int i, int half) {
-          if (!base || i >= count || p.stall) return;
-          if (in == 0) mbar_arrive_expect_tx(&sh.base_full[group][half], boxes * kBox * 128u);
-          __syncwarp();
-          if (in < boxes)
-            tma_load_2d(mine + half * kRowTile + in * kBox * 128, &map_base, &sh.base_full[group][half], (sub0 + i) * kTileRows + half * 64,
-                        tile.row0 + in * kBox);
-        };
-        if (in < 32) fetch(group, 0), fetch(group, 1);
-        griddep_wait();  // before row_scale is read
-        const float scale = row < tile.rows ? p.row_scale[tile.row0 + row] : 0.0f;
-        uint32_t turn = 0;
-        bool ok = true;
-        for (int i = group; i < count; i += 2, ++turn) {
-          if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns)))) break;
-          tc_fence_after();
-          const int n0 = (sub0 + i) * kTileRows;
+        const int first = (used ^ group) & 1, boxes = (tile.rows + kBox - 1) / kBox;
+        used += count;
+        if (tile.rows <= kBox) {
+          // Lanes are outputs, columns rows.  Base comes kAhead tiles ahead, in
+          // two boxes of 64 outputs each.
+          auto fetch = [&](int i, uint32_t number) {
+            if (!base || i >= count || p.stall) return;
+            uint8_t* box = mine + number % kAhead * (2 * kBox * 128);
+            uint64_t* bar = &sh.base_ahead[group][number % kAhead];
+            if (lane == 0) mbar_arrive_expect_tx(bar, 2 * kBox * 128u);
+            __syncwarp();
+            if (lane < 2) tma_load_2d(box + lane * kBox * 128, &map_base, bar, (sub0 + i) * kTileRows + lane * 64, tile.row0);
+          };
+          if (in < 32)
+            for (int j = 0; j < kAhead; ++j) fetch(first + 2 * j, aheads + j);
+          if (!waited) griddep_wait(), waited = true;  // before row_scale is read
+          int i = first;
+          for (; i < count; i += 2, ++turn, ++aheads) {
+            if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns) &&
+                                                   (!base || lora_wait(sh, &sh.base_ahead[group][aheads % kAhead], aheads / kAhead, p.wait_limit_ns)))))
+              break;
+            tc_fence_after();
+            uint32_t v[kBox];
+            tmem_ld16(acc, v);
+            tmem_ld_wait();
+            reg_fence<kBox>(v);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
+            const int n = (sub0 + i) * kTileRows + row;
+            const uint8_t* box = mine + aheads % kAhead * (2 * kBox * 128) + (row >> 6) * kBox * 128;
+#pragma unroll
+            for (int t = 0; t < kBox; ++t) {
+              if (t >= tile.rows) break;
+              const int64_t r = tile.row0 + t;
+              const float b = base ? El<T>::to_float(*reinterpret_cast<const T*>(box + t * 128 + (((row >> 3) ^ t) & 7) * 16 + (row & 7) * 2)) : 0.0f;
+              if (n < p.outputs) out[r * p.out_row + n] = El<T>::from_float(fmaf(__uint_as_float(v[t]), p.row_scale[r], b));
+            }
+            group_sync(group);  // the box has been read
+            if (in < 32) fetch(i + 2 * kAhead, aheads + kAhead);
+          }
+          // no copy in flight is left behind
+          if (!ok && base && !p.stall)
+            for (uint32_t j = aheads; i < count && j < aheads + kAhead; ++j, i += 2)
+              mbar_wait(&sh.base_ahead[group][j % kAhead], (j / kAhead) & 1, p.wait_limit_ns);
+        } else {
+          // A lane has a row.  Base comes to shared memory in boxes of 64
+          // outputs, the sum replaces it there, and goes out a row of 128 bytes
+          // to eight lanes; the next tile's box is on its way while the other
+          // half is worked on.
+          const bool busy = quarter * 32 < tile.rows;
+          auto fetch = [&](int i, int half) {
+            if (!base || i >= count || p.stall) return;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.base_half[group][half], boxes * kBox * 128u);
+            __syncwarp();
+            if (lane < boxes)
+              tma_load_2d(mine + half * kRowTile + lane * kBox * 128, &map_base, &sh.base_half[group][half], (sub0 + i) * kTileRows + half * 64,
+                          tile.row0 + lane * kBox);
+          };
+          if (in < 32) fetch(first, 0), fetch(first, 1);
+          if (!waited) griddep_wait(), waited = true;
+          const float scale = row < tile.rows ? p.row_scale[tile.row0 + row] : 0.0f;
+          for (int i = first; i < count; i += 2, ++turn, ++halves) {
+            if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.acc_full[group], turn, p.wait_limit_ns)))) break;
+            tc_fence_after();
+            const int n0 = (sub0 + i) * kTileRows;
 #pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            uint8_t* box = mine + half * kRowTile;
-            if (base && !(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.base_full[group][half], turn, p.wait_limit_ns)))) break;
-            if (busy) {
-              uint32_t v[64];
-              tmem_ld32p(tmem + lanes + group * kTileRows + half * 64, v);
-              tmem_ld32p(tmem + lanes + group * kTileRows + half * 64 + 32, v + 32);
-              tmem_ld_wait();
-              reg_fence<64>(v);
+            for (int half = 0; half < 2; ++half) {
+              uint8_t* box = mine + half * kRowTile;
+              if (base && !(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.base_half[group][half], halves, p.wait_limit_ns)))) break;
+              if (busy) {
+                uint32_t v[64];
+                tmem_ld32p(acc + half * 64, v);
+                tmem_ld32p(acc + half * 64 + 32, v + 32);
+                tmem_ld_wait();
+                reg_fence<64>(v);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                uint8_t* at = box + row * 128 + ((j ^ row) & 7) * 16;  // pieces of 8 outputs, in the order that boxes are swizzled in
-                Chunk<T, 8> sum;
-                if (base) sum.load(reinterpret_cast<const T*>(at));
-                else sum.zero();
-                float f[8];
-                sum.get(f);
+                for (int j = 0; j < 8; ++j) {
+                  uint8_t* at = box + row * 128 + ((j ^ row) & 7) * 16;  // pieces of 8 outputs, in the order that boxes are swizzled in
+                  Chunk<T, 8> sum;
+                  if (base) sum.load(reinterpret_cast<const T*>(at));
+                  else sum.zero();
+                  float f[8];
+                  sum.get(f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[j * 8 + e]), scale, f[e]);
-                sum.set(f);
-                sum.store(reinterpret_cast<T*>(at));
+                  for (int e = 0; e < 8; ++e) f[e] = fmaf(__uint_as_float(v[j * 8 + e]), scale, f[e]);
+                  sum.set(f);
+                  sum.store(reinterpret_cast<T*>(at));
+                }
               }
-            }
-            if (half == 1) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
-            }
-            group_sync(group);
-            const int piece = in & 7, col = n0 + half * 64 + piece * 8;
-            if (col < p.outputs) {
+              if (half == 1) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
+              }
+              group_sync(group);
+              const int piece = in & 7, col = n0 + half * 64 + piece * 8;
+              if (col < p.outputs) {
 #pragma unroll 4
-              for (int r = in >> 3; r < tile.rows; r += 16) {
-                const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + ((piece ^ r) & 7) * 16);
-                *reinterpret_cast<uint4*>(out + (tile.row0 + r) * p.out_row + col) = v;
+                for (int r = in >> 3; r < tile.rows; r += 16) {
+                  const uint4 v = *reinterpret_cast<const uint4*>(box + r * 128 + ((piece ^ r) & 7) * 16);
+                  *reinterpret_cast<uint4*>(out + (tile.row0 + r) * p.out_row + col) = v;
+                }
               }
+              fence_proxy_async_smem();  // the next box of base goes where these reads and writes were
+              group_sync(group);
+              if (in < 32) fetch(i + 2, half);
             }
-            fence_proxy_async_smem();  // the next box of base goes where these reads and writes were
-            group_sync(group);
-            if (in < 32) fetch(i + 2, half);
+            if (!ok) break;
           }
-          if (!ok) break;
+          // no copy in flight is left behind
+          if (!ok && base && !p.stall)
+            for (int half = 0; half < 2; ++half) mbar_wait(&sh.base_half[group][half], halves & 1, p.wait_limit_ns);
         }
-        // no copy in flight is left behind
-        if (!ok && base && !p.stall)
-          for (int half = 0; half < 2; ++half) mbar_wait(&sh.base_full[group][half], turn & 1, p.wait_limit_ns);
       }
+      if (!waited) griddep_wait();  // this kernel does not end before the first
     }
   }
   __syncwarp();
@@ -667,8 +798,9 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   static std::atomic<uint64_t> allowed_inner{0}, allowed_outer{0};
   CUtensorMap map_x, map_box, map_a, map_h, map_b, map_base;
   const uint64_t x_row = a.rows > 1 ? a.x_row : a.inputs;
-  EG_TRY(encode(a, a.x, a.inputs, a.rows, x_row, kTileRows, &map_x));
   EG_TRY(encode(a, a.x, a.inputs, a.rows, x_row, kBox, &map_box));
+  if (a.rows > 4 * kBox) EG_TRY(encode(a, a.x, a.inputs, a.rows, x_row, kTileRows, &map_x));
+  else map_x = map_box;  // not used
   // nothing is read of an empty bank, but a map has to have some place
   const uint64_t bank = std::max(a.adapters, 1);
   EG_TRY(encode(a, a.adapters ? a.a : a.x, a.inputs, bank * a.rank, a.inputs, a.rank, &map_a));
@@ -683,16 +815,13 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   p.ring = (113 * 1024 - static_cast<int>(sizeof(LoraShared))) / 1024 * 1024;
   const int inner_bytes = p.ring + static_cast<int>(sizeof(LoraShared));
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= sms * 5 / 2 && p.chunks >= p.splits * 8) p.splits *= 2;
+  while (p.splits < 8 && tiles * p.splits * 2 <= sms * 2 && p.chunks >= p.splits * 8) p.splits *= 2;
   // Second kernel: one CTA an SM, whose tiles of outputs and of base come far ahead.
   const int h_tile = (2 * p.rank16 + 63) / 64 * static_cast<int>(kRowTile), b_tile = (p.rank16 + 63) / 64 * static_cast<int>(kRowTile);
   const int staged = 4 * static_cast<int>(kRowTile);
   p.stages_out = std::min(kStages, (226 * 1024 - static_cast<int>(sizeof(LoraShared)) - h_tile - staged) / b_tile);
   const int outer_bytes = h_tile + staged + p.stages_out * b_tile + static_cast<int>(sizeof(LoraShared));
   p.subs = (a.outputs + kTileRows - 1) / kTileRows;
-  const int each = std::max(1, sms / tiles);  // CTAs that share a tile's outputs
-  p.subs_each = (p.subs + each - 1) / each;
-  const int groups = (p.subs + p.subs_each - 1) / p.subs_each;
 
   auto inner = lora_inner_kernel<T>;
   auto outer = lora_outer_kernel<T>;
@@ -710,7 +839,7 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, inner, p, map_x, map_box, map_a);
   if (e != cudaSuccess) return host_cuda_fail(e, "launching lora's first product");
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles) * groups);
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>(sms, static_cast<int64_t>(tiles) * p.subs)));
   cfg.blockDim = dim3(kOuterThreads);
   cfg.dynamicSmemBytes = outer_bytes;
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -51,15 +51,29 @@ __device__ __forceinline__ float scale_of(uint32_t most, float top) {
   return s == 0.0f ? 1.0f : s;
 }
 
-template <bool E4M3>
-__device__ __forceinline__ uint32_t code_of(float h, float scale) {
-  const float t = __fdiv_rn(h, scale);  // IEEE division, as the definition states
-  if constexpr (E4M3) {
-    return __nv_cvt_float_to_fp8(t, __NV_SATFINITE, __NV_E4M3);
+// What h is multiplied by for its code; 0 where that would overflow and h is
+// divided by the scale instead.
+__device__ __forceinline__ float inverse_of(float scale) { return scale < 0x1p-126f ? 0.0f : __frcp_rn(scale); }
+
+// The codes of two values, the first in the low byte.
+__device__ __forceinline__ uint32_t codes_of(uint64_t h, float scale, float inverse, bool int8) {
+  float a, b;
+  if (inverse != 0.0f) {
+    unpack64(mul2(h, pack64(inverse, inverse)), &a, &b);
   } else {
-    const int r = __float2int_rn(t);
-    return static_cast<uint8_t>(static_cast<int8_t>(r > 127 ? 127 : r < -127 ? -127 : r));
+    unpack64(h, &a, &b);
+    a = __fdiv_rn(a, scale), b = __fdiv_rn(b, scale);
   }
+  if (!int8) return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const int x = min(max(__float2int_rn(a), -127), 127), y = min(max(__float2int_rn(b), -127), 127);
+  return static_cast<uint32_t>(x & 0xFF) | static_cast<uint32_t>(y & 0xFF) << 8;
+}
+
+// The larger of a and |b|, NaN where either is.
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+  return y;
 }
 
 // Sum, or largest bits, over the threads of a row: a warp, or the whole CTA.
@@ -100,75 +114,80 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
   const int vectors = p.width / CH;
   const T* x = static_cast<const T*>(p.x) + row * p.x_row;
-  Chunk<T, CH> c[V];
+  const T* w = static_cast<const T*>(p.weight);
+  Chunk<T, CH> c[V], wc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
     if (v < vectors) c[i].load(x + v * CH);
     else c[i].zero();
   }
+  uint64_t s[V][CH / 2];  // the sum's pairs, then the normed ones
   if (p.residual) {
     const T* r = static_cast<const T*>(p.residual) + row * p.residual_row;
-    T* s = static_cast<T*>(p.sum) + row * p.sum_row;
+    T* sum = static_cast<T*>(p.sum) + row * p.sum_row;
     Chunk<T, CH> d[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * step + tid;
       if (v < vectors) d[i].load(r + v * CH);
+      else d[i].zero();
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * step + tid;
-      if (v >= vectors) continue;
-      float a[CH], b[CH];
-      c[i].get(a), d[i].get(b);
 #pragma unroll
-      for (int e = 0; e < CH; ++e) a[e] += b[e];
-      c[i].set(a);
-      c[i].store(s + v * CH);
+      for (int j = 0; j < CH / 2; ++j) c[i].set_pair(j, add2(c[i].pair(j), d[i].pair(j)));
+      if (v < vectors) c[i].store(sum + v * CH);
     }
   }
-  float square = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    float a[CH];
-    c[i].get(a);
-#pragma unroll
-    for (int e = 0; e < CH; ++e) square = fmaf(a[e], a[e], square);
-  }
-  square = row_sum<WARP>(square, red_sum);
-  const float r = rsqrtf(fmaf(square, p.inv_width, p.eps));
-  const T* w = static_cast<const T*>(p.weight);
-  // h of one vector
-  auto normed = [&](int i, int v, float (&h)[CH]) {
-    Chunk<T, CH> wc;
-    wc.load(w + v * CH);
-    float f[CH];
-    wc.get(f), c[i].get(h);
-#pragma unroll
-    for (int e = 0; e < CH; ++e) h[e] = h[e] * r * f[e];
-  };
-  uint32_t most[V], top = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
-    most[i] = 0;
-    if (v >= vectors) continue;
-    float h[CH];
-    normed(i, v, h);
-    if (p.out) {
+    if (v < vectors) wc[i].load(w + v * CH);
+    else wc[i].zero();
+  }
+  uint64_t square2 = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < CH / 2; ++j) {
+      s[i][j] = c[i].pair(j);
+      square2 = fma2(s[i][j], s[i][j], square2);
+    }
+  float square, other;
+  unpack64(square2, &square, &other);
+  square = row_sum<WARP>(square + other, red_sum);
+  const float r = rsqrtf(fmaf(square, p.inv_width, p.eps));
+  const uint64_t r2 = pack64(r, r);
+  float most[V], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int v = i * step + tid;
+    most[i] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < CH / 2; ++j) {
+      s[i][j] = mul2(mul2(s[i][j], r2), wc[i].pair(j));
+      float a, b;
+      unpack64(s[i][j], &a, &b);
+      most[i] = max_abs(max_abs(most[i], a), b);
+    }
+    // a row without a vector here has zeros, which may be no numbers after the product
+    if (v >= vectors) most[i] = 0.0f;
+    top = max_abs(top, most[i]);
+    if (p.out && v < vectors) {
       Chunk<T, CH> o;
-      o.set(h);
+#pragma unroll
+      for (int j = 0; j < CH / 2; ++j) o.set_pair(j, s[i][j]);
       o.store(static_cast<T*>(p.out) + row * p.out_row + v * CH);
     }
-#pragma unroll
-    for (int e = 0; e < CH; ++e) most[i] = max(most[i], __float_as_uint(h[e]) & 0x7FFFFFFFu);
-    top = max(top, most[i]);
   }
   if (p.quant == EG_NORM_PLAIN) return;
-  float scale = 1.0f;
+  const bool int8 = p.quant == EG_NORM_INT8;
+  float scale = 1.0f, inverse = 1.0f;
   if (p.quant != EG_NORM_E4M3_BLOCK) {
-    scale = scale_of(row_max<WARP>(top, red_max), p.quant == EG_NORM_INT8 ? 127.0f : 448.0f);
+    scale = scale_of(row_max<WARP>(__float_as_uint(top), red_max), int8 ? 127.0f : 448.0f);
+    inverse = inverse_of(scale);
     if (tid == 0) p.scales[row] = scale;
   }
   uint8_t* codes = p.codes + row * p.codes_row;
@@ -178,17 +197,15 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
     if (p.quant == EG_NORM_E4M3_BLOCK) {
       // a block is 128 / CH neighbouring lanes; the lanes past the row's end hold zeros of no block
 #pragma unroll
-      for (int o = 64 / CH; o > 0; o >>= 1) most[i] = max(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
-      scale = scale_of(most[i], 448.0f);
+      for (int o = 64 / CH; o > 0; o >>= 1) most[i] = max_abs(most[i], __shfl_xor_sync(0xffffffffu, most[i], o));
+      scale = scale_of(__float_as_uint(most[i]), 448.0f);
+      inverse = inverse_of(scale);
       if (v < vectors && v % (128 / CH) == 0) p.scales[static_cast<int64_t>(row) * (p.width >> 7) + v / (128 / CH)] = scale;
     }
     if (v >= vectors) continue;
-    float h[CH];
-    normed(i, v, h);
-    uint32_t word[2] = {0u, 0u};
+    uint32_t word[CH / 4];
 #pragma unroll
-    for (int e = 0; e < CH; ++e)
-      word[e >> 2] |= (p.quant == EG_NORM_INT8 ? code_of<false>(h[e], scale) : code_of<true>(h[e], scale)) << (8 * (e & 3));
+    for (int j = 0; j < CH / 4; ++j) word[j] = codes_of(s[i][2 * j], scale, inverse, int8) | codes_of(s[i][2 * j + 1], scale, inverse, int8) << 16;
     if constexpr (CH == 8) *reinterpret_cast<uint2*>(codes + v * CH) = make_uint2(word[0], word[1]);
     else *reinterpret_cast<uint32_t*>(codes + v * CH) = word[0];
   }
@@ -237,18 +254,19 @@ __global__ void __launch_bounds__(kAnyThreads) norm_any_kernel(const NormParams 
         h[e] = normed(b * 128 + e * 32 + (tid & 31));
         most = max(most, __float_as_uint(h[e]) & 0x7FFFFFFFu);
       }
-      const float scale = scale_of(__reduce_max_sync(0xffffffffu, most), 448.0f);
+      const float scale = scale_of(__reduce_max_sync(0xffffffffu, most), 448.0f), inverse = inverse_of(scale);
       if ((tid & 31) == 0) p.scales[static_cast<int64_t>(row) * (p.width >> 7) + b] = scale;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) codes[b * 128 + e * 32 + (tid & 31)] = static_cast<uint8_t>(code_of<true>(h[e], scale));
+      for (int e = 0; e < 4; ++e) codes[b * 128 + e * 32 + (tid & 31)] = static_cast<uint8_t>(codes_of(pack64(h[e], 0.0f), scale, inverse, false));
     }
   } else if (p.quant != EG_NORM_PLAIN) {
     uint32_t most = 0;
     for (int k = tid; k < p.width; k += kAnyThreads) most = max(most, __float_as_uint(normed(k)) & 0x7FFFFFFFu);
     const float scale = scale_of(row_max<false>(most, red_max), p.quant == EG_NORM_INT8 ? 127.0f : 448.0f);
     if (tid == 0) p.scales[row] = scale;
+    const float inverse = inverse_of(scale);
     for (int k = tid; k < p.width; k += kAnyThreads)
-      codes[k] = static_cast<uint8_t>(p.quant == EG_NORM_INT8 ? code_of<false>(normed(k), scale) : code_of<true>(normed(k), scale));
+      codes[k] = static_cast<uint8_t>(codes_of(pack64(normed(k), 0.0f), scale, inverse, p.quant == EG_NORM_INT8));
   }
   if (p.out) {
     if (p.quant == EG_NORM_E4M3_BLOCK) __syncthreads();  // out may be x: every block has been read
@@ -272,59 +290,71 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* red) {
 }
 
 template <typename T, int CH, int V>
-__global__ void __launch_bounds__(1024) norm_backward_kernel(const NormGradParams p) {
+__global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_kernel(const NormGradParams p) {
   griddep_launch_dependents();
   __shared__ float2 red[2][32];
   const int tid = threadIdx.x, step = blockDim.x, vectors = p.width / CH;
-  float dw[V][CH];
+  uint64_t dw[V][CH / 2];
+  Chunk<T, CH> d[V], z[V], add[V], w[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i)
+  for (int i = 0; i < V; ++i) {
 #pragma unroll
-    for (int e = 0; e < CH; ++e) dw[i][e] = 0.0f;
+    for (int j = 0; j < CH / 2; ++j) dw[i][j] = 0;
+    if (i * step + tid < vectors) w[i].load(static_cast<const T*>(p.weight) + (i * step + tid) * CH);
+    else w[i].zero();
+  }
+  auto load = [&](int64_t row, Chunk<T, CH> (&d_)[V], Chunk<T, CH> (&z_)[V], Chunk<T, CH> (&add_)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int v = i * step + tid;
+      d_[i].zero(), z_[i].zero(), add_[i].zero();
+      if (v >= vectors) continue;
+      d_[i].load(static_cast<const T*>(p.d_out) + row * p.d_out_row + v * CH);
+      z_[i].load(static_cast<const T*>(p.sum) + row * p.sum_row + v * CH);
+      if (p.d_sum) add_[i].load(static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH);
+    }
+  };
+  load(blockIdx.x, d, z, add);
   int turn = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    const T* d_row = static_cast<const T*>(p.d_out) + row * p.d_out_row;
-    const T* z_row = static_cast<const T*>(p.sum) + row * p.sum_row;
-    Chunk<T, CH> d[V], z[V], add[V];
+    // the next row is on its way while this one's sums go round
+    constexpr bool kNext = V < 4;
+    Chunk<T, CH> d_[V], z_[V], add_[V];
+    if (kNext && row + gridDim.x < p.rows) load(row + gridDim.x, d_, z_, add_);
+    uint64_t square2 = 0, gz2 = 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = i * step + tid;
-      if (v < vectors) d[i].load(d_row + v * CH), z[i].load(z_row + v * CH);
-      else d[i].zero(), z[i].zero();
-      add[i].zero();
-      if (p.d_sum && v < vectors) add[i].load(static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH);
-    }
-    float2 both = make_float2(0.0f, 0.0f);  // sums of z^2 and of g z
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int v = i * step + tid;
-      if (v >= vectors) continue;
-      Chunk<T, CH> wc;
-      wc.load(static_cast<const T*>(p.weight) + v * CH);
-      float a[CH], b[CH], w[CH];
-      d[i].get(a), z[i].get(b), wc.get(w);
-#pragma unroll
-      for (int e = 0; e < CH; ++e) both.x = fmaf(b[e], b[e], both.x), both.y = fmaf(a[e] * w[e], b[e], both.y);
-    }
+      for (int j = 0; j < CH / 2; ++j) {
+        const uint64_t b = z[i].pair(j);
+        square2 = fma2(b, b, square2);
+        gz2 = fma2(mul2(d[i].pair(j), w[i].pair(j)), b, gz2);
+      }
+    float2 both, other;  // sums of z^2 and of g z
+    unpack64(square2, &both.x, &other.x), unpack64(gz2, &both.y, &other.y);
+    both.x += other.x, both.y += other.y;
     both = cta_sum2(both, red[turn]);
     const float r = rsqrtf(fmaf(both.x, p.inv_width, p.eps));
-    const float back = r * r * (both.y * p.inv_width) * r;
+    const float back = -(r * r * (both.y * p.inv_width) * r);
+    const uint64_t r2 = pack64(r, r), back2 = pack64(back, back);
     T* dx = static_cast<T*>(p.dx) + row * p.dx_row;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * step + tid;
-      if (v >= vectors) continue;
-      Chunk<T, CH> wc, o;
-      wc.load(static_cast<const T*>(p.weight) + v * CH);
-      float a[CH], b[CH], w[CH], s[CH], y[CH];
-      d[i].get(a), z[i].get(b), wc.get(w), add[i].get(s);
+      Chunk<T, CH> o;
 #pragma unroll
-      for (int e = 0; e < CH; ++e) {
-        y[e] = fmaf(a[e] * w[e], r, fmaf(-back, b[e], s[e]));
-        dw[i][e] = fmaf(a[e], b[e] * r, dw[i][e]);
+      for (int j = 0; j < CH / 2; ++j) {
+        const uint64_t a = d[i].pair(j), b = z[i].pair(j);
+        o.set_pair(j, fma2(mul2(a, w[i].pair(j)), r2, fma2(b, back2, add[i].pair(j))));
+        dw[i][j] = fma2(a, mul2(b, r2), dw[i][j]);
       }
-      o.set(y);
-      o.store(dx + v * CH);
+      if (v < vectors) o.store(dx + v * CH);
+    }
+    if (kNext) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = d_[i], z[i] = z_[i], add[i] = add_[i];
+    } else if (row + gridDim.x < p.rows) {
+      load(row + gridDim.x, d, z, add);
     }
   }
   if (!p.partial) return;
@@ -334,7 +364,7 @@ __global__ void __launch_bounds__(1024) norm_backward_kernel(const NormGradParam
     const int v = i * step + tid;
     if (v >= vectors) continue;
 #pragma unroll
-    for (int e = 0; e < CH; e += 4) *reinterpret_cast<float4*>(out + v * CH + e) = make_float4(dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]);
+    for (int j = 0; j < CH / 2; j += 2) *reinterpret_cast<ulonglong2*>(out + v * CH + 2 * j) = make_ulonglong2(dw[i][j], dw[i][j + 1]);
   }
 }
 
@@ -429,10 +459,11 @@ bool vectors_fit(int64_t width, int64_t rows, int ch, int bytes, std::initialize
   return true;
 }
 
-// Vectors a thread holds of a row of `vectors`, and the threads of a row.
-void split_row(int vectors, int want, int* v, int* threads) {
+// Vectors a thread holds of a row of `vectors` (`want`, or as many as it takes
+// for at most `most` threads, at most `limit`), and the threads of a row.
+void split_row(int vectors, int want, int most, int limit, int* v, int* threads) {
   *v = want;
-  while (*v < 8 && (vectors + *v - 1) / *v > 1024) *v *= 2;
+  while (*v < limit && (vectors + *v - 1) / *v > most) *v *= 2;
   *threads = std::max(32, ((vectors + *v - 1) / *v + 31) / 32 * 32);
 }
 
@@ -460,7 +491,7 @@ void launch_backward(const NormGradParams& p, int v, int threads, int grid, cuda
 }
 
 // Most CTAs of the gradient: each leaves a row of sums.
-int backward_ctas(int sms, int64_t rows) { return static_cast<int>(std::min<int64_t>(std::max<int64_t>(rows, 1), sms * 4)); }
+int backward_ctas(int sms, int64_t rows) { return static_cast<int>(std::min<int64_t>(std::max<int64_t>(rows, 1), sms * 2)); }
 
 eg_status check_grads(const eg_norm_grads* a) {
   if (!a) return host_fail(EG_ERR_INVALID_ARG, "args is NULL");
@@ -509,7 +540,7 @@ eg_status eg_add_rms_norm(const eg_norm_args* args, void* stream) {
                     (!quant || vectors_fit(a.width, a.rows, ch, 1, {{a.codes, a.codes_row}}));
   if (fits) {
     int v = 0, threads = 0;
-    split_row(p.width / ch, 4, &v, &threads);
+    split_row(p.width / ch, 4, 1024, 8, &v, &threads);
     if (a.dtype == EG_EL_F32) launch_norm<float, 4>(p, v, threads, st);
     else if (a.dtype == EG_EL_BF16) launch_norm<__nv_bfloat16, 8>(p, v, threads, st);
     else launch_norm<__half, 8>(p, v, threads, st);
@@ -562,10 +593,10 @@ eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream) {
   p.dx = a.dx, p.dx_row = a.dx_row;
   p.partial = a.d_weight ? static_cast<float*>(a.workspace) : nullptr;
   const int ch = 16 / bytes;
-  const bool fits = a.width / ch <= 4 * 1024 && vectors_fit(a.width, a.rows, ch, bytes, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.weight, 0}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}});
+  const bool fits = a.width / ch <= (ch == 4 ? 4 * 1024 : 4 * 512) && vectors_fit(a.width, a.rows, ch, bytes, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.weight, 0}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}});
   if (fits) {
     int v = 0, threads = 0;
-    split_row(p.width / ch, 1, &v, &threads);
+    split_row(p.width / ch, 1, 512, 4, &v, &threads);
     if (a.dtype == EG_EL_F32) launch_backward<float, 4>(p, v, threads, grid, st);
     else if (a.dtype == EG_EL_BF16) launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, st);
     else launch_backward<__half, 8>(p, v, threads, grid, st);

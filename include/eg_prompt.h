@@ -33,7 +33,8 @@ extern "C" {
  *
  *   EG_NORM_E4M3, EG_NORM_INT8: a = max |h| of the row
  *   EG_NORM_E4M3_BLOCK: a = max |h| of each block of 128 columns
- *   scale = a / 448 (INT8: a / 127), 1 where that is 0; code = h / scale,
+ *   scale = a / 448 (INT8: a / 127), 1 where that is 0; code = h times the
+ *   float32 reciprocal of scale (h / scale where scale is below 2^-126),
  *   nearest even, saturated (+-448; +-127)
  *
  * A row (block) with a NaN has a NaN scale.  sum may be x or residual, out may
