@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <initializer_list>
 
 #include "../../include/eg_prompt.h"
@@ -42,6 +43,7 @@ struct NormGradParams {
   void* dx;
   int64_t dx_row;
   float* partial;  // [CTAs][width] sums of d_weight, or NULL
+  int32_t stages;  // rows in shared memory
 };
 
 // The scale of values whose largest magnitude has the bits `most` (a NaN's are
@@ -293,6 +295,7 @@ template <typename T, int CH, int V>
 __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_kernel(const NormGradParams p) {
   griddep_launch_dependents();
   __shared__ float2 red[2][32];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int tid = threadIdx.x, step = blockDim.x, vectors = p.width / CH;
   uint64_t dw[V][CH / 2];
   Chunk<T, CH> d[V], z[V], add[V], w[V];
@@ -303,24 +306,37 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
     if (i * step + tid < vectors) w[i].load(static_cast<const T*>(p.weight) + (i * step + tid) * CH);
     else w[i].zero();
   }
-  auto load = [&](int64_t row, Chunk<T, CH> (&d_)[V], Chunk<T, CH> (&z_)[V], Chunk<T, CH> (&add_)[V]) {
+  // Rows come to shared memory some turns ahead; a thread copies what it will
+  // read itself, so they need no barrier.
+  auto place = [&](int stage, int tensor, int i) { return smem + ((stage * 3 + tensor) * V + i) * (step * 16) + tid * 16; };
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int v = i * step + tid;
+        if (v >= vectors) continue;
+        cp_async_16(place(stage, 0, i), static_cast<const T*>(p.d_out) + row * p.d_out_row + v * CH, 16);
+        cp_async_16(place(stage, 1, i), static_cast<const T*>(p.sum) + row * p.sum_row + v * CH, 16);
+        if (p.d_sum) cp_async_16(place(stage, 2, i), static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH, 16);
+      }
+    }
+    cp_async_commit();
+  };
+  const int stages = p.stages;
+  for (int s = 0; s < stages; ++s) fetch(blockIdx.x + static_cast<int64_t>(s) * gridDim.x, s);
+  int turn = 0, stage = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
+    if (stages == 4) cp_async_wait<3>();
+    else if (stages == 2) cp_async_wait<1>();
+    else cp_async_wait<0>();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int v = i * step + tid;
-      d_[i].zero(), z_[i].zero(), add_[i].zero();
-      if (v >= vectors) continue;
-      d_[i].load(static_cast<const T*>(p.d_out) + row * p.d_out_row + v * CH);
-      z_[i].load(static_cast<const T*>(p.sum) + row * p.sum_row + v * CH);
-      if (p.d_sum) add_[i].load(static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH);
+      d[i].zero(), z[i].zero(), add[i].zero();
+      if (i * step + tid >= vectors) continue;
+      d[i].load(reinterpret_cast<const T*>(place(stage, 0, i)));
+      z[i].load(reinterpret_cast<const T*>(place(stage, 1, i)));
+      if (p.d_sum) add[i].load(reinterpret_cast<const T*>(place(stage, 2, i)));
     }
-  };
-  load(blockIdx.x, d, z, add);
-  int turn = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, turn ^= 1) {
-    // the next row is on its way while this one's sums go round
-    constexpr bool kNext = V < 4;
-    Chunk<T, CH> d_[V], z_[V], add_[V];
-    if (kNext && row + gridDim.x < p.rows) load(row + gridDim.x, d_, z_, add_);
     uint64_t square2 = 0, gz2 = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -334,6 +350,9 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
     unpack64(square2, &both.x, &other.x), unpack64(gz2, &both.y, &other.y);
     both.x += other.x, both.y += other.y;
     both = cta_sum2(both, red[turn]);
+    // this row has been read: its place is free
+    fetch(row + static_cast<int64_t>(stages) * gridDim.x, stage);
+    if (++stage == stages) stage = 0;
     const float r = rsqrtf(fmaf(both.x, p.inv_width, p.eps));
     const float back = -(r * r * (both.y * p.inv_width) * r);
     const uint64_t r2 = pack64(r, r), back2 = pack64(back, back);
@@ -349,12 +368,6 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
         dw[i][j] = fma2(a, mul2(b, r2), dw[i][j]);
       }
       if (v < vectors) o.store(dx + v * CH);
-    }
-    if (kNext) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) d[i] = d_[i], z[i] = z_[i], add[i] = add_[i];
-    } else if (row + gridDim.x < p.rows) {
-      load(row + gridDim.x, d, z, add);
     }
   }
   if (!p.partial) return;
@@ -483,11 +496,21 @@ void launch_norm(const NormParams& p, int v, int threads, cudaStream_t st) {
   else norm_kernel<T, CH, 8, false><<<p.rows, threads, 0, st>>>(p);
 }
 
+template <typename T, int CH, int V>
+eg_status launch_backward(NormGradParams p, int threads, int grid, int dev, cudaStream_t st) {
+  static std::atomic<uint64_t> allowed{0};
+  // four rows ahead where two CTAs an SM have room for that, else two, else none
+  const int stage = 3 * V * threads * 16;
+  p.stages = 4 * stage <= 110 * 1024 ? 4 : 2 * stage <= 220 * 1024 ? 2 : 1;
+  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<T, CH, V>), 224 * 1024, dev, &allowed));
+  norm_backward_kernel<T, CH, V><<<grid, threads, p.stages * stage, st>>>(p);
+  return EG_OK;
+}
 template <typename T, int CH>
-void launch_backward(const NormGradParams& p, int v, int threads, int grid, cudaStream_t st) {
-  if (v == 1) norm_backward_kernel<T, CH, 1><<<grid, threads, 0, st>>>(p);
-  else if (v == 2) norm_backward_kernel<T, CH, 2><<<grid, threads, 0, st>>>(p);
-  else norm_backward_kernel<T, CH, 4><<<grid, threads, 0, st>>>(p);
+eg_status launch_backward(const NormGradParams& p, int v, int threads, int grid, int dev, cudaStream_t st) {
+  return v == 1   ? launch_backward<T, CH, 1>(p, threads, grid, dev, st)
+         : v == 2 ? launch_backward<T, CH, 2>(p, threads, grid, dev, st)
+                  : launch_backward<T, CH, 4>(p, threads, grid, dev, st);
 }
 
 // Most CTAs of the gradient: each leaves a row of sums.
@@ -597,9 +620,9 @@ eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream) {
   if (fits) {
     int v = 0, threads = 0;
     split_row(p.width / ch, 1, 512, 4, &v, &threads);
-    if (a.dtype == EG_EL_F32) launch_backward<float, 4>(p, v, threads, grid, st);
-    else if (a.dtype == EG_EL_BF16) launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, st);
-    else launch_backward<__half, 8>(p, v, threads, grid, st);
+    EG_TRY(a.dtype == EG_EL_F32    ? (launch_backward<float, 4>(p, v, threads, grid, dev, st))
+           : a.dtype == EG_EL_BF16 ? (launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, dev, st))
+                                   : (launch_backward<__half, 8>(p, v, threads, grid, dev, st)));
   } else if (a.dtype == EG_EL_F32) norm_backward_any_kernel<float><<<grid, kAnyThreads, 0, st>>>(p);
   else if (a.dtype == EG_EL_BF16) norm_backward_any_kernel<__nv_bfloat16><<<grid, kAnyThreads, 0, st>>>(p);
   else norm_backward_any_kernel<__half><<<grid, kAnyThreads, 0, st>>>(p);
