@@ -90,10 +90,10 @@ __device__ __forceinline__ float attn_ex2(float x) {
 // Position of a tile's values in the ring's order: K0, K1, V0, K2, V1, ...
 __device__ __forceinline__ uint32_t attn_pos_v(uint32_t i, uint32_t count) { return i + 1 < count ? 2 * i + 2 : 2 * count - 1; }
 
-// Four columns of one row of an item that CTAs lead..last have parts of, joined
-// in the order of the CTAs.
+// Four columns of one row of an item that CTAs lead, lead + step, ... last have
+// parts of, joined in the order of the CTAs.
 template <typename T, int HD, typename Params>
-__device__ __forceinline__ void attn_join_piece(const Params& p, int lead, int last, int r, int col, int64_t packed, int head) {
+__device__ __forceinline__ void attn_join_piece(const Params& p, int lead, int last, int step, int r, int col, int64_t packed, int head) {
   constexpr float kShift = El<T>::kBf16 ? 0.0f : 7.0f;
   const int64_t rows = static_cast<int64_t>(128) * p.q_tiles;
   const float2* ml = reinterpret_cast<const float2*>(p.partial_ml) + r;
@@ -102,7 +102,7 @@ __device__ __forceinline__ void attn_join_piece(const Params& p, int lead, int l
   float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float top = -CUDART_INF_F, weight = 0.0f;
 #pragma unroll 4
-  for (int c = lead; c <= last; ++c) {
+  for (int c = lead; c <= last; c += step) {
     const int64_t slot = (static_cast<int64_t>(c) * 2 + (c == lead ? 1 : 0)) * rows;
     const float2 w = __ldcg(ml + slot);
     const float4 x = __ldcg(reinterpret_cast<const float4*>(part + slot * HD));

@@ -53,56 +53,63 @@ constexpr uint32_t kChunkKeys = 128;
 
 // One sequence's lengths, cut to what the table, the packed rows and the plan
 // hold, and its items: row groups (of item_tokens tokens with the heads that
-// share a cached one) of each cached head.
+// share a cached one) of each cached head.  `team` neighbouring groups are one
+// super: as many neighbouring CTAs (a team) have the same range of supers'
+// units, each one group of every super, so that they read the same keys and
+// values at the same time.
 struct ChunkSeq {
   int32_t start, n;    // packed rows
   int32_t ctx, keys;   // cached places, with the new tokens
   int32_t groups;      // items of a cached head
   int32_t low_groups;  // those of them whose window starts at place 0
-  int32_t last_cost;   // row tiles of the last one
+  int32_t team, supers;
+  int32_t last_cost;   // row tiles of the last super's groups, at most
 };
 
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int32_t start, int32_t n, int32_t ctx) {
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int32_t team, int32_t start, int32_t n, int32_t ctx) {
   ChunkSeq s;
   const int32_t room = static_cast<int32_t>(p.table_stride * p.page_size);
   s.start = start, s.n = n, s.ctx = ctx;
   s.keys = min(ctx + n, room);
   s.groups = (n + p.item_tokens - 1) / p.item_tokens;
   s.low_groups = p.window == 0 ? s.groups : p.window > ctx ? min(s.groups, (p.window - ctx - 1) / p.item_tokens + 1) : 0;
-  s.last_cost = (n - (s.groups - 1) * p.item_tokens) * p.group > p.tile_rows ? 2 : 1;
+  s.team = team, s.supers = (s.groups + team - 1) / team;
+  const bool more = s.groups - (s.supers - 1) * team > 1;
+  s.last_cost = p.q_tiles == 2 && (more || (n - (s.groups - 1) * p.item_tokens) * p.group > p.tile_rows) ? 2 : 1;
   return s;
 }
-__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int b) {
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkParams& p, int32_t team, int b) {
   const int32_t room = static_cast<int32_t>(p.table_stride * p.page_size);
   const int32_t from = __ldg(p.q_start + b), to = __ldg(p.q_start + b + 1), ctx = __ldg(p.context_lens + b);
   const int32_t start = min(max(from, 0), p.tokens);
-  return chunk_seq(p, start, min(min(max(to, start), p.tokens) - start, p.max_chunk), min(max(ctx, 0), room));
+  return chunk_seq(p, team, start, min(min(max(to, start), p.tokens) - start, p.max_chunk), min(max(ctx, 0), room));
 }
 
-// Units are places: an item counts some span of places, an estimate of what its
-// rows attend to, once for each of its row tiles, and kChunkFixed more for what
-// it costs beside its tiles.  Spans are linear in the row group, so that their
-// sums need no loop.  Tile k of an item belongs to the CTA that has the item's
-// unit fixed + min(128 k, span - 1), times its row tiles.
+// Units are places: a super counts some span of places, an estimate of what the
+// rows of its last group attend to, once for each of an item's row tiles, and
+// kChunkFixed more for what an item costs beside its tiles.  Spans are linear in
+// the super, so that their sums need no loop.  Tile k of an item belongs to the
+// CTA that has the super's unit fixed + min(128 k, span - 1), times the row
+// tiles.
 constexpr int32_t kChunkFixed = 512;
 
-__device__ __forceinline__ int64_t chunk_span(const ChunkParams& p, const ChunkSeq& s, int32_t g) {
+__device__ __forceinline__ int64_t chunk_span(const ChunkParams& p, const ChunkSeq& s, int32_t super) {
+  const int32_t g = min((super + 1) * s.team, s.groups) - 1;
   if (g < s.low_groups) return static_cast<int64_t>(s.ctx) + (g + 1) * static_cast<int64_t>(p.item_tokens);
   return static_cast<int64_t>(p.item_tokens) + p.window + min(p.sinks, s.ctx);
 }
-// Units of the first g items of a cached head, were all of them full.
-__device__ __forceinline__ int64_t chunk_before(const ChunkParams& p, const ChunkSeq& s, int32_t g) {
-  const int64_t low = min(g, s.low_groups), rest = g - low;
-  const int64_t places = low * (kChunkFixed + static_cast<int64_t>(s.ctx)) + p.item_tokens * (low * (low + 1) / 2) +
+// Units of the first supers of a cached head, were all of them full.
+__device__ __forceinline__ int64_t chunk_before(const ChunkParams& p, const ChunkSeq& s, int32_t super) {
+  const int64_t low = min(super, s.low_groups / s.team), rest = super - low, tokens = static_cast<int64_t>(s.team) * p.item_tokens;
+  const int64_t places = low * (kChunkFixed + static_cast<int64_t>(s.ctx)) + tokens * (low * (low + 1) / 2) +
                          rest * (kChunkFixed + static_cast<int64_t>(p.item_tokens) + p.window + min(p.sinks, s.ctx));
   return places * p.q_tiles;
 }
-// Units of a cached head's items.
+// Units of a cached head's supers.
 __device__ __forceinline__ int64_t chunk_of_head(const ChunkParams& p, const ChunkSeq& s) {
-  if (s.groups == 0) return 0;
-  return chunk_before(p, s, s.groups - 1) + (kChunkFixed + chunk_span(p, s, s.groups - 1)) * min(s.last_cost, p.q_tiles);
+  if (s.supers == 0) return 0;
+  return chunk_before(p, s, s.supers - 1) + (kChunkFixed + chunk_span(p, s, s.supers - 1)) * s.last_cost;
 }
-
 __device__ __forceinline__ int64_t chunk_units(const ChunkParams& p, const ChunkSeq& s) { return chunk_of_head(p, s) * p.kv_heads; }
 
 // An item: its rows, and the key tiles that any of them attends to: `sink_tiles`
@@ -113,21 +120,28 @@ struct ChunkItem {
   int32_t lo, hi;           // places of the window that any row attends to, [lo, hi)
   int32_t sinks;            // first places that rows attend to, window or not
   int32_t sink_tiles, low_tile, tiles;
+  int32_t unit_cost;        // of the super's units
   int64_t span;             // units of one row tile, without the fixed ones
-  __device__ __forceinline__ int64_t units() const { return (kChunkFixed + span) * cost; }
+  __device__ __forceinline__ int64_t units() const { return (kChunkFixed + span) * unit_cost; }
   // the item's tiles that have their first unit before unit `in` of it
   __device__ __forceinline__ int32_t tiles_before(int64_t in) const {
-    const int64_t u = cost == 2 ? (in + 1) >> 1 : in;  // units of one row tile, rounded up
+    const int64_t u = unit_cost == 2 ? (in + 1) >> 1 : in;  // units of one row tile, rounded up
     if (u <= kChunkFixed) return 0;
     if (u >= kChunkFixed + span) return tiles;
     return static_cast<int32_t>(min(static_cast<int64_t>(tiles), (u - kChunkFixed + 127) >> 7));
   }
   __device__ __forceinline__ int64_t first_unit(int32_t tile) const {
-    return (kChunkFixed + min(static_cast<int64_t>(tile) << 7, span - 1)) * cost;
+    return (kChunkFixed + min(static_cast<int64_t>(tile) << 7, span - 1)) * unit_cost;
   }
 };
-__device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const ChunkSeq& s, int32_t g) {
-  ChunkItem item;
+// The item of a team's member in a super: one without tiles where the sequence
+// has no such group.
+__device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const ChunkSeq& s, int32_t super, int32_t member) {
+  ChunkItem item{};
+  const int32_t g = super * s.team + member;
+  item.unit_cost = super + 1 == s.supers ? s.last_cost : p.q_tiles;
+  item.span = chunk_span(p, s, super);
+  if (g >= s.groups) return item;
   const int32_t t0 = g * p.item_tokens, tokens = min(s.n - t0, p.item_tokens);
   item.row0 = t0 * p.group, item.rows = tokens * p.group;
   item.cost = item.rows > p.tile_rows ? 2 : 1;
@@ -140,12 +154,11 @@ __device__ __forceinline__ ChunkItem chunk_item(const ChunkParams& p, const Chun
   // rows that attend to nothing still have a tile, so that they are written
   if (item.low_tile >= end && item.sink_tiles == 0) item.low_tile = end - 1;
   item.tiles = item.sink_tiles + max(end - item.low_tile, 0);
-  item.span = chunk_span(p, s, g);
   return item;
 }
 
-// The first unit of CTA c, and the CTA that has unit u, when `total` units are
-// cut into `ctas` equal ranges.
+// The first unit of team c, and the team that has unit u, when `total` units
+// are cut into `ctas` equal ranges.
 __device__ __forceinline__ int64_t chunk_from(int64_t total, int32_t ctas, int32_t c) { return total * c / ctas; }
 __device__ __forceinline__ int32_t chunk_owner(int64_t total, int32_t ctas, int64_t u) {
   return static_cast<int32_t>(((u + 1) * ctas + total - 1) / total) - 1;
@@ -172,47 +185,48 @@ struct ChunkSegment {
 // A walk over a CTA's range, one segment at a time.
 struct ChunkWalk : ChunkSegment {
   int64_t at, to;
-  int32_t group;              // the row group that `at` is in
+  int32_t super, member;      // the super that `at` is in, and which of its groups this CTA has
   const int32_t (*near_)[4];  // start, n, ctx of the sequences from near_b on
   int32_t near_b;
 
   __device__ __forceinline__ void load(const ChunkParams& p) {
     const int i = b - near_b;
-    seq = i < kChunkNear ? chunk_seq(p, near_[i][0], near_[i][1], near_[i][2]) : chunk_seq(p, b);
+    seq = i < kChunkNear ? chunk_seq(p, seq.team, near_[i][0], near_[i][1], near_[i][2]) : chunk_seq(p, seq.team, b);
   }
   // to unit `from`, in sequence b, whose units start at `before`
-  __device__ __forceinline__ void start(const ChunkParams& p, int32_t b_, int64_t before, int64_t from, int64_t to_) {
-    b = b_, at = from, to = to_;
+  __device__ __forceinline__ void start(const ChunkParams& p, int32_t team, int32_t member_, int32_t b_, int64_t before, int64_t from, int64_t to_) {
+    b = b_, at = from, to = to_, member = member_;
+    seq.team = team;
     load(p);
     const int64_t each = chunk_of_head(p, seq), in = from - before;
     head = static_cast<int32_t>(in / each);
     const int64_t rest = in - head * each;
-    int32_t low = 0, high = seq.groups - 1;  // the last group whose units start at `rest` or before
+    int32_t low = 0, high = seq.supers - 1;  // the last super whose units start at `rest` or before
     while (low < high) {
       const int32_t mid = (low + high + 1) >> 1;
       if (chunk_before(p, seq, mid) <= rest) low = mid;
       else high = mid - 1;
     }
-    group = low;
-    begin = before + head * each + chunk_before(p, seq, group);
-    item = chunk_item(p, seq, group);
+    super = low;
+    begin = before + head * each + chunk_before(p, seq, super);
+    item = chunk_item(p, seq, super, member);
   }
   __device__ __forceinline__ bool next(const ChunkParams& p) {
     for (;;) {
       if (at >= to) return false;
       if (at >= begin + item.units()) {
         begin += item.units();
-        if (++group == seq.groups) {
-          group = 0;
+        if (++super == seq.supers) {
+          super = 0;
           if (++head == p.kv_heads) {
             head = 0;
             do {
               ++b;
               load(p);
-            } while (seq.groups == 0);
+            } while (seq.supers == 0);
           }
         }
-        item = chunk_item(p, seq, group);
+        item = chunk_item(p, seq, super, member);
       }
       const int64_t in = at - begin, take = min(item.units() - in, to - at);
       at += take;
@@ -240,7 +254,8 @@ struct ChunkShared {
   ChunkSegment segments[2];
   union {
     float2 stats[2][128];         // a warpgroup's row references and weights
-    int64_t warps[2][12];         // before any: units of each warp's sequences
+    int64_t warps[2][12];         // before any: units of each warp's sequences,
+    int64_t sums[5][12];          // and what the size of teams is chosen by
   };
 };
 static_assert(sizeof(ChunkShared) <= ChunkSmem<64>::kExtra, "fits the room after the tiles");
@@ -266,22 +281,6 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 
   griddep_launch_dependents();
 
-  // ---- this CTA's range of units.  One pass over the sequences where every
-  // thread has one; else a pass for the total and one to find the place.
-  const bool once = p.batch <= kChunkThreads;
-  int64_t mine = 0;
-  ChunkSeq seq{};
-  for (int b = tid; b < p.batch; b += kChunkThreads) {
-    seq = chunk_seq(p, b);
-    mine += chunk_units(p, seq);
-  }
-  int64_t upto = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
-  }
-  if (lane == 31) sh.warps[0][warp] = upto;
   if (tid == 0) {
     for (uint32_t i = 0; i < stages; ++i) mbar_init(&sh.full[i], 1), mbar_init(&sh.empty[i], 2);
     for (int i = 0; i < 2; ++i) mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_ready[i], 4), mbar_init(&sh.o_done[i], 1);
@@ -295,6 +294,62 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     sh.abort = 0;
     for (int i = 0; i < 4; ++i) sh.poisoned[i >> 1][i & 1] = 0;
   }
+
+  // ---- CTAs of a team.  Where a sequence's row groups on different CTAs go
+  // through more keys and values than the L2 keeps, each read them from memory
+  // by itself (two chunks of 512 tokens after 65536 and 98304 places: 5.4 GB for
+  // 0.69 GB, 1029 us for 966); as a team they read them once.  A team of eight, four
+  // or two is taken where its CTAs without a group and its rounding up cost at
+  // most a sixteenth more.
+  int32_t team = 1;
+  if (p.q_tiles == 2 && gridDim.x >= 8) {
+    int64_t sums[5] = {0, 0, 0, 0, 0};  // units of one, two, four, eight; places
+    for (int b = tid; b < p.batch; b += kChunkThreads) {
+      ChunkSeq s = chunk_seq(p, 1, b);
+      sums[0] += chunk_units(p, s);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) {
+        s = chunk_seq(p, 1 << i, s.start, s.n, s.ctx);
+        sums[i] += chunk_units(p, s) << i;
+      }
+      if (s.groups > 1) sums[4] += p.window ? min(static_cast<int64_t>(s.keys), static_cast<int64_t>(p.window) + s.n) : s.keys;
+    }
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sums[i] += __shfl_xor_sync(0xffffffffu, sums[i], o);
+      if (lane == 0) sh.sums[i][warp] = sums[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      sums[i] = 0;
+#pragma unroll
+      for (int w = 0; w < kChunkThreads / 32; ++w) sums[i] += sh.sums[i][w];
+    }
+    if (sums[4] * p.kv_heads * HD * 4 > (64ll << 20))
+#pragma unroll
+      for (int i = 1; i < 4; ++i)
+        if (sums[i] * 16 <= sums[0] * 17) team = 1 << i;
+    __syncthreads();
+  }
+
+  // ---- this CTA's range of units.  One pass over the sequences where every
+  // thread has one; else a pass for the total and one to find the place.
+  const bool once = p.batch <= kChunkThreads;
+  int64_t mine = 0;
+  ChunkSeq seq{};
+  for (int b = tid; b < p.batch; b += kChunkThreads) {
+    seq = chunk_seq(p, team, b);
+    mine += chunk_units(p, seq);
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) sh.warps[0][warp] = upto;
   __syncthreads();
   int64_t total = 0, base = 0;
 #pragma unroll
@@ -304,18 +359,19 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   }
   // a range is no shorter than a tile's units, so that a CTA between the first
   // and the last of an item has a tile of it
-  const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x), total >> (p.q_tiles == 2 ? 8 : 7)));
-  if (static_cast<int32_t>(blockIdx.x) >= ctas) {
+  const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x / team), total >> (p.q_tiles == 2 ? 8 : 7)));
+  const int32_t number = blockIdx.x / team, member = blockIdx.x % team;
+  if (number >= ctas) {
     if (blockIdx.x == 0 && tid == 0) p.meta[0].ctas = 0;
     return;
   }
-  const int64_t from = chunk_from(total, ctas, blockIdx.x), to = chunk_from(total, ctas, blockIdx.x + 1);
+  const int64_t from = chunk_from(total, ctas, number), to = chunk_from(total, ctas, number + 1);
   if (once) {
     if (base + upto - mine <= from && from < base + upto) sh.b = tid, sh.before = base + upto - mine;
   } else {
     int64_t before = 0;
     for (int b0 = 0; b0 < p.batch; b0 += kChunkThreads) {
-      const int64_t units = b0 + tid < p.batch ? chunk_units(p, chunk_seq(p, b0 + tid)) : 0;
+      const int64_t units = b0 + tid < p.batch ? chunk_units(p, chunk_seq(p, team, b0 + tid)) : 0;
       upto = units;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -339,7 +395,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   __syncthreads();
   const int near_b = sh.b;
   if (once ? tid >= near_b && tid < min(near_b + kChunkNear, p.batch) : tid < kChunkNear && near_b + tid < p.batch) {
-    if (!once) seq = chunk_seq(p, near_b + tid);
+    if (!once) seq = chunk_seq(p, team, near_b + tid);
     int32_t* at = sh.near_[once ? tid - near_b : tid];
     at[0] = seq.start, at[1] = seq.n, at[2] = seq.ctx;
   }
@@ -379,7 +435,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   setmaxnreg_dec<88>();
   ChunkWalk walk;
   walk.near_ = sh.near_, walk.near_b = near_b;
-  walk.start(p, near_b, sh.before, from, to);
+  walk.start(p, team, member, near_b, sh.before, from, to);
   if (warp == 8) {
     // ------------------------------------------------------- producer ----
     uint32_t pos = 0;  // loads so far
@@ -561,8 +617,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       ChunkMeta m;
       m.from = from;
       m.begin = walk.begin, m.total = total, m.ctas = ctas;
-      m.lead = m.begin + walk.item.first_unit(0), m.last = m.begin + walk.item.first_unit(walk.item.tiles - 1);
-      m.start = walk.seq.start, m.row0 = walk.item.row0, m.head = walk.head, m.rows = walk.item.rows, m.pad = 0;
+      m.lead = m.begin + walk.item.first_unit(0), m.last = m.begin + walk.item.first_unit(max(walk.item.tiles - 1, 0));
+      m.start = walk.seq.start, m.row0 = walk.item.row0, m.head = walk.head, m.rows = walk.item.rows, m.team = team;
       p.meta[blockIdx.x] = m;
     }
     // The walk for the softmax warpgroups, whose registers have no room for it,
@@ -902,12 +958,12 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       tc_fence_after();
       if (joining) {
         // the CTA that leaves the last part of the item joins all of them
-        const int32_t lead = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(0));
-        const int32_t last = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(walk.item.tiles - 1));
+        const int32_t lead = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(0)) * team + member;
+        const int32_t last = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(walk.item.tiles - 1)) * team + member;
         if (tid == 0) {
           const int before = atomicAdd(p.arrivals + lead, 1);
-          sh.joins = before == last - lead;
-          if (before == last - lead) p.arrivals[lead] = 0;
+          sh.joins = before == (last - lead) / team;
+          if (sh.joins) p.arrivals[lead] = 0;
           __threadfence();
         }
         mbar_arrive(&sh.exchange);
@@ -917,7 +973,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const int rows = walk.item.rows, pieces = rows * (HD / 4);
           for (int i = tid; i < pieces; i += 256) {
             const int at_row = walk.item.row0 + i % rows, t_ = at_row / p.group;
-            attn_join_piece<T, HD>(p, lead, last, i % rows, i / rows * 4, walk.seq.start + t_, walk.head * p.group + at_row - t_ * p.group);
+            attn_join_piece<T, HD>(p, lead, last, team, i % rows, i / rows * 4, walk.seq.start + t_, walk.head * p.group + at_row - t_ * p.group);
           }
         }
       }
@@ -946,18 +1002,21 @@ __global__ void __launch_bounds__(HD * 2) chunk_join_kernel(const ChunkParams p)
   griddep_wait();
   const int cut = blockIdx.x + 1;
   const int ctas = p.meta[0].ctas;
+  if (ctas == 0) return;
+  const int team = p.meta[0].team;
+  if (cut < team || cut >= ctas * team) return;
   const ChunkMeta m = p.meta[cut];
-  const int64_t from_before = p.meta[cut - 1].from;
-  if (cut >= ctas || m.from <= m.begin || from_before > m.begin) return;
+  const int64_t from_before = p.meta[cut - team].from;
+  if (m.from <= m.begin || from_before > m.begin) return;
   // the CTAs with the item's first tile and with its last: those between them
   // have some too
-  const int lead = chunk_owner(m.total, ctas, m.lead), last = chunk_owner(m.total, ctas, m.last);
+  const int lead = chunk_owner(m.total, ctas, m.lead) * team + cut % team, last = chunk_owner(m.total, ctas, m.last) * team + cut % team;
   if (lead == last) return;
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + (lane & 7);
   if (r >= m.rows) return;
   const int t = (m.row0 + r) / p.group;
-  attn_join_piece<T, HD>(p, lead, last, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
+  attn_join_piece<T, HD>(p, lead, last, team, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
 }
 
 }  // namespace eg

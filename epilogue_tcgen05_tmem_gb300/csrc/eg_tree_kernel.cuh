@@ -786,7 +786,7 @@ __global__ void __launch_bounds__(kTreeThreads, 1)
           const int pieces = walk.rows * (HD / 4);
           for (int i = tid; i < pieces; i += 256) {
             const int r_ = i % walk.rows, t_ = (walk.row0 + r_) / p.group;
-            attn_join_piece<T, HD>(p, lead, last, r_, i / walk.rows * 4, walk.seq.start + t_,
+            attn_join_piece<T, HD>(p, lead, last, 1, r_, i / walk.rows * 4, walk.seq.start + t_,
                                    walk.head * p.group + (walk.row0 + r_) - t_ * p.group);
           }
         }
@@ -827,7 +827,7 @@ __global__ void __launch_bounds__(HD * 2) tree_join_kernel(const TreeParams p) {
   const int r = blockIdx.y * 8 + (lane & 7);
   if (r >= m.rows) return;
   const int t = (m.row0 + r) / p.group;
-  attn_join_piece<T, HD>(p, lead, last, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
+  attn_join_piece<T, HD>(p, lead, last, 1, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
 }
 
 }  // namespace eg

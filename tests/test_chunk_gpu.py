@@ -146,6 +146,12 @@ CASES = [
     ("bf16", 8, 2, 128, 16, [100, 3000], [40, 600], 100000, 3, False),         # a window that reaches everything
     ("bf16", 8, 2, 128, 16, [100, 3000], [40, 600], 2 ** 31 - 1, 2 ** 31 - 1, False),
     ("f16", 2, 1, 72, 40, list(range(0, 400, 7)), [1 + 5 * (i % 4) for i in range(58)], 90, 10, False),
+    # caches above what the L2 keeps: row groups go through them as teams of eight, four, two, and not
+    ("bf16", 32, 8, 128, 64, [9000, 8500], [512, 512], 0, 0, False),
+    ("f16", 32, 8, 128, 64, [17000], [251], 0, 0, True),
+    ("bf16", 32, 8, 128, 64, [9000, 8001], [100, 120], 0, 0, False),
+    ("bf16", 32, 8, 128, 64, [9000, 8500, 40], [512, 130, 1], 0, 0, False),
+    ("bf16", 32, 8, 128, 64, [12000, 11000], [512, 500], 9000, 5, False),
     # more sequences than a CTA has threads, some without tokens
     ("bf16", 4, 2, 64, 8, [37 * i % 300 for i in range(900)], [i % 3 for i in range(900)], 0, 0, False),
     ("bf16", 4, 2, 64, 8, [37 * i % 300 for i in range(900)], [5 * (i % 3) for i in range(900)], 50, 9, False),
