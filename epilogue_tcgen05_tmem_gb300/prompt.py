@@ -14,6 +14,7 @@ plans do not.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple
 
 from .decoder import EL_DTYPES, _b, _cache, _code, _fail, _heads, _new, _out, _packer, _rows, _side, _stream_of
@@ -57,6 +58,7 @@ class eg_lora_args(ctypes.Structure):
 
 _pack_norm, _pack_norm_grads = _packer(eg_norm_args), _packer(eg_norm_grads)
 _pack_chunk, _pack_lora = _packer(eg_chunk_args), _packer(eg_lora_args)
+_packers = {"add_rms_norm_workspace_bytes": _pack_norm_grads, "lora_workspace_bytes": _pack_lora}
 
 
 def declare(L: ctypes.CDLL) -> None:
@@ -80,10 +82,21 @@ def declare(L: ctypes.CDLL) -> None:
 
 def _matrix(name, t, shape, dtype, device):
     """(pointer, row stride) of a [rows, width] tensor."""
-    if t.shape != shape or t.dtype is not dtype or t.device != device or (shape[1] > 1 and t.stride(1) != 1):
+    if t.shape != shape or t.dtype is not dtype or t.device != device or ((s := t.stride())[1] != 1 and shape[1] > 1):
         raise ValueError(f"{name} must be {dtype} {tuple(shape)} on {device} with a contiguous last dimension: got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
-    return t.data_ptr(), t.stride(0)
+    return t.data_ptr(), s[0]
+
+
+@functools.lru_cache(maxsize=256)
+def _bytes(call, device, *fields):
+    """What a workspace call says of these sizes on the current device (of that
+    number); it says the same every time."""
+    need = _size(0)
+    status = getattr(_b, call)(_packers[call](*fields), ctypes.byref(need))
+    if status:
+        _fail(status)
+    return need.value
 
 
 def _result(name, given, shape, dtype, device, stream):
@@ -168,15 +181,11 @@ def add_rms_norm_backward(d_out, sum, weight, eps=1e-6, d_sum=None, dx=None, str
     if d_sum is not None:
         pa, a_row = _matrix("d_sum", d_sum, shape, dtype, device)
     dx, px, x_row = _result("dx", dx, shape, dtype, device, stream)
-    need = _size(0)
-    status = _b.add_rms_norm_workspace_bytes(_pack_norm_grads(rows, width, code, eps, pd, pz, w, pa, d_row, z_row, a_row, px, x_row, 0, 0, 0),
-                                             ctypes.byref(need))
-    if status:
-        _fail(status)
-    work = _new(need.value // 4, _b.f32, device, stream)
+    need = _bytes("add_rms_norm_workspace_bytes", _b.current(), rows, width, code, eps, *(0,) * 12)
+    work = _new(need // 4, _b.f32, device, stream)
     dw = _new(width, _b.f32, device, stream)
     status = _b.add_rms_norm_backward(_pack_norm_grads(rows, width, code, eps, pd, pz, w, pa, d_row, z_row, a_row, px, x_row, dw.data_ptr(),
-                                                       work.data_ptr(), need.value), st)
+                                                       work.data_ptr(), need), st)
     if status:
         _fail(status)
     return dx, dw
@@ -299,13 +308,11 @@ def lora(x, a, b, seq_start, adapter, scales=None, base=None, out=None, stream=N
     if base is not None:
         pbase, base_row = _matrix("base", base, (rows, outputs), dtype, device)
     out, po, out_row = _result("out", out, (rows, outputs), dtype, device, stream)
-    head = (rows, sequences, adapters, inputs, outputs, rank, _code(x), px, x_row, pa, pb, ps, start, which, pbase, base_row, po, out_row)
-    need = _size(0)
-    status = _b.lora_workspace_bytes(_pack_lora(*head, 0, 0), ctypes.byref(need))
-    if status:
-        _fail(status)
-    work = _new(need.value, _b.torch.uint8, device, stream)
-    status = _b.lora(_pack_lora(*head, work.data_ptr(), need.value), st)
+    code = _code(x)
+    need = _bytes("lora_workspace_bytes", _b.current(), rows, sequences, adapters, inputs, outputs, rank, code, *(0,) * 13)
+    work = _new(need, _b.torch.uint8, device, stream)
+    status = _b.lora(_pack_lora(rows, sequences, adapters, inputs, outputs, rank, code, px, x_row, pa, pb, ps, start, which, pbase, base_row, po, out_row,
+                                work.data_ptr(), need), st)
     if status:
         _fail(status)
     return out
