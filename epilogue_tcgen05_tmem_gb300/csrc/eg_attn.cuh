@@ -74,6 +74,13 @@ __device__ __forceinline__ void umma_f16_ts_add(uint32_t d_tmem, uint32_t a_tmem
       : "memory");
 }
 
+// 32 bytes, to a multiple of 32.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(__cvta_generic_to_global(p)), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 // The largest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;

@@ -256,6 +256,7 @@ eg_status eg_chunk_plan_run(eg_chunk_plan* plan, const eg_chunk_args* args, cons
   p.q_tiles = plan->q_tiles, p.stages = plan->stages;
   p.box_tokens = row_box(p.group) / p.group, p.tile_rows = plan->tile_rows, p.item_rows = plan->tile_rows * plan->q_tiles;
   p.item_tokens = p.item_rows / p.group;
+  p.teams = p.q_tiles == 2 && plan->grid >= 8 && static_cast<double>(a.batch) * a.table_stride * b.page_size * b.kv_heads * plan->hd * 4 > kChunkKept;
   p.batch = a.batch, p.tokens = a.tokens;
   p.o = a.o, p.o_token = a.o_token, p.o_head = a.o_head;
   p.block_table = a.block_table, p.table_stride = a.table_stride, p.context_lens = a.context_lens, p.q_start = a.q_start;

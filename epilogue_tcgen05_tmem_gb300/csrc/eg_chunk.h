@@ -31,6 +31,7 @@ struct ChunkParams {
   int32_t item_rows;    // tile_rows * q_tiles
   int32_t item_tokens;  // item_rows / group
   int32_t stages;
+  int32_t teams;        // the run's tables can hold more keys and values than the L2 keeps
   // the run
   int32_t batch, tokens;
   int32_t window, sinks;  // window: 0 for none

@@ -50,6 +50,7 @@ namespace eg {
 
 constexpr int kChunkThreads = 384;
 constexpr uint32_t kChunkKeys = 128;
+constexpr int64_t kChunkKept = 64 << 20;  // bytes of keys and values that the L2 (of 129 MB) keeps beside the rest
 
 // One sequence's lengths, cut to what the table, the packed rows and the plan
 // hold, and its items: row groups (of item_tokens tokens with the heads that
@@ -302,7 +303,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   // or two is taken where its CTAs without a group and its rounding up cost at
   // most a sixteenth more.
   int32_t team = 1;
-  if (p.q_tiles == 2 && gridDim.x >= 8) {
+  if (p.teams) {
     int64_t sums[5] = {0, 0, 0, 0, 0};  // units of one, two, four, eight; places
     for (int b = tid; b < p.batch; b += kChunkThreads) {
       ChunkSeq s = chunk_seq(p, 1, b);
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 #pragma unroll
       for (int w = 0; w < kChunkThreads / 32; ++w) sums[i] += sh.sums[i][w];
     }
-    if (sums[4] * p.kv_heads * HD * 4 > (64ll << 20))
+    if (sums[4] * p.kv_heads * HD * 4 > kChunkKept)
 #pragma unroll
       for (int i = 1; i < 4; ++i)
         if (sums[i] * 16 <= sums[0] * 17) team = 1 << i;
@@ -559,21 +560,27 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       auto next_k = [&](uint32_t i) { step(slot_k, turn_k, i == 0 ? 1 : 2); };
       auto next_v = [&](uint32_t i) { step(slot_v, turn_v, i + 2 == count ? 1 : 2); };
       if (pair) {
-        for (uint32_t i = 0; i <= count; ++i) {
-          // sums of tile i - 1, scores of tile i, whose keys came before those values
-          if (!(ok = (i == count || wait_all(&sh.full[slot_k], turn_k)) && (i == 0 || wait_all(&sh.full[slot_v], turn_v)) && my_turn() &&
-                     (i == 0 || wait_all(&sh.p_ready[mine], (mine ? used1 : used0) + i - 1))))
-            break;
+        // tile i's keys, then the values of the one before, in the ring's order
+        if (!(ok = wait_all(&sh.full[slot_k], turn_k) && my_turn())) break;
+        tc_fence_after();
+        if (elect_one()) scores(mine);
+        pass();
+        next_k(0);
+        uint32_t weights = mine ? used1 : used0;
+        for (uint32_t i = 1; i < count; ++i, ++weights) {
+          if (!(ok = wait_all(&sh.full[slot_k], turn_k) && wait_all(&sh.full[slot_v], turn_v) && my_turn() && wait_all(&sh.p_ready[mine], weights))) break;
           tc_fence_after();
-          if (elect_one()) {
-            if (i > 0) sums(mine, i > 1);
-            if (i < count) scores(mine);
-            if (i + 1 == count) umma_commit(&sh.q_empty);
-          }
+          if (elect_one()) sums(mine, i > 1), scores(mine);
           pass();
           next_k(i);
-          if (i > 0) next_v(i - 1);
+          next_v(i - 1);
         }
+        if (!ok) break;
+        if (elect_one()) umma_commit(&sh.q_empty);
+        if (!(ok = wait_all(&sh.full[slot_v], turn_v) && my_turn() && wait_all(&sh.p_ready[mine], weights))) break;
+        tc_fence_after();
+        if (elect_one()) sums(mine, count > 1);
+        pass();
         used0 += count, used1 += count;
       } else if (mine == 0) {
         // scores run two tiles ahead of the sums
@@ -884,6 +891,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int64_t at = slot * 128 * p.q_tiles + r;
         const int part_rows = 128 * p.q_tiles;
         T* o = static_cast<T*>(p.o) + packed * p.o_token + static_cast<int64_t>(head) * p.o_head;
+        // a lane's row goes out in whole sectors where they lie on them
+        const bool wide = ((reinterpret_cast<uintptr_t>(p.o) | static_cast<uint64_t>(p.o_token) * 2 | static_cast<uint64_t>(p.o_head) * 2) & 31) == 0 &&
+                          p.head_dim % 16 == 0;
         // [slot][4 columns][row][column]: a warp's rows are stored side by side
         float* part = p.partial + slot * part_rows * HD + r * 4;
 #pragma unroll 1
@@ -907,6 +917,18 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             for (int k = 0; k < kCols; ++k) a[k] = __float_as_uint(__uint_as_float(a[k]) * f0);
           }
           if (!valid) continue;
+          if (whole && wide) {
+#pragma unroll
+            for (int k = 0; k < kCols; k += 16) {
+              if (j + k >= p.head_dim) continue;
+              uint32_t y[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                y[e] = weight == 0.0f ? 0u : El<T>::pack2(__uint_as_float(a[k + 2 * e]) * scale, __uint_as_float(a[k + 2 * e + 1]) * scale);
+              st_global_32(o + j + k, y);
+            }
+            continue;
+          }
 #pragma unroll
           for (int k = 0; k < kCols; k += 8) {
             if (j + k >= p.head_dim) continue;
