@@ -117,6 +117,37 @@ eg_status encode_cache(const eg_chunk_problem& p, const eg_kv_cache& c, const vo
   return EG_OK;
 }
 
+// How a cache of heads of 128 columns is read with both halves of the columns
+// in one box, which small pages need: a box costs the same whatever it holds
+// (64 sequences' single tokens with a window of 4096, pages of 16: 178 us, with
+// a box for each half 213 us; pages of 64: 169 us either way).  1 where the
+// heads of a token lie side by side, so that the halves of all heads are one
+// dimension; 2 where the pages' heads are evenly apart, so that these are one;
+// 0 where neither holds, or the boxes are large.
+int grouped_of(const eg_chunk_problem& p, const eg_kv_cache& c, int box_rows) {
+  if (p.head_dim != 128 || box_rows > 32) return 0;
+  if (p.kv_heads == 1 || c.head_stride == 128) return 1;
+  if ((c.num_pages == 1 || c.page_stride == c.head_stride * p.kv_heads) && c.num_pages * p.kv_heads <= INT32_MAX) return 2;
+  return 0;
+}
+
+eg_status encode_grouped(const eg_chunk_problem& p, const eg_kv_cache& c, const void* base, int box_rows, int grouped, CUtensorMap* map) {
+  EncodeTiledFn fn = host_encode_tiled();
+  if (!fn) return host_fail(EG_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const cuuint64_t heads = static_cast<cuuint64_t>(p.kv_heads), pages = static_cast<cuuint64_t>(c.num_pages);
+  const cuuint64_t place_bytes = static_cast<cuuint64_t>(c.token_stride) * 2;
+  const cuuint64_t page_bytes = c.num_pages > 1 ? static_cast<cuuint64_t>(c.page_stride) * 2 : 16;
+  const cuuint64_t dims[5] = {64, 8, grouped == 1 ? 2 * heads : 2, static_cast<cuuint64_t>(p.page_size) / 8, grouped == 1 ? pages : pages * heads};
+  const cuuint64_t strides[4] = {place_bytes, 128, place_bytes * 8, grouped == 1 ? page_bytes : static_cast<cuuint64_t>(c.head_stride) * 2};
+  const cuuint32_t box[5] = {64, 8, 2, static_cast<cuuint32_t>(box_rows) / 8, 1};
+  const cuuint32_t steps[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(map, p.dtype == EG_EL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 5,
+                        const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return host_fail(EG_ERR_INVALID_ARG, "cuTensorMapEncodeTiled failed (%d) for the cache", static_cast<int>(r));
+  return EG_OK;
+}
+
 // The tensor map of queries: columns, heads, packed tokens; boxes of 64
 // columns by the heads of one cached head by `box_tokens` tokens.
 eg_status encode_queries(const eg_chunk_problem& p, const eg_chunk_args& a, int box_tokens, CUtensorMap* map) {
@@ -136,9 +167,10 @@ eg_status encode_queries(const eg_chunk_problem& p, const eg_chunk_args& a, int 
 using ChunkKernel = void (*)(ChunkParams, CUtensorMap, CUtensorMap, CUtensorMap);
 using JoinKernel = void (*)(ChunkParams);
 
-ChunkKernel main_kernel(const eg_chunk_plan& pl) {
-  if (pl.prob.dtype == EG_EL_BF16) return pl.hd == 64 ? chunk_kernel<__nv_bfloat16, 64> : chunk_kernel<__nv_bfloat16, 128>;
-  return pl.hd == 64 ? chunk_kernel<__half, 64> : chunk_kernel<__half, 128>;
+ChunkKernel main_kernel(const eg_chunk_plan& pl, bool grouped) {
+  if (pl.prob.dtype == EG_EL_BF16)
+    return pl.hd == 64 ? chunk_kernel<__nv_bfloat16, 64, false> : grouped ? chunk_kernel<__nv_bfloat16, 128, true> : chunk_kernel<__nv_bfloat16, 128, false>;
+  return pl.hd == 64 ? chunk_kernel<__half, 64, false> : grouped ? chunk_kernel<__half, 128, true> : chunk_kernel<__half, 128, false>;
 }
 JoinKernel join_kernel(const eg_chunk_plan& pl) {
   if (pl.prob.dtype == EG_EL_BF16) return pl.hd == 64 ? chunk_join_kernel<__nv_bfloat16, 64> : chunk_join_kernel<__nv_bfloat16, 128>;
@@ -194,9 +226,10 @@ eg_status set_up(eg_chunk_plan* pl) {
   pl->ws_bytes = pl->status_at + 16;
   if ((e = cudaMalloc(&pl->ws, pl->ws_bytes)) != cudaSuccess) return host_cuda_fail(e, "allocating the plan's workspace");
   if ((s = clear_words(pl, pl->meta_at, "clearing the plan's workspace")) != EG_OK) return s;
-  if ((e = cudaFuncSetAttribute(reinterpret_cast<const void*>(main_kernel(*pl)), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(pl->smem))) != cudaSuccess)
-    return host_cuda_fail(e, "cudaFuncSetAttribute");
+  for (bool grouped : {false, true})
+    if ((e = cudaFuncSetAttribute(reinterpret_cast<const void*>(main_kernel(*pl, grouped)), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  static_cast<int>(pl->smem))) != cudaSuccess)
+      return host_cuda_fail(e, "cudaFuncSetAttribute");
   pl->wait_limit_ns = host_wait_limit_ns();
   // One CTA reads at most the parts of the most CTAs that share an item (those
   // of a single sequence: the grid over the cached heads).  Up to 256 KB are
@@ -271,15 +304,20 @@ eg_status eg_chunk_plan_run(eg_chunk_plan* plan, const eg_chunk_args* args, cons
   p.wait_limit_ns = plan->wait_limit_ns, p.stall = plan->stall;
   CUtensorMap map_q, map_k, map_v;
   if ((s = encode_queries(b, a, p.box_tokens, &map_q)) != EG_OK) return s;
-  if ((s = encode_cache(b, *cache, cache->k, p.box_rows, p.heads_inner != 0, &map_k)) != EG_OK) return s;
-  if ((s = encode_cache(b, *cache, cache->v, p.box_rows, p.heads_inner != 0, &map_v)) != EG_OK) return s;
+  p.grouped = grouped_of(b, *cache, p.box_rows);
+  for (int i = 0; i < 2; ++i) {
+    const void* base = i ? cache->v : cache->k;
+    CUtensorMap* map = i ? &map_v : &map_k;
+    s = p.grouped ? encode_grouped(b, *cache, base, p.box_rows, p.grouped, map) : encode_cache(b, *cache, base, p.box_rows, p.heads_inner != 0, map);
+    if (s != EG_OK) return s;
+  }
 
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(plan->grid));
   cfg.blockDim = dim3(kChunkThreads);
   cfg.dynamicSmemBytes = plan->smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
-  cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan), p, map_q, map_k, map_v);
+  cudaError_t e = cudaLaunchKernelEx(&cfg, main_kernel(*plan, p.grouped != 0), p, map_q, map_k, map_v);
   if (e != cudaSuccess) return host_cuda_fail(e, "launching chunk attention");
   if (plan->joins_itself) return EG_OK;
   cudaLaunchAttribute attr[1];

@@ -261,13 +261,18 @@ struct ChunkShared {
 };
 static_assert(sizeof(ChunkShared) <= ChunkSmem<64>::kExtra, "fits the room after the tiles");
 
-template <typename T, int HD>
+// GROUPED: a box holds both halves of the columns, which lie in shared memory by
+// turns, 8 keys of each (ChunkParams::grouped); else each half has a box, and
+// all keys of the first half come first.
+template <typename T, int HD, bool GROUPED>
 __global__ void __launch_bounds__(kChunkThreads, 1)
     chunk_kernel(const ChunkParams p, const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v) {
   constexpr uint32_t kTile = ChunkSmem<HD>::kTileBytes;
   constexpr int kChunks = HD / 64;           // 64-column parts of a tile, 16 KB each
   constexpr uint32_t kPart = 128u * 128u;    // bytes of one part
+  // keys and values: bytes from 8 keys to the next 8, and from the first half of the columns to the other
+  constexpr uint32_t kKeys8 = GROUPED ? 2048u : 1024u, kHalf = GROUPED ? 1024u : kPart;
   constexpr uint32_t kFmt = sizeof(T) == 2 && El<T>::kBf16 ? 1u : 0u;
   // the scores' reference lies this far below their maximum, so that small
   // weights keep their bits as fp16 (its normal numbers end at 2^-14)
@@ -465,10 +470,16 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
         __syncwarp();
         if (has) {
-          const uint32_t dst = smem_u32(ring + slot * kTile) + lane * p.box_rows * 128u;
+          const uint32_t dst = smem_u32(ring + slot * kTile) + lane * p.box_rows * (kKeys8 / 8);
+          if constexpr (GROUPED) {
+            const bool there = page >= 0 && page < p.num_pages;  // reads as zeros else
+            if (p.grouped == 1) tma_load_5d(dst, map, &sh.full[slot], 0, 0, 2 * walk.head, off >> 3, page);
+            else tma_load_5d(dst, map, &sh.full[slot], 0, 0, 0, off >> 3, there ? page * p.kv_heads + walk.head : -1);
+          } else {
 #pragma unroll
-          for (int c = 0; c < kChunks; ++c)
-            tma_load_4d(dst + c * kPart, map, &sh.full[slot], c * 64, p.heads_inner ? walk.head : off, p.heads_inner ? off : walk.head, page);
+            for (int c = 0; c < kChunks; ++c)
+              tma_load_4d(dst + c * kPart, map, &sh.full[slot], c * 64, p.heads_inner ? walk.head : off, p.heads_inner ? off : walk.head, page);
+          }
         }
         return true;
       };
@@ -508,8 +519,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     constexpr uint32_t kIdescS = idesc_f32acc(kFmt, kFmt, 128, 128);
     constexpr uint32_t kIdescO = idesc_f32acc(kFmt, kFmt, 128, HD) | (1u << 16);  // values: keys are the strided index
     const uint32_t mine = warp - 9;
-    const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem)), k_desc = sdesc_k_sw128(smem_u32(ring));
-    const uint64_t v_desc = sdesc_mn_sw128(smem_u32(ring), kPart);
+    const uint64_t q_desc = sdesc_k_sw128(smem_u32(q_smem));
+    constexpr uint64_t kMore = static_cast<uint64_t>((kKeys8 - 1024) >> 4) << 32;  // of the stride from 8 keys to the next
+    const uint64_t k_desc = sdesc_k_sw128(smem_u32(ring)) + kMore, v_desc = sdesc_mn_sw128(smem_u32(ring), kHalf) + kMore;
     uint32_t segment = 0, used0 = 0, used1 = 0;  // segments, and tiles given to each warpgroup
     uint32_t slot0 = 0, turn0 = 0;               // the segment's first place in the ring, and how often the ring was full
     uint32_t turns = 0;                          // of a pair
@@ -536,7 +548,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const uint32_t w = tmem + s * 128, o = w + 256;
         umma_f16_ts(o, w, v, kIdescO, add ? 1 : 0);
 #pragma unroll
-        for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2048 >> 4), kIdescO);
+        for (int k = 1; k < 8; ++k) umma_f16_ts_add(o, w + k * 8, v + k * (2 * kKeys8 >> 4), kIdescO);
         umma_commit(&sh.o_done[s]);
         umma_commit(&sh.empty[slot_v]);
         if (!pair) umma_commit(&sh.empty[slot_v]);  // for the other issuer
@@ -548,8 +560,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         umma_f16(d, q, key, kIdescS, 0);
 #pragma unroll
         for (int k = 1; k < HD / 16; ++k) {
-          const uint32_t at = ((k / 4) * kPart + (k % 4) * 32) >> 4;
-          umma_f16_add(d, q + at, key + at, kIdescS);
+          umma_f16_add(d, q + (((k / 4) * kPart + (k % 4) * 32) >> 4), key + (((k / 4) * kHalf + (k % 4) * 32) >> 4), kIdescS);
         }
         umma_commit(&sh.s_full[s]);
         umma_commit(&sh.empty[slot_k]);
@@ -716,9 +727,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           const uint32_t at = base + attn_pos_v(i, count), slot = at % stages;
           if (!(ok = wait_all(&sh.full[slot], at / stages))) break;
           const int key = key0 + row_in;
-          uint8_t* v_row = ring + slot * kTile + row_in * 128;
+          uint8_t* v_row = ring + slot * kTile + (row_in >> 3) * kKeys8 + (row_in & 7) * 128;
           // a lane's pieces of its row, in an order that keeps lanes off each other's banks
-          auto piece = [&](int j) { return reinterpret_cast<uint4*>(v_row + (j >> 3) * kPart + ((j ^ lane) & 7) * 16); };
+          auto piece = [&](int j) { return reinterpret_cast<uint4*>(v_row + (j >> 3) * kHalf + ((j ^ lane) & 7) * 16); };
           if (key >= hi || (key < lo && key >= sinks)) {
 #pragma unroll
             for (int j = 0; j < kChunks * 8; ++j) *piece(j) = make_uint4(0, 0, 0, 0);
