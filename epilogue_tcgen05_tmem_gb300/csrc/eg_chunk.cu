@@ -208,10 +208,8 @@ eg_status set_up(eg_chunk_plan* pl) {
   pl->hd = p.head_dim <= 64 ? 64 : 128;
   const int group = p.q_heads / p.kv_heads;
   pl->tile_rows = 128 / row_box(group) * row_box(group);
-  // two tiles of rows share each key tile where a tree can have more than one;
-  // with one the second tile's shared memory is a stage of the ring (16
-  // sequences of 32 to 64 tokens of 64 heads over 8 cached: two 163 us, one at a
-  // time 197 us)
+  // two tiles of rows share each key tile where a chunk can have more than one;
+  // with one the second tile's shared memory is a stage of the ring
   pl->q_tiles = static_cast<int64_t>(p.max_chunk) * group > pl->tile_rows ? 2 : 1;
   const uint32_t tile = pl->hd == 64 ? ChunkSmem<64>::kTileBytes : ChunkSmem<128>::kTileBytes;
   const uint32_t extra = ChunkSmem<64>::kExtra;
@@ -233,11 +231,9 @@ eg_status set_up(eg_chunk_plan* pl) {
   pl->wait_limit_ns = host_wait_limit_ns();
   // One CTA reads at most the parts of the most CTAs that share an item (those
   // of a single sequence: the grid over the cached heads).  Up to 256 KB are
-  // joined by the last of them, which spares a second kernel (32 query heads
-  // over 8 cached ones, one token after 517 and after 8000, cold L2: 19.1 and
-  // 27.3 us, with the second kernel 21.1 and 32.4 us); above, the second kernel
-  // joins with the whole GPU (32 tokens after 8000: 33.4 us, 76 us by the last;
-  // 16 sequences of 32 to 64 tokens of 64 heads: 163 and 189 us).
+  // joined by the last of them, which spares a second kernel; above, that joins
+  // with the whole GPU.  Tree attention, which does the same, was measured at
+  // both sides of the bound.
   const int64_t parts = pl->grid / p.kv_heads + 2;
   pl->joins_itself = parts * rows_of(*pl) * pl->hd * 4 <= 256 * 1024;
   return EG_OK;

@@ -1,47 +1,51 @@
-// eg_chunk_kernel.cuh -- attention of drafted token trees over a paged cache.
+// eg_chunk_kernel.cuh -- attention of chunks of new tokens over a paged cache,
+// all of it or a sliding window and the first places.
 //
-// Mathematics.  The rows of one item are the n tokens of a sequence's tree
+// Mathematics.  The rows of one item are a group of a sequence's new tokens
 // times the G query heads that share a cached head: for key tiles of 128,
 //   S = Q K^T,  P = 2^(c S - m),  O += P V,  l += rowsum P,
 // with c = scale log2 e and m a row reference at least the row maximum less 8:
 // O and l are only brought to a new reference when the maximum grew by more
-// than 2^8, which few tiles do.  Weights are rounded to 16 bits for the second
-// product, whose operands are: at most 2^-8 (bf16) or 2^-11 (fp16) of each
-// weight, the output type's own rounding, which makes the error against 64 bits
-// up to 1.4 times that of weights in float32.  l sums them before that
-// rounding, in float32 as S, O and m are.
+// than 2^8, which few tiles do.  So weights are formed against the reference at
+// hand while the maximum is formed beside them, and a tile that turns out too
+// high is done again.  Weights are rounded to 16 bits for the second product,
+// whose operands are: at most 2^-8 (bf16) or 2^-11 (fp16) of each weight, the
+// output type's own rounding, which makes the error against 64 bits up to 1.4
+// times that of weights in float32.  l sums them before that rounding, in
+// float32 as S, O and m are.
 //
-// Work.  Every item has units for its key tiles (see kChunkFixed); all items'
-// units in a row are cut into equal ranges, one for each CTA (one CTA an SM),
-// on the device from the sequences' lengths.  An item that a cut divides leaves
-// float32 partial results that its last CTA or a second small kernel joins in a
-// fixed order, so equal inputs give equal bits.
+// Work.  Every item has units for the places that its rows attend to (see
+// kChunkFixed); all items' units in a row are cut into equal ranges, one for
+// each CTA (one CTA an SM), on the device from the sequences' lengths.  An item
+// that a cut divides leaves float32 partial results that its last CTA or a
+// second small kernel joins in a fixed order, so equal inputs give equal bits.
+// Tiles outside a window are not looked at, and boxes of keys that no row of
+// the item attends to are not loaded.
 //
-// One CTA: a producer warp (TMA boxes of pages into a ring of 128-key tiles,
-// K and V alike), one issuing thread (tcgen05.mma), two softmax warpgroups, a
-// warp that fetches queries and one that walks the range for the softmax
-// warpgroups (who spill registers when they do it: 4 % slower in the wide case below).  S and
-// O of both warpgroups fill tensor memory (4 x 128 columns); P overwrites S as
-// 16-bit values and feeds the second product from there.  With at most 128 rows
-// the warpgroups take turns on the key tiles and are joined at the end of the
-// range; with more rows each has 128 of them and K and V tiles are used twice.
-// So while one warpgroup forms weights the tensor cores work for the other.
+// One CTA: a producer warp (TMA boxes of pages into a ring of 128-key tiles, K
+// and V alike), two issuing warps (tcgen05.mma), two softmax warpgroups, and a
+// warp that walks the range for the warpgroups and fetches queries.  S and O of
+// both warpgroups fill tensor memory (4 x 128 columns); P overwrites S as 16-bit
+// values and feeds the second product from there.  With at most 128 rows the
+// warpgroups take turns on the key tiles and are joined at the end of the range;
+// with more rows (a pair) each has 128 of them and K and V tiles are used twice.
 //
-// Measured in succession, and what bounds it.  Two sequences of 98304 and
-// 131072 places, 32 query heads over 8 cached, one token each: 151 us, 6.2 TB/s
-// of the 6.8 that a copy reaches; CTAs get uneven shares of the bandwidth, and
-// the last decides.
-// 24 sequences of up to 13 tokens and 9001 places: 97 us, 4.3 TB/s; a CTA has
-// 2.1 segments, and each costs some 4 us beside its tiles.  16 sequences of 32
-// to 64 tokens, 64 query heads, 3800 to 8200 places: 167 us, 812 TFLOP/s of the
-// 1954 of a plain product.  There a tile's two products take 1050 cycles of
-// the tensor cores and its weights 1480 of their warpgroup (read and maximum
-// 380, exponentials 680, store and signal 320), so a warpgroup's turn is 1700
-// cycles where two full overlaps would be 1050.  Two warpgroups for each row
-// tile, half the keys each, were 17 % slower (104 registers a thread spill), and
-// so were a signal after half the weights (2 %) and scores in halves of 64 keys,
-// each formed while the other's weights are (25 %: products of 64 columns take
-// the tensor cores nearly as long as 128).
+// Measured in succession, and what bounds it.
+// One prompt of 8192 tokens, 32 query heads over 8 cached: 402 to 435 us from
+// run to run, 1.26 to 1.37 PFLOP/s of the 1.90 of a plain product; two chunks of
+// 512 after 65536 and 98304: 888 to 978 us, 1.41 to 1.55.  There a pair of
+// row tiles takes 2800 cycles a key tile where its products take 2060: from a
+// warpgroup's weights to its next scores, one after the other, pass 180 cycles
+// until the issuer sees them, 1300 of products and their start, 270 until the
+// scores are seen, 920 of weights, 220 of storing them.  One issuer for both was
+// 483 us for the prompt (each wait of the issuer costs 200 cycles that no
+// product hides), two that do not take turns 494 us (the warpgroups fall into
+// step), tiles that are masked through the fast path too 436 us.
+// Five prompts of 700 to 4001 tokens, 64 query heads over 8 cached, a window of
+// 1024: 511 to 541 us; an item has 9.3 tiles, three of them edges, and 7000
+// cycles from its last product to the next item's first.
+// 64 single tokens with a window of 4096: 176 us, 5.6 TB/s of the 6.8 that a
+// copy reaches (without a window 573 us, 6.6 TB/s).
 #pragma once
 #include "eg_attn.cuh"
 #include "eg_chunk.h"

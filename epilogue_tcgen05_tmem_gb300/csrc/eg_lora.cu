@@ -15,7 +15,20 @@
 // Tiles of at most 16 rows (single tokens) take the second product the other
 // way round: 128 outputs are the rows of tensor memory and the tokens its
 // columns, so that one product covers 128 outputs with no idle rows and a warp
-// writes neighbouring outputs of a token.
+// writes neighbouring outputs of a token.  In other tiles a lane has a row, and
+// rows go out through shared memory: stored from the lanes themselves, 32 rows
+// an instruction, the second kernel took 96 us for the five prompts below, so
+// 37 us.
+//
+// Measured in succession, bf16 (a copy reaches 6.8 TB/s).  Five prompts of 8191
+// tokens, 5120 to 5120, rank 64, added to a base: 70 us, 3.7 TB/s; each kernel
+// streams at 5.5 to 7 TB/s (11.6 us in the first, 29 in the second), and the
+// rest is what they cannot overlap: finding the work, the first boxes, the sum
+// over the cluster, the wait of the second for the first.  64 single tokens,
+// nearly each with its own adapter, 4096 to 12288, rank 64: 45 us, 2.7 TB/s; an
+// issuer's turn of 1000 cycles for 16 KB of B.  Two prompts among 31 single
+// tokens, 12288 to 4096, rank 128, fp16: 88 us; the first kernel reads x and A
+// of 6 MB a tile from L2 at what an SM takes in.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>
@@ -810,8 +823,9 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   if (a.base) EG_TRY(encode(a, a.base, a.outputs, a.rows, a.rows > 1 ? a.base_row : a.outputs, kBox, &map_base));
   else map_base = map_h;  // not used
 
-  // First kernel: two CTAs an SM, CTAs for those, at least four columns of 64
-  // each.
+  // First kernel: two CTAs an SM, a cluster as large as lets them all run at
+  // once (80 tiles of up to 12288 inputs as 320 CTAs: 58 us, as 160 50 us), at
+  // least four columns of 64 each.
   p.ring = (113 * 1024 - static_cast<int>(sizeof(LoraShared))) / 1024 * 1024;
   const int inner_bytes = p.ring + static_cast<int>(sizeof(LoraShared));
   p.splits = 1;
