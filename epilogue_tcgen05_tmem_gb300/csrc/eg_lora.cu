@@ -52,7 +52,8 @@ namespace {
   } while (0)
 
 constexpr int kTileRows = 128;  // rows of a tile, and outputs of one of the second product
-constexpr int kBox = 16;        // rows of one TMA box of x and h; tiles of at most as many are small
+constexpr int kBox = 16;        // rows of one TMA box of x; tiles of at most as many are small
+constexpr int kFew = 8;         // rows of one box of h; tiles of at most as many have h's two parts side by side
 constexpr int kInnerThreads = 224, kOuterThreads = 320;
 constexpr uint32_t kRowTile = 128u * 128u;  // bytes of 128 rows of 64 elements
 
@@ -208,20 +209,22 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
   // theirs while they wait for this kernel
   griddep_launch_dependents();
   const uint32_t tmem = sh.tmem;
-  const int from = p.chunks * part / p.splits, to = p.chunks * (part + 1) / p.splits;
-  const int count = to - from;
-  // Rows come in one box of 128, or 16 a box where that is less to read.  A
-  // stage has the rows that come and A's; a product reads 128 rows of it, the
-  // idle ones from whatever follows, so that much follows the last stage too.
+  // Rows come in one box of 128, or 16 a box where that is less to read; then a
+  // stage has two times 64 columns, since a stage's turn costs more than its
+  // few rows.  A product reads 128 rows of x, the idle ones from whatever
+  // follows, so that much follows the last stage too.
   const int boxes = (tile.rows + kBox - 1) / kBox;
   const bool big = boxes > 4;
-  const uint32_t x_bytes = big ? kRowTile : boxes * kBox * 128u, a_at = x_bytes;
-  const uint32_t stage_bytes = x_bytes + (p.rank16 * 128u + 1023u) / 1024u * 1024u;
-  const int stages = min(kStages, static_cast<int>((p.ring - max(stage_bytes, kRowTile)) / stage_bytes) + 1);
+  const int wide = big ? 1 : 2, units = (p.chunks + wide - 1) / wide;  // the last one's second half may be past x: zeros
+  const int from = units * part / p.splits, to = units * (part + 1) / p.splits;
+  const int count = to - from;
+  const uint32_t x_one = big ? kRowTile : boxes * kBox * 128u, a_one = (p.rank16 * 128u + 1023u) / 1024u * 1024u;
+  const uint32_t a_at = wide * x_one, stage_bytes = wide * (x_one + a_one);
+  const int stages = min(kStages, static_cast<int>((p.ring - max(stage_bytes, (wide - 1) * x_one + kRowTile)) / stage_bytes) + 1);
 
   if (warp == 0) {
     // ------------------------------------------------------- loads ----
-    const uint32_t bytes = x_bytes + p.rank * 128u;
+    const uint32_t bytes = wide * (x_one + p.rank * 128u);
     int i = 0, slot = 0, turn = 0;
     for (; i < count; ++i) {
       if (!__all_sync(0xffffffffu, lora_wait(sh, &sh.empty[slot], turn + 1, p.wait_limit_ns))) break;
@@ -229,9 +232,13 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
       if (!p.stall) {
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], bytes);
         __syncwarp();
-        if (big ? lane == 0 : lane < boxes)
-          tma_load_2d(stage + lane * kBox * 128, big ? &map_x : &map_box, &sh.full[slot], (from + i) * 64, tile.row0 + lane * kBox);
-        if (lane == 31) tma_load_2d(stage + a_at, &map_a, &sh.full[slot], (from + i) * 64, tile.adapter * p.rank);
+        const int k0 = (from + i) * wide * 64;
+        if (big) {
+          if (lane == 0) tma_load_2d(stage, &map_x, &sh.full[slot], k0, tile.row0);
+        } else if (lane < 2 * boxes) {
+          tma_load_2d(stage + (lane & 1) * x_one + (lane >> 1) * kBox * 128, &map_box, &sh.full[slot], k0 + (lane & 1) * 64, tile.row0 + (lane >> 1) * kBox);
+        }
+        if (lane >= 32 - wide) tma_load_2d(stage + a_at + (31 - lane) * a_one, &map_a, &sh.full[slot], k0 + (31 - lane) * 64, tile.adapter * p.rank);
       }
       if (++slot == stages) slot = 0, ++turn;
     }
@@ -258,6 +265,9 @@ __global__ void __launch_bounds__(kInnerThreads) lora_inner_kernel(const LoraPar
         if (elected()) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) umma_f16(d, x + k * 2, a + k * 2, idesc, i >= 2 || k > 0);
+          if (wide == 2)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_f16(d, x + (x_one >> 4) + k * 2, a + (a_one >> 4) + k * 2, idesc, 1);
           umma_commit(&sh.empty[slot]);
         }
       } else if (lane == 0) {
@@ -465,27 +475,28 @@ __device__ __forceinline__ bool find_range(const LoraParams& p, LoraShared& sh, 
 }
 
 // D = h B^T of STEPS steps of 16 for the high parts, and as many for the low
-// ones against the same B.  SMALL: D^T.
-template <bool SMALL, int STEPS>
+// ones against the same B.  HOW 1: D^T; 2: D^T of both parts at once, which are
+// rows of the same tile.
+template <int HOW, int STEPS>
 __device__ __forceinline__ void outer_products(uint32_t d, uint64_t h, uint64_t b, uint32_t idesc) {
 #pragma unroll
-  for (int k = 0; k < 2 * STEPS; ++k) {
+  for (int k = 0; k < (HOW == 2 ? STEPS : 2 * STEPS); ++k) {
     const int kb = k % STEPS;
     const uint64_t hk = h + (k / 4) * (kRowTile >> 4) + (k % 4) * 2, bk = b + (kb / 4) * (kRowTile >> 4) + (kb % 4) * 2;
-    umma_f16(d, SMALL ? bk : hk, SMALL ? hk : bk, idesc, k > 0);
+    umma_f16(d, HOW ? bk : hk, HOW ? hk : bk, idesc, k > 0);
   }
 }
-template <bool SMALL>
+template <int HOW>
 __device__ __forceinline__ void outer_products(int steps, uint32_t d, uint64_t h, uint64_t b, uint32_t idesc) {
   switch (steps) {
-    case 1: return outer_products<SMALL, 1>(d, h, b, idesc);
-    case 2: return outer_products<SMALL, 2>(d, h, b, idesc);
-    case 3: return outer_products<SMALL, 3>(d, h, b, idesc);
-    case 4: return outer_products<SMALL, 4>(d, h, b, idesc);
-    case 5: return outer_products<SMALL, 5>(d, h, b, idesc);
-    case 6: return outer_products<SMALL, 6>(d, h, b, idesc);
-    case 7: return outer_products<SMALL, 7>(d, h, b, idesc);
-    default: return outer_products<SMALL, 8>(d, h, b, idesc);
+    case 1: return outer_products<HOW, 1>(d, h, b, idesc);
+    case 2: return outer_products<HOW, 2>(d, h, b, idesc);
+    case 3: return outer_products<HOW, 3>(d, h, b, idesc);
+    case 4: return outer_products<HOW, 4>(d, h, b, idesc);
+    case 5: return outer_products<HOW, 5>(d, h, b, idesc);
+    case 6: return outer_products<HOW, 6>(d, h, b, idesc);
+    case 7: return outer_products<HOW, 7>(d, h, b, idesc);
+    default: return outer_products<HOW, 8>(d, h, b, idesc);
   }
 }
 
@@ -533,17 +544,21 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
       const LoraTile& tile = walk.tile;
       if (tile.adapter < 0) continue;
       // B does not wait for the first kernel, whose h follows the ring's filling
-      const int ahead = min(walk.count, p.stages_out), boxes = (tile.rows + kBox - 1) / kBox;
+      const int ahead = min(walk.count, p.stages_out);
       for (int i = 0; i <= walk.count; ++i) {
         if (i == ahead) {
           if (segment == 0) griddep_wait();
           if (!(ok = __all_sync(0xffffffffu, lora_wait(sh, &sh.h_empty, segment + 1, p.wait_limit_ns)))) break;
           if (!p.stall) {
-            if (lane == 0) mbar_arrive_expect_tx(&sh.h_full, boxes * kBox * 128u * h_parts);
+            // a few rows: the low parts follow the high ones, 8 rows on
+            const bool few = tile.rows <= kFew;
+            const int boxes = few ? 2 : (tile.rows + kFew - 1) / kFew, of_parts = few ? parts : h_parts;
+            if (lane == 0) mbar_arrive_expect_tx(&sh.h_full, boxes * of_parts * kFew * 128u);
             __syncwarp();
-            for (int j = lane; j < boxes * h_parts; j += 32) {
+            for (int j = lane; j < boxes * of_parts; j += 32) {
               const int part = j / boxes, box = j % boxes;
-              tma_load_2d(h_smem + part * kRowTile + box * kBox * 128, &map_h, &sh.h_full, part * 64, tile.row0 + box * kBox);
+              tma_load_2d(h_smem + part * kRowTile + box * kFew * 128, &map_h, &sh.h_full, part * 64 + (few ? box * p.rank16 : 0),
+                          tile.row0 + (few ? 0 : box * kFew));
             }
           }
           ++segment;
@@ -594,8 +609,9 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
           tc_fence_after();
           const uint64_t bs = b0 + (slot * b_bytes >> 4);
           if (elected()) {
-            if (small) outer_products<true>(steps, tmem + buf * kTileRows, h0, bs, idesc);
-            else outer_products<false>(steps, tmem + buf * kTileRows, h0, bs, idesc);
+            if (walk.tile.rows <= kFew) outer_products<2>(steps, tmem + buf * kTileRows, h0, bs, idesc);
+            else if (small) outer_products<1>(steps, tmem + buf * kTileRows, h0, bs, idesc);
+            else outer_products<0>(steps, tmem + buf * kTileRows, h0, bs, idesc);
             umma_commit(&sh.empty[slot]);
             umma_commit(&sh.acc_full[buf]);
             if (i + 1 == walk.count) umma_commit(&sh.h_empty);
@@ -659,6 +675,9 @@ __global__ void __launch_bounds__(kOuterThreads, 1) lora_outer_kernel(const Lora
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.acc_empty[group]);
+            if (tile.rows <= kFew)
+#pragma unroll
+              for (int t = 0; t < kFew; ++t) v[t] = __float_as_uint(__uint_as_float(v[t]) + __uint_as_float(v[t + kFew]));
             const int n = (sub0 + i) * kTileRows + row;
             const uint8_t* box = mine + aheads % kAhead * (2 * kBox * 128) + (row >> 6) * kBox * 128;
 #pragma unroll
@@ -817,7 +836,7 @@ eg_status launch(const eg_lora_args& a, LoraParams p, int tiles, int sms, int de
   // nothing is read of an empty bank, but a map has to have some place
   const uint64_t bank = std::max(a.adapters, 1);
   EG_TRY(encode(a, a.adapters ? a.a : a.x, a.inputs, bank * a.rank, a.inputs, a.rank, &map_a));
-  EG_TRY(encode(a, p.h, 2 * p.rank16, a.rows, 2 * p.rank16, kBox, &map_h));
+  EG_TRY(encode(a, p.h, 2 * p.rank16, a.rows, 2 * p.rank16, kFew, &map_h));
   EG_TRY(encode(a, a.adapters ? a.b : a.x, a.rank, bank * a.outputs, a.rank, kTileRows, &map_b));
 
   if (a.base) EG_TRY(encode(a, a.base, a.outputs, a.rows, a.rows > 1 ? a.base_row : a.outputs, kBox, &map_base));
