@@ -121,10 +121,41 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
+// A vector of a row's elements from k0 on, of which only those in [0, width)
+// are the row's: the others are zeros, and are not stored.
+template <typename T, int CH>
+__device__ __forceinline__ void load_part(Chunk<T, CH>& c, const T* row, int k0, int width) {
+  if (k0 >= 0 && k0 + CH <= width) return c.load(row + k0);
+  float f[CH];
+#pragma unroll
+  for (int e = 0; e < CH; ++e) f[e] = k0 + e >= 0 && k0 + e < width ? El<T>::to_float(row[k0 + e]) : 0.0f;
+  c.set(f);
+}
+template <typename T, int CH>
+__device__ __forceinline__ void store_part(const Chunk<T, CH>& c, T* row, int k0, int width) {
+  if (k0 >= 0 && k0 + CH <= width) return c.store(row + k0);
+  float f[CH];
+  c.get(f);
+#pragma unroll
+  for (int e = 0; e < CH; ++e)
+    if (k0 + e >= 0 && k0 + e < width) row[k0 + e] = El<T>::from_float(f[e]);
+}
+// The same from any address.
+template <typename T, int CH>
+__device__ __forceinline__ void load_singles(Chunk<T, CH>& c, const T* row, int k0, int width) {
+  float f[CH];
+#pragma unroll
+  for (int e = 0; e < CH; ++e) f[e] = k0 + e >= 0 && k0 + e < width ? El<T>::to_float(row[k0 + e]) : 0.0f;
+  c.set(f);
+}
+
 // Rows whose vectors of CH elements are aligned.  A thread keeps V vectors of
-// its row; WARP: a row is a warp's, else a CTA's.
-template <typename T, int CH, int V, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParams p) {
+// its row; WARP: a row is a warp's, else a CTA's.  SHIFT: rows start at any
+// element, all tensors' at the same place of a vector; the first vector starts
+// before the row and the last one ends behind it, and only the weight is read
+// by elements.
+template <typename T, int CH, int V, bool WARP, bool SHIFT>
+__global__ void __launch_bounds__(WARP ? 128 : SHIFT && V == 2 ? 512 : 1024) norm_kernel(const NormParams p) {
   // a linear plan launched as this kernel's dependent may stream its weights
   griddep_launch_dependents();
   __shared__ float red_sum[32];
@@ -132,14 +163,15 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
   const int row = WARP ? blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && row >= p.rows) return;
   const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, step = WARP ? 32 : blockDim.x;
-  const int vectors = p.width / CH;
+  const int shift = SHIFT ? static_cast<int>(row * (p.x_row & (CH - 1)) & (CH - 1)) : 0;  // elements before the row in its first vector
+  const int vectors = SHIFT ? (p.width + shift + CH - 1) / CH : p.width / CH;
   const T* x = static_cast<const T*>(p.x) + row * p.x_row;
   const T* w = static_cast<const T*>(p.weight);
   Chunk<T, CH> c[V], wc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
-    if (v < vectors) c[i].load(x + v * CH);
+    if (v < vectors) SHIFT ? load_part(c[i], x, v * CH - shift, p.width) : c[i].load(x + v * CH);
     else c[i].zero();
   }
   uint64_t s[V][CH / 2];  // the sum's pairs, then the normed ones
@@ -150,7 +182,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int v = i * step + tid;
-      if (v < vectors) d[i].load(r + v * CH);
+      if (v < vectors) SHIFT ? load_part(d[i], r, v * CH - shift, p.width) : d[i].load(r + v * CH);
       else d[i].zero();
     }
 #pragma unroll
@@ -158,13 +190,13 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
       const int v = i * step + tid;
 #pragma unroll
       for (int j = 0; j < CH / 2; ++j) c[i].set_pair(j, add2(c[i].pair(j), d[i].pair(j)));
-      if (v < vectors) c[i].store(sum + v * CH);
+      if (v < vectors) SHIFT ? store_part(c[i], sum, v * CH - shift, p.width) : c[i].store(sum + v * CH);
     }
   }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
-    if (v < vectors) wc[i].load(w + v * CH);
+    if (v < vectors) SHIFT ? load_singles(wc[i], w, v * CH - shift, p.width) : wc[i].load(w + v * CH);
     else wc[i].zero();
   }
   uint64_t square2 = 0;
@@ -194,12 +226,24 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
     }
     // a row without a vector here has zeros, which may be no numbers after the product
     if (v >= vectors) most[i] = 0.0f;
+    if (SHIFT && v < vectors && (v * CH < shift || v * CH - shift + CH > p.width)) {
+      most[i] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < CH / 2; ++j) {
+        const int k0 = v * CH - shift + 2 * j;
+        float a, b;
+        unpack64(s[i][j], &a, &b);
+        if (k0 >= 0 && k0 < p.width) most[i] = max_abs(most[i], a);
+        if (k0 + 1 >= 0 && k0 + 1 < p.width) most[i] = max_abs(most[i], b);
+      }
+    }
     top = max_abs(top, most[i]);
     if (p.out && v < vectors) {
       Chunk<T, CH> o;
 #pragma unroll
       for (int j = 0; j < CH / 2; ++j) o.set_pair(j, s[i][j]);
-      o.store(static_cast<T*>(p.out) + row * p.out_row + v * CH);
+      T* out = static_cast<T*>(p.out) + row * p.out_row;
+      SHIFT ? store_part(o, out, v * CH - shift, p.width) : o.store(out + v * CH);
     }
   }
   if (p.quant == EG_NORM_PLAIN) return;
@@ -226,8 +270,16 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
     uint32_t word[CH / 4];
 #pragma unroll
     for (int j = 0; j < CH / 4; ++j) word[j] = codes_of(s[i][2 * j], scale, inverse, int8) | codes_of(s[i][2 * j + 1], scale, inverse, int8) << 16;
-    if constexpr (CH == 8) *reinterpret_cast<uint2*>(codes + v * CH) = make_uint2(word[0], word[1]);
-    else *reinterpret_cast<uint32_t*>(codes + v * CH) = word[0];
+    if (SHIFT && (v * CH < shift || v * CH - shift + CH > p.width)) {
+#pragma unroll
+      for (int e = 0; e < CH; ++e) {
+        const int k0 = v * CH - shift + e;
+        if (k0 >= 0 && k0 < p.width) codes[k0] = static_cast<uint8_t>(word[e >> 2] >> (8 * (e & 3)));
+      }
+      continue;
+    }
+    if constexpr (CH == 8) *reinterpret_cast<uint2*>(codes + v * CH - shift) = make_uint2(word[0], word[1]);
+    else *reinterpret_cast<uint32_t*>(codes + v * CH - shift) = word[0];
   }
 }
 
@@ -374,20 +426,25 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* red) {
   return v;
 }
 
-template <typename T, int CH, int V>
+// SHIFT: as in norm_kernel; the CTAs are a multiple of CH in number, so that all
+// rows of one start at the same place of a vector.
+template <typename T, int CH, int V, bool SHIFT>
 __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_kernel(const NormGradParams p) {
   griddep_launch_dependents();
   __shared__ float2 red[2][32];
   extern __shared__ __align__(16) uint8_t smem[];
-  const int tid = threadIdx.x, step = blockDim.x, vectors = p.width / CH;
+  const int tid = threadIdx.x, step = blockDim.x;
+  const int shift = SHIFT ? static_cast<int>(blockIdx.x * (p.sum_row & (CH - 1)) & (CH - 1)) : 0;
+  const int vectors = SHIFT ? (p.width + shift + CH - 1) / CH : p.width / CH;
   uint64_t dw[V][CH / 2];
   Chunk<T, CH> d[V], z[V], add[V], w[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
 #pragma unroll
     for (int j = 0; j < CH / 2; ++j) dw[i][j] = 0;
-    if (i * step + tid < vectors) w[i].load(static_cast<const T*>(p.weight) + (i * step + tid) * CH);
-    else w[i].zero();
+    const int v = i * step + tid;
+    w[i].zero();
+    if (v < vectors) SHIFT ? load_singles(w[i], static_cast<const T*>(p.weight), v * CH - shift, p.width) : w[i].load(static_cast<const T*>(p.weight) + v * CH);
   }
   // Rows come to shared memory some turns ahead; a thread copies what it will
   // read itself, so they need no barrier.
@@ -398,9 +455,12 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
       for (int i = 0; i < V; ++i) {
         const int v = i * step + tid;
         if (v >= vectors) continue;
-        cp_async_16(place(stage, 0, i), static_cast<const T*>(p.d_out) + row * p.d_out_row + v * CH, 16);
-        cp_async_16(place(stage, 1, i), static_cast<const T*>(p.sum) + row * p.sum_row + v * CH, 16);
-        if (p.d_sum) cp_async_16(place(stage, 2, i), static_cast<const T*>(p.d_sum) + row * p.d_sum_row + v * CH, 16);
+        // what lies behind the row is not read; what lies before it in the first vector is the row before's
+        const int k0 = v * CH - shift;
+        const uint32_t bytes = SHIFT ? min(CH, p.width - k0) * static_cast<int>(sizeof(T)) : 16;
+        cp_async_16(place(stage, 0, i), static_cast<const T*>(p.d_out) + row * p.d_out_row + k0, bytes);
+        cp_async_16(place(stage, 1, i), static_cast<const T*>(p.sum) + row * p.sum_row + k0, bytes);
+        if (p.d_sum) cp_async_16(place(stage, 2, i), static_cast<const T*>(p.d_sum) + row * p.d_sum_row + k0, bytes);
       }
     }
     cp_async_commit();
@@ -419,6 +479,14 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
       d[i].load(reinterpret_cast<const T*>(place(stage, 0, i)));
       z[i].load(reinterpret_cast<const T*>(place(stage, 1, i)));
       if (p.d_sum) add[i].load(reinterpret_cast<const T*>(place(stage, 2, i)));
+      if (SHIFT && i == 0 && tid == 0) {
+        float f[CH], g[CH];
+        d[0].get(f), z[0].get(g);
+#pragma unroll
+        for (int e = 0; e < CH; ++e)
+          if (e < shift) f[e] = g[e] = 0.0f;
+        d[0].set(f), z[0].set(g);
+      }
     }
     uint64_t square2 = 0, gz2 = 0;
 #pragma unroll
@@ -450,7 +518,7 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
         o.set_pair(j, fma2(mul2(a, w[i].pair(j)), r2, fma2(b, back2, add[i].pair(j))));
         dw[i][j] = fma2(a, mul2(b, r2), dw[i][j]);
       }
-      if (v < vectors) o.store(dx + v * CH);
+      if (v < vectors) SHIFT ? store_part(o, dx, v * CH - shift, p.width) : o.store(dx + v * CH);
     }
   }
   if (!p.partial) return;
@@ -459,6 +527,17 @@ __global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
     if (v >= vectors) continue;
+    if (SHIFT) {
+#pragma unroll
+      for (int j = 0; j < CH / 2; ++j) {
+        const int k0 = v * CH - shift + 2 * j;
+        float a, b;
+        unpack64(dw[i][j], &a, &b);
+        if (k0 >= 0 && k0 < p.width) out[k0] = a;
+        if (k0 + 1 >= 0 && k0 + 1 < p.width) out[k0 + 1] = b;
+      }
+      continue;
+    }
 #pragma unroll
     for (int j = 0; j < CH / 2; j += 2) *reinterpret_cast<ulonglong2*>(out + v * CH + 2 * j) = make_ulonglong2(dw[i][j], dw[i][j + 1]);
   }
@@ -598,6 +677,15 @@ bool vectors_fit(int64_t width, int64_t rows, int ch, int bytes, std::initialize
   return true;
 }
 
+// Whether all rows start at the same place of a vector, those of the first row
+// on one.
+bool vectors_shift(int64_t width, int64_t rows, int ch, int bytes, int64_t stride, std::initializer_list<Operand> operands) {
+  if (width < ch) return false;
+  for (const Operand& o : operands)
+    if (o.ptr && (reinterpret_cast<uintptr_t>(o.ptr) % (ch * bytes) || (rows > 1 && (o.stride - stride) % ch))) return false;
+  return true;
+}
+
 // Vectors a thread holds of a row of `vectors` (`want`, or as many as it takes
 // for at most `most` threads, at most `limit`), and the threads of a row.
 void split_row(int vectors, int want, int most, int limit, int* v, int* threads) {
@@ -607,19 +695,27 @@ void split_row(int vectors, int want, int most, int limit, int* v, int* threads)
 }
 
 template <typename T, int CH>
+void launch_shifted(const NormParams& p, cudaStream_t st) {
+  int v = 0, threads = 0;
+  split_row(p.width / CH + 2, 2, 512, 4, &v, &threads);
+  if (v == 2) norm_kernel<T, CH, 2, false, true><<<p.rows, threads, 0, st>>>(p);
+  else norm_kernel<T, CH, 4, false, true><<<p.rows, threads, 0, st>>>(p);
+}
+
+template <typename T, int CH>
 void launch_norm(const NormParams& p, int v, int threads, cudaStream_t st) {
   if (threads == 32) {
     // four rows a CTA
     const unsigned grid = static_cast<unsigned>((p.rows + 3) / 4);
-    if (v == 1) norm_kernel<T, CH, 1, true><<<grid, 128, 0, st>>>(p);
-    else if (v == 2) norm_kernel<T, CH, 2, true><<<grid, 128, 0, st>>>(p);
-    else norm_kernel<T, CH, 4, true><<<grid, 128, 0, st>>>(p);
+    if (v == 1) norm_kernel<T, CH, 1, true, false><<<grid, 128, 0, st>>>(p);
+    else if (v == 2) norm_kernel<T, CH, 2, true, false><<<grid, 128, 0, st>>>(p);
+    else norm_kernel<T, CH, 4, true, false><<<grid, 128, 0, st>>>(p);
     return;
   }
-  if (v == 1) norm_kernel<T, CH, 1, false><<<p.rows, threads, 0, st>>>(p);
-  else if (v == 2) norm_kernel<T, CH, 2, false><<<p.rows, threads, 0, st>>>(p);
-  else if (v == 4) norm_kernel<T, CH, 4, false><<<p.rows, threads, 0, st>>>(p);
-  else norm_kernel<T, CH, 8, false><<<p.rows, threads, 0, st>>>(p);
+  if (v == 1) norm_kernel<T, CH, 1, false, false><<<p.rows, threads, 0, st>>>(p);
+  else if (v == 2) norm_kernel<T, CH, 2, false, false><<<p.rows, threads, 0, st>>>(p);
+  else if (v == 4) norm_kernel<T, CH, 4, false, false><<<p.rows, threads, 0, st>>>(p);
+  else norm_kernel<T, CH, 8, false, false><<<p.rows, threads, 0, st>>>(p);
 }
 
 // Threads of a row that holds `v` elements each.
@@ -641,15 +737,23 @@ void launch_singles(const NormGradParams& p, int grid, cudaStream_t st) {
   else norm_backward_any_kernel<T><<<grid, kAnyThreads, 0, st>>>(p);
 }
 
-template <typename T, int CH, int V>
+template <typename T, int CH, int V, bool SHIFT = false>
 eg_status launch_backward(NormGradParams p, int threads, int grid, int dev, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   // four rows ahead where two CTAs an SM have room for that, else two, else none
   const int stage = 3 * V * threads * 16;
   p.stages = 4 * stage <= 110 * 1024 ? 4 : 2 * stage <= 220 * 1024 ? 2 : 1;
-  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<T, CH, V>), 224 * 1024, dev, &allowed));
-  norm_backward_kernel<T, CH, V><<<grid, threads, p.stages * stage, st>>>(p);
+  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<T, CH, V, SHIFT>), 224 * 1024, dev, &allowed));
+  norm_backward_kernel<T, CH, V, SHIFT><<<grid, threads, p.stages * stage, st>>>(p);
   return EG_OK;
+}
+template <typename T, int CH>
+eg_status launch_shifted(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
+  int v = 0, threads = 0;
+  split_row(p.width / CH + 2, 1, 512, 4, &v, &threads);
+  return v == 1   ? launch_backward<T, CH, 1, true>(p, threads, grid, dev, st)
+         : v == 2 ? launch_backward<T, CH, 2, true>(p, threads, grid, dev, st)
+                  : launch_backward<T, CH, 4, true>(p, threads, grid, dev, st);
 }
 template <typename T, int CH>
 eg_status launch_backward(const NormGradParams& p, int v, int threads, int grid, int dev, cudaStream_t st) {
@@ -712,6 +816,12 @@ eg_status eg_add_rms_norm(const eg_norm_args* args, void* stream) {
     if (a.dtype == EG_EL_F32) launch_norm<float, 4>(p, v, threads, st);
     else if (a.dtype == EG_EL_BF16) launch_norm<__nv_bfloat16, 8>(p, v, threads, st);
     else launch_norm<__half, 8>(p, v, threads, st);
+  } else if (a.quant != EG_NORM_E4M3_BLOCK && a.width / ch + 2 <= 4 * 1024 &&
+             vectors_shift(a.width, a.rows, ch, bytes, a.x_row, {{a.x, a.x_row}, {a.residual, a.residual_row}, {a.residual ? a.sum : nullptr, a.sum_row}, {a.out, a.out_row}}) &&
+             (!quant || vectors_shift(a.width, a.rows, ch, 1, a.x_row, {{a.codes, a.codes_row}}))) {
+    if (a.dtype == EG_EL_F32) launch_shifted<float, 4>(p, st);
+    else if (a.dtype == EG_EL_BF16) launch_shifted<__nv_bfloat16, 8>(p, st);
+    else launch_shifted<__half, 8>(p, st);
   } else if (a.dtype == EG_EL_F32) launch_singles<float>(p, st);
   else if (a.dtype == EG_EL_BF16) launch_singles<__nv_bfloat16>(p, st);
   else launch_singles<__half>(p, st);
@@ -768,6 +878,11 @@ eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream) {
     EG_TRY(a.dtype == EG_EL_F32    ? (launch_backward<float, 4>(p, v, threads, grid, dev, st))
            : a.dtype == EG_EL_BF16 ? (launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, dev, st))
                                    : (launch_backward<__half, 8>(p, v, threads, grid, dev, st)));
+  } else if (a.width / ch + 2 <= (ch == 4 ? 4 * 1024 : 4 * 512) && (grid == a.rows || grid % ch == 0) &&
+             vectors_shift(a.width, a.rows, ch, bytes, a.sum_row, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}})) {
+    EG_TRY(a.dtype == EG_EL_F32    ? (launch_shifted<float, 4>(p, grid, dev, st))
+           : a.dtype == EG_EL_BF16 ? (launch_shifted<__nv_bfloat16, 8>(p, grid, dev, st))
+                                   : (launch_shifted<__half, 8>(p, grid, dev, st)));
   } else if (a.dtype == EG_EL_F32) launch_singles<float>(p, grid, st);
   else if (a.dtype == EG_EL_BF16) launch_singles<__nv_bfloat16>(p, grid, st);
   else launch_singles<__half>(p, grid, st);

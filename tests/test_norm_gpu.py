@@ -52,7 +52,8 @@ def _check_codes(r, h, quant, width):
     assert value.abs().max() <= (127 if quant == "int8" else 448)
 
 
-SHAPES = [(1, 1), (3, 7), (5, 8), (4, 64), (9, 100), (1, 128), (17, 256), (6, 1000), (5, 1024), (3, 1032), (7, 4096), (2, 5120), (2, 8200), (3, 16384), (1, 40000), (1, 65536)]
+SHAPES = [(1, 1), (3, 7), (5, 8), (4, 64), (9, 100), (1, 128), (17, 256), (6, 1000), (5, 1024), (3, 1032), (7, 4096), (2, 5120), (2, 8200), (3, 16384), (1, 40000), (1, 65536),
+          (21, 9), (10, 333), (9, 1001), (17, 4099), (6, 8202), (9, 12001), (5, 16383), (2, 20001)]  # rows at every place of a vector
 
 
 @pytest.mark.parametrize("rows,width", SHAPES)
@@ -103,6 +104,48 @@ def test_norm_of_strided_rows_in_place(shift):
         _check_out(y, h, "bf16", width)
         if quant:
             _check_codes(r, h, quant, width)
+
+
+@pytest.mark.parametrize("width", [100, 2500, 5000, 9000, 20000])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tensors_at_different_places_of_a_vector(width, dtype):
+    """x at an odd place, the others not: element by element, the gradient too."""
+    g = torch.Generator().manual_seed(width)
+    rows = 7
+    wide = rand(g, rows, width + 3, dtype=dtype).cuda()
+    x, res, w = wide[:, 1:1 + width], rand(g, rows, width, dtype=dtype).cuda(), rand(g, width, dtype=dtype).cuda()
+    z, h = _reference(x.cpu(), w.cpu(), res.cpu(), EPS)
+    for quant in (None, "e4m3", "int8"):
+        r = eg.add_rms_norm(x, w, res, EPS, quant=quant, keep_out=True)
+        assert torch.equal(r.sum.cpu().double(), z)
+        _check_out(r.out, h, dtype, width)
+        if quant:
+            _check_codes(r, h, quant, width)
+    dx, dw = eg.add_rms_norm_backward(x, res, w, EPS, d_sum=r.sum)
+    ref, size, ref_w, size_w = _gradient(x.cpu(), res.cpu(), w.cpu(), r.sum.cpu(), EPS)
+    assert ((dx.cpu().double() - ref).abs() <= UNIT[dtype] * ref.abs() + (3 * _steps(width) + 8) * F32 * size + TINY[dtype]).all()
+    assert ((dw.cpu().double() - ref_w).abs() <= (_steps(width) + 57) * F32 * size_w + 1e-37).all()
+
+
+def test_rows_beside_others_are_left_as_they_were():
+    """Odd rows with others between them, in place: the vectors at their ends hold elements of those."""
+    g = torch.Generator().manual_seed(31)
+    wide = rand(g, 40, 2 * 333 + 7).cuda()
+    res, w, d = rand(g, 40, 2 * 333 + 7).cuda(), rand(g, 333).cuda(), rand(g, 40, 2 * 333 + 7).cuda()
+    kept = [t.clone() for t in (wide, res, d)]
+    x, r, dd = (t[:, 328:328 + 333] for t in (wide, res, d))
+    z, h = _reference(x.cpu(), w.cpu(), r.cpu(), EPS)
+    eg.add_rms_norm(x, w, r, EPS, out=x, sum_out=r)
+    assert torch.equal(r.cpu().double(), z)
+    _check_out(x, h, "bf16", 333)
+    ref, size, ref_w, size_w = _gradient(dd.cpu(), r.cpu(), w.cpu(), None, EPS)
+    dx, dw = eg.add_rms_norm_backward(dd, r, w, EPS, dx=dd)
+    # not bit for bit what another alignment gives: a thread's elements, so the order of a row's sum, go by it
+    assert ((dx.cpu().double() - ref).abs() <= UNIT["bf16"] * ref.abs() + (3 * _steps(333) + 8) * F32 * size + TINY["bf16"]).all()
+    assert ((dw.cpu().double() - ref_w).abs() <= (_steps(333) + 57) * F32 * size_w + 1e-37).all()
+    for t, old in zip((wide, res, d), kept):
+        t[:, 328:328 + 333] = old[:, 328:328 + 333]
+        assert torch.equal(t, old)
 
 
 def test_a_residual_broadcast_over_rows():
@@ -235,7 +278,8 @@ def _gradient(d_out, z, weight, d_sum, eps):
     return dx, size, terms.sum(0), terms.abs().sum(0)
 
 
-@pytest.mark.parametrize("rows,width", [(1, 1), (3, 7), (2, 8), (40, 100), (7, 256), (700, 264), (1300, 64), (5, 1000), (9, 4096), (2, 8200), (3, 16384), (1, 40000)])
+@pytest.mark.parametrize("rows,width", [(1, 1), (3, 7), (2, 8), (40, 100), (7, 256), (700, 264), (1300, 64), (5, 1000), (9, 4096), (2, 8200), (3, 16384), (1, 40000),
+                                        (21, 9), (400, 333), (1300, 1001), (700, 77), (310, 4099), (6, 8202), (9, 12001), (5, 16383), (2, 20001)])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("with_sum", [True, False])
 def test_gradient(rows, width, dtype, with_sum):
