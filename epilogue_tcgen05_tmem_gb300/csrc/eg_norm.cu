@@ -428,8 +428,8 @@ __device__ __forceinline__ float2 cta_sum2(float2 v, float2* red) {
 
 // SHIFT: as in norm_kernel; the CTAs are a multiple of CH in number, so that all
 // rows of one start at the same place of a vector.
-template <typename T, int CH, int V, bool SHIFT>
-__global__ void __launch_bounds__(V == 4 && CH == 4 ? 1024 : 512) norm_backward_kernel(const NormGradParams p) {
+template <typename T, int CH, int V, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormGradParams p) {
   griddep_launch_dependents();
   __shared__ float2 red[2][32];
   extern __shared__ __align__(16) uint8_t smem[];
@@ -737,14 +737,14 @@ void launch_singles(const NormGradParams& p, int grid, cudaStream_t st) {
   else norm_backward_any_kernel<T><<<grid, kAnyThreads, 0, st>>>(p);
 }
 
-template <typename T, int CH, int V, bool SHIFT = false>
+template <typename T, int CH, int V, bool SHIFT = false, int THREADS = 512>
 eg_status launch_backward(NormGradParams p, int threads, int grid, int dev, cudaStream_t st) {
   static std::atomic<uint64_t> allowed{0};
   // four rows ahead where two CTAs an SM have room for that, else two, else none
   const int stage = 3 * V * threads * 16;
   p.stages = 4 * stage <= 110 * 1024 ? 4 : 2 * stage <= 220 * 1024 ? 2 : 1;
-  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<T, CH, V, SHIFT>), 224 * 1024, dev, &allowed));
-  norm_backward_kernel<T, CH, V, SHIFT><<<grid, threads, p.stages * stage, st>>>(p);
+  EG_TRY(host_allow_smem(reinterpret_cast<const void*>(norm_backward_kernel<T, CH, V, SHIFT, THREADS>), 224 * 1024, dev, &allowed));
+  norm_backward_kernel<T, CH, V, SHIFT, THREADS><<<grid, threads, p.stages * stage, st>>>(p);
   return EG_OK;
 }
 template <typename T, int CH>
@@ -753,13 +753,15 @@ eg_status launch_shifted(const NormGradParams& p, int grid, int dev, cudaStream_
   split_row(p.width / CH + 2, 1, 512, 4, &v, &threads);
   return v == 1   ? launch_backward<T, CH, 1, true>(p, threads, grid, dev, st)
          : v == 2 ? launch_backward<T, CH, 2, true>(p, threads, grid, dev, st)
-                  : launch_backward<T, CH, 4, true>(p, threads, grid, dev, st);
+         : threads <= 512 ? launch_backward<T, CH, 4, true>(p, threads, grid, dev, st)
+                          : launch_backward<T, CH, 4, true, 1024>(p, threads, grid, dev, st);
 }
 template <typename T, int CH>
 eg_status launch_backward(const NormGradParams& p, int v, int threads, int grid, int dev, cudaStream_t st) {
   return v == 1   ? launch_backward<T, CH, 1>(p, threads, grid, dev, st)
          : v == 2 ? launch_backward<T, CH, 2>(p, threads, grid, dev, st)
-                  : launch_backward<T, CH, 4>(p, threads, grid, dev, st);
+         : threads <= 512 ? launch_backward<T, CH, 4>(p, threads, grid, dev, st)
+                          : launch_backward<T, CH, 4, false, 1024>(p, threads, grid, dev, st);
 }
 
 // Most CTAs of the gradient: each leaves a row of sums.
