@@ -25,10 +25,10 @@
 // streams at 5.5 to 7 TB/s (11.6 us in the first, 29 in the second), and the
 // rest is what they cannot overlap: finding the work, the first boxes, the sum
 // over the cluster, the wait of the second for the first.  64 single tokens,
-// nearly each with its own adapter, 4096 to 12288, rank 64: 45 us, 2.7 TB/s; an
-// issuer's turn of 1000 cycles for 16 KB of B.  Two prompts among 31 single
-// tokens, 12288 to 4096, rank 128, fp16: 88 us; the first kernel reads x and A
-// of 6 MB a tile from L2 at what an SM takes in.
+// nearly each with its own adapter, 4096 to 12288, rank 64: 41 us, 3.0 TB/s (45
+// us with h's two parts one after the other and 64 inputs a stage).  Two prompts
+// among 31 single tokens, 12288 to 4096, rank 128, fp16: 84 us; the first kernel
+// reads x and A of 6 MB a tile from L2 at what an SM takes in.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math_constants.h>

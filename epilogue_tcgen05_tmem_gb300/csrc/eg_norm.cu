@@ -17,8 +17,13 @@
 // asynchronous copies four ahead, for with one ahead in registers an SM had too
 // little on its way (111 us).
 //
+// Rows of an odd width start at any place of a vector.  Where all tensors' do at
+// the same, vectors that begin before the row and end behind it are used (8191
+// rows of 5121 to E4M3 73 us, element by element 180 us, 5120 columns 49 us;
+// gradient 80, 383 and 55 us).
+//
 // The sums of squares are float32, at most 32 a thread before the trees of a
-// warp and of the CTA.
+// warp and of the CTA (a 256th of the row where registers do not hold it).
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -283,10 +288,9 @@ __global__ void __launch_bounds__(WARP ? 128 : SHIFT && V == 2 ? 512 : 1024) nor
   }
 }
 
-// Rows that do not start on a vector, or whose width is no multiple of one:
-// element by element, V of them in a thread's registers.  A warp has 128
-// neighbouring columns at a time, a lane every 32nd of them, so a block of the
-// block scales is a warp's.
+// Rows that start at different places of a vector: element by element, V of
+// them in a thread's registers.  A warp has 128 neighbouring columns at a time,
+// a lane every 32nd of them, so a block of the block scales is a warp's.
 template <typename T, int V>
 __global__ void __launch_bounds__(1024) norm_single_kernel(const NormParams p) {
   griddep_launch_dependents();
@@ -543,7 +547,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormGradPa
   }
 }
 
-// The same for rows that do not start on a vector.
+// The same for rows that start at different places of a vector.
 template <typename T, int V, int THREADS>
 __global__ void __launch_bounds__(THREADS, 1) norm_backward_single_kernel(const NormGradParams p) {
   griddep_launch_dependents();
