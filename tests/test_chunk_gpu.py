@@ -275,6 +275,29 @@ def test_queries_and_results_by_strides():
     plan.close()
 
 
+@pytest.mark.parametrize("page", [8, 16, 40, 256])
+@pytest.mark.parametrize("layout", ["keys and values in turn", "wide heads", "heads first, keys and values in turn"])
+def test_caches_by_strides(page, layout):
+    """Caches that are parts of other tensors, small pages (boxes of both halves of the columns, where the strides allow them) and large."""
+    c = Case("bf16", 8, 2, 128, page, [700, 90], [150, 1], 200, 3, seed=page)
+    d, plan = c.device(), c.plan()
+    pages = d["k_cache"].shape[0]
+    if layout == "keys and values in turn":
+        both = torch.full((pages, 2, page, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+        k, v = both[:, 0], both[:, 1]
+    elif layout == "wide heads":
+        k, v = torch.full((2, pages, page, 2, 192), math.nan, dtype=torch.bfloat16, device="cuda")[..., 64:]
+    else:
+        both = torch.full((pages, 2, 2, page, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+        k, v = both[:, 0].permute(0, 2, 1, 3), both[:, 1].permute(0, 2, 1, 3)
+    k.copy_(d["k_cache"]), v.copy_(d["v_cache"])
+    _check(c, plan.run(**dict(d, k_cache=k, v_cache=v)))
+    d["block_table"][1, 1:] = torch.where(d["block_table"][1, 1:] < 0, 1 << 30, d["block_table"][1, 1:])  # past the pages: any number
+    _check(c, plan.run(**dict(d, k_cache=k, v_cache=v)))
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
 def test_same_every_time_and_on_another_stream():
     c = Case("bf16", 32, 8, 128, 16, [3000, 20, 0, 911], [50, 1, 300, 8], 700, 3, seed=9)
     d, plan = c.device(), c.plan()

@@ -263,6 +263,26 @@ def test_codes_go_into_a_linear_plan(quant, scale):
     assert ((y.cpu().double() - ref).abs() <= 2.0 ** -8 * ref.abs() + 2.0 ** -13 * size).all()
 
 
+def test_a_plan_may_start_while_the_norm_runs():
+    """A linear plan as the norm's programmatic dependent: its inputs are the codes and scales of this call, not of the last one."""
+    g = torch.Generator().manual_seed(11)
+    rows, width, outputs = 64, 2048, 512
+    w, weight = rand(g, width).cuda(), torch.randn(outputs, width, generator=g).to(torch.float8_e4m3fn).view(torch.uint8).cuda()
+    s_w = (torch.rand(outputs, generator=g) + 0.5).cuda()
+    plans = [eg.Plan(rows, outputs, width, "e4m3", "token_channel", pdl=pdl) for pdl in (True, False)]
+    inputs = [(rand(g, rows, width).cuda(), rand(g, rows, width, scale=3.0).cuda()) for _ in range(12)]
+    got = []
+    for plan in plans:
+        outs = [torch.empty(rows, outputs, dtype=torch.bfloat16, device="cuda") for _ in inputs]
+        for (x, res), y in zip(inputs, outs):
+            r = eg.add_rms_norm(x, w, res, quant="e4m3")
+            plan.run(r.codes, weight, y, s_a=r.scales, s_w=s_w)
+        torch.cuda.synchronize()
+        assert plan.device_status() == eg.EG_OK
+        got.append(outs)
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
 # --------------------------------------------------------------- gradient --
 
 def _gradient(d_out, z, weight, d_sum, eps):
