@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormGradPa
   for (int i = 0; i < V; ++i) {
     const int v = i * step + tid;
     if (v >= vectors) continue;
-    if (SHIFT) {
+    if constexpr (SHIFT) {
 #pragma unroll
       for (int j = 0; j < CH / 2; ++j) {
         const int k0 = v * CH - shift + 2 * j;
@@ -540,10 +540,10 @@ __global__ void __launch_bounds__(THREADS) norm_backward_kernel(const NormGradPa
         if (k0 >= 0 && k0 < p.width) out[k0] = a;
         if (k0 + 1 >= 0 && k0 + 1 < p.width) out[k0 + 1] = b;
       }
-      continue;
-    }
+    } else {
 #pragma unroll
-    for (int j = 0; j < CH / 2; j += 2) *reinterpret_cast<ulonglong2*>(out + v * CH + 2 * j) = make_ulonglong2(dw[i][j], dw[i][j + 1]);
+      for (int j = 0; j < CH / 2; j += 2) *reinterpret_cast<ulonglong2*>(out + v * CH + 2 * j) = make_ulonglong2(dw[i][j], dw[i][j + 1]);
+    }
   }
 }
 
@@ -710,15 +710,10 @@ template <typename T, int CH>
 void launch_norm(const NormParams& p, int v, int threads, cudaStream_t st) {
   if (threads == 32) {
     // four rows a CTA
-    const unsigned grid = static_cast<unsigned>((p.rows + 3) / 4);
-    if (v == 1) norm_kernel<T, CH, 1, true, false><<<grid, 128, 0, st>>>(p);
-    else if (v == 2) norm_kernel<T, CH, 2, true, false><<<grid, 128, 0, st>>>(p);
-    else norm_kernel<T, CH, 4, true, false><<<grid, 128, 0, st>>>(p);
+    norm_kernel<T, CH, 4, true, false><<<static_cast<unsigned>((p.rows + 3) / 4), 128, 0, st>>>(p);
     return;
   }
-  if (v == 1) norm_kernel<T, CH, 1, false, false><<<p.rows, threads, 0, st>>>(p);
-  else if (v == 2) norm_kernel<T, CH, 2, false, false><<<p.rows, threads, 0, st>>>(p);
-  else if (v == 4) norm_kernel<T, CH, 4, false, false><<<p.rows, threads, 0, st>>>(p);
+  if (v == 4) norm_kernel<T, CH, 4, false, false><<<p.rows, threads, 0, st>>>(p);
   else norm_kernel<T, CH, 8, false, false><<<p.rows, threads, 0, st>>>(p);
 }
 
@@ -751,21 +746,17 @@ eg_status launch_backward(NormGradParams p, int threads, int grid, int dev, cuda
   norm_backward_kernel<T, CH, V, SHIFT, THREADS><<<grid, threads, p.stages * stage, st>>>(p);
   return EG_OK;
 }
-template <typename T, int CH>
-eg_status launch_shifted(const NormGradParams& p, int grid, int dev, cudaStream_t st) {
+// Rows of `vectors` vectors; more than 512 threads only in float32, whose rows
+// of up to 16384 columns are twice as many vectors.
+template <typename T, int CH, bool SHIFT>
+eg_status launch_rows(const NormGradParams& p, int vectors, int grid, int dev, cudaStream_t st) {
   int v = 0, threads = 0;
-  split_row(p.width / CH + 2, 1, 512, 4, &v, &threads);
-  return v == 1   ? launch_backward<T, CH, 1, true>(p, threads, grid, dev, st)
-         : v == 2 ? launch_backward<T, CH, 2, true>(p, threads, grid, dev, st)
-         : threads <= 512 ? launch_backward<T, CH, 4, true>(p, threads, grid, dev, st)
-                          : launch_backward<T, CH, 4, true, 1024>(p, threads, grid, dev, st);
-}
-template <typename T, int CH>
-eg_status launch_backward(const NormGradParams& p, int v, int threads, int grid, int dev, cudaStream_t st) {
-  return v == 1   ? launch_backward<T, CH, 1>(p, threads, grid, dev, st)
-         : v == 2 ? launch_backward<T, CH, 2>(p, threads, grid, dev, st)
-         : threads <= 512 ? launch_backward<T, CH, 4>(p, threads, grid, dev, st)
-                          : launch_backward<T, CH, 4, false, 1024>(p, threads, grid, dev, st);
+  split_row(vectors, 1, 512, 4, &v, &threads);
+  if (v == 1) return launch_backward<T, CH, 1, SHIFT>(p, threads, grid, dev, st);
+  if (v == 2) return launch_backward<T, CH, 2, SHIFT>(p, threads, grid, dev, st);
+  if constexpr (CH == 4)
+    if (threads > 512) return launch_backward<T, CH, 4, SHIFT, 1024>(p, threads, grid, dev, st);
+  return launch_backward<T, CH, 4, SHIFT>(p, threads, grid, dev, st);
 }
 
 // Most CTAs of the gradient: each leaves a row of sums.
@@ -879,16 +870,16 @@ eg_status eg_add_rms_norm_backward(const eg_norm_grads* args, void* stream) {
   const int ch = 16 / bytes;
   const bool fits = a.width / ch <= (ch == 4 ? 4 * 1024 : 4 * 512) && vectors_fit(a.width, a.rows, ch, bytes, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.weight, 0}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}});
   if (fits) {
-    int v = 0, threads = 0;
-    split_row(p.width / ch, 1, 512, 4, &v, &threads);
-    EG_TRY(a.dtype == EG_EL_F32    ? (launch_backward<float, 4>(p, v, threads, grid, dev, st))
-           : a.dtype == EG_EL_BF16 ? (launch_backward<__nv_bfloat16, 8>(p, v, threads, grid, dev, st))
-                                   : (launch_backward<__half, 8>(p, v, threads, grid, dev, st)));
+    const int vectors = p.width / ch;
+    EG_TRY(a.dtype == EG_EL_F32    ? (launch_rows<float, 4, false>(p, vectors, grid, dev, st))
+           : a.dtype == EG_EL_BF16 ? (launch_rows<__nv_bfloat16, 8, false>(p, vectors, grid, dev, st))
+                                   : (launch_rows<__half, 8, false>(p, vectors, grid, dev, st)));
   } else if (a.width / ch + 2 <= (ch == 4 ? 4 * 1024 : 4 * 512) && (grid == a.rows || grid % ch == 0) &&
              vectors_shift(a.width, a.rows, ch, bytes, a.sum_row, {{a.d_out, a.d_out_row}, {a.sum, a.sum_row}, {a.d_sum, a.d_sum_row}, {a.dx, a.dx_row}})) {
-    EG_TRY(a.dtype == EG_EL_F32    ? (launch_shifted<float, 4>(p, grid, dev, st))
-           : a.dtype == EG_EL_BF16 ? (launch_shifted<__nv_bfloat16, 8>(p, grid, dev, st))
-                                   : (launch_shifted<__half, 8>(p, grid, dev, st)));
+    const int vectors = p.width / ch + 2;
+    EG_TRY(a.dtype == EG_EL_F32    ? (launch_rows<float, 4, true>(p, vectors, grid, dev, st))
+           : a.dtype == EG_EL_BF16 ? (launch_rows<__nv_bfloat16, 8, true>(p, vectors, grid, dev, st))
+                                   : (launch_rows<__half, 8, true>(p, vectors, grid, dev, st)));
   } else if (a.dtype == EG_EL_F32) launch_singles<float>(p, grid, st);
   else if (a.dtype == EG_EL_BF16) launch_singles<__nv_bfloat16>(p, grid, st);
   else launch_singles<__half>(p, grid, st);
