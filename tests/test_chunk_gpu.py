@@ -298,6 +298,28 @@ def test_caches_by_strides(page, layout):
     plan.close()
 
 
+def test_offsets_past_32_bits():
+    """Pages behind 2^31 elements of the cache, also where values that are not finite are read again."""
+    c = Case("bf16", 8, 2, 128, 256, [700, 60], [150, 10], seed=43)
+    d, plan = c.device(), c.plan()
+    pages, used = 33000, d["k_cache"].shape[0]
+    assert (pages - used) * 256 * 2 * 128 > 1 << 31
+    d["block_table"] = torch.where(d["block_table"] < 0, -1, d["block_table"] + (pages - used))
+    for name in ("k_cache", "v_cache"):
+        cache = torch.full((pages, 256, 2, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+        cache[-used:] = d[name]
+        d[name] = cache
+    o = plan.run(**d)
+    _check(c, o)
+    d["v_cache"][int(d["block_table"][1, 0]), 0, 1, 5] = INF  # the second sequence's first place, cached head 1
+    again = plan.run(**d)
+    assert (again[150:, 4:, 5] == INF).all()
+    again[150:, 4:, 5] = o[150:, 4:, 5]
+    assert torch.equal(again, o)
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
 def test_same_every_time_and_on_another_stream():
     c = Case("bf16", 32, 8, 128, 16, [3000, 20, 0, 911], [50, 1, 300, 8], 700, 3, seed=9)
     d, plan = c.device(), c.plan()

@@ -249,6 +249,21 @@ def test_beside_a_linear_plan(act):
         _check(c, eg.lora(**dict(d, base=y), out=y))
 
 
+def test_offsets_past_32_bits():
+    c = Case("bf16", [5, 130], [1, 0], 64, 8200, 16, 2, seed=41)
+    rows, last = 262150, sum(c.n)
+    assert (rows - last) * 8200 > 1 << 31
+    d = c.device()
+    wide = torch.full((rows, 8200), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = wide.clone()
+    x = wide[:, 8:72]
+    x[-last:], out[-last:] = d["x"], d["base"]
+    eg.lora(**dict(d, x=x, seq_start=d["seq_start"] + (rows - last), base=out, out=out))
+    assert eg.lora_device_status() == eg.EG_OK
+    _check(c, out[-last:])
+    assert (out[:-last] == 7).all()
+
+
 def test_nothing_to_do():
     c = Case("bf16", [4], [0], 64, 64, 8, 2)
     d = c.device()

@@ -353,6 +353,46 @@ def test_gradient_in_place_and_strided():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("width", [1001, 512])
+def test_gradient_in_place_of_many_rows(width):
+    """Rows that share a vector with the next one's start, over the gradient they come from; and two calls at once."""
+    g = torch.Generator().manual_seed(width)
+    rows = 2003
+    z, d, ds = (rand(g, rows, width).cuda() for _ in range(3))
+    w = rand(g, width).cuda()
+    ref = eg.add_rms_norm_backward(d, z, w, d_sum=ds)
+    for over in range(2):
+        both = [d.clone(), ds.clone()]
+        dx, dw = eg.add_rms_norm_backward(both[0], z, w, d_sum=both[1], dx=both[over])
+        assert dx is both[over] and torch.equal(dx, ref[0]) and torch.equal(dw, ref[1])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [eg.add_rms_norm_backward(d, z, w, d_sum=ds, stream=s.cuda_stream) for _ in range(4) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, ref[0]) and torch.equal(y, ref[1]) for x, y in got)
+
+
+def test_offsets_past_32_bits():
+    g = torch.Generator().manual_seed(31)
+    rows, width, last = 524297, 4104, 5
+    assert rows * width > 1 << 31
+    x = torch.zeros(rows, width, dtype=torch.bfloat16, device="cuda")
+    x[-last:] = rand(g, last, width, scale=2.0).cuda()
+    res, w = rand(g, 1, width).cuda(), rand(g, width).cuda()
+    big = eg.add_rms_norm(x, w, res.expand(rows, width), quant="e4m3", keep_out=True)
+    small = eg.add_rms_norm(x[-last:], w, res.expand(last, width), quant="e4m3", keep_out=True)
+    for a, b in zip(big, small):
+        assert torch.equal(a[-last:], b)
+    total = big.sum
+    del big
+    d = x
+    d.zero_()
+    d[-1] = rand(g, width).cuda()  # one row: the weight's gradient is its product, whatever the order of sums
+    dx, dw = eg.add_rms_norm_backward(d, total, w)
+    one = eg.add_rms_norm_backward(d[-last:], total[-last:], w)
+    assert torch.equal(dx[-last:], one[0]) and torch.equal(dw, one[1]) and dx[:last].abs().max() == 0
+
+
 def test_refusals_of_the_binding():
     x, w = torch.zeros(4, 64, device="cuda"), torch.ones(64, device="cuda")
     for bad in (lambda: eg.add_rms_norm(x.cpu(), w), lambda: eg.add_rms_norm(x[0], w), lambda: eg.add_rms_norm(x, w[:32]),
