@@ -8,16 +8,14 @@
 
 namespace eg {
 
-// What a CTA of the main kernel tells the joining kernel: where its range of
-// work units starts and which item (sequence, cached head, row group) that
-// unit belongs to.
-struct ChunkMeta {
-  int64_t from;         // the CTA's first unit
-  int64_t begin;        // the first unit of the item that holds it,
-  int64_t lead, last;   // and the first units of that item's first and last tile
-  int64_t total;        // units of the run
-  int32_t ctas, team;   // teams that have units, and CTAs of each
-  int32_t start, rows, row0, head;  // the item's first packed row, rows, first row in the sequence, cached head
+// What a CTA of the main kernel tells the joining kernel: the item (sequence,
+// cached head, row group) whose first cut is the start of its range of work
+// units, where there is one that CTAs share.
+struct __align__(16) ChunkMeta {
+  int32_t rows;               // of the item; 0: there is none
+  int32_t lead, last, team;   // CTAs lead, lead + team, ... last have parts of it
+  int32_t start, row0, head;  // its first packed row, first row in the sequence, cached head
+  int32_t pad;
 };
 
 struct ChunkParams {
@@ -51,7 +49,7 @@ struct ChunkParams {
   // the plan's
   float* partial;       // [CTAs][2][128 q_tiles][HD] sums, then
   float* partial_ml;    // [CTAs][2][128 q_tiles][2] their maximum (log2) and weight
-  ChunkMeta* meta;      // [CTAs]
+  ChunkMeta* meta;      // [CTAs], for the second kernel
   int32_t* arrivals;    // [CTAs] parts left of the item whose first part that CTA has; NULL: a second kernel joins
   int32_t* status;
   uint64_t wait_limit_ns;

@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
   const int32_t ctas = static_cast<int32_t>(min(static_cast<int64_t>(gridDim.x / team), total >> (p.q_tiles == 2 ? 8 : 7)));
   const int32_t number = blockIdx.x / team, member = blockIdx.x % team;
   if (number >= ctas) {
-    if (blockIdx.x == 0 && tid == 0) p.meta[0].ctas = 0;
+    if (tid == 0 && !p.arrivals) p.meta[blockIdx.x].rows = 0;
     return;
   }
   const int64_t from = chunk_from(total, ctas, number), to = chunk_from(total, ctas, number + 1);
@@ -634,13 +634,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     if (!mbar_wait(&sh.drained, 0, p.wait_limit_ns)) mbar_wait(&sh.drained, 0, 8 * p.wait_limit_ns);
   } else {
     // ---------------------------------- the walk's segments and queries ----
-    if (tid == kChunkThreads - 1) {
-      // what the joining kernel has to know of this CTA's first item
-      ChunkMeta m;
-      m.from = from;
-      m.begin = walk.begin, m.total = total, m.ctas = ctas;
-      m.lead = m.begin + walk.item.first_unit(0), m.last = m.begin + walk.item.first_unit(max(walk.item.tiles - 1, 0));
-      m.start = walk.seq.start, m.row0 = walk.item.row0, m.head = walk.head, m.rows = walk.item.rows, m.team = team;
+    if (tid == kChunkThreads - 1 && !p.arrivals) {
+      // The joining kernel's work at this cut: the item that it divides, where
+      // it is the item's first.  The CTAs with the item's first tile and with
+      // its last: those between them have some too.
+      ChunkMeta m{};
+      if (number > 0 && from > walk.begin && chunk_from(total, ctas, number - 1) <= walk.begin) {
+        m.lead = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(0)) * team + member;
+        m.last = chunk_owner(total, ctas, walk.begin + walk.item.first_unit(max(walk.item.tiles - 1, 0))) * team + member;
+        m.team = team, m.rows = m.lead == m.last ? 0 : walk.item.rows;
+        m.start = walk.seq.start, m.row0 = walk.item.row0, m.head = walk.head;
+      }
       p.meta[blockIdx.x] = m;
     }
     // The walk for the softmax warpgroups, whose registers have no room for it,
@@ -1030,30 +1034,21 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
 }
 
 // Joins the partial results of the items that a cut between CTAs divides, where
-// the main kernel leaves that to it: the blocks of cut x (between CTAs x - 1
-// and x) serve the item whose first cut it is, eight rows each.  A thread has
+// the main kernel leaves that to it: the blocks of cut x (where CTA x starts)
+// serve the item whose first cut it is, eight rows each; which CTAs have parts
+// of it the main kernel found (its two divisions of 64 bits in every thread
+// here: 18 us for the prompt of 8192, so 13).  A thread has
 // four columns of a row; a warp has eight rows of 16 columns, which is how they
 // lie side by side.
 template <typename T, int HD>
 __global__ void __launch_bounds__(HD * 2) chunk_join_kernel(const ChunkParams p) {
   griddep_wait();
-  const int cut = blockIdx.x + 1;
-  const int ctas = p.meta[0].ctas;
-  if (ctas == 0) return;
-  const int team = p.meta[0].team;
-  if (cut < team || cut >= ctas * team) return;
-  const ChunkMeta m = p.meta[cut];
-  const int64_t from_before = p.meta[cut - team].from;
-  if (m.from <= m.begin || from_before > m.begin) return;
-  // the CTAs with the item's first tile and with its last: those between them
-  // have some too
-  const int lead = chunk_owner(m.total, ctas, m.lead) * team + cut % team, last = chunk_owner(m.total, ctas, m.last) * team + cut % team;
-  if (lead == last) return;
+  const ChunkMeta m = p.meta[blockIdx.x + 1];
   const int lane = threadIdx.x & 31;
   const int r = blockIdx.y * 8 + (lane & 7);
   if (r >= m.rows) return;
   const int t = (m.row0 + r) / p.group;
-  attn_join_piece<T, HD>(p, lead, last, team, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
+  attn_join_piece<T, HD>(p, m.lead, m.last, m.team, r, ((threadIdx.x >> 5) * 4 + (lane >> 3)) * 4, m.start + t, m.head * p.group + (m.row0 + r) - t * p.group);
 }
 
 }  // namespace eg
