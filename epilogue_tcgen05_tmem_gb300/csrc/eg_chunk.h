@@ -60,7 +60,7 @@ struct ChunkParams {
 template <int HD>
 struct ChunkSmem {
   static constexpr uint32_t kTileBytes = 128u * HD * 2u;  // 128 rows of queries, keys or values
-  static constexpr uint32_t kExtra = 3072u;               // barriers, schedule, exchange of row statistics
+  static constexpr uint32_t kExtra = 3 * 1024u;              // barriers, schedule, exchange of row statistics
 };
 
 }  // namespace eg

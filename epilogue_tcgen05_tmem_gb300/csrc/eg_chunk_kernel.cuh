@@ -539,10 +539,17 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (lane == 0) mbar_arrive(&sh.turn[mine ^ 1]);
       ++turns;
     };
+    // The second warpgroup's products change hands between a pair and other
+    // items.  Who takes them over waits until the last of the other issuer's
+    // are over: else scores come where that warpgroup's weights still lie, and
+    // a wait for its weights passes at once.  The other's turns are over first,
+    // so the wait for its last sums is for no earlier ones.
+    bool theirs = false;
     bool ok = true;
     while (ok && walk.next(p)) {
       const uint32_t count = walk.count;
       const bool pair = walk.item.cost == 2;
+      if (pair != (mine == 1)) theirs = true;
       uint32_t slot_k = slot0, turn_k = turn0, slot_v = slot0, turn_v = turn0;
       step(slot_v, turn_v, count == 1 ? 1 : 2);
       if (!(ok = wait_all(&sh.q_full, segment))) break;
@@ -577,6 +584,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
       if (pair) {
         // tile i's keys, then the values of the one before, in the ring's order
         if (!(ok = wait_all(&sh.full[slot_k], turn_k) && my_turn())) break;
+        if (mine && theirs) {
+          if (used1 > 0 && !(ok = wait_all(&sh.o_done[1], used1 - 1))) break;
+          theirs = false;
+        }
         tc_fence_after();
         if (elect_one()) scores(mine);
         pass();
@@ -610,6 +621,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
           }
           if (j < count) {
             if (!(ok = wait_all(&sh.full[slot_k], turn_k))) break;
+            if (s && theirs) {
+              if (!(ok = my_turn() && wait_all(&sh.o_done[1], used1 - 1))) break;
+              theirs = false;
+            }
             tc_fence_after();
             if (elect_one()) {
               scores(s);

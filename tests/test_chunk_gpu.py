@@ -320,6 +320,20 @@ def test_offsets_past_32_bits():
     plan.close()
 
 
+@pytest.mark.parametrize("dtype,dim,hq,hk,window", [("f16", 80, 12, 3, 0), ("bf16", 128, 12, 3, 0), ("bf16", 64, 8, 2, 0), ("f16", 128, 8, 1, 200)])
+def test_many_sequences_whose_last_rows_are_few(dtype, dim, hq, hk, window):
+    """A CTA goes from pairs of row tiles to single ones and back; every run gives the same bits."""
+    rng = np.random.RandomState(dim)
+    n = rng.randint(247, 744, 47)
+    c = Case(dtype, hq, hk, dim, 64, np.zeros_like(n), n, window, 4 if window else 0, heads_first=True, seed=dim)
+    d, plan = c.device(), c.plan()
+    outs = [plan.run(**d) for _ in range(40)]
+    _check(c, outs[0])
+    assert all(torch.equal(o, outs[0]) for o in outs)
+    assert plan.device_status() == eg.EG_OK
+    plan.close()
+
+
 def test_same_every_time_and_on_another_stream():
     c = Case("bf16", 32, 8, 128, 16, [3000, 20, 0, 911], [50, 1, 300, 8], 700, 3, seed=9)
     d, plan = c.device(), c.plan()
